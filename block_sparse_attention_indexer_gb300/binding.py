@@ -28,8 +28,11 @@ _lib = ctypes.CDLL(LIB_PATH)
 # ---------------------------------------------------------------------------- C types
 MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_CUDA = range(5)
 MSA_OP_INDEXER_SCORES, MSA_OP_SELECT_BLOCKS, MSA_OP_SPARSE_ATTN, MSA_OP_DECODE = range(4)
-MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SEQLEN, MSA_DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+MSA_OP_FP8_APPEND, MSA_OP_FP8_ATTN, MSA_OP_FP8_ATTN_WEIGHTS, MSA_OP_EVICT = range(4, 8)
+MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SEQLEN, MSA_DEVERR_TIMEOUT, MSA_DEVERR_BAD_SCALE = 0x1, 0x2, 0x4, 0x8
 MSA_SCORE_MAX, MSA_SCORE_LSE = 0, 1
+MSA_TYPE_F32, MSA_TYPE_BF16, MSA_TYPE_E4M3 = range(3)
+MSA_E8M0_MIN, MSA_E8M0_MAX = 87, 167
 
 
 class _Config(ctypes.Structure):
@@ -45,6 +48,11 @@ class _Cache(ctypes.Structure):
                 ("num_pages", ctypes.c_int64)]
 
 
+class _Fp8Cache(ctypes.Structure):
+    _fields_ = [("k_data", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_data", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64)]
+
+
 class _Batch(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("max_blocks", ctypes.c_int32), ("q_len", ctypes.c_int32)]
@@ -52,6 +60,7 @@ class _Batch(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _CP, _CC, _CB = ctypes.POINTER(_Config), ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
+_CF = ctypes.POINTER(_Fp8Cache)
 _SIGS = {
     "msa_abi_version": (ctypes.c_int32, []),
     "msa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -66,6 +75,12 @@ _SIGS = {
     "msa_dcp_merge": (ctypes.c_int, [_CP, _CB, ctypes.c_int32, _P, _P, _P, _P]),
     "msa_sparse_attn_decode": (ctypes.c_int, [_CP, _CC, _CB, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "msa_decode": (ctypes.c_int, [_CP, _CC, _CB, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "msa_fp8_append": (ctypes.c_int, [_CP, _CF, _CB, _P, _P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _P,
+                                      ctypes.c_size_t, _P]),
+    "msa_fp8_attn": (ctypes.c_int, [_CP, _CF, _CB, _P, ctypes.c_int32, ctypes.c_int64, _P, _P, _P, _P, ctypes.c_float,
+                                    _P, _P, ctypes.c_size_t, _P]),
+    "msa_evict_blocks": (ctypes.c_int, [_CB, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P,
+                                        _P, ctypes.c_size_t, _P]),
     "msa_sparse_attn_decode_noalloc": (ctypes.c_int, [_CP, _CC, _CB, _P, _P, _P, _P, _P]),
     "msa_noalloc_read_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _P]),
     "msa_test_indexer_stall": (ctypes.c_int, [_CP, _CC, _CB, _P, _P, _P, ctypes.c_size_t, ctypes.c_uint32, _P]),
@@ -103,6 +118,38 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _shaped(t: Optional[torch.Tensor], shape, dtype, name):
+    """_ptr of a contiguous tensor that must have exactly this shape (None passes)."""
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _ptr(t, dtype, name)
+
+
+def _token_rows(t: torch.Tensor, shape, name):
+    """(pointer, token stride in elements) of a [B, T, heads, dim] tensor whose heads are
+    contiguous within a token and whose tokens are evenly spaced, b * T + t in order: a
+    contiguous tensor, or a slice of the heads of one (no copy is made)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    B, T, heads, dim = t.shape
+    sb, st, sh, sd = t.stride()
+    token = st if T > 1 else sb if B > 1 else heads * dim
+    if (sd != 1 or (heads > 1 and sh != dim) or (B > 1 and T > 1 and sb != T * st)):
+        raise ValueError(f"{name} must hold each token's heads contiguously and its tokens evenly spaced, "
+                         f"got strides {t.stride()}")
+    return t.data_ptr(), token
+
+
+def _on_one_device(*named):
+    """The device of the tensors of a call, all on one; the call is made with it current."""
+    got = {t.device for t in named if t is not None}
+    if len(got) > 1 or any(d.type != "cuda" for d in got):
+        raise ValueError(f"the tensors of a call must be on one CUDA device, got {sorted(map(str, got))}")
+    return torch.cuda.device(got.pop())
 
 
 def _stream(stream) -> int:
@@ -161,6 +208,56 @@ class PagedCache:
     @property
     def nbytes(self):
         return sum(t.numel() for t in self.tensors())
+
+
+class Fp8Cache:
+    """The FP8 K/V page pools (device tensors, uint8): E4M3 codes [P, groups, 128, 128] and
+    E8M0 scales [P, groups] (value = code * 2^(scale - 127)); new pages hold zeros."""
+
+    def __init__(self, num_pages: int, groups: int = 4, dim: int = 128, block: int = 128, device="cuda"):
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.k_data = torch.zeros(num_pages, groups, block, dim, **u8)
+        self.k_scale = torch.full((num_pages, groups), MSA_E8M0_MIN, **u8)
+        self.v_data = torch.zeros(num_pages, groups, block, dim, **u8)
+        self.v_scale = torch.full((num_pages, groups), MSA_E8M0_MIN, **u8)
+
+    @classmethod
+    def from_tensors(cls, k_data: torch.Tensor, k_scale: torch.Tensor, v_data: torch.Tensor, v_scale: torch.Tensor):
+        """A cache over pools the caller holds (no copy)."""
+        if k_data.dim() != 4:
+            raise ValueError("k_data must be [pages, groups, block, dim]")
+        self = cls.__new__(cls)
+        self.k_data, self.k_scale, self.v_data, self.v_scale = k_data, k_scale, v_data, v_scale
+        self.c()  # shapes, types and devices
+        return self
+
+    @property
+    def num_pages(self):
+        return self.k_data.shape[0]
+
+    @property
+    def groups(self):
+        return self.k_data.shape[1]
+
+    def tensors(self):
+        return (self.k_data, self.k_scale, self.v_data, self.v_scale)
+
+    def c(self):
+        pool, heads = tuple(self.k_data.shape), tuple(self.k_data.shape[:2])
+        return ctypes.byref(_Fp8Cache(_shaped(self.k_data, pool, torch.uint8, "k_data"),
+                                      _shaped(self.k_scale, heads, torch.uint8, "k_scale"),
+                                      _shaped(self.v_data, pool, torch.uint8, "v_data"),
+                                      _shaped(self.v_scale, heads, torch.uint8, "v_scale"), self.num_pages))
+
+    @property
+    def nbytes(self):
+        return sum(t.numel() for t in self.tensors())
+
+
+def _check_fp8_call(cfg: Config, cache: Fp8Cache):
+    want = (cfg.num_kv_groups, cfg.block_size, cfg.head_dim)
+    if tuple(cache.k_data.shape[1:]) != want:
+        raise ValueError(f"the cache's pages are {tuple(cache.k_data.shape[1:])}, the configuration's {want}")
 
 
 @dataclasses.dataclass
@@ -302,6 +399,70 @@ def msa_decode(cfg: Config, cache: PagedCache, batch: Batch, q: torch.Tensor, in
         _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"),
         _ptr(selection_out, torch.int32, "selection_out"), _ptr(workspace, None, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def msa_fp8_append(cfg: Config, cache: Fp8Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor,
+                   workspace: torch.Tensor, stream=None):
+    """The q_len newest K and V rows of every sequence into their FP8 pages (include/msa.h).
+    k, v: float32 or bfloat16 [B, T, G, 128], contiguous or a slice of the heads of a fused
+    projection's rows.  workspace: alloc_workspace(MSA_OP_FP8_APPEND, ...)."""
+    _check_fp8_call(cfg, cache)
+    types = {torch.float32: MSA_TYPE_F32, torch.bfloat16: MSA_TYPE_BF16}
+    if k.dtype not in types or v.dtype != k.dtype:
+        raise TypeError(f"k and v must both be float32 or both bfloat16, got {k.dtype} and {v.dtype}")
+    shape = (batch.batch, batch.q_len, cfg.num_kv_groups, cfg.head_dim)
+    with _on_one_device(k, v, *cache.tensors(), batch.block_table, batch.seq_lens, workspace):
+        kp, ks = _token_rows(k, shape, "k")
+        vp, vs = _token_rows(v, shape, "v")
+        _check("msa_fp8_append", _lib.msa_fp8_append(
+            cfg.c(), cache.c(), batch.c(), kp, vp, types[k.dtype], ks, vs, _ptr(workspace, None, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def msa_fp8_attn(cfg: Config, cache: Fp8Cache, batch: Batch, q: torch.Tensor, out: torch.Tensor,
+                 lse: Optional[torch.Tensor], workspace: torch.Tensor, selection: Optional[torch.Tensor] = None,
+                 weight_in: Optional[torch.Tensor] = None, weight_out: Optional[torch.Tensor] = None,
+                 weight_decay: float = 1.0, stream=None):
+    """Attention over the FP8 pages (include/msa.h): dense causal, or over selection
+    [B, T, G, 16].  q: uint8 (E4M3 codes) or bfloat16 [B, T, H, 128], contiguous or a slice of the
+    heads of wider rows; out: bfloat16 [B, T, H, 128]; lse: float32 [B, T, H] or None.
+    weight_out (float32 [B, max_blocks]) receives weight_decay * weight_in plus the attention
+    weight that each block collected; it may be weight_in.  workspace:
+    alloc_workspace(MSA_OP_FP8_ATTN_WEIGHTS, ...) with weight_out, else MSA_OP_FP8_ATTN."""
+    _check_fp8_call(cfg, cache)
+    types = {torch.uint8: MSA_TYPE_E4M3, torch.bfloat16: MSA_TYPE_BF16}
+    if q.dtype not in types:
+        raise TypeError(f"q must be uint8 (E4M3 codes) or bfloat16, got {q.dtype}")
+    B, T, H = batch.batch, batch.q_len, cfg.num_heads
+    table = (B, batch.max_blocks)
+    with _on_one_device(q, *cache.tensors(), batch.block_table, batch.seq_lens, workspace, selection, out, lse,
+                        weight_in, weight_out):
+        qp, qs = _token_rows(q, (B, T, H, cfg.head_dim), "q")
+        _check("msa_fp8_attn", _lib.msa_fp8_attn(
+            cfg.c(), cache.c(), batch.c(), qp, types[q.dtype], qs,
+            _shaped(selection, (B, T, cfg.num_kv_groups, 16), torch.int32, "selection"),
+            _shaped(out, (B, T, H, cfg.head_dim), torch.bfloat16, "out"),
+            _shaped(lse, (B, T, H), torch.float32, "lse"), _shaped(weight_in, table, torch.float32, "weight_in"),
+            weight_decay, _shaped(weight_out, table, torch.float32, "weight_out"), _ptr(workspace, None, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def msa_evict_blocks(batch: Batch, weight: torch.Tensor, budget: int, keep_first: int, keep_last: int,
+                     table_out: torch.Tensor, seq_lens_out: torch.Tensor, weight_out: torch.Tensor,
+                     freed: torch.Tensor, freed_count: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """Cuts every sequence to at most `budget` blocks by dropping those of least weight
+    (include/msa.h).  table_out, seq_lens_out and weight_out may be batch.block_table,
+    batch.seq_lens and weight.  workspace: alloc_workspace(MSA_OP_EVICT, ...)."""
+    B, table = batch.batch, (batch.batch, batch.max_blocks)
+    with _on_one_device(batch.block_table, batch.seq_lens, weight, table_out, seq_lens_out, weight_out, freed,
+                        freed_count, workspace):
+        _check("msa_evict_blocks", _lib.msa_evict_blocks(
+            batch.c(), _shaped(weight, table, torch.float32, "weight"), budget, keep_first, keep_last,
+            _shaped(table_out, table, torch.int32, "table_out"),
+            _shaped(seq_lens_out, (B,), torch.int32, "seq_lens_out"),
+            _shaped(weight_out, table, torch.float32, "weight_out"), _shaped(freed, table, torch.int32, "freed"),
+            _shaped(freed_count, (B,), torch.int32, "freed_count"), _ptr(workspace, None, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def msa_read_device_error(workspace: torch.Tensor, stream=None) -> int:

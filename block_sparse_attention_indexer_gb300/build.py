@@ -17,9 +17,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmsa.so")
-SOURCES = ["api.cu", "quant.cu", "indexer.cu", "prefill.cu", "select.cu", "attention.cu", "prefill_attn.cu", "spec_indexer.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "quant.cu", "indexer.cu", "prefill.cu", "select.cu", "attention.cu", "prefill_attn.cu", "spec_indexer.cu", "noalloc.cu",
+           "api_fp8.cu", "fp8_append.cu", "fp8_attn.cu", "evict.cu"]
 HEADERS = ["msa_device.cuh", "msa_kernels.h", "api_internal.h", "select_row.cuh", "umma.cuh", "indexer_tile.cuh",
-           "attention_tile.cuh", "attention_team.cuh"]
+           "attention_tile.cuh", "attention_team.cuh", "fp8_device.cuh", "fp8_kernels.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

@@ -12,16 +12,7 @@
 
 using namespace msa;
 
-namespace {
-
-constexpr size_t kWsAlign = 256;
-constexpr size_t kErrBytes = 256;  // error word + padding
-constexpr int kMaxDevices = 64;
-
-size_t align_up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-msa_status_t check_config(const msa_config_t* c) {
+msa_status_t msa::check_config(const msa_config_t* c) {
   if (c == nullptr) return MSA_ERR_INVALID_ARG;
   if (c->num_kv_groups < 1 || c->num_kv_groups > 8 || c->heads_per_group < 1 || c->heads_per_group > 8)
     return MSA_ERR_UNSUPPORTED;
@@ -34,7 +25,7 @@ msa_status_t check_config(const msa_config_t* c) {
   return MSA_OK;
 }
 
-msa_status_t check_batch(const msa_batch_t* b) {
+msa_status_t msa::check_batch(const msa_batch_t* b) {
   if (b == nullptr) return MSA_ERR_INVALID_ARG;
   if (b->batch < 0 || b->max_blocks < 1 || b->q_len < 1) return MSA_ERR_INVALID_ARG;
   if (b->batch > 0 && (b->block_table == nullptr || b->seq_lens == nullptr)) return MSA_ERR_INVALID_ARG;
@@ -43,6 +34,10 @@ msa_status_t check_batch(const msa_batch_t* b) {
   if (static_cast<int64_t>(b->max_blocks) * 128 > INT32_MAX) return MSA_ERR_UNSUPPORTED;
   return MSA_OK;
 }
+
+namespace {
+
+constexpr int kMaxDevices = 64;
 
 msa_status_t check_cache(const msa_cache_t* c, bool idx, bool kv) {
   if (c == nullptr || c->num_pages < 1 || c->num_pages > INT32_MAX) return MSA_ERR_INVALID_ARG;
@@ -55,7 +50,9 @@ msa_status_t check_cache(const msa_cache_t* c, bool idx, bool kv) {
   return MSA_OK;
 }
 
-int num_sms_of_current_device() {
+}  // namespace
+
+int msa::num_sms_of_current_device() {
   static int cache[kMaxDevices] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
@@ -65,6 +62,8 @@ int num_sms_of_current_device() {
   if (dev < kMaxDevices) cache[dev] = n;
   return n;
 }
+
+namespace {
 
 int64_t rows_tg(const msa_batch_t* b, const msa_config_t* c) {
   return static_cast<int64_t>(b->batch) * b->q_len * c->num_kv_groups;
@@ -89,12 +88,14 @@ size_t attn_scratch_bytes(const msa_config_t* c, const msa_batch_t* b) {
              : partial_bytes();
 }
 
+}  // namespace
 
-
-float scale_log2(const msa_config_t* c) {
+float msa::scale_log2(const msa_config_t* c) {
   const float sm = c->softmax_scale > 0.0f ? c->softmax_scale : 1.0f / std::sqrt(static_cast<float>(c->head_dim));
   return sm * 1.4426950408889634f;
 }
+
+namespace {
 
 msa_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
 
@@ -247,6 +248,10 @@ size_t msa_workspace_bytes(msa_op_t op, const msa_config_t* cfg, const msa_batch
     case MSA_OP_SPARSE_ATTN: return kErrBytes + attn_scratch_bytes(cfg, batch);
     case MSA_OP_DECODE:
       return kErrBytes + scores_bytes(cfg, batch) + 2 * sel_bytes(cfg, batch) + attn_scratch_bytes(cfg, batch);
+    case MSA_OP_FP8_APPEND:
+    case MSA_OP_EVICT: return kErrBytes;
+    case MSA_OP_FP8_ATTN: return fp8_attn_workspace_bytes(cfg, batch, false);
+    case MSA_OP_FP8_ATTN_WEIGHTS: return fp8_attn_workspace_bytes(cfg, batch, true);
   }
   return 0;
 }

@@ -71,6 +71,7 @@ typedef enum {
 #define MSA_DEVERR_BAD_PAGE 0x1u    /* a block-table entry outside [0, num_pages) */
 #define MSA_DEVERR_BAD_SEQLEN 0x2u  /* seq_len < q_len (but > 0), or > max_blocks*128 */
 #define MSA_DEVERR_TIMEOUT 0x4u     /* a bounded wait inside a kernel gave up */
+#define MSA_DEVERR_BAD_SCALE 0x8u   /* an FP8 page scale outside MSA_E8M0_MIN..MSA_E8M0_MAX */
 
 /* Block-score reduction over the visible keys of a block ("MiniMax M3 x vLLM：百万 token
  * 多模态推理的 Day-0 部署", §Prefill 执行 step 2: a block-level rule such as max or
@@ -125,8 +126,37 @@ typedef enum {
   MSA_OP_INDEXER_SCORES = 0,
   MSA_OP_SELECT_BLOCKS = 1,
   MSA_OP_SPARSE_ATTN = 2,
-  MSA_OP_DECODE = 3
+  MSA_OP_DECODE = 3,
+  MSA_OP_FP8_APPEND = 4,
+  MSA_OP_FP8_ATTN = 5,          /* msa_fp8_attn without weight_out */
+  MSA_OP_FP8_ATTN_WEIGHTS = 6,  /* msa_fp8_attn with weight_out (or without) */
+  MSA_OP_EVICT = 7
 } msa_op_t;
+
+/* Element types of the arguments that come in more than one. */
+#define MSA_TYPE_F32 0
+#define MSA_TYPE_BF16 1
+#define MSA_TYPE_E4M3 2
+
+/* The paged FP8 K/V cache (device, caller-owned): E4M3 codes with one power-of-two scale for
+ * each page (block of 128 tokens) and KV head, stored as an E8M0 byte; the value of a code is
+ * code * 2^(scale - 127).  It shares block tables and page numbers with the NVFP4 pools
+ * ("vLLM liefert Day-0-Unterstützung für MiniMax-M3.1-Flash", §Was ist neu in der
+ * MiniMax-M3.1-Architektur, sizes the FP8 K/V cache it compares with at 61,440 B/token).
+ *   k_data, v_data    uint8 E4M3 [num_pages][G][128][128]
+ *   k_scale, v_scale  uint8 E8M0 [num_pages][G], MSA_E8M0_MIN..MSA_E8M0_MAX (2^-40 .. 2^40:
+ *                     any K scale times any logit, and any V scale over any other, stays
+ *                     inside float32's range)
+ * The data pointers are 16-byte aligned; the scale pointers may have any alignment. */
+#define MSA_E8M0_MIN 87
+#define MSA_E8M0_MAX 167
+typedef struct {
+  uint8_t* k_data;
+  uint8_t* k_scale;
+  uint8_t* v_data;
+  uint8_t* v_scale;
+  int64_t num_pages;
+} msa_fp8_cache_t;
 
 /* ABI version of the loaded library (MSA_ABI_VERSION). */
 int32_t msa_abi_version(void);
@@ -247,6 +277,87 @@ msa_status_t msa_sparse_attn_decode(const msa_config_t* cfg, const msa_cache_t* 
 msa_status_t msa_decode(const msa_config_t* cfg, const msa_cache_t* cache, const msa_batch_t* batch,
                         const uint8_t* q, const uint8_t* index_q, uint16_t* out, float* lse,
                         int32_t* selection_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* FP8 cache write: the q_len newest K and V rows of every sequence (positions
+ * seq_lens[b] - q_len .. seq_lens[b] - 1) into their pages, as E4M3 with the scale of their
+ * (page, KV head).
+ *   k, v      float32 or bfloat16 (x_type MSA_TYPE_F32 / MSA_TYPE_BF16)
+ *             [batch][q_len][G][head_dim]; the heads of a token are contiguous, token i (=
+ *             b * q_len + t) starts k_stride (v_stride) elements after token i - 1, so that
+ *             slices of one fused projection's rows need no copy.  Both pointers and both
+ *             strides in bytes are multiples of 16; strides >= G * head_dim.
+ *   cache     written: the pages holding those positions
+ * For each touched (page, KV head), e is the smallest exponent in -40..40 with amax of the
+ * new rows <= 448 * 2^e (NaN elements do not count; -40 for all zeros).  A page that already
+ * holds older tokens of the sequence (positions before seq_lens[b] - q_len) keeps its scale
+ * when that is larger than 2^e; otherwise its older rows are re-encoded under 2^e, each code
+ * times 2^(e_old - e) rounded to E4M3 once more.  Codes: x * 2^-e rounded to nearest even, saturating at
+ * +-448 (infinities too), the sign of zero kept, NaN as a NaN code.  Rows of the page at
+ * seq_lens[b] and beyond are left as they are, and so is every other page.
+ * A page is written by one sequence per call: two sequences whose tables give one page to
+ * written blocks leave its contents unspecified.  Sequences of length 0 write nothing; an old scale
+ * outside MSA_E8M0_MIN..MAX sets MSA_DEVERR_BAD_SCALE and leaves the page head alone.
+ * workspace: msa_workspace_bytes(MSA_OP_FP8_APPEND, ...) (the error word). */
+msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cache, const msa_batch_t* batch,
+                            const void* k, const void* v, int32_t x_type, int64_t k_stride, int64_t v_stride,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention over the FP8 cache, dense or sparse: the layers that keep full attention next to
+ * the MSA layers, MSA layers over an 8-bit cache, and what eviction needs to know.
+ * Query row (b, t, h), position pos = seq_lens[b] - q_len + t, attends with logits
+ * z_j = (q . k_j) * softmax_scale to the keys j <= pos (selection NULL: dense causal), or to
+ * those of them in the blocks selection[b][t][h / Hg][:] (the layout of msa_select_blocks, -1
+ * for an empty place, a block listed once):
+ *   out  = sum_j e^{z_j - lse} v_j   bfloat16 [batch][q_len][G*Hg][D]
+ *   lse  = ln sum_j e^{z_j}          float [batch][q_len][G*Hg], may be NULL
+ * A row with no key (padding, an empty selection, only bad pages) gives out 0 and lse -inf.
+ *   q       E4M3 or bfloat16 (q_type MSA_TYPE_E4M3 / MSA_TYPE_BF16) [batch][q_len][G*Hg][D];
+ *           the heads of a token are contiguous, tokens are q_stride elements apart; pointer
+ *           and stride in bytes multiples of 16, q_stride >= G * Hg * D.  bfloat16 values more
+ *           than 2^14 below the largest of their row may be rounded, by at most 2^-18 of that
+ *           largest value.
+ *   weight_out  float [batch][max_blocks] or NULL: how much attention each block collected,
+ *           weight_out[b][n] = weight_decay * weight_in[b][n]
+ *                              + sum over t, h and the keys j of block n of e^{z_j - lse}
+ *           for every n in 0 .. max_blocks - 1 (a missing weight_in counts as 0).  weight_in may be
+ *           weight_out, but not overlap it otherwise.  weight_decay in 0..1.
+ * K and V codes must be finite where they are visible to some row of the call, else that
+ * row's results are NaN as the formula has it; codes past seq_lens[b] may be anything, and a
+ * NaN code reaches only rows that see its key.  A page whose table entry or scale is bad is skipped
+ * (MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SCALE), a sequence whose length is bad gives empty rows
+ * (MSA_DEVERR_BAD_SEQLEN).
+ * Results do not depend on how the work is split beyond rounding, and are the same bits in
+ * every call with the same arguments on one GPU.
+ * workspace: msa_workspace_bytes(MSA_OP_FP8_ATTN_WEIGHTS, ...) with weight_out, else
+ * MSA_OP_FP8_ATTN; calls that can overlap need a workspace each.
+ * Errors: MSA_ERR_UNSUPPORTED for num_pages * G > 2^24 (a tensor map's row coordinate). */
+msa_status_t msa_fp8_attn(const msa_config_t* cfg, const msa_fp8_cache_t* cache, const msa_batch_t* batch,
+                          const void* q, int32_t q_type, int64_t q_stride, const int32_t* selection, uint16_t* out,
+                          float* lse, const float* weight_in, float weight_decay, float* weight_out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Eviction by accumulated attention weight: cuts every sequence to at most `budget` blocks by
+ * dropping the blocks of least weight from its block table.
+ * Of the ceil(seq_lens[b] / 128) blocks of a sequence with more than `budget`, the first
+ * keep_first and the last keep_last stay, and the best of the others by (weight descending,
+ * block ascending; NaN below -inf) up to `budget` in all; shorter sequences stay whole.
+ *   weight         float [batch][max_blocks]  (msa_fp8_attn's weight_out, or any other score)
+ *   table_out      int32 [batch][max_blocks]  pages of the blocks that stay, in order; -1 behind
+ *   seq_lens_out   int32 [batch]              seq_lens[b] - 128 * (blocks dropped)
+ *   weight_out     float [batch][max_blocks]  their weights; 0 behind
+ *   freed          int32 [batch][max_blocks]  table entries of the dropped blocks, in order; -1 behind
+ *   freed_count    int32 [batch]
+ * table_out, seq_lens_out and weight_out may be the inputs themselves; any other overlap of
+ * two arrays is MSA_ERR_INVALID_ARG.  1 <= keep_last, 0 <= keep_first, keep_first + keep_last
+ * <= budget.  Keys keep the rotary position they were written with; causal order among what
+ * stays is unchanged, so every entry point runs on the shorter table (the index keys of the
+ * dropped pages go with them).  Table entries are moved, never followed.  A length below 0 or above
+ * max_blocks * 128 sets MSA_DEVERR_BAD_SEQLEN and the row is copied as it is, nothing freed.
+ * workspace: msa_workspace_bytes(MSA_OP_EVICT, ...) (the error word; cfg is only checked). */
+msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int32_t budget, int32_t keep_first,
+                              int32_t keep_last, int32_t* table_out, int32_t* seq_lens_out, float* weight_out,
+                              int32_t* freed, int32_t* freed_count, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /* The stage-3 sparse attention of msa_sparse_attn_decode for callers that cannot allocate
  * device memory, or cannot hand the library a workspace: for example a plugin inside a host
