@@ -120,36 +120,69 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor"):
     return t.data_ptr()
 
 
-def _shaped(t: Optional[torch.Tensor], shape, dtype, name):
-    """_ptr of a contiguous tensor that must have exactly this shape (None passes)."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _on(t: torch.Tensor, name: str) -> int:
+    """Index of the CUDA device that t is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _at(t: Optional[torch.Tensor], shape, dtype, dev: int, name: str):
+    """Pointer of a contiguous tensor that must have exactly this shape and type and be on
+    device `dev` (None passes).  The calls below make these checks for up to nine tensors, so
+    each is a plain comparison: a decode step's launch is a few microseconds."""
+    if t is None:
+        return None
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _ptr(t, dtype, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on CUDA device {dev} like the block table, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _token_rows(t: torch.Tensor, shape, name):
+def _space(t: torch.Tensor, dev: int):
+    """(pointer, bytes) of a workspace."""
+    if t.get_device() != dev:
+        raise ValueError(f"workspace must be on CUDA device {dev} like the block table, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _launch(name: str, fn, dev: int, stream, *args):
+    """Calls the C entry point with device `dev` current, on `stream` or that device's current
+    stream."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    _check(name, status)
+
+
+def _token_rows(t: torch.Tensor, shape, dev: int, name: str):
     """(pointer, token stride in elements) of a [B, T, heads, dim] tensor whose heads are
     contiguous within a token and whose tokens are evenly spaced, b * T + t in order: a
     contiguous tensor, or a slice of the heads of one (no copy is made)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on CUDA device {dev} like the block table, got {t.device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    B, T, heads, dim = t.shape
+    B, T, heads, dim = shape
     sb, st, sh, sd = t.stride()
-    token = st if T > 1 else sb if B > 1 else heads * dim
-    if (sd != 1 or (heads > 1 and sh != dim) or (B > 1 and T > 1 and sb != T * st)):
+    if sd != 1 or (heads > 1 and sh != dim) or (B > 1 and T > 1 and sb != T * st):
         raise ValueError(f"{name} must hold each token's heads contiguously and its tokens evenly spaced, "
                          f"got strides {t.stride()}")
-    return t.data_ptr(), token
-
-
-def _on_one_device(*named):
-    """The device of the tensors of a call, all on one; the call is made with it current."""
-    got = {t.device for t in named if t is not None}
-    if len(got) > 1 or any(d.type != "cuda" for d in got):
-        raise ValueError(f"the tensors of a call must be on one CUDA device, got {sorted(map(str, got))}")
-    return torch.cuda.device(got.pop())
+    return t.data_ptr(), st if T > 1 else sb if B > 1 else heads * dim
 
 
 def _stream(stream) -> int:
@@ -216,48 +249,65 @@ class Fp8Cache:
 
     def __init__(self, num_pages: int, groups: int = 4, dim: int = 128, block: int = 128, device="cuda"):
         u8 = dict(dtype=torch.uint8, device=device)
-        self.k_data = torch.zeros(num_pages, groups, block, dim, **u8)
-        self.k_scale = torch.full((num_pages, groups), MSA_E8M0_MIN, **u8)
-        self.v_data = torch.zeros(num_pages, groups, block, dim, **u8)
-        self.v_scale = torch.full((num_pages, groups), MSA_E8M0_MIN, **u8)
+        pool, heads = (num_pages, groups, block, dim), (num_pages, groups)
+        self._hold(torch.zeros(pool, **u8), torch.full(heads, MSA_E8M0_MIN, **u8),
+                   torch.zeros(pool, **u8), torch.full(heads, MSA_E8M0_MIN, **u8))
 
     @classmethod
     def from_tensors(cls, k_data: torch.Tensor, k_scale: torch.Tensor, v_data: torch.Tensor, v_scale: torch.Tensor):
         """A cache over pools the caller holds (no copy)."""
-        if k_data.dim() != 4:
-            raise ValueError("k_data must be [pages, groups, block, dim]")
         self = cls.__new__(cls)
-        self.k_data, self.k_scale, self.v_data, self.v_scale = k_data, k_scale, v_data, v_scale
-        self.c()  # shapes, types and devices
+        self._hold(k_data, k_scale, v_data, v_scale)
         return self
 
-    @property
-    def num_pages(self):
-        return self.k_data.shape[0]
+    def _hold(self, k_data, k_scale, v_data, v_scale):
+        # checked once: the pools of a cache are not replaced, so a call takes the struct as it is
+        if k_data.dim() != 4:
+            raise ValueError("k_data must be [pages, groups, block, dim]")
+        pool, heads, self.device_index = k_data.shape, k_data.shape[:2], _on(k_data, "k_data")
+        self._tensors = (k_data, k_scale, v_data, v_scale)
+        u8 = torch.uint8
+        self._c = _Fp8Cache(_at(k_data, pool, u8, self.device_index, "k_data"),
+                            _at(k_scale, heads, u8, self.device_index, "k_scale"),
+                            _at(v_data, pool, u8, self.device_index, "v_data"),
+                            _at(v_scale, heads, u8, self.device_index, "v_scale"), pool[0])
+        self._pages = tuple(pool[1:])
 
-    @property
-    def groups(self):
-        return self.k_data.shape[1]
+    k_data = property(lambda self: self._tensors[0])
+    k_scale = property(lambda self: self._tensors[1])
+    v_data = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    num_pages = property(lambda self: self._c.num_pages)
+    groups = property(lambda self: self._pages[0])
 
     def tensors(self):
-        return (self.k_data, self.k_scale, self.v_data, self.v_scale)
+        return self._tensors
 
     def c(self):
-        pool, heads = tuple(self.k_data.shape), tuple(self.k_data.shape[:2])
-        return ctypes.byref(_Fp8Cache(_shaped(self.k_data, pool, torch.uint8, "k_data"),
-                                      _shaped(self.k_scale, heads, torch.uint8, "k_scale"),
-                                      _shaped(self.v_data, pool, torch.uint8, "v_data"),
-                                      _shaped(self.v_scale, heads, torch.uint8, "v_scale"), self.num_pages))
+        return ctypes.byref(self._c)
 
     @property
     def nbytes(self):
-        return sum(t.numel() for t in self.tensors())
+        return sum(t.numel() for t in self._tensors)
 
 
-def _check_fp8_call(cfg: Config, cache: Fp8Cache):
-    want = (cfg.num_kv_groups, cfg.block_size, cfg.head_dim)
-    if tuple(cache.k_data.shape[1:]) != want:
-        raise ValueError(f"the cache's pages are {tuple(cache.k_data.shape[1:])}, the configuration's {want}")
+def _fp8_call(cfg: Config, cache: Fp8Cache, batch: Batch) -> int:
+    """Checks that the configuration fits the cache, and both tensors of the batch: their device."""
+    if cache._pages != (cfg.num_kv_groups, cfg.block_size, cfg.head_dim):
+        raise ValueError(f"the cache's pages are {cache._pages}, the configuration's "
+                         f"{(cfg.num_kv_groups, cfg.block_size, cfg.head_dim)}")
+    dev = _batch_device(batch)
+    if cache.device_index != dev:
+        raise ValueError(f"the cache is on CUDA device {cache.device_index}, the block table on {dev}")
+    return dev
+
+
+def _batch_device(batch: Batch) -> int:
+    dev = _on(batch.block_table, "block_table")
+    if batch.seq_lens.get_device() != dev or batch.seq_lens.shape != (batch.block_table.shape[0],):
+        raise ValueError(f"seq_lens must be [batch] on CUDA device {dev} like the block table, "
+                         f"got {tuple(batch.seq_lens.shape)} on {batch.seq_lens.device}")
+    return dev
 
 
 @dataclasses.dataclass
@@ -401,22 +451,24 @@ def msa_decode(cfg: Config, cache: PagedCache, batch: Batch, q: torch.Tensor, in
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+_ROW_TYPES = {torch.float32: MSA_TYPE_F32, torch.bfloat16: MSA_TYPE_BF16}
+_QUERY_TYPES = {torch.uint8: MSA_TYPE_E4M3, torch.bfloat16: MSA_TYPE_BF16}
+
+
 def msa_fp8_append(cfg: Config, cache: Fp8Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor,
                    workspace: torch.Tensor, stream=None):
     """The q_len newest K and V rows of every sequence into their FP8 pages (include/msa.h).
     k, v: float32 or bfloat16 [B, T, G, 128], contiguous or a slice of the heads of a fused
     projection's rows.  workspace: alloc_workspace(MSA_OP_FP8_APPEND, ...)."""
-    _check_fp8_call(cfg, cache)
-    types = {torch.float32: MSA_TYPE_F32, torch.bfloat16: MSA_TYPE_BF16}
-    if k.dtype not in types or v.dtype != k.dtype:
+    dev = _fp8_call(cfg, cache, batch)
+    kind = _ROW_TYPES.get(k.dtype)
+    if kind is None or v.dtype != k.dtype:
         raise TypeError(f"k and v must both be float32 or both bfloat16, got {k.dtype} and {v.dtype}")
     shape = (batch.batch, batch.q_len, cfg.num_kv_groups, cfg.head_dim)
-    with _on_one_device(k, v, *cache.tensors(), batch.block_table, batch.seq_lens, workspace):
-        kp, ks = _token_rows(k, shape, "k")
-        vp, vs = _token_rows(v, shape, "v")
-        _check("msa_fp8_append", _lib.msa_fp8_append(
-            cfg.c(), cache.c(), batch.c(), kp, vp, types[k.dtype], ks, vs, _ptr(workspace, None, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream(stream)))
+    kp, ks = _token_rows(k, shape, dev, "k")
+    vp, vs = _token_rows(v, shape, dev, "v")
+    _launch("msa_fp8_append", _lib.msa_fp8_append, dev, stream, cfg.c(), cache.c(), batch.c(), kp, vp, kind, ks, vs,
+            *_space(workspace, dev))
 
 
 def msa_fp8_attn(cfg: Config, cache: Fp8Cache, batch: Batch, q: torch.Tensor, out: torch.Tensor,
@@ -429,22 +481,19 @@ def msa_fp8_attn(cfg: Config, cache: Fp8Cache, batch: Batch, q: torch.Tensor, ou
     weight_out (float32 [B, max_blocks]) receives weight_decay * weight_in plus the attention
     weight that each block collected; it may be weight_in.  workspace:
     alloc_workspace(MSA_OP_FP8_ATTN_WEIGHTS, ...) with weight_out, else MSA_OP_FP8_ATTN."""
-    _check_fp8_call(cfg, cache)
-    types = {torch.uint8: MSA_TYPE_E4M3, torch.bfloat16: MSA_TYPE_BF16}
-    if q.dtype not in types:
+    dev = _fp8_call(cfg, cache, batch)
+    kind = _QUERY_TYPES.get(q.dtype)
+    if kind is None:
         raise TypeError(f"q must be uint8 (E4M3 codes) or bfloat16, got {q.dtype}")
-    B, T, H = batch.batch, batch.q_len, cfg.num_heads
-    table = (B, batch.max_blocks)
-    with _on_one_device(q, *cache.tensors(), batch.block_table, batch.seq_lens, workspace, selection, out, lse,
-                        weight_in, weight_out):
-        qp, qs = _token_rows(q, (B, T, H, cfg.head_dim), "q")
-        _check("msa_fp8_attn", _lib.msa_fp8_attn(
-            cfg.c(), cache.c(), batch.c(), qp, types[q.dtype], qs,
-            _shaped(selection, (B, T, cfg.num_kv_groups, 16), torch.int32, "selection"),
-            _shaped(out, (B, T, H, cfg.head_dim), torch.bfloat16, "out"),
-            _shaped(lse, (B, T, H), torch.float32, "lse"), _shaped(weight_in, table, torch.float32, "weight_in"),
-            weight_decay, _shaped(weight_out, table, torch.float32, "weight_out"), _ptr(workspace, None, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream(stream)))
+    table, T, H = batch.block_table.shape, batch.q_len, cfg.num_heads
+    B = table[0]
+    rows = (B, T, H, cfg.head_dim)
+    qp, qs = _token_rows(q, rows, dev, "q")
+    _launch("msa_fp8_attn", _lib.msa_fp8_attn, dev, stream, cfg.c(), cache.c(), batch.c(), qp, kind, qs,
+            _at(selection, (B, T, cfg.num_kv_groups, 16), torch.int32, dev, "selection"),
+            _at(out, rows, torch.bfloat16, dev, "out"), _at(lse, rows[:3], torch.float32, dev, "lse"),
+            _at(weight_in, table, torch.float32, dev, "weight_in"), weight_decay,
+            _at(weight_out, table, torch.float32, dev, "weight_out"), *_space(workspace, dev))
 
 
 def msa_evict_blocks(batch: Batch, weight: torch.Tensor, budget: int, keep_first: int, keep_last: int,
@@ -453,16 +502,14 @@ def msa_evict_blocks(batch: Batch, weight: torch.Tensor, budget: int, keep_first
     """Cuts every sequence to at most `budget` blocks by dropping those of least weight
     (include/msa.h).  table_out, seq_lens_out and weight_out may be batch.block_table,
     batch.seq_lens and weight.  workspace: alloc_workspace(MSA_OP_EVICT, ...)."""
-    B, table = batch.batch, (batch.batch, batch.max_blocks)
-    with _on_one_device(batch.block_table, batch.seq_lens, weight, table_out, seq_lens_out, weight_out, freed,
-                        freed_count, workspace):
-        _check("msa_evict_blocks", _lib.msa_evict_blocks(
-            batch.c(), _shaped(weight, table, torch.float32, "weight"), budget, keep_first, keep_last,
-            _shaped(table_out, table, torch.int32, "table_out"),
-            _shaped(seq_lens_out, (B,), torch.int32, "seq_lens_out"),
-            _shaped(weight_out, table, torch.float32, "weight_out"), _shaped(freed, table, torch.int32, "freed"),
-            _shaped(freed_count, (B,), torch.int32, "freed_count"), _ptr(workspace, None, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _batch_device(batch)
+    table = batch.block_table.shape
+    rows, i32, f32 = table[:1], torch.int32, torch.float32
+    _launch("msa_evict_blocks", _lib.msa_evict_blocks, dev, stream, batch.c(), _at(weight, table, f32, dev, "weight"),
+            budget, keep_first, keep_last, _at(table_out, table, i32, dev, "table_out"),
+            _at(seq_lens_out, rows, i32, dev, "seq_lens_out"), _at(weight_out, table, f32, dev, "weight_out"),
+            _at(freed, table, i32, dev, "freed"), _at(freed_count, rows, i32, dev, "freed_count"),
+            *_space(workspace, dev))
 
 
 def msa_read_device_error(workspace: torch.Tensor, stream=None) -> int:

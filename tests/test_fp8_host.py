@@ -98,35 +98,89 @@ def test_evict_refusals(msa):
     assert call(bt=b._Batch(None, None, 0, 8, 1)) == 0
 
 
-def test_binding_checks_strides_and_devices(msa):
+class _Dev:
+    """A tensor's shape, type and strides as if it were on a device (nothing is followed)."""
+
+    is_cuda = True
+
+    def __init__(self, t, dev=0):
+        self.t, self.shape, self.dtype, self.dev, self.device = t, t.shape, t.dtype, dev, f"cuda:{dev}"
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.dev
+
+    def data_ptr(self):
+        return 64
+
+
+def test_binding_checks_strides(msa):
     import torch
-    b = msa.binding
-    f = b._token_rows
-    with pytest.raises(ValueError, match="CUDA"):
-        f(torch.zeros(2, 3, 4, 128), (2, 3, 4, 128), "k")
-    with pytest.raises(ValueError, match="one CUDA device"):
-        b._on_one_device(torch.zeros(1))
-
-    class T:  # a tensor's shape and strides, without a device
-        is_cuda = True
-
-        def __init__(self, t):
-            self.t, self.shape = t, t.shape
-
-        def stride(self):
-            return self.t.stride()
-
-        def data_ptr(self):
-            return 64
-
+    f = msa.binding._token_rows
+    with pytest.raises(ValueError, match="device"):
+        f(torch.zeros(2, 3, 4, 128), (2, 3, 4, 128), 0, "k")
+    with pytest.raises(ValueError, match="device 0"):
+        f(_Dev(torch.zeros(2, 3, 4, 128), 1), (2, 3, 4, 128), 0, "k")
     wide = torch.zeros(2, 5, 8, 128)
-    assert f(T(wide), (2, 5, 8, 128), "k") == (64, 1024)
-    assert f(T(wide[:, :, 4:]), (2, 5, 4, 128), "k") == (64, 1024)
-    assert f(T(wide[:, :1]), (2, 1, 8, 128), "k") == (64, wide.stride(0))
-    assert f(T(wide[:1, :1]), (1, 1, 8, 128), "k") == (64, 1024)
-    assert f(T(wide[:, :, 3:4]), (2, 5, 1, 128), "k") == (64, 1024)
+    assert f(_Dev(wide), (2, 5, 8, 128), 0, "k") == (64, 1024)
+    assert f(_Dev(wide[:, :, 4:]), (2, 5, 4, 128), 0, "k") == (64, 1024)
+    assert f(_Dev(wide[:, :1]), (2, 1, 8, 128), 0, "k") == (64, 5120)
+    assert f(_Dev(wide[:1, :1]), (1, 1, 8, 128), 0, "k") == (64, 1024)
+    assert f(_Dev(wide[:, :, 3:4]), (2, 5, 1, 128), 0, "k") == (64, 1024)
     for bad in (wide.transpose(0, 1), wide[:, :, ::2], wide[..., ::2], wide[:, ::2], wide[:, :2]):
         with pytest.raises(ValueError):
-            f(T(bad), tuple(bad.shape), "k")
+            f(_Dev(bad), tuple(bad.shape), 0, "k")
     with pytest.raises(ValueError, match="shape"):
-        f(T(wide), (2, 5, 4, 128), "k")
+        f(_Dev(wide), (2, 5, 4, 128), 0, "k")
+
+
+def test_binding_checks_tensors(msa):
+    import torch
+    u8 = torch.uint8
+
+    def cache(k=(3, 4, 128, 128), ks=(3, 4), v=(3, 4, 128, 128), vs=(3, 4), dtype=u8, dev=0):
+        return msa.Fp8Cache.from_tensors(_Dev(torch.zeros(k, dtype=u8)), _Dev(torch.zeros(ks, dtype=u8)),
+                                         _Dev(torch.zeros(v, dtype=dtype)), _Dev(torch.zeros(vs, dtype=u8), dev))
+
+    ca = cache()
+    assert (ca.num_pages, ca.groups) == (3, 4) and ca.nbytes == 2 * 3 * 4 * (128 * 128 + 1)
+    for bad in (dict(ks=(4, 3)), dict(v=(2, 4, 128, 128)), dict(vs=(3,)), dict(dev=1)):
+        with pytest.raises(ValueError):
+            cache(**bad)
+    with pytest.raises(TypeError):
+        cache(dtype=torch.int8)
+    with pytest.raises(AttributeError):
+        ca.k_data = None
+    with pytest.raises(ValueError, match="CUDA"):
+        msa.Fp8Cache.from_tensors(*(torch.zeros(3, 4, 128, 128, dtype=u8) for _ in range(4)))
+
+    i32 = torch.int32
+    table, lens = _Dev(torch.zeros(2, 8, dtype=i32)), _Dev(torch.zeros(2, dtype=i32))
+    batch, ws = msa.Batch(table, lens, 3), _Dev(torch.zeros(1 << 10, dtype=u8))
+    x = _Dev(torch.zeros(2, 3, 4, 128))
+    with pytest.raises(ValueError, match="pages"):
+        msa.msa_fp8_append(msa.Config(num_kv_groups=2), ca, batch, x, x, ws)
+    with pytest.raises(TypeError, match="float32"):
+        msa.msa_fp8_append(msa.Config(), ca, batch, _Dev(torch.zeros(2, 3, 4, 128, dtype=torch.float16)), x, ws)
+    with pytest.raises(TypeError, match="float32"):
+        msa.msa_fp8_append(msa.Config(), ca, batch, x, _Dev(torch.zeros(2, 3, 4, 128, dtype=torch.bfloat16)), ws)
+    with pytest.raises(ValueError, match="seq_lens"):
+        msa.msa_fp8_append(msa.Config(), ca, msa.Batch(table, _Dev(torch.zeros(3, dtype=i32)), 3), x, x, ws)
+    q, out = _Dev(torch.zeros(2, 3, 32, 128, dtype=u8)), _Dev(torch.zeros(2, 3, 32, 128, dtype=torch.bfloat16))
+    cfg = msa.Config()
+    with pytest.raises(TypeError, match="q must"):
+        msa.msa_fp8_attn(cfg, ca, batch, _Dev(torch.zeros(2, 3, 32, 128)), out, None, ws)
+    for kw, what in ((dict(selection=_Dev(torch.zeros(2, 3, 4, 15, dtype=i32))), "selection"),
+                     (dict(weight_out=_Dev(torch.zeros(2, 9))), "weight_out"),
+                     (dict(weight_in=_Dev(torch.zeros(8, 2).t())), "weight_in")):
+        with pytest.raises(ValueError, match=what):
+            msa.msa_fp8_attn(cfg, ca, batch, q, out, None, ws, **kw)
+    with pytest.raises(TypeError, match="out"):
+        msa.msa_fp8_attn(cfg, ca, batch, q, q, None, ws)
+    w, ints, row = (_Dev(torch.zeros(2, 8)), _Dev(torch.zeros(2, 8, dtype=i32)), _Dev(torch.zeros(2, dtype=i32)))
+    with pytest.raises(ValueError, match="freed_count"):
+        msa.msa_evict_blocks(batch, w, 4, 1, 1, ints, row, w, ints, ints, ws)
+    with pytest.raises(ValueError, match="workspace"):
+        msa.msa_evict_blocks(batch, w, 4, 1, 1, ints, row, w, ints, row, _Dev(torch.zeros(256, dtype=u8), 1))
