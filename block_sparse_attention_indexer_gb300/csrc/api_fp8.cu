@@ -12,8 +12,6 @@ using namespace msa;
 
 namespace {
 
-constexpr int kFp8Parts = 4;  // parts of a page whose shares are kept apart
-
 msa_status_t check_fp8_cache(const msa_fp8_cache_t* c) {
   if (c == nullptr || c->num_pages < 1 || c->num_pages > INT32_MAX) return MSA_ERR_INVALID_ARG;
   if (c->k_data == nullptr || c->k_scale == nullptr || c->v_data == nullptr || c->v_scale == nullptr ||
@@ -35,18 +33,19 @@ bool overlap(const void* p, size_t np, const void* q, size_t nq) {
 msa_status_t status_of(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
 
 struct AttnLayout {
-  size_t partial, share, stat, mass, total;
+  size_t prefix, partial, share, stat, mass, total;
 };
 
 AttnLayout attn_layout(const msa_config_t* c, const msa_batch_t* b, bool weights) {
   AttnLayout w{};
-  w.partial = kErrBytes;
-  w.total = w.partial + align_up(fp8_attn_partial_bytes());
+  w.prefix = kErrBytes;
+  w.partial = w.prefix + align_up((static_cast<size_t>(b->batch) + 1) * sizeof(int32_t));
+  w.total = w.partial + align_up(fp8_attn_partial_bytes(static_cast<int64_t>(b->q_len) * c->heads_per_group));
   if (!weights) return w;
   const size_t rows = static_cast<size_t>(b->batch) * b->q_len * c->num_kv_groups * c->heads_per_group;
   const size_t places = b->max_blocks > kSelTopK ? b->max_blocks : kSelTopK;
   w.share = w.total;
-  w.stat = w.share + align_up(rows * places * kFp8Parts * sizeof(float2));
+  w.stat = w.share + align_up(rows * places * kFp8StreamParts * sizeof(float2));
   w.mass = w.stat + align_up(rows * sizeof(float2));
   w.total = w.mass + align_up(static_cast<size_t>(b->batch) * b->max_blocks * sizeof(unsigned long long));
   return w;
@@ -104,6 +103,7 @@ msa_status_t msa_fp8_attn(const msa_config_t* cfg, const msa_fp8_cache_t* cache,
     return st;
   if (q_type != MSA_TYPE_E4M3 && q_type != MSA_TYPE_BF16) return MSA_ERR_UNSUPPORTED;
   if (cache->num_pages * cfg->num_kv_groups > (1 << 24)) return MSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch->batch) * batch->max_blocks * cfg->num_kv_groups > INT32_MAX) return MSA_ERR_UNSUPPORTED;
   if (!(weight_decay >= 0.0f && weight_decay <= 1.0f) || (weight_in != nullptr && weight_out == nullptr))
     return MSA_ERR_INVALID_ARG;
   if (batch->batch == 0) return MSA_OK;
@@ -142,6 +142,7 @@ msa_status_t msa_fp8_attn(const msa_config_t* cfg, const msa_fp8_cache_t* cache,
   a.weight_in = weight_in;
   a.weight_decay = weight_decay;
   a.weight_out = weight_out;
+  a.block_prefix = reinterpret_cast<int32_t*>(ws + w.prefix);
   a.partial = reinterpret_cast<float*>(ws + w.partial);
   if (weight_out != nullptr) {
     a.share = reinterpret_cast<float2*>(ws + w.share);

@@ -1,4 +1,6 @@
 // Attention over the FP8 page cache: dense causal, or over selected blocks.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include "fp8_device.cuh"
@@ -214,43 +216,60 @@ __global__ void __launch_bounds__(256) fp8_weights_sparse_kernel(const Fp8AttnAr
   a.weight_out[i] = decayed(a, i) + sum;
 }
 
-template <typename... Par, typename... Arg>
-static cudaError_t launch_dependent(void (*kernel)(Par...), int64_t grid, int block, size_t smem, cudaStream_t s,
-                                    Arg... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+// ---------------------------------------------------------------- tensor maps and dispatch
+
+cudaError_t fp8_page_maps(const Fp8AttnArgs& a, Fp8Maps* maps) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  // row coordinates are signed 32-bit: the host has checked num_pages * G <= 2^24
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(a.num_pages) * a.groups * kBlock};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, kBlock};
+  const cuuint32_t estr[2] = {1, 1};
+  for (int i = 0; i < 2; ++i) {
+    const CUresult r = encode(i ? &maps->v : &maps->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                              const_cast<uint8_t*>(i ? a.v_data : a.k_data), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
 }
 
-size_t fp8_attn_partial_bytes() { return 0; }
+size_t fp8_attn_partial_bytes(int64_t rows) {
+  (void)rows;
+  return fp8_stream_partial_bytes();
+}
 
 cudaError_t launch_fp8_attn(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
-  (void)num_sms;
   cudaError_t e = cudaSuccess;
   const int64_t blocks = static_cast<int64_t>(a.batch) * a.max_blocks;
   const bool sparse = a.selection != nullptr, weights = a.weight_out != nullptr;
   const int64_t units = static_cast<int64_t>(a.batch) * a.q_len * a.groups;
-  const int parts = 1;
+  const bool stream = sparse || a.q_len * a.heads_per_group <= kFp8StreamRows;
+  const int parts = stream ? kFp8StreamParts : 1;
   if (sparse && weights && (e = cudaMemsetAsync(a.mass, 0, blocks * sizeof(*a.mass), s)) != cudaSuccess) return e;
-  if ((e = launch_dependent(fp8_attn_simple_kernel, units, 128, 0, s, a)) != cudaSuccess || !weights) return e;
+  e = stream ? launch_fp8_stream(a, num_sms, s)
+             : launch_dependent(fp8_attn_simple_kernel, dim3(static_cast<unsigned>(units)), 128, 0, s, a);
+  if (e != cudaSuccess || !weights) return e;
   if (sparse) {
-    if ((e = launch_dependent(fp8_weights_scatter_kernel, (units * kTopK + 255) / 256, 256, 0, s, a, parts)) !=
-        cudaSuccess)
-      return e;
-    return launch_dependent(fp8_weights_sparse_kernel, (blocks + 255) / 256, 256, 0, s, a);
+    e = launch_dependent(fp8_weights_scatter_kernel, dim3(static_cast<unsigned>((units * kTopK + 255) / 256)), 256, 0, s,
+                         a, parts);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(fp8_weights_sparse_kernel, dim3(static_cast<unsigned>((blocks + 255) / 256)), 256, 0, s, a);
   }
   const int64_t each = static_cast<int64_t>(a.groups) * parts * a.q_len * a.heads_per_group;
-  return each <= 2048 ? launch_dependent(fp8_weights_dense_kernel<32>, (blocks + 7) / 8, 256, 0, s, a, parts)
-                      : launch_dependent(fp8_weights_dense_kernel<256>, blocks, 256, 0, s, a, parts);
+  return each <= 2048 ? launch_dependent(fp8_weights_dense_kernel<32>, dim3(static_cast<unsigned>((blocks + 7) / 8)), 256, 0,
+                                         s, a, parts)
+                      : launch_dependent(fp8_weights_dense_kernel<256>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a,
+                                         parts);
 }
 
 }  // namespace msa

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/msa.h"
+#include "fp8_kernels.h"
 #include "msa_device.cuh"
 
 namespace msa {
@@ -55,6 +56,38 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& r0, uint32
 
 __device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// 2^x (approximate to 2 ulp; -inf gives 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One 2-D tiled tensor copy global -> shared completing on `bar`, with an L2 policy (x, the byte
+// offset within a key row, is always 0 here: 16-byte aligned).
+__device__ __forceinline__ void tma_page(void* dst, const void* map, int y, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+      "{%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+// Byte offset of 16-byte chunk c of key row r in a page as the tensor copy lands it (128-byte
+// rows, 128-byte swizzle).
+__device__ __forceinline__ int page_chunk(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// Whether sequence length L is one that the call can attend with (0 is a padding row).
+__device__ __forceinline__ bool length_ok(const Fp8AttnArgs& a, int L) {
+  return L > 0 && L >= a.q_len && L <= static_cast<int64_t>(a.max_blocks) * kBlock;
 }
 
 // Four E4M3 codes times f, rounded to E4M3 again.

@@ -3,6 +3,7 @@
 // pointer is device memory.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -49,15 +50,51 @@ struct Fp8AttnArgs {
   float* weight_out;
   // Scratch.  A unit is the query rows that share a list of pages: dense, the T * Hg rows
   // (t, h) of (sequence, group); sparse, the Hg heads of (sequence, token, group).
+  int32_t* block_prefix;       // [B + 1] blocks of the sequences before each (dense; padding rows count one)
   float* partial;              // partial softmax states of units cut by the split of the work
   float2* share;               // [unit][page place][part][row]: (sum of 2^(z - ref), ref) over the
                                // keys of a part of the page; places: block (dense) or slot (sparse)
   float2* row_stat;            // [unit][row]: (M, 1 / sum of 2^(z - M)); 0 weight for empty rows
   unsigned long long* mass;    // [B][max_blocks] fixed point (sparse)
 };
-// Bytes of `partial`, whatever the batch.
-size_t fp8_attn_partial_bytes();
+// Query rows of a unit up to which the streaming (mma.sync) form takes it; sparse units
+// (at most 8 rows) always fit.
+constexpr int kFp8StreamRows = 16;
+// Parts of a page whose shares are kept apart.
+constexpr int kFp8StreamParts = 4;
+// Upper bound of the persistent grids (one CTA per SM); `partial` is sized for it.
+constexpr int kFp8MaxCtas = 160;
+// Bytes of `partial` for a batch with `rows` = q_len * heads_per_group rows per dense unit.
+size_t fp8_attn_partial_bytes(int64_t rows);
 cudaError_t launch_fp8_attn(const Fp8AttnArgs& a, int num_sms, cudaStream_t s);
+// The streaming form: dense units of at most kFp8StreamRows rows, or a selection.
+cudaError_t launch_fp8_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t s);
+size_t fp8_stream_partial_bytes();
+
+// Tensor maps of the K and V code pools as rows of 128 bytes ([pages * G * 128][128]), one page
+// head (128 rows) per box, 128-byte swizzle.
+struct Fp8Maps {
+  CUtensorMap k, v;
+};
+cudaError_t fp8_page_maps(const Fp8AttnArgs& a, Fp8Maps* maps);
+
+// Launch with programmatic stream serialization (every kernel here waits for the one before it).
+template <typename... Par, typename... Arg>
+cudaError_t launch_dependent(void (*kernel)(Par...), dim3 grid, int block, size_t smem, cudaStream_t s,
+                             const Arg&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 struct EvictArgs {
   const int32_t* block_table;
