@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmsa.so")
 SOURCES = ["api.cu", "quant.cu", "indexer.cu", "prefill.cu", "select.cu", "attention.cu", "prefill_attn.cu", "spec_indexer.cu", "noalloc.cu",
-           "api_fp8.cu", "fp8_append.cu", "fp8_attn.cu", "fp8_stream.cu", "evict.cu"]
+           "api_fp8.cu", "fp8_append.cu", "fp8_attn.cu", "fp8_stream.cu",
+           "fp8_tile.cu", "evict.cu"]
 HEADERS = ["msa_device.cuh", "msa_kernels.h", "api_internal.h", "select_row.cuh", "umma.cuh", "indexer_tile.cuh",
            "attention_tile.cuh", "attention_team.cuh", "fp8_device.cuh", "fp8_kernels.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -38,15 +38,16 @@ struct AttnLayout {
 
 AttnLayout attn_layout(const msa_config_t* c, const msa_batch_t* b, bool weights) {
   AttnLayout w{};
+  const int64_t rows = static_cast<int64_t>(b->q_len) * c->heads_per_group;  // per (sequence, group)
   w.prefix = kErrBytes;
-  w.partial = w.prefix + align_up((static_cast<size_t>(b->batch) + 1) * sizeof(int32_t));
-  w.total = w.partial + align_up(fp8_attn_partial_bytes(static_cast<int64_t>(b->q_len) * c->heads_per_group));
+  w.partial = w.prefix + align_up((static_cast<size_t>(b->batch) * fp8_tile_units_per_seq(rows) + 1) * sizeof(int32_t));
+  w.total = w.partial + align_up(fp8_attn_partial_bytes(rows));
   if (!weights) return w;
-  const size_t rows = static_cast<size_t>(b->batch) * b->q_len * c->num_kv_groups * c->heads_per_group;
+  const size_t all = static_cast<size_t>(b->batch) * c->num_kv_groups * rows;
   const size_t places = b->max_blocks > kSelTopK ? b->max_blocks : kSelTopK;
   w.share = w.total;
-  w.stat = w.share + align_up(rows * places * kFp8StreamParts * sizeof(float2));
-  w.mass = w.stat + align_up(rows * sizeof(float2));
+  w.stat = w.share + align_up(all * places * kFp8StreamParts * sizeof(float2));
+  w.mass = w.stat + align_up(all * sizeof(float2));
   w.total = w.mass + align_up(static_cast<size_t>(b->batch) * b->max_blocks * sizeof(unsigned long long));
   return w;
 }
@@ -103,7 +104,10 @@ msa_status_t msa_fp8_attn(const msa_config_t* cfg, const msa_fp8_cache_t* cache,
     return st;
   if (q_type != MSA_TYPE_E4M3 && q_type != MSA_TYPE_BF16) return MSA_ERR_UNSUPPORTED;
   if (cache->num_pages * cfg->num_kv_groups > (1 << 24)) return MSA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(batch->batch) * batch->max_blocks * cfg->num_kv_groups > INT32_MAX) return MSA_ERR_UNSUPPORTED;
+  // the flat list of (unit, page) steps is counted in 32 bits
+  const int64_t tiles = 2 * static_cast<int64_t>(fp8_tile_units_per_seq(static_cast<int64_t>(batch->q_len) * cfg->heads_per_group));
+  if (batch->batch * tiles > INT32_MAX / (static_cast<int64_t>(batch->max_blocks) * cfg->num_kv_groups))
+    return MSA_ERR_UNSUPPORTED;
   if (!(weight_decay >= 0.0f && weight_decay <= 1.0f) || (weight_in != nullptr && weight_out == nullptr))
     return MSA_ERR_INVALID_ARG;
   if (batch->batch == 0) return MSA_OK;

@@ -50,7 +50,8 @@ struct Fp8AttnArgs {
   float* weight_out;
   // Scratch.  A unit is the query rows that share a list of pages: dense, the T * Hg rows
   // (t, h) of (sequence, group); sparse, the Hg heads of (sequence, token, group).
-  int32_t* block_prefix;       // [B + 1] blocks of the sequences before each (dense; padding rows count one)
+  int32_t* block_prefix;       // dense, prefix sums of the work: [B + 1] blocks of the sequences before each
+                               // (streaming form), [B * tile units + 1] steps of the units before each (tile form)
   float* partial;              // partial softmax states of units cut by the split of the work
   float2* share;               // [unit][page place][part][row]: (sum of 2^(z - ref), ref) over the
                                // keys of a part of the page; places: block (dense) or slot (sparse)
@@ -70,6 +71,10 @@ cudaError_t launch_fp8_attn(const Fp8AttnArgs& a, int num_sms, cudaStream_t s);
 // The streaming form: dense units of at most kFp8StreamRows rows, or a selection.
 cudaError_t launch_fp8_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t s);
 size_t fp8_stream_partial_bytes();
+// The tile form: dense units of any number of rows.
+cudaError_t launch_fp8_tile(const Fp8AttnArgs& a, int num_sms, cudaStream_t s);
+size_t fp8_tile_partial_bytes();
+int fp8_tile_units_per_seq(int64_t rows);
 
 // Tensor maps of the K and V code pools as rows of 128 bytes ([pages * G * 128][128]), one page
 // head (128 rows) per box, 128-byte swizzle.

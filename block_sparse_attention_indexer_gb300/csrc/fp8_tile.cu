@@ -1,0 +1,951 @@
+// Dense attention over the FP8 page cache for more than 16 query rows per (sequence, group):
+// draft tokens and prompt chunks, on the tcgen05 tensor cores.
+//
+// Mathematics: as fp8_stream.cu has it, P_j = 2^(e_j - M) with e_j = z_j log2(e) + b (2^b the page's V scale)
+// and an integer reference M that is raised only when some e_j exceeds it by more than 8.
+//
+// Work.  A unit is 256 query rows (token, head) of a (sequence, group), as two tiles of 128, or the
+// at most 128 rows of a last one, as one tile.  A unit's products are counted in (tile, page) steps;
+// the units of the call, in order, are one flat list of steps that a persistent grid (one CTA an SM)
+// cuts into equal ranges (fp8_tile_plan_kernel has the units' prefix sums; causal units differ in
+// length).  Two accumulator slots work in turn: with two tiles each page is used by slot 0 (tile 0)
+// and slot 1 (tile 1), so a page is loaded and its V converted once for 256 rows; with one tile the
+// pages alternate between the slots and the two states are added at the end.
+//   * S = Q K^T: kind::f8f6f4, E4M3 from the page as it is (a tensor copy lands the 128-byte key rows
+//     in the operand's 128-byte swizzle), exact products, float32 sums.  bf16 queries are split into
+//     two parts, q = 2^k (hi + lo) with the row's largest value in [2^7, 2^8): hi is q 2^-k rounded to
+//     E4M3, and the rest is at most 8 units of bf16's last place, which E5M2's three significant bits hold
+//     exactly for values of at least 2^-6 (2^-13 of the largest); below, it is rounded by at most 2^-14.
+//   * O += P V: kind::f16, P in fp16 written over S in tensor memory (the A operand), V converted
+//     exactly to fp16 as the MN-major B operand (keys as K rows, as the page has them: no transpose).
+// TMEM: S of the two slots, then O of the two slots: 4 x 128 columns, all of it.
+//
+// Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread, its 128 scores in registers), 8-11
+// load Q and convert V, 12 resolves pages and issues the copies, 13 issues the products; 14 and 15
+// only fill the last warpgroup, which with 8-11 gives registers to the softmax (setmaxnreg).
+// Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
+// the others at the end, where TMEM is freed.
+//
+// Bound by the tensor pipe for prompt chunks (768 cycles of products per step), by the page stream
+// for a few draft tokens.
+#include <cuda_bf16.h>
+
+#include "fp8_device.cuh"
+#include "fp8_kernels.h"
+#include "msa_device.cuh"
+#include "umma.cuh"
+
+namespace msa {
+
+constexpr int kFtRows = 128;                 // rows per tile
+constexpr int kFtThreads = 512;
+constexpr int kFtK = 3, kFtRaw = 2, kFtV = 2;  // stages: K pages, raw V pages, V as fp16
+constexpr int kFtItems = 8;                  // page records in flight
+constexpr int kFtVBytes = kBlock * kDim * 2;
+constexpr int kFtPlaceFloats = 2 * kFtRows * (kDim + 2);  // a partial state of 256 rows
+constexpr uint32_t kFtO = 256;               // TMEM column of slot 0's O
+
+struct FtItem {
+  int unit;       // index into the plan's units; -1: no more items
+  int g;
+  int block;      // -1: a unit (or a part of one) with no page
+  int place;      // partial-state place of a cut unit; -1: the whole unit is this CTA's
+  float k_scale;  // 2^a * softmax_scale * log2(e)
+  float v_exp;    // b
+};
+
+struct FtShared {
+  uint64_t k_full[kFtK], k_empty[kFtK], raw_full[kFtRaw], raw_empty[kFtRaw], v_full[kFtV], v_empty[kFtV];
+  uint64_t item_full[kFtItems], item_empty[kFtItems];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full, fin, other;  // Q of a unit loaded; a unit written; slot 1's statistics left
+  uint64_t drain;               // every product issued has ended (after a wait that gave up)
+  uint32_t tmem;
+  int nan_any;
+  FtItem item[kFtItems];
+  float q_fac[2 * kFtRows];     // the power of two taken out of each row (bf16)
+  float other_m[kFtRows], other_l[kFtRows];
+  int nan_key[kDim];            // first key of the unit's edge pages with a NaN code in V, per dim
+};
+
+constexpr size_t kFtQ = 4 * kFtRows * 128;   // [part hi / lo][tile]
+constexpr size_t kFtSmem = 1024 + kFtQ + kFtK * kFp8PageBytes + kFtRaw * kFp8PageBytes + kFtV * kFtVBytes + sizeof(FtShared);
+static_assert(kFtSmem <= 232448, "227 KB of shared memory per CTA");
+
+// ---------------------------------------------------------------- the plan
+
+// Tiles of 256 rows per (sequence, group), and of one of them: first row, rows, steps per page, pages.
+struct FtUnit {
+  int b, row0, rows, width, pages;
+  bool live;
+};
+__device__ __forceinline__ FtUnit ft_unit(const Fp8AttnArgs& a, int u, int per_seq) {
+  FtUnit t;
+  t.b = u / per_seq;
+  t.row0 = (u - t.b * per_seq) * 2 * kFtRows;
+  const int all = a.q_len * a.heads_per_group;
+  t.rows = min(all - t.row0, 2 * kFtRows);
+  t.width = t.rows > kFtRows ? 2 : 1;
+  const int L = a.seq_lens[t.b];
+  t.live = length_ok(a, L);
+  t.pages = t.live ? (L - a.q_len + (t.row0 + t.rows - 1) / a.heads_per_group) / kBlock + 1 : 1;
+  return t;
+}
+
+// prefix[u]: steps (per group) of the units before u; one CTA.
+constexpr int kFtPlanThreads = 1024;
+__global__ void __launch_bounds__(kFtPlanThreads) fp8_tile_plan_kernel(const Fp8AttnArgs a, int per_seq) {
+  __shared__ int s_warp[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int units = a.batch * per_seq;
+  int base = 0;
+  for (int u0 = 0; u0 < units; u0 += kFtPlanThreads) {
+    const int u = u0 + tid;
+    int v = 0;
+    if (u < units) {
+      const FtUnit t = ft_unit(a, u, per_seq);
+      v = t.width * t.pages;
+      if (t.row0 == 0 && !t.live && a.seq_lens[t.b] != 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
+    }
+    int x = v;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, s);
+      if (lane >= s) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int w = s_warp[lane];
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, s);
+      if (lane >= s) w += y;
+    }
+    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    if (u < units) a.block_prefix[u] = base + x - v + (warp > 0 ? before : 0);
+    base += __shfl_sync(0xffffffffu, w, 31);
+    __syncthreads();
+  }
+  if (tid == 0) a.block_prefix[units] = base;
+}
+
+// First step of CTA c of n.
+__device__ __forceinline__ int ft_lo(int64_t E, int c, int n) { return static_cast<int>(E * c / n); }
+
+// The last unit u with prefix[u] * G <= x.
+__device__ __forceinline__ int ft_find(const int32_t* prefix, int units, int groups, int x) {
+  int lo = 0, hi = units;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(prefix[mid]) * groups <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------- tcgen05 forms used here only
+
+// kind::f8f6f4, both operands in shared memory
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// kind::f16 with A in tensor memory
+__device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// Four floats as E5M2 codes, the first in the low byte
+__device__ __forceinline__ uint32_t f32x4_to_e5m2x4(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n"
+      " .reg .b16 lo, hi;\n"
+      " cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n"
+      " cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n"
+      " mov.b32 %0, {lo, hi};\n"
+      "}"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
+}
+
+// Descriptor of an MN-major operand tile with the 128-byte swizzle: 64 fp16 of N per 128-byte row,
+// one row per k; 8-row groups 1024 bytes apart along k, the next 64 of N `next` bytes on.
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t next) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(next >> 4) << 16;  // leading byte offset
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;  // stride byte offset
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Waits for the warp's TMEM loads; the registers given are not used before it.
+template <int N, int M>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N], uint32_t (&w)[M]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+#pragma unroll
+  for (int i = 0; i < M; ++i) asm volatile("" : "+r"(w[i]));
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// (a.x, a.y) * f + c and (a.x, a.y) + (b.x, b.y): two floats an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 f, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(f)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// Output dim of accumulator column n: the upper 64 dims' 16-byte chunks are stored in swapped
+// pairs (the converters' shared stores are then free of bank conflicts).  Of column group n / 8:
+__device__ __forceinline__ int ft_dim8(int group) { return group < 8 ? group : group ^ 1; }
+
+// ---------------------------------------------------------------- the kernel
+
+__global__ void __launch_bounds__(kFtThreads, 1)
+    fp8_tile_kernel(const Fp8AttnArgs a, const __grid_constant__ Fp8Maps maps, int per_seq) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* q_tile = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* k_ring = q_tile + kFtQ;
+  uint8_t* raw_ring = k_ring + kFtK * kFp8PageBytes;
+  uint8_t* v_ring = raw_ring + kFtRaw * kFp8PageBytes;
+  FtShared* sh = reinterpret_cast<FtShared*>(v_ring + kFtV * kFtVBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.q_len, Hg = a.heads_per_group, G = a.groups;
+
+  if (tid == 0) {
+    for (int i = 0; i < kFtK; ++i) {
+      mbar_init(&sh->k_full[i], 1);
+      mbar_init(&sh->k_empty[i], 1);
+    }
+    for (int i = 0; i < kFtRaw; ++i) {
+      mbar_init(&sh->raw_full[i], 1);
+      mbar_init(&sh->raw_empty[i], 4);
+    }
+    for (int i = 0; i < kFtV; ++i) {
+      mbar_init(&sh->v_full[i], 4);
+      mbar_init(&sh->v_empty[i], 1);
+    }
+    for (int i = 0; i < kFtItems; ++i) {
+      mbar_init(&sh->item_full[i], 1);
+      mbar_init(&sh->item_empty[i], 13);  // eight softmax warps, four converters, the issuer
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], 4);
+      mbar_init(&sh->pv_done[i], 1);
+    }
+    mbar_init(&sh->q_full, 4);
+    mbar_init(&sh->fin, 9);  // eight softmax warps, the issuer
+    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->other, 4);
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  grid_dependency_wait();
+  grid_dependents_launch();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  const int units = a.batch * per_seq;
+  bool failed = false;
+
+  // The next page record, for a whole warp; `n` counts records.  free_item: this warp is done with it.
+  auto take_item = [&](int n, FtItem& it) -> bool {
+    if (!mbar_wait_warp(&sh->item_full[n % kFtItems], (n / kFtItems) & 1)) return false;
+    it = sh->item[n % kFtItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_empty[n % kFtItems]);
+    return true;
+  };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    // ---- softmax of slot `slot`: row r of its tile
+    const int slot = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kFtO + slot * 128 + lane_base;
+    int unit = -1, g = 0, done[2] = {0, 0}, pages = 0, valid_pages = 0, loads = 0, others = 0;
+    int place = -1, at_start[2] = {0, 0};
+    FtUnit t{};
+    int row = 0, pos = 0, pos_first = 0, pos0 = 0;  // pos0: of the sequence's first query token
+    float M = -INFINITY, l = 0.f, q_fac = 1.f;
+
+    // writes the unit's rows (or its partial state)
+    auto finish = [&]() -> bool {
+      const bool mine = done[slot] > at_start[slot];
+      if (mine && !mbar_wait_warp(&sh->pv_done[slot], (done[slot] - 1) & 1)) return false;
+      if (t.width == 1) {
+        if (slot == 1) {
+          sh->other_m[r] = M;
+          sh->other_l[r] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->other);
+          return true;
+        }
+        if (!mbar_wait_warp(&sh->other, others & 1)) return false;
+        if (done[1] > at_start[1] && !mbar_wait_warp(&sh->pv_done[1], (done[1] - 1) & 1)) return false;
+      }
+      tc_fence_after();
+      // state of the row = fa * own O + fb * the other slot's O
+      float fa = mine ? 1.f : 0.f, fb = 0.f;
+      const bool both = t.width == 1 && done[1] > at_start[1];
+      if (both) {
+        const float mo = sh->other_m[r], lo = sh->other_l[r];
+        const float mn = fmaxf(M, mo);
+        fa = mn == -INFINITY ? 1.f : ex2(M - mn);
+        fb = mn == -INFINITY ? 1.f : ex2(mo - mn);
+        l = l * fa + lo * fb;
+        M = mn;
+      }
+      const bool valid = row < t.row0 + t.rows;
+      const bool any = l != 0.f;  // (NaN counts as any)
+      const float inv = any ? 1.f / l : 0.f;
+      const float out_f = place < 0 ? inv : 1.f;
+      const int64_t token = static_cast<int64_t>(t.b) * T + row / Hg;
+      const int64_t hr = token * G * Hg + g * Hg + row % Hg;
+      const int pr = row - t.row0;  // row of the partial state
+      float* part = place < 0 ? nullptr
+                              : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kFtPlaceFloats;
+      const bool poison = sh->nan_any != 0;
+      for (int c = 0; c < 8; ++c) {  // 16 columns = dims of two groups of 8
+        uint32_t x[16], y[16];
+        if (mine) tmem_ld16(tO + 16 * c, x);
+        if (both) tmem_ld16(tO + 128 + 16 * c, y);
+        tmem_wait_ld(x, y);
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          v[i] = mine ? __uint_as_float(x[i]) * fa : 0.f;
+          if (both) v[i] += __uint_as_float(y[i]) * fb;
+          if (poison && pos >= sh->nan_key[8 * ft_dim8(2 * c + (i >> 3)) + (i & 7)]) v[i] = NAN;
+          v[i] *= out_f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!valid) break;
+          const int d = 8 * ft_dim8(2 * c + i);
+          if (place < 0) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+              w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(a.out + hr * kDim + d) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(part + pr * kDim + d);
+            dst[0] = make_float4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
+            dst[1] = make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+          }
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        if (place < 0) {
+          if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (a.weight_out != nullptr)
+            a.row_stat[(static_cast<int64_t>(t.b) * G + g) * T * Hg + row] = make_float2(any ? M : 0.f, inv);
+        } else {
+          part[2 * kFtRows * kDim + pr] = M;
+          part[2 * kFtRows * (kDim + 1) + pr] = l;
+        }
+      }
+      tc_fence_before();
+      return true;
+    };
+
+    for (int n = 0;; ++n) {
+      FtItem it;
+      if (!take_item(n, it)) {
+        failed = true;
+        break;
+      }
+      if (it.unit < 0 || it.unit != unit || it.g != g) {
+        if (unit >= 0) {
+          if (!finish()) {
+            failed = true;
+            break;
+          }
+          if (t.width == 1) ++others;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->fin);
+        }
+        unit = it.unit;
+        g = it.g;
+        if (unit < 0) break;
+        t = ft_unit(a, unit, per_seq);
+        place = it.place;
+        pages = 0;
+        at_start[0] = done[0];
+        at_start[1] = done[1];
+        row = t.row0 + (t.width == 2 ? slot * kFtRows : 0) + r;
+        pos0 = a.seq_lens[t.b] - T;
+        pos = pos0 + min(row, T * Hg - 1) / Hg;
+        pos_first = pos0 + (t.row0 + (t.width == 2 ? slot * kFtRows : 0)) / Hg;
+        M = -INFINITY;
+        l = 0.f;
+        if (!mbar_wait_warp(&sh->q_full, loads & 1)) {
+          failed = true;
+          break;
+        }
+        ++loads;
+        q_fac = sh->q_fac[row - t.row0];
+      }
+      if (it.block < 0) continue;
+      // the page's V stage, and whether its step is this slot's
+      const int vstage = valid_pages % kFtV, vphase = (valid_pages / kFtV) & 1;
+      ++valid_pages;
+      const int turn = pages & 1;
+      ++pages;
+      if (t.width == 1 && turn != slot) {
+        ++done[turn];
+        continue;
+      }
+      const bool had = done[slot] > at_start[slot];
+      // the converters' NaN marks of a page that some row of the sequence does not see whole are read
+      // when the unit is written: seeing the page's stage full orders them before that (the stage
+      // is not used again before this step's P)
+      if (!mbar_wait_warp(&sh->s_full[slot], done[slot] & 1) ||
+          (it.block * kBlock + kBlock - 1 > pos0 && !mbar_wait_warp(&sh->v_full[vstage], vphase))) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+      const float f = fmaxf(it.k_scale * q_fac, 1.2e-38f);  // (positive: -inf times it stays -inf)
+      uint32_t v0[64], v1[64];
+      float mx;
+      const bool edge = it.block * kBlock + kBlock - 1 > pos_first;
+      if (!edge) {
+        float m0, m1;
+        tmem_ld64_max(tS, v0, m0);
+        tmem_ld64_max(tS + 64, v1, m1);
+        tmem_wait_ld(v0, v1);
+        asm volatile("" : "+f"(m0), "+f"(m1));
+        mx = fmaxf(m0, m1);
+      } else {
+        tmem_ld64(tS, v0);
+        tmem_ld64(tS + 64, v1);
+        tmem_wait_ld(v0, v1);
+        const int vis = pos - it.block * kBlock + 1;  // visible columns
+        mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          if (i >= vis) v0[i] = 0xff800000u;
+          if (i + 64 >= vis) v1[i] = 0xff800000u;
+          mx = fmaxf(mx, fmaxf(__uint_as_float(v0[i]), __uint_as_float(v1[i])));
+        }
+      }
+      mx = fmaf(mx, f, it.v_exp);
+      if (__any_sync(0xffffffffu, mx > M + 8.f)) {
+        float alpha = 1.f;
+        if (mx > M + 8.f) {
+          const float mn = ceilf(mx);
+          alpha = ex2(M - mn);
+          M = mn;
+          l *= alpha;
+        }
+        if (had) {  // (the issuer has waited for the slot's products before it issued this S)
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16];
+            tmem_ld16(tO + 16 * c, x);
+            tmem_wait_ld(x, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+            tmem_st16(tO + 16 * c, x);
+          }
+        }
+      }
+      const float c0 = it.v_exp - (M == -INFINITY ? 0.f : M);
+      const float2 ff = make_float2(f, f), cc = make_float2(c0, c0);
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 e0 = fma2(make_float2(__uint_as_float(v0[2 * i]), __uint_as_float(v0[2 * i + 1])), ff, cc);
+        const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y));
+        sum0 = add2(sum0, p0);
+        v0[i] = pack_f16x2(p0.x, p0.y);
+      }
+      tmem_st32(tS, v0);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 e1 = fma2(make_float2(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1])), ff, cc);
+        const float2 p1 = make_float2(ex2(e1.x), ex2(e1.y));
+        sum1 = add2(sum1, p1);
+        v1[i] = pack_f16x2(p1.x, p1.y);
+      }
+      tmem_st32(tS + 32, v1);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[slot]);
+      ++done[slot];
+      if (t.width == 2) ++done[slot ^ 1];
+      const float sum = (sum0.x + sum1.x) + (sum0.y + sum1.y);
+      l = fmaf(sum, ex2(-it.v_exp), l);
+      if (a.weight_out != nullptr && row < t.row0 + t.rows)
+        a.share[((static_cast<int64_t>(t.b) * G + g) * a.max_blocks + it.block) * T * Hg + row] =
+            make_float2(sum, (M == -INFINITY ? 0.f : M) - it.v_exp);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < 12) {
+      // ---- Q tiles, V conversion
+      const int ct = tid - 256;
+      int unit = -1, g = 0, page = 0, units_done = 0;
+      FtUnit t{};
+      int L = 0;
+      for (int n = 0; !failed; ++n) {
+        FtItem it;
+        if (!take_item(n, it)) {
+          failed = true;
+          break;
+        }
+        if (it.unit < 0 || it.unit != unit || it.g != g) {
+          unit = it.unit;
+          g = it.g;
+          if (unit < 0) break;
+          // the unit before is written: its products are done, its factors and NaN marks read
+          if (units_done > 0 && !mbar_wait_warp(&sh->fin, (units_done - 1) & 1)) {
+            failed = true;
+            break;
+          }
+          ++units_done;
+          t = ft_unit(a, unit, per_seq);
+          L = a.seq_lens[t.b];
+          sh->nan_key[ct] = INT32_MAX;
+          if (ct == 0) sh->nan_any = 0;
+          const int c = ct & 7;  // dims 16 c .. 16 c + 15 of rows ct / 8, + 16, ...
+          for (int rr = ct >> 3; rr < t.width * kFtRows; rr += 16) {
+            const int row = t.row0 + rr;
+            const bool valid = rr < t.rows;
+            const int64_t at = (static_cast<int64_t>(t.b) * T + row / Hg) * a.q_stride + (g * Hg + row % Hg) * kDim + 16 * c;
+            uint8_t* dst = q_tile + (rr >> 7) * (kFtRows * 128) + sw128(rr & 127, c);
+            float fac = 1.f;
+            if (!a.q_bf16) {
+              const uint4 u = valid ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(dst) = u;
+            } else {
+              float v[16];
+              float m = 0.f;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint4 u = valid ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[i]
+                                      : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                  v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+              for (int s = 1; s < 8; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+              // the largest value of the row into [2^7, 2^8)
+              const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -100), 112);
+              fac = exp2_int(k);
+              const float inv = exp2_int(-k);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = v[4 * i + j] * inv;
+                hi[i] = f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]);
+                uint32_t h0, h1;
+                e4m3x4_to_f16x4(hi[i], h0, h1);
+                const float2 p = f16x2_to_float2(h0), s = f16x2_to_float2(h1);
+                lo[i] = f32x4_to_e5m2x4(x[0] - p.x, x[1] - p.y, x[2] - s.x, x[3] - s.y);
+              }
+              *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(dst + 2 * kFtRows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (c == 0) sh->q_fac[rr] = fac;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->q_full);
+          // every converter has reset its marks before any page sets one
+          if (!mbar_wait_warp(&sh->q_full, (units_done - 1) & 1)) {
+            failed = true;
+            break;
+          }
+        }
+        if (it.block < 0) continue;
+        const int rs = page % kFtRaw, vs = page % kFtV;
+        if (!mbar_wait_warp(&sh->raw_full[rs], (page / kFtRaw) & 1) ||
+            (page >= kFtV && !mbar_wait_warp(&sh->v_empty[vs], (page / kFtV - 1) & 1))) {
+          failed = true;
+          break;
+        }
+        const uint8_t* src = raw_ring + rs * kFp8PageBytes;
+        uint8_t* dst = v_ring + vs * kFtVBytes;
+        const bool edge = it.block * kBlock + kBlock - 1 > L - T;  // hidden from some row of the sequence
+        const int c = ct & 7;
+        const int h0 = c < 4 ? 2 * c : 2 * (c & 3) + 1;  // chunk of the first 8 dims within its half
+        uint8_t* half = dst + (c < 4 ? 0 : kFtVBytes / 2);
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          const int r = 16 * i + (ct >> 3);
+          const uint4 u = lds128(src + page_chunk(r, c));
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          if (edge) {
+            const int key = it.block * kBlock + r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t nan = __vcmpeq4(w[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              w[j] &= ~nan;
+              if (nan != 0u && key < L) {
+                sh->nan_any = 1;
+                for (int q = 0; q < 4; ++q)
+                  if (nan >> (8 * q) & 1u) atomicMin(&sh->nan_key[16 * c + 4 * j + q], key);
+              }
+            }
+          }
+          uint32_t x[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e4m3x4_to_f16x4(w[j], x[2 * j], x[2 * j + 1]);
+          *reinterpret_cast<uint4*>(half + sw128(r, h0)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(half + sw128(r, h0 ^ 1)) = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh->v_full[vs]);
+          mbar_arrive(&sh->raw_empty[rs]);
+        }
+        ++page;
+      }
+    } else if (warp == 12) {
+      // ---- producer: page records and copies
+      const int64_t E = static_cast<int64_t>(a.block_prefix[units]) * G;
+      const int x0 = ft_lo(E, blockIdx.x, gridDim.x), x1 = ft_lo(E, blockIdx.x + 1, gridDim.x);
+      // every sequence's tiles read its pages again: keep them in L2, unless one tile has them all
+      const uint64_t policy = per_seq > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
+      int n = 0, page_n = 0;
+      auto record = [&](const FtItem& it) -> bool {
+        if (n >= kFtItems && !mbar_wait_warp(&sh->item_empty[n % kFtItems], (n / kFtItems - 1) & 1)) return false;
+        if (lane == 0) {
+          sh->item[n % kFtItems] = it;
+          mbar_arrive(&sh->item_full[n % kFtItems]);
+        }
+        ++n;
+        return true;
+      };
+      int u = x0 < x1 ? ft_find(a.block_prefix, units, G, x0) : units;
+      for (; u < units && !failed; ++u) {
+        const int64_t first = static_cast<int64_t>(a.block_prefix[u]) * G;
+        if (first >= x1) break;
+        const FtUnit t = ft_unit(a, u, per_seq);
+        const int steps = t.width * t.pages;
+        for (int g = 0; g < G && !failed; ++g) {
+          const int64_t u0 = first + static_cast<int64_t>(g) * steps;
+          if (u0 >= x1) break;
+          const int lo = static_cast<int>(max(x0 - u0, int64_t{0}) / t.width);
+          const int hi = min(static_cast<int>((x1 - u0) / t.width), t.pages);
+          if (lo >= hi) continue;
+          const int place = lo == 0 && hi == t.pages ? -1 : lo == 0 ? 1 : 0;
+          FtItem it{u, g, -1, place, 0.f, 0.f};
+          bool any = false;
+          for (int p0 = lo; p0 < hi && !failed; p0 += 32) {
+            const int p = p0 + lane;
+            int row = -1;
+            float ks = 0.f, ve = 0.f;
+            if (p < hi && t.live) {
+              const int pg = a.block_table[static_cast<int64_t>(t.b) * a.max_blocks + p];
+              if (pg >= 0 && pg < a.num_pages) {
+                const int ph = pg * G + g;
+                const int kb = a.k_scale[ph], vb = a.v_scale[ph];
+                if (e8m0_ok(kb) && e8m0_ok(vb)) {
+                  row = ph * kBlock;
+                  ks = exp2_int(kb - kE8m0One) * a.scale_log2;
+                  ve = static_cast<float>(vb - kE8m0One);
+                } else {
+                  flag_error(a.err, MSA_DEVERR_BAD_SCALE);
+                }
+              } else {
+                flag_error(a.err, MSA_DEVERR_BAD_PAGE);
+              }
+              if (row < 0 && a.weight_out != nullptr) {  // a skipped page collects nothing
+                float2* share = a.share + ((static_cast<int64_t>(t.b) * G + g) * a.max_blocks + p) * T * Hg + t.row0;
+                for (int i = 0; i < t.rows; ++i) share[i] = make_float2(0.f, 0.f);
+              }
+            }
+            const int count = min(hi - p0, 32);
+            for (int j = 0; j < count && !failed; ++j) {
+              const int y = __shfl_sync(0xffffffffu, row, j);
+              it.k_scale = __shfl_sync(0xffffffffu, ks, j);
+              it.v_exp = __shfl_sync(0xffffffffu, ve, j);
+              if (y < 0) continue;
+              any = true;
+              it.block = p0 + j;
+              const int ksl = page_n % kFtK, rsl = page_n % kFtRaw;
+              if (!record(it) || (page_n >= kFtK && !mbar_wait_warp(&sh->k_empty[ksl], (page_n / kFtK - 1) & 1)) ||
+                  (page_n >= kFtRaw && !mbar_wait_warp(&sh->raw_empty[rsl], (page_n / kFtRaw - 1) & 1))) {
+                failed = true;
+                break;
+              }
+              if (lane == 0) {
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(&sh->k_full[ksl], kFp8PageBytes);
+                tma_page(k_ring + ksl * kFp8PageBytes, &maps.k, y, &sh->k_full[ksl], policy);
+                mbar_arrive_expect_tx(&sh->raw_full[rsl], kFp8PageBytes);
+                tma_page(raw_ring + rsl * kFp8PageBytes, &maps.v, y, &sh->raw_full[rsl], policy);
+              }
+              ++page_n;
+            }
+          }
+          if (!any && !failed) {
+            it.block = -1;
+            failed = !record(it);
+          }
+        }
+      }
+      if (!failed) failed = !record(FtItem{-1, 0, -1, -1, 0.f, 0.f});
+      if (failed) {
+        // wait (bounded) for the copies still in flight
+        for (int k = max(0, page_n - kFtK); k < page_n; ++k) mbar_wait(&sh->k_full[k % kFtK], (k / kFtK) & 1);
+        for (int k = max(0, page_n - kFtRaw); k < page_n; ++k) mbar_wait(&sh->raw_full[k % kFtRaw], (k / kFtRaw) & 1);
+      }
+    } else if (warp == 13) {
+      // ---- product issuer: S of a step, then P V of the step before it
+      const uint32_t id_s = umma_idesc_f16(kFtRows, kBlock);               // (E4M3 has format code 0 too)
+      const uint32_t id_lo = id_s | (1u << 7);                             // A is E5M2
+      const uint32_t id_o = umma_idesc_f16(kFtRows, kDim) | (1u << 16);    // B MN-major
+      const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
+      int unit = -1, g = 0, width = 1, pages = 0, page = 0, loads = 0, done[2] = {0, 0}, at_start[2] = {0, 0};
+      int wait_slot = -1, wait_page = 0, wait_acc = 0;  // the step whose P V is still to come
+      bool wait_last = false;
+      auto products = [&]() -> bool {
+        if (wait_slot < 0) return true;
+        const int s = wait_slot, vs = wait_page % kFtV;
+        wait_slot = -1;
+        if (!mbar_wait_warp(&sh->v_full[vs], (wait_page / kFtV) & 1) ||
+            !mbar_wait_warp(&sh->p_full[s], (done[s] - 1) & 1))
+          return false;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
+            umma_f16_tmem_a(tmem + kFtO + s * 128, tmem + s * 128 + kk * 8,
+                            umma_desc_mn(vb + vs * kFtVBytes + kk * 2048, kFtVBytes / 2), id_o,
+                            wait_acc || kk > 0 ? 1u : 0u);
+          umma_commit(&sh->pv_done[s]);
+          if (wait_last) umma_commit(&sh->v_empty[vs]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int n = 0; !failed; ++n) {
+        FtItem it;
+        if (!take_item(n, it)) {
+          failed = true;
+          break;
+        }
+        if (it.unit < 0 || it.unit != unit || it.g != g) {
+          if (!products()) {
+            failed = true;
+            break;
+          }
+          if (unit >= 0 && lane == 0) mbar_arrive(&sh->fin);
+          unit = it.unit;
+          g = it.g;
+          if (unit < 0) break;
+          width = ft_unit(a, unit, per_seq).width;
+          pages = 0;
+          at_start[0] = done[0];
+          at_start[1] = done[1];
+          if (!mbar_wait_warp(&sh->q_full, loads & 1)) {
+            failed = true;
+            break;
+          }
+          ++loads;
+        }
+        if (it.block < 0) continue;
+        const int ks = page % kFtK;
+        if (!mbar_wait_warp(&sh->k_full[ks], (page / kFtK) & 1)) {
+          failed = true;
+          break;
+        }
+        for (int i = 0; i < width && !failed; ++i) {
+          const int s = width == 2 ? i : pages & 1;
+          // the slot's P (which S overwrites) has been multiplied
+          if (done[s] > 0 && !mbar_wait_warp(&sh->pv_done[s], (done[s] - 1) & 1)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t qt = qb + (width == 2 ? s : 0) * (kFtRows * 128), kt = kb + ks * kFp8PageBytes;
+            for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)  // 32 dims a step
+                umma_f8(tmem + s * 128, umma_desc(qt + part * (2 * kFtRows * 128) + 32 * kk), umma_desc(kt + 32 * kk),
+                        part > 0 ? id_lo : id_s, part > 0 || kk > 0 ? 1u : 0u);
+            umma_commit(&sh->s_full[s]);
+            if (i == width - 1) umma_commit(&sh->k_empty[ks]);
+          }
+          __syncwarp();
+          if (!products()) {
+            failed = true;
+            break;
+          }
+          wait_slot = s;
+          wait_page = page;
+          wait_acc = done[s] > at_start[s];
+          wait_last = i == width - 1;
+          ++done[s];
+        }
+        ++pages;
+        ++page;
+      }
+      if (failed) {  // the products still running end before TMEM is freed
+        if (lane == 0) umma_commit(&sh->drain);
+        __syncwarp();
+        mbar_wait_warp(&sh->drain, 0);
+      }
+    }
+  }
+  if (failed && lane == 0) flag_error(a.err, MSA_DEVERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// Units cut by range boundaries: CTA x takes the unit that boundary x + 1 cuts, if it is the unit's
+// first cut; a warp per row (8 of its rows per CTA), 4 dims a lane, the parts eight at a time.
+__global__ void __launch_bounds__(256) fp8_tile_merge_kernel(const Fp8AttnArgs a, int per_seq, int ctas) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int units = a.batch * per_seq, G = a.groups, Hg = a.heads_per_group, T = a.q_len;
+  const int64_t E = static_cast<int64_t>(a.block_prefix[units]) * G;
+  const int x = blockIdx.x, xb = ft_lo(E, x + 1, ctas), xa = ft_lo(E, x, ctas);
+  if (xb >= E) return;
+  const int u = ft_find(a.block_prefix, units, G, xb);
+  const FtUnit t = ft_unit(a, u, per_seq);
+  const int steps = t.width * t.pages;
+  const int64_t first = static_cast<int64_t>(a.block_prefix[u]) * G;
+  const int g = static_cast<int>((xb - first) / steps);
+  const int64_t u0 = first + static_cast<int64_t>(g) * steps;
+  const int cut = static_cast<int>((xb - u0) / t.width);  // pages before the boundary
+  if (cut == 0 || (xa > u0 && (xa - u0) / t.width > 0)) return;
+  const int pr = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (pr >= t.rows) return;
+  float M = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + steps; c0 += 8) {
+    float ms[8], ls[8];
+    float4 os[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + i;
+      ms[i] = -INFINITY;
+      ls[i] = 0.f;
+      os[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c >= ctas) continue;
+      const int64_t a0 = ft_lo(E, c, ctas) - u0, a1 = ft_lo(E, c + 1, ctas) - u0;
+      const int lo = static_cast<int>(max(a0, int64_t{0}) / t.width);
+      const int hi = static_cast<int>(min(a1 / t.width, static_cast<int64_t>(t.pages)));
+      if (a0 >= steps || lo >= hi) continue;
+      const float* part = a.partial + (2 * static_cast<int64_t>(c) + (lo == 0 ? 1 : 0)) * kFtPlaceFloats;
+      ms[i] = __ldcg(part + 2 * kFtRows * kDim + pr);
+      ls[i] = __ldcg(part + 2 * kFtRows * (kDim + 1) + pr);
+      os[i] = __ldcg(reinterpret_cast<const float4*>(part + pr * kDim) + lane);
+    }
+    float mb = M;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mb = fmaxf(mb, ms[i]);
+    const float f = mb == -INFINITY ? 1.f : ex2(M - mb);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = mb == -INFINITY ? 1.f : ex2(ms[i] - mb);
+      l += w * ls[i];
+      o.x += w * os[i].x;
+      o.y += w * os[i].y;
+      o.z += w * os[i].z;
+      o.w += w * os[i].w;
+    }
+    M = mb;
+  }
+  const bool any = l != 0.f;
+  const float inv = any ? 1.f / l : 0.f;
+  const int row = t.row0 + pr;
+  const int64_t hr = (static_cast<int64_t>(t.b) * T + row / Hg) * G * Hg + g * Hg + row % Hg;
+  const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(a.out + hr * kDim)[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+  if (lane == 0) {
+    if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (a.weight_out != nullptr)
+      a.row_stat[(static_cast<int64_t>(t.b) * G + g) * T * Hg + row] = make_float2(any ? M : 0.f, inv);
+  }
+}
+
+int fp8_tile_units_per_seq(int64_t rows) { return static_cast<int>((rows + 2 * kFtRows - 1) / (2 * kFtRows)); }
+
+size_t fp8_tile_partial_bytes() { return static_cast<size_t>(2) * kFp8MaxCtas * kFtPlaceFloats * sizeof(float); }
+
+cudaError_t launch_fp8_tile(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
+  Fp8Maps maps;
+  cudaError_t e = fp8_page_maps(a, &maps);
+  if (e != cudaSuccess) return e;
+  const int per_seq = fp8_tile_units_per_seq(static_cast<int64_t>(a.q_len) * a.heads_per_group);
+  const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas;
+  if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(fp8_tile_kernel), kFtSmem)) != cudaSuccess) return e;
+  if ((e = launch_dependent(fp8_tile_plan_kernel, dim3(1), kFtPlanThreads, 0, s, a, per_seq)) != cudaSuccess) return e;
+  if ((e = launch_dependent(fp8_tile_kernel, dim3(ctas), kFtThreads, kFtSmem, s, a, maps, per_seq)) != cudaSuccess)
+    return e;
+  if (ctas == 1) return cudaSuccess;
+  const int rows = a.q_len * a.heads_per_group < 2 * kFtRows ? a.q_len * a.heads_per_group : 2 * kFtRows;
+  return launch_dependent(fp8_tile_merge_kernel, dim3(ctas - 1, (rows + 7) / 8), 256, 0, s, a, per_seq, ctas);
+}
+
+}  // namespace msa

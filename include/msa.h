@@ -314,7 +314,7 @@ msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cach
  *   q       E4M3 or bfloat16 (q_type MSA_TYPE_E4M3 / MSA_TYPE_BF16) [batch][q_len][G*Hg][D];
  *           the heads of a token are contiguous, tokens are q_stride elements apart; pointer
  *           and stride in bytes multiples of 16, q_stride >= G * Hg * D.  bfloat16 values more
- *           than 2^14 below the largest of their row may be rounded, by at most 2^-18 of that
+ *           than 2^13 below the largest of their row may be rounded, by at most 2^-21 of that
  *           largest value.
  *   weight_out  float [batch][max_blocks] or NULL: how much attention each block collected,
  *           weight_out[b][n] = weight_decay * weight_in[b][n]
@@ -331,7 +331,7 @@ msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cach
  * workspace: msa_workspace_bytes(MSA_OP_FP8_ATTN_WEIGHTS, ...) with weight_out, else
  * MSA_OP_FP8_ATTN; calls that can overlap need a workspace each.
  * Errors: MSA_ERR_UNSUPPORTED for num_pages * G > 2^24 (a tensor map's row coordinate) or
- * batch * max_blocks * G > 2^31 - 1; MSA_ERR_CUDA also when the driver's tensor-map encoder is
+ * 2 * batch * ceil(q_len * Hg / 256) * max_blocks * G > 2^31 - 1 (the pages to visit); MSA_ERR_CUDA also when the driver's tensor-map encoder is
  * not available. */
 msa_status_t msa_fp8_attn(const msa_config_t* cfg, const msa_fp8_cache_t* cache, const msa_batch_t* batch,
                           const void* q, int32_t q_type, int64_t q_stride, const int32_t* selection, uint16_t* out,

@@ -112,7 +112,7 @@ def attention_bounds(case, ref):
     probabilities, element by element:
       * a logit: 128 products accumulated in float32 in any order, 128 * 2^-24 of sum |q k| (and
         the products with the scale and the reference's subtraction, 4 * 2^-24 of its size); a bf16
-        query element may be off by 2^-18 of its row's largest;
+        query element may be off by 2^-21 of its row's largest;
       * a probability: the logit's error twice (in it and in the sum), 2^-11 for its rounding to
         fp16, 2^-20 for exp2, the sums and the merges; below fp16's normal range 2^-24 of the largest
         probability, for each key;
@@ -121,7 +121,7 @@ def attention_bounds(case, ref):
     scale = case.softmax_scale or 1.0 / np.sqrt(128.0)
     dz = scale * ref["logit"] * (128 + 4) * 2.0 ** -24
     if case.q_type != "e4m3":
-        dz = dz + scale * 2.0 ** -18 * np.abs(case.q).max(-1) * ref["k_abs"]
+        dz = dz + scale * 2.0 ** -21 * np.abs(case.q).max(-1) * ref["k_abs"]
     rel = 2 * dz + 2.0 ** -20
     flush = (ref["keys"] * 2.0 ** -24 * ref["p_max"])[..., None] * ref["v_abs"]
     out = 2.0 ** -8 * np.abs(ref["out"]) + (rel + 2.0 ** -11)[..., None] * ref["spread"] + flush + 1e-30
