@@ -21,8 +21,7 @@
 // TMEM: S of the two slots, then O of the two slots: 4 x 128 columns, all of it.
 //
 // Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread, its 128 scores in registers), 8-11
-// load Q and convert V, 12 resolves pages and issues the copies, 13 issues the products; 14 and 15
-// only fill the last warpgroup, which with 8-11 gives registers to the softmax (setmaxnreg).
+// load Q and convert V, 12 resolves pages and issues the copies, 13 issues S, 14 issues P V.
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
 //
@@ -38,14 +37,14 @@
 namespace msa {
 
 constexpr int kFtRows = 128;                 // rows per tile
-constexpr int kFtThreads = 512;
+constexpr int kFtThreads = 480;
 constexpr int kFtK = 3, kFtRaw = 2, kFtV = 2;  // stages: K pages, raw V pages, V as fp16
 constexpr int kFtItems = 8;                  // page records in flight
 constexpr int kFtVBytes = kBlock * kDim * 2;
 constexpr int kFtPlaceFloats = 2 * kFtRows * (kDim + 2);  // a partial state of 256 rows
 constexpr uint32_t kFtO = 256;               // TMEM column of slot 0's O
 
-struct FtItem {
+struct alignas(16) FtItem {
   int unit;       // index into the plan's units; -1: no more items
   int g;
   int block;      // -1: a unit (or a part of one) with no page
@@ -57,9 +56,9 @@ struct FtItem {
 struct FtShared {
   uint64_t k_full[kFtK], k_empty[kFtK], raw_full[kFtRaw], raw_empty[kFtRaw], v_full[kFtV], v_empty[kFtV];
   uint64_t item_full[kFtItems], item_empty[kFtItems];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [slot], [slot][half of the page's keys]
   uint64_t q_full, fin, other;  // Q of a unit loaded; a unit written; slot 1's statistics left
-  uint64_t drain;               // every product issued has ended (after a wait that gave up)
+  uint64_t drain[2];             // every product issued has ended (after a wait that gave up)
   uint32_t tmem;
   int nan_any;
   FtItem item[kFtItems];
@@ -188,17 +187,6 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t next) 
   return d;
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -208,13 +196,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
 }
 
 // Waits for the warp's TMEM loads; the registers given are not used before it.
-template <int N, int M>
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N], uint32_t (&w)[M]) {
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
-#pragma unroll
-  for (int i = 0; i < M; ++i) asm volatile("" : "+r"(w[i]));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -266,16 +252,19 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     }
     for (int i = 0; i < kFtItems; ++i) {
       mbar_init(&sh->item_full[i], 1);
-      mbar_init(&sh->item_empty[i], 13);  // eight softmax warps, four converters, the issuer
+      mbar_init(&sh->item_empty[i], 14);  // eight softmax warps, four converters, two issuers
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
-      mbar_init(&sh->p_full[i], 4);
-      mbar_init(&sh->pv_done[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh->p_full[i][h], 4);
+        mbar_init(&sh->pv_done[i][h], 1);
+      }
     }
     mbar_init(&sh->q_full, 4);
-    mbar_init(&sh->fin, 9);  // eight softmax warps, the issuer
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->fin, 9);  // eight softmax warps, the issuer of S
+    mbar_init(&sh->drain[0], 1);
+    mbar_init(&sh->drain[1], 1);
     mbar_init(&sh->other, 4);
     fence_mbar_init();
   }
@@ -302,21 +291,21 @@ __global__ void __launch_bounds__(kFtThreads, 1)
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---- softmax of slot `slot`: row r of its tile
     const int slot = warp >> 2, r = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kFtO + slot * 128 + lane_base;
-    int unit = -1, g = 0, done[2] = {0, 0}, pages = 0, valid_pages = 0, loads = 0, others = 0;
-    int place = -1, at_start[2] = {0, 0};
+    // steps of this slot and of the other one so far, and at the unit's start
+    int unit = -1, g = 0, done = 0, done_o = 0, pages = 0, valid_pages = 0, loads = 0, others = 0;
+    int place = -1, start = 0, start_o = 0;
     FtUnit t{};
     int row = 0, pos = 0, pos_first = 0, pos0 = 0;  // pos0: of the sequence's first query token
     float M = -INFINITY, l = 0.f, q_fac = 1.f;
 
     // writes the unit's rows (or its partial state)
     auto finish = [&]() -> bool {
-      const bool mine = done[slot] > at_start[slot];
-      if (mine && !mbar_wait_warp(&sh->pv_done[slot], (done[slot] - 1) & 1)) return false;
+      const bool mine = done > start;
+      if (mine && !mbar_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) return false;
       if (t.width == 1) {
         if (slot == 1) {
           sh->other_m[r] = M;
@@ -326,12 +315,12 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           return true;
         }
         if (!mbar_wait_warp(&sh->other, others & 1)) return false;
-        if (done[1] > at_start[1] && !mbar_wait_warp(&sh->pv_done[1], (done[1] - 1) & 1)) return false;
+        if (done_o > start_o && !mbar_wait_warp(&sh->pv_done[1][1], (done_o - 1) & 1)) return false;
       }
       tc_fence_after();
       // state of the row = fa * own O + fb * the other slot's O
       float fa = mine ? 1.f : 0.f, fb = 0.f;
-      const bool both = t.width == 1 && done[1] > at_start[1];
+      const bool both = t.width == 1 && done_o > start_o;
       if (both) {
         const float mo = sh->other_m[r], lo = sh->other_l[r];
         const float mn = fmaxf(M, mo);
@@ -350,16 +339,24 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       float* part = place < 0 ? nullptr
                               : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kFtPlaceFloats;
       const bool poison = sh->nan_any != 0;
+#pragma unroll 1
       for (int c = 0; c < 8; ++c) {  // 16 columns = dims of two groups of 8
-        uint32_t x[16], y[16];
-        if (mine) tmem_ld16(tO + 16 * c, x);
-        if (both) tmem_ld16(tO + 128 + 16 * c, y);
-        tmem_wait_ld(x, y);
+        uint32_t x[16];
         float v[16];
+        if (mine) {
+          tmem_ld16(tO + 16 * c, x);
+          tmem_wait_ld(x);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = mine ? __uint_as_float(x[i]) * fa : 0.f;
+        if (both) {
+          tmem_ld16(tO + 128 + 16 * c, x);
+          tmem_wait_ld(x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(x[i]) * fb;
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          v[i] = mine ? __uint_as_float(x[i]) * fa : 0.f;
-          if (both) v[i] += __uint_as_float(y[i]) * fb;
           if (poison && pos >= sh->nan_key[8 * ft_dim8(2 * c + (i >> 3)) + (i & 7)]) v[i] = NAN;
           v[i] *= out_f;
         }
@@ -419,8 +416,8 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         t = ft_unit(a, unit, per_seq);
         place = it.place;
         pages = 0;
-        at_start[0] = done[0];
-        at_start[1] = done[1];
+        start = done;
+        start_o = done_o;
         row = t.row0 + (t.width == 2 ? slot * kFtRows : 0) + r;
         pos0 = a.seq_lens[t.b] - T;
         pos = pos0 + min(row, T * Hg - 1) / Hg;
@@ -441,96 +438,102 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       const int turn = pages & 1;
       ++pages;
       if (t.width == 1 && turn != slot) {
-        ++done[turn];
+        ++done_o;
         continue;
       }
-      const bool had = done[slot] > at_start[slot];
+      const bool had = done > start;
       // the converters' NaN marks of a page that some row of the sequence does not see whole are read
       // when the unit is written: seeing the page's stage full orders them before that (the stage
       // is not used again before this step's P)
-      if (!mbar_wait_warp(&sh->s_full[slot], done[slot] & 1) ||
+      if (!mbar_wait_warp(&sh->s_full[slot], done & 1) ||
           (it.block * kBlock + kBlock - 1 > pos0 && !mbar_wait_warp(&sh->v_full[vstage], vphase))) {
         failed = true;
         break;
       }
       tc_fence_after();
       const float f = fmaxf(it.k_scale * q_fac, 1.2e-38f);  // (positive: -inf times it stays -inf)
-      uint32_t v0[64], v1[64];
-      float mx;
-      const bool edge = it.block * kBlock + kBlock - 1 > pos_first;
-      if (!edge) {
-        float m0, m1;
-        tmem_ld64_max(tS, v0, m0);
-        tmem_ld64_max(tS + 64, v1, m1);
-        tmem_wait_ld(v0, v1);
-        asm volatile("" : "+f"(m0), "+f"(m1));
-        mx = fmaxf(m0, m1);
-      } else {
-        tmem_ld64(tS, v0);
-        tmem_ld64(tS + 64, v1);
-        tmem_wait_ld(v0, v1);
-        const int vis = pos - it.block * kBlock + 1;  // visible columns
-        mx = -INFINITY;
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t tH = tS + 64 * h;
+        if (it.block * kBlock + 64 * h + 63 > pos_first) {
+          // some row of the tile must not see one of these keys: -inf over those scores, in place
+          const int vis = pos - it.block * kBlock - 64 * h + 1;  // visible columns
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t y[16];
+            tmem_ld16(tH + c, y);
+            tmem_wait_ld(y);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          if (i >= vis) v0[i] = 0xff800000u;
-          if (i + 64 >= vis) v1[i] = 0xff800000u;
-          mx = fmaxf(mx, fmaxf(__uint_as_float(v0[i]), __uint_as_float(v1[i])));
+            for (int j = 0; j < 16; ++j) y[j] = c + j < vis ? y[j] : 0xff800000u;
+            tmem_st16(tH + c, y);
+          }
+          tmem_wait_st();
         }
-      }
-      mx = fmaf(mx, f, it.v_exp);
-      if (__any_sync(0xffffffffu, mx > M + 8.f)) {
-        float alpha = 1.f;
-        if (mx > M + 8.f) {
-          const float mn = ceilf(mx);
-          alpha = ex2(M - mn);
-          M = mn;
-          l *= alpha;
-        }
-        if (had) {  // (the issuer has waited for the slot's products before it issued this S)
-          for (int c = 0; c < 8; ++c) {
-            uint32_t x[16];
-            tmem_ld16(tO + 16 * c, x);
-            tmem_wait_ld(x, x);
+        uint32_t v[64];
+        float mx;
+        tmem_ld64_max(tH, v, mx);
+        tmem_wait_ld(v);
+        asm volatile("" : "+f"(mx));
+        mx = fmaf(mx, f, it.v_exp);
+        if (__any_sync(0xffffffffu, mx > M + 8.f)) {
+          float alpha = 1.f;
+          if (mx > M + 8.f) {
+            const float mn = ceilf(mx);
+            alpha = ex2(M - mn);
+            M = mn;
+            l *= alpha;
+            sum.x *= alpha;
+            sum.y *= alpha;
+          }
+          if (had || h > 0) {  // O as the products issued so far leave it, rescaled
+            if (!mbar_wait_warp(&sh->pv_done[slot][h ^ 1], (h ? done : done - 1) & 1)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t y[16];
+              tmem_ld16(tO + 16 * c, y);
+              tmem_wait_ld(y);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-            tmem_st16(tO + 16 * c, x);
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * alpha);
+              tmem_st16(tO + 16 * c, y);
+            }
           }
         }
-      }
-      const float c0 = it.v_exp - (M == -INFINITY ? 0.f : M);
-      const float2 ff = make_float2(f, f), cc = make_float2(c0, c0);
-      float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        // P goes over the first 32 columns of S
+        const float c0 = it.v_exp - (M == -INFINITY ? 0.f : M);
+        const float2 ff = make_float2(f, f), cc = make_float2(c0, c0);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 e0 = fma2(make_float2(__uint_as_float(v0[2 * i]), __uint_as_float(v0[2 * i + 1])), ff, cc);
-        const float2 p0 = make_float2(ex2(e0.x), ex2(e0.y));
-        sum0 = add2(sum0, p0);
-        v0[i] = pack_f16x2(p0.x, p0.y);
-      }
-      tmem_st32(tS, v0);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t pk[16];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 e1 = fma2(make_float2(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1])), ff, cc);
-        const float2 p1 = make_float2(ex2(e1.x), ex2(e1.y));
-        sum1 = add2(sum1, p1);
-        v1[i] = pack_f16x2(p1.x, p1.y);
+          for (int j = 0; j < 16; ++j) {
+            const int k = 32 * i + 2 * j;
+            const float2 e = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, cc);
+            const float2 p = make_float2(ex2(e.x), ex2(e.y));
+            sum = add2(sum, p);
+            pk[j] = pack_f16x2(p.x, p.y);
+          }
+          tmem_st16(tH + 16 * i, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full[slot][h]);
       }
-      tmem_st32(tS + 32, v1);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_full[slot]);
-      ++done[slot];
-      if (t.width == 2) ++done[slot ^ 1];
-      const float sum = (sum0.x + sum1.x) + (sum0.y + sum1.y);
-      l = fmaf(sum, ex2(-it.v_exp), l);
+      if (failed) break;
+      ++done;
+      if (t.width == 2) ++done_o;
+      const float total = sum.x + sum.y;
+      l = fmaf(total, ex2(-it.v_exp), l);
       if (a.weight_out != nullptr && row < t.row0 + t.rows)
         a.share[((static_cast<int64_t>(t.b) * G + g) * a.max_blocks + it.block) * T * Hg + row] =
-            make_float2(sum, (M == -INFINITY ? 0.f : M) - it.v_exp);
+            make_float2(total, (M == -INFINITY ? 0.f : M) - it.v_exp);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp < 12) {
       // ---- Q tiles, V conversion
       const int ct = tid - 256;
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         const int c = ct & 7;
         const int h0 = c < 4 ? 2 * c : 2 * (c & 3) + 1;  // chunk of the first 8 dims within its half
         uint8_t* half = dst + (c < 4 ? 0 : kFtVBytes / 2);
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < 8; ++i) {
           const int r = 16 * i + (ct >> 3);
           const uint4 u = lds128(src + page_chunk(r, c));
@@ -752,35 +755,16 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         for (int k = max(0, page_n - kFtK); k < page_n; ++k) mbar_wait(&sh->k_full[k % kFtK], (k / kFtK) & 1);
         for (int k = max(0, page_n - kFtRaw); k < page_n; ++k) mbar_wait(&sh->raw_full[k % kFtRaw], (k / kFtRaw) & 1);
       }
-    } else if (warp == 13) {
-      // ---- product issuer: S of a step, then P V of the step before it
-      const uint32_t id_s = umma_idesc_f16(kFtRows, kBlock);               // (E4M3 has format code 0 too)
-      const uint32_t id_lo = id_s | (1u << 7);                             // A is E5M2
-      const uint32_t id_o = umma_idesc_f16(kFtRows, kDim) | (1u << 16);    // B MN-major
+    } else if (warp == 13 || warp == 14) {
+      // ---- product issuers: warp 13 S, warp 14 P V.  Two warps, because issuing blocks while the tensor
+      // pipe is full: each waits for its operands while the other's products run.
+      const bool scores = warp == 13;
+      const uint32_t id_s = umma_idesc_f16(kFtRows, kBlock);             // (E4M3 has format code 0 too)
+      const uint32_t id_lo = id_s | (1u << 7);                           // A is E5M2
+      const uint32_t id_o = umma_idesc_f16(kFtRows, kDim) | (1u << 16);  // B MN-major
       const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
-      int unit = -1, g = 0, width = 1, pages = 0, page = 0, loads = 0, done[2] = {0, 0}, at_start[2] = {0, 0};
-      int wait_slot = -1, wait_page = 0, wait_acc = 0;  // the step whose P V is still to come
-      bool wait_last = false;
-      auto products = [&]() -> bool {
-        if (wait_slot < 0) return true;
-        const int s = wait_slot, vs = wait_page % kFtV;
-        wait_slot = -1;
-        if (!mbar_wait_warp(&sh->v_full[vs], (wait_page / kFtV) & 1) ||
-            !mbar_wait_warp(&sh->p_full[s], (done[s] - 1) & 1))
-          return false;
-        tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
-            umma_f16_tmem_a(tmem + kFtO + s * 128, tmem + s * 128 + kk * 8,
-                            umma_desc_mn(vb + vs * kFtVBytes + kk * 2048, kFtVBytes / 2), id_o,
-                            wait_acc || kk > 0 ? 1u : 0u);
-          umma_commit(&sh->pv_done[s]);
-          if (wait_last) umma_commit(&sh->v_empty[vs]);
-        }
-        __syncwarp();
-        return true;
-      };
+      int unit = -1, g = 0, width = 1, pages = 0, page = 0, loads = 0;
+      int done0 = 0, done1 = 0, start0 = 0, start1 = 0;  // steps of the slots so far, and at the unit's start
       for (int n = 0; !failed; ++n) {
         FtItem it;
         if (!take_item(n, it)) {
@@ -788,66 +772,78 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           break;
         }
         if (it.unit < 0 || it.unit != unit || it.g != g) {
-          if (!products()) {
-            failed = true;
-            break;
-          }
-          if (unit >= 0 && lane == 0) mbar_arrive(&sh->fin);
+          if (scores && unit >= 0 && lane == 0) mbar_arrive(&sh->fin);
           unit = it.unit;
           g = it.g;
           if (unit < 0) break;
           width = ft_unit(a, unit, per_seq).width;
           pages = 0;
-          at_start[0] = done[0];
-          at_start[1] = done[1];
-          if (!mbar_wait_warp(&sh->q_full, loads & 1)) {
+          start0 = done0;
+          start1 = done1;
+          if (scores && !mbar_wait_warp(&sh->q_full, loads & 1)) {
             failed = true;
             break;
           }
           ++loads;
         }
         if (it.block < 0) continue;
-        const int ks = page % kFtK;
-        if (!mbar_wait_warp(&sh->k_full[ks], (page / kFtK) & 1)) {
+        const int ks = page % kFtK, vs = page % kFtV;
+        if (scores ? !mbar_wait_warp(&sh->k_full[ks], (page / kFtK) & 1)
+                   : !mbar_wait_warp(&sh->v_full[vs], (page / kFtV) & 1)) {
           failed = true;
           break;
         }
         for (int i = 0; i < width && !failed; ++i) {
           const int s = width == 2 ? i : pages & 1;
-          // the slot's P (which S overwrites) has been multiplied
-          if (done[s] > 0 && !mbar_wait_warp(&sh->pv_done[s], (done[s] - 1) & 1)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t qt = qb + (width == 2 ? s : 0) * (kFtRows * 128), kt = kb + ks * kFp8PageBytes;
-            for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
+          const int d = s ? done1 : done0;
+          const bool last = i == width - 1;
+          if (scores) {
+            // S overwrites the slot's P: it waits until that has been multiplied
+            if (d > 0 && !mbar_wait_warp(&sh->pv_done[s][1], (d - 1) & 1)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t qt = qb + (width == 2 ? s : 0) * (kFtRows * 128), kt = kb + ks * kFp8PageBytes;
+              for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)  // 32 dims a step
-                umma_f8(tmem + s * 128, umma_desc(qt + part * (2 * kFtRows * 128) + 32 * kk), umma_desc(kt + 32 * kk),
-                        part > 0 ? id_lo : id_s, part > 0 || kk > 0 ? 1u : 0u);
-            umma_commit(&sh->s_full[s]);
-            if (i == width - 1) umma_commit(&sh->k_empty[ks]);
+                for (int kk = 0; kk < 4; ++kk)  // 32 dims a step
+                  umma_f8(tmem + s * 128, umma_desc(qt + part * (2 * kFtRows * 128) + 32 * kk), umma_desc(kt + 32 * kk),
+                          part > 0 ? id_lo : id_s, part > 0 || kk > 0 ? 1u : 0u);
+              umma_commit(&sh->s_full[s]);
+              if (last) umma_commit(&sh->k_empty[ks]);
+            }
+            __syncwarp();
+          } else {
+            for (int h = 0; h < 2; ++h) {  // 64 keys: the products of the first half run beside the softmax of the second
+              if (!mbar_wait_warp(&sh->p_full[s][h], d & 1)) {
+                failed = true;
+                break;
+              }
+              tc_fence_after();
+              if (lane == 0) {
+                const bool add = h > 0 || d > (s ? start1 : start0);
+                const uint32_t vt = vb + vs * kFtVBytes + h * 64 * 128;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
+                  umma_f16_tmem_a(tmem + kFtO + s * 128, tmem + s * 128 + h * 64 + 8 * kk,
+                                  umma_desc_mn(vt + kk * 2048, kFtVBytes / 2), id_o, add || kk > 0 ? 1u : 0u);
+                umma_commit(&sh->pv_done[s][h]);
+                if (last && h == 1) umma_commit(&sh->v_empty[vs]);
+              }
+              __syncwarp();
+            }
           }
-          __syncwarp();
-          if (!products()) {
-            failed = true;
-            break;
-          }
-          wait_slot = s;
-          wait_page = page;
-          wait_acc = done[s] > at_start[s];
-          wait_last = i == width - 1;
-          ++done[s];
+          s ? ++done1 : ++done0;
         }
         ++pages;
         ++page;
       }
       if (failed) {  // the products still running end before TMEM is freed
-        if (lane == 0) umma_commit(&sh->drain);
+        if (lane == 0) umma_commit(&sh->drain[scores]);
         __syncwarp();
-        mbar_wait_warp(&sh->drain, 0);
+        mbar_wait_warp(&sh->drain[scores], 0);
       }
     }
   }
