@@ -21,7 +21,7 @@ SOURCES = ["api.cu", "quant.cu", "indexer.cu", "prefill.cu", "select.cu", "atten
            "api_fp8.cu", "fp8_append.cu", "fp8_attn.cu", "fp8_stream.cu",
            "fp8_tile.cu", "evict.cu"]
 HEADERS = ["msa_device.cuh", "msa_kernels.h", "api_internal.h", "select_row.cuh", "umma.cuh", "indexer_tile.cuh",
-           "attention_tile.cuh", "attention_team.cuh", "fp8_device.cuh", "fp8_kernels.h"]
+           "attention_tile.cuh", "attention_team.cuh", "fp8_device.cuh", "fp8_kernels.h", "fp8_merge.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

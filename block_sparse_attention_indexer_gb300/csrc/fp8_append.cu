@@ -62,7 +62,7 @@ __device__ __forceinline__ uint4 encode16(const float (&v)[16], float f) {
 }
 
 template <typename X>
-__global__ void __launch_bounds__(kApThreads) fp8_append_kernel(const Fp8AppendArgs a, int touched) {
+__global__ void __launch_bounds__(kApThreads, 3) fp8_append_kernel(const Fp8AppendArgs a, int touched) {
   __shared__ uint32_t s_amax;
   const int tid = threadIdx.x;
   if (tid == 0) s_amax = 0u;

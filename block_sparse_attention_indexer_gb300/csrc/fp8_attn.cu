@@ -18,8 +18,8 @@ __device__ __forceinline__ float decayed(const Fp8AttnArgs& a, int64_t i) {
   return a.weight_in != nullptr ? a.weight_decay * a.weight_in[i] : 0.f;
 }
 
-// Dense: one warp per (sequence, block) for few rows, else one CTA of 256 threads; each thread
-// takes every 32nd (256th) (part, row) of the groups in turn, then a tree: a fixed order.
+// Dense: one warp per (sequence, block) for few shares, else one CTA of 256 threads; each thread
+// takes every 32nd (256th) of the block's shares (group, part, row), then a tree: a fixed order.
 // Rows before the block's first key have no share there.
 template <int kTeam>
 __global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const Fp8AttnArgs a, int parts) {
@@ -31,22 +31,19 @@ __global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const Fp8AttnArg
   const int b = static_cast<int>(idx / a.max_blocks), n = static_cast<int>(idx % a.max_blocks);
   const int tid = threadIdx.x % kTeam;
   const int L = a.seq_lens[b], T = a.q_len;
-  const bool ok = L > 0 && L >= T && L <= static_cast<int64_t>(a.max_blocks) * kBlock && n <= (L - 1) / kBlock;
+  const bool ok = length_ok(a, L) && n <= (L - 1) / kBlock;
   float sum = 0.f;
   if (ok) {
     const int rows = T * a.heads_per_group;
     // first row that sees the block: token t with L - T + t >= 128 n
-    const int r0 = max(n * kBlock - (L - T), 0) * a.heads_per_group;
-    for (int g = 0; g < a.groups; ++g) {
+    const int r0 = max(n * kBlock - (L - T), 0) * a.heads_per_group, seen = rows - r0;
+    const int all = a.groups * parts * seen;
+#pragma unroll 4
+    for (int i = tid; i < all; i += kTeam) {
+      const int gp = i / seen, r = r0 + i - gp * seen, g = gp / parts, p = gp - g * parts;
       const int64_t unit = static_cast<int64_t>(b) * a.groups + g;
-      const float2* stat = a.row_stat + unit * rows;
-      for (int p = 0; p < parts; ++p) {
-        const float2* share = a.share + ((unit * a.max_blocks + n) * parts + p) * rows;
-        for (int r = r0 + tid; r < rows; r += kTeam) {
-          const float2 s = share[r], st = stat[r];
-          if (s.x != 0.f) sum += s.x * exp2f(s.y - st.x) * st.y;
-        }
-      }
+      const float2 s = a.share[((unit * a.max_blocks + n) * parts + p) * rows + r], st = a.row_stat[unit * rows + r];
+      sum += s.x != 0.f ? s.x * exp2f(s.y - st.x) * st.y : 0.f;
     }
   }
 #pragma unroll
@@ -56,33 +53,42 @@ __global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const Fp8AttnArg
     __syncthreads();
     sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kTeam / 32; ++w) sum += s_sum[w % 8];
+    for (int w = 0; w < 8; ++w) sum += s_sum[w];
   }
   if (tid == 0) a.weight_out[idx] = decayed(a, idx) + sum;
 }
 
 // Sparse: each (row of the selection, slot) adds its share to its block as a fixed-point number
 // with 40 fraction bits, so that the sum does not depend on the order (a sequence collects at
-// most T * H < 2^22: it fits bit 62; bit 63 marks a NaN).
-__global__ void __launch_bounds__(256) fp8_weights_scatter_kernel(const Fp8AttnArgs a, int parts) {
+// most T * H < 2^22: it fits bit 62; bit 63 marks a NaN).  Eight lanes take one entry, a head each.
+__global__ void __launch_bounds__(256) fp8_weights_scatter_kernel(const Fp8AttnArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t units = static_cast<int64_t>(a.batch) * a.q_len * a.groups;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= units * kTopK) return;
-  const int64_t unit = i / kTopK;
-  const int bt = static_cast<int>(unit / a.groups), b = bt / a.q_len, t = bt % a.q_len;
-  const int L = a.seq_lens[b], n = a.selection[i];
-  if (!(L > 0 && L >= a.q_len && L <= static_cast<int64_t>(a.max_blocks) * kBlock) || n < 0 ||
-      n > (L - a.q_len + t) / kBlock)
-    return;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 8;
+  const int h = threadIdx.x & 7;
   const int Hg = a.heads_per_group;
   float sum = 0.f;
-  for (int p = 0; p < parts; ++p)
-    for (int h = 0; h < Hg; ++h) {
-      const float2 s = a.share[(i * parts + p) * Hg + h], st = a.row_stat[unit * Hg + h];
-      if (s.x != 0.f) sum += s.x * exp2f(s.y - st.x) * st.y;
+  int b = 0, n = -1;
+  if (i < units * kTopK) {
+    const int64_t unit = i / kTopK;
+    const int bt = static_cast<int>(unit / a.groups);
+    b = bt / a.q_len;
+    const int L = a.seq_lens[b];
+    n = a.selection[i];
+    if (!length_ok(a, L) || n > (L - a.q_len + bt - b * a.q_len) / kBlock) n = -1;
+    if (n >= 0 && h < Hg) {
+      const float2 st = a.row_stat[unit * Hg + h];
+      float2 s[kFp8StreamParts];
+#pragma unroll
+      for (int p = 0; p < kFp8StreamParts; ++p) s[p] = a.share[(i * kFp8StreamParts + p) * Hg + h];
+#pragma unroll
+      for (int p = 0; p < kFp8StreamParts; ++p) sum += s[p].x != 0.f ? s[p].x * exp2f(s[p].y - st.x) * st.y : 0.f;
     }
+  }
+#pragma unroll
+  for (int s = 4; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  if (h != 0 || n < 0) return;
   unsigned long long* m = a.mass + static_cast<int64_t>(b) * a.max_blocks + n;
   if (sum != sum)
     atomicOr(m, 1ull << 63);
@@ -145,8 +151,7 @@ cudaError_t launch_fp8_attn(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
   e = stream ? launch_fp8_stream(a, num_sms, s) : launch_fp8_tile(a, num_sms, s);
   if (e != cudaSuccess || !weights) return e;
   if (sparse) {
-    e = launch_dependent(fp8_weights_scatter_kernel, dim3(static_cast<unsigned>((units * kTopK + 255) / 256)), 256, 0, s,
-                         a, parts);
+    e = launch_dependent(fp8_weights_scatter_kernel, dim3(static_cast<unsigned>((units * kTopK + 31) / 32)), 256, 0, s, a);
     if (e != cudaSuccess) return e;
     return launch_dependent(fp8_weights_sparse_kernel, dim3(static_cast<unsigned>((blocks + 255) / 256)), 256, 0, s, a);
   }

@@ -28,6 +28,7 @@
 
 #include "fp8_device.cuh"
 #include "fp8_kernels.h"
+#include "fp8_merge.cuh"
 #include "msa_device.cuh"
 
 namespace msa {
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
           dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
           dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
           if (gq == 0) {
-            if (a.lse != nullptr) a.lse[hr] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (a.lse != nullptr) a.lse[hr] = any ? (m + log2f(l)) * kLn2F : -INFINITY;
             if (a.weight_out != nullptr) a.row_stat[static_cast<int64_t>(unit) * rows + r] = make_float2(any ? m : 0.f, inv);
           }
         } else {
@@ -725,17 +726,12 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
   if (failed && lane == 0) flag_error(a.err, MSA_DEVERR_TIMEOUT);
 }
 
-// Units cut by range boundaries: the partial states that their teams left, added.  blockIdx.y is
-// the row, blockIdx.x the unit (by_unit) or the boundary whose unit the CTA takes if it is the
-// unit's first: whichever is fewer.  Threads: four groups of 64, each with every fourth state
-// eight at a time, two dims a thread; the groups' sums meet in shared memory.
-constexpr int kFsMergeThreads = 256;
-
-template <int NT>
-__global__ void __launch_bounds__(kFsMergeThreads) fp8_stream_merge_kernel(const Fp8AttnArgs a, int teams, int by_unit) {
-  using S = FsShape<NT>;
-  __shared__ float2 s_o[4][64];
-  __shared__ float s_m[4], s_l[4];
+// Units cut by range boundaries: the partial states that their teams left, added (fp8_merge.cuh).
+// blockIdx.x is the unit (by_unit) or the boundary whose unit the CTA takes if it is the unit's
+// first, whichever is fewer; blockIdx.y the row (kSplit) or eight of them.
+template <int NT, bool kSplit>
+__global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(const Fp8AttnArgs a, int teams, int by_unit) {
+  __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
   const bool sparse = a.selection != nullptr;
@@ -758,79 +754,29 @@ __global__ void __launch_bounds__(kFsMergeThreads) fp8_stream_merge_kernel(const
   }
   const int ca = fs_owner(E, u0, teams), cb = fs_owner(E, u1 - 1, teams);
   if (ca == cb || (!by_unit && static_cast<int>(blockIdx.x) != ca)) return;  // whole, or another boundary's
-  const int r = blockIdx.y, grp = threadIdx.x / 64, d = 2 * (threadIdx.x % 64);
-  const int rows = sparse ? a.heads_per_group : a.q_len * a.heads_per_group;
-  float M = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int c0 = ca + grp; c0 <= cb; c0 += 32) {
-    float ms[8], ls[8];
-    float2 os[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + 4 * i;
-      ms[i] = -INFINITY;
-      ls[i] = 0.f;
-      os[i] = make_float2(0.f, 0.f);
+  if (threadIdx.x < 32) {  // the teams ca .. cb with a range, in order
+    int n = 0;
+    for (int c0 = ca; c0 <= cb; c0 += 32) {
+      const int c = c0 + threadIdx.x;
       const int lo = fs_lo(E, c, teams);
-      if (c <= cb && lo < fs_lo(E, c + 1, teams)) {
-        // the state is in the team's first place if the unit is the first of its range
-        const float* part = a.partial + (2 * static_cast<int64_t>(c) + (lo >= u0 ? 0 : 1)) * S::kSlotFloats;
-        ms[i] = __ldcg(part + S::kRows * kDim + r);
-        ls[i] = __ldcg(part + S::kRows * (kDim + 1) + r);
-        os[i] = __ldcg(reinterpret_cast<const float2*>(part + r * kDim + d));
-      }
+      const bool some = c <= cb && lo < fs_lo(E, c + 1, teams);
+      const unsigned m = __ballot_sync(0xffffffffu, some);
+      // the state is in the team's first place if the unit is the first of its range
+      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * c + (lo >= u0 ? 0 : 1);
+      n += __popc(m);
     }
-    float mb = M;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mb = fmaxf(mb, ms[i]);
-    if (mb == -INFINITY) {
-      // no key so far: only a NaN could be in the sums
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        l += ls[i];
-        o0 += os[i].x;
-        o1 += os[i].y;
-      }
-      continue;
-    }
-    const float f = ex2(M - mb);
-    l *= f;
-    o0 *= f;
-    o1 *= f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float w = ex2(ms[i] - mb);
-      l += w * ls[i];
-      o0 += w * os[i].x;
-      o1 += w * os[i].y;
-    }
-    M = mb;
-  }
-  s_o[grp][d / 2] = make_float2(o0, o1);
-  if (d == 0) {
-    s_m[grp] = M;
-    s_l[grp] = l;
+    if (threadIdx.x == 0) sh.n = n;
   }
   __syncthreads();
-  if (grp != 0) return;
-  const float mb = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  l = o0 = o1 = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float w = mb == -INFINITY ? 1.f : ex2(s_m[i] - mb);
-    l += w * s_l[i];
-    o0 += w * s_o[i][d / 2].x;
-    o1 += w * s_o[i][d / 2].y;
-  }
-  const bool any = l != 0.f;
-  const float inv = any ? 1.f / l : 0.f;
-  const int Hg = a.heads_per_group;
+  const int Hg = a.heads_per_group, rows = sparse ? Hg : a.q_len * Hg;
+  const int r = kSplit ? blockIdx.y : blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  float4 o;
+  float M, l;
+  fp8_merge_row<kSplit>(a.partial, FsShape<NT>::kRows, r, sh, o, M, l);
+  if (kSplit && threadIdx.x >= 32) return;
   const int64_t token = sparse ? unit / a.groups : static_cast<int64_t>(unit / a.groups) * a.q_len + r / Hg;
-  const int64_t hr = token * a.groups * Hg + unit % a.groups * Hg + r % Hg;
-  *reinterpret_cast<__nv_bfloat162*>(a.out + hr * kDim + d) = __floats2bfloat162_rn(o0 * inv, o1 * inv);
-  if (d == 0) {
-    if (a.lse != nullptr) a.lse[hr] = any ? (mb + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    if (a.weight_out != nullptr) a.row_stat[static_cast<int64_t>(unit) * rows + r] = make_float2(any ? mb : 0.f, inv);
-  }
+  fp8_write_row(a, token * a.groups * Hg + unit % a.groups * Hg + r % Hg, static_cast<int64_t>(unit) * rows + r, o, M, l);
 }
 
 size_t fp8_stream_partial_bytes() {
@@ -853,8 +799,11 @@ static cudaError_t launch_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t
   const int64_t units = static_cast<int64_t>(a.batch) * a.groups * (sparse ? a.q_len : 1);
   const int rows = sparse ? a.heads_per_group : a.q_len * a.heads_per_group;
   const int by_unit = units < teams - 1 ? 1 : 0;
-  return launch_dependent(fp8_stream_merge_kernel<NT>, dim3(by_unit ? static_cast<unsigned>(units) : teams - 1, rows),
-                          kFsMergeThreads, 0, s, a, teams, by_unit);
+  const unsigned grid = by_unit ? static_cast<unsigned>(units) : static_cast<unsigned>(teams - 1);
+  return teams / units >= kFp8MergeSplitParts
+             ? launch_dependent(fp8_stream_merge_kernel<NT, true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, teams, by_unit)
+             : launch_dependent(fp8_stream_merge_kernel<NT, false>, dim3(grid, (rows + 7) / 8), kFp8MergeThreads, 0, s, a,
+                                teams, by_unit);
 }
 
 cudaError_t launch_fp8_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {

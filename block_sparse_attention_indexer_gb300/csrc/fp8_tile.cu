@@ -31,6 +31,7 @@
 
 #include "fp8_device.cuh"
 #include "fp8_kernels.h"
+#include "fp8_merge.cuh"
 #include "msa_device.cuh"
 #include "umma.cuh"
 
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       }
       if (valid) {
         if (place < 0) {
-          if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * kLn2F : -INFINITY;
           if (a.weight_out != nullptr)
             a.row_stat[(static_cast<int64_t>(t.b) * G + g) * T * Hg + row] = make_float2(any ? M : 0.f, inv);
         } else {
@@ -854,75 +855,57 @@ __global__ void __launch_bounds__(kFtThreads, 1)
   if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Units cut by range boundaries: CTA x takes the unit that boundary x + 1 cuts, if it is the unit's
-// first cut; a warp per row (8 of its rows per CTA), 4 dims a lane, the parts eight at a time.
-__global__ void __launch_bounds__(256) fp8_tile_merge_kernel(const Fp8AttnArgs a, int per_seq, int ctas) {
+// Units cut by range boundaries: the partial states that their CTAs left, added (fp8_merge.cuh).
+// blockIdx.x is the unit (by_unit) or the boundary whose unit the CTA takes if it is the unit's first
+// cut, whichever is fewer; blockIdx.y the row (kSplit) or eight of them.
+template <bool kSplit>
+__global__ void __launch_bounds__(kFp8MergeThreads) fp8_tile_merge_kernel(const Fp8AttnArgs a, int per_seq, int ctas, int by_unit) {
+  __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
   const int units = a.batch * per_seq, G = a.groups, Hg = a.heads_per_group, T = a.q_len;
   const int64_t E = static_cast<int64_t>(a.block_prefix[units]) * G;
-  const int x = blockIdx.x, xb = ft_lo(E, x + 1, ctas), xa = ft_lo(E, x, ctas);
-  if (xb >= E) return;
-  const int u = ft_find(a.block_prefix, units, G, xb);
+  const int x = blockIdx.x;
+  int u = x / G, xb = 0;
+  if (!by_unit) {
+    xb = ft_lo(E, x + 1, ctas);
+    if (xb >= E) return;
+    u = ft_find(a.block_prefix, units, G, xb);
+  }
   const FtUnit t = ft_unit(a, u, per_seq);
   const int steps = t.width * t.pages;
   const int64_t first = static_cast<int64_t>(a.block_prefix[u]) * G;
-  const int g = static_cast<int>((xb - first) / steps);
+  const int g = by_unit ? x - u * G : static_cast<int>((xb - first) / steps);
   const int64_t u0 = first + static_cast<int64_t>(g) * steps;
-  const int cut = static_cast<int>((xb - u0) / t.width);  // pages before the boundary
-  if (cut == 0 || (xa > u0 && (xa - u0) / t.width > 0)) return;
-  const int pr = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (pr >= t.rows) return;
-  float M = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + steps; c0 += 8) {
-    float ms[8], ls[8];
-    float4 os[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + i;
-      ms[i] = -INFINITY;
-      ls[i] = 0.f;
-      os[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c >= ctas) continue;
+  if (!by_unit) {
+    const int xa = ft_lo(E, x, ctas);
+    if ((xb - u0) / t.width == 0 || (xa > u0 && (xa - u0) / t.width > 0)) return;  // no page before it, or not the first
+  }
+  if (threadIdx.x < 32) {  // the CTAs with pages of the unit, in order
+    int n = 0;
+    for (int c0 = by_unit ? static_cast<int>(((u0 + 1) * ctas - 1) / E) : x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + steps; c0 += 32) {
+      const int c = c0 + threadIdx.x;
       const int64_t a0 = ft_lo(E, c, ctas) - u0, a1 = ft_lo(E, c + 1, ctas) - u0;
       const int lo = static_cast<int>(max(a0, int64_t{0}) / t.width);
       const int hi = static_cast<int>(min(a1 / t.width, static_cast<int64_t>(t.pages)));
-      if (a0 >= steps || lo >= hi) continue;
-      const float* part = a.partial + (2 * static_cast<int64_t>(c) + (lo == 0 ? 1 : 0)) * kFtPlaceFloats;
-      ms[i] = __ldcg(part + 2 * kFtRows * kDim + pr);
-      ls[i] = __ldcg(part + 2 * kFtRows * (kDim + 1) + pr);
-      os[i] = __ldcg(reinterpret_cast<const float4*>(part + pr * kDim) + lane);
+      const bool some = c < ctas && a0 < steps && lo < hi;
+      const unsigned m = __ballot_sync(0xffffffffu, some);
+      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * c + (lo == 0 ? 1 : 0);
+      n += __popc(m);
     }
-    float mb = M;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mb = fmaxf(mb, ms[i]);
-    const float f = mb == -INFINITY ? 1.f : ex2(M - mb);
-    l *= f;
-    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float w = mb == -INFINITY ? 1.f : ex2(ms[i] - mb);
-      l += w * ls[i];
-      o.x += w * os[i].x;
-      o.y += w * os[i].y;
-      o.z += w * os[i].z;
-      o.w += w * os[i].w;
-    }
-    M = mb;
+    if (threadIdx.x == 0) sh.n = n;
   }
-  const bool any = l != 0.f;
-  const float inv = any ? 1.f / l : 0.f;
+  __syncthreads();
+  if (sh.n < 2) return;  // one CTA's: written by it
+  const int pr = kSplit ? blockIdx.y : blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (pr >= t.rows) return;
+  float4 o;
+  float M, l;
+  fp8_merge_row<kSplit>(a.partial, 2 * kFtRows, pr, sh, o, M, l);
+  if (kSplit && threadIdx.x >= 32) return;
   const int row = t.row0 + pr;
-  const int64_t hr = (static_cast<int64_t>(t.b) * T + row / Hg) * G * Hg + g * Hg + row % Hg;
-  const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(a.out + hr * kDim)[lane] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-  if (lane == 0) {
-    if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    if (a.weight_out != nullptr)
-      a.row_stat[(static_cast<int64_t>(t.b) * G + g) * T * Hg + row] = make_float2(any ? M : 0.f, inv);
-  }
+  fp8_write_row(a, (static_cast<int64_t>(t.b) * T + row / Hg) * G * Hg + g * Hg + row % Hg,
+                (static_cast<int64_t>(t.b) * G + g) * T * Hg + row, o, M, l);
 }
 
 int fp8_tile_units_per_seq(int64_t rows) { return static_cast<int>((rows + 2 * kFtRows - 1) / (2 * kFtRows)); }
@@ -941,7 +924,13 @@ cudaError_t launch_fp8_tile(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
     return e;
   if (ctas == 1) return cudaSuccess;
   const int rows = a.q_len * a.heads_per_group < 2 * kFtRows ? a.q_len * a.heads_per_group : 2 * kFtRows;
-  return launch_dependent(fp8_tile_merge_kernel, dim3(ctas - 1, (rows + 7) / 8), 256, 0, s, a, per_seq, ctas);
+  const int64_t units = static_cast<int64_t>(a.batch) * per_seq * a.groups;
+  const int by_unit = units < ctas - 1 ? 1 : 0;
+  const unsigned grid = by_unit ? static_cast<unsigned>(units) : static_cast<unsigned>(ctas - 1);
+  return ctas / units >= kFp8MergeSplitParts
+             ? launch_dependent(fp8_tile_merge_kernel<true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, per_seq, ctas, by_unit)
+             : launch_dependent(fp8_tile_merge_kernel<false>, dim3(grid, (rows + 7) / 8), kFp8MergeThreads, 0, s, a, per_seq,
+                                ctas, by_unit);
 }
 
 }  // namespace msa
