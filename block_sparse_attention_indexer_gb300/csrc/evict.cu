@@ -66,7 +66,7 @@ __device__ __forceinline__ int cta_before(int v, EvCounts<kThreads>& count, int&
 }
 
 template <int kThreads, bool kBins>
-__global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, kBins ? 2048 / kThreads : 4) evict_kernel(const EvictArgs a) {
   __shared__ EvShared<kThreads, kBins> sh;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -85,20 +85,33 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_kernel(const 
   const int mine = (tid >> 5) * 32 * kEvItems + lane;   // this thread's first block of a step
   int turn = 0;
 
-  // 0 for blocks that are no candidates (and for NaN, the lowest); a row of at most kStep blocks
-  // stays in registers for the search, and its weights and pages are read again to be moved
+  // A row of at most kStep blocks stays in registers for the search: its order values, 0 for blocks that
+  // are no candidates (and for NaN, the lowest), and where the row is short also its weights and pages
+  // (otherwise these are read again to be moved, so that four CTAs of 512 threads fit an SM).
   const bool once = nb <= kStep;
+  const bool held = !kBins && once;
+  float w[kEvItems];
+  int32_t page[kEvItems];
   uint32_t order[kEvItems];
-  auto load = [&](int base) {
-    float w[kEvItems];
+  auto fetch = [&](int base) {
 #pragma unroll
     for (int j = 0; j < kEvItems; ++j) {
       const int i = base + mine + 32 * j;
-      w[j] = i >= c0 && i < c1 ? weight[i] : NAN;
+      w[j] = i < nb ? weight[i] : 0.f;
+      page[j] = i < nb ? table[i] : -1;
+    }
+  };
+  auto load = [&](int base) {
+    float x[kEvItems];
+#pragma unroll
+    for (int j = 0; j < kEvItems; ++j) {
+      const int i = base + mine + 32 * j;
+      x[j] = i < c0 || i >= c1 ? NAN : held ? w[j] : weight[i];
     }
 #pragma unroll
-    for (int j = 0; j < kEvItems; ++j) order[j] = score_order(w[j]);
+    for (int j = 0; j < kEvItems; ++j) order[j] = score_order(x[j]);
   };
+  if (held) fetch(0);
   // Candidates with an order value above kth stay, and the lowest `equal` of those with kth itself.
   uint32_t kth = 0u;
   int equal = 0;
@@ -134,8 +147,9 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_kernel(const 
     }
   };
   if (cut && k > 0) {
-    for (int i = tid * 32; i < nb; i += kThreads * 32)  // the table on its way to L2 meanwhile
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(table + i));
+    if (!held)
+      for (int i = tid * 32; i < nb; i += kThreads * 32)  // the table on its way to L2 meanwhile
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(table + i));
     if constexpr (!kBins) {
       if (once) load(0);
       search(30);
@@ -243,14 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_kernel(const 
 
   int stayed = 0, gone = 0, ties = 0;
   for (int base = 0; base < nb; base += kStep) {
-    float w[kEvItems];
-    int32_t page[kEvItems];
-#pragma unroll
-    for (int j = 0; j < kEvItems; ++j) {
-      const int i = base + mine + 32 * j;
-      w[j] = i < nb ? weight[i] : 0.f;
-      page[j] = i < nb ? table[i] : -1;
-    }
+    if (!held) fetch(base);
     uint32_t stay = 0, tie = 0;  // bit j: block j of this thread
     int tie_here = 0;            // of the warp
 #pragma unroll
