@@ -225,6 +225,38 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // pairs (the converters' shared stores are then free of bank conflicts).  Of column group n / 8:
 __device__ __forceinline__ int ft_dim8(int group) { return group < 8 ? group : group ^ 1; }
 
+// A lane's 16 bf16 dims of a row (eight lanes hold the row) as the E4M3 and E5M2 parts hi + lo = q 2^-k;
+// returns 2^k, which puts the row's largest value into [2^7, 2^8).
+__device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, uint4& hi, uint4& lo) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float v[16], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    m = fmaxf(m, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
+  }
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -100), 112);
+  const float inv = exp2_int(-k);
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = v[4 * i + j] * inv;
+    h[i] = f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]);
+    uint32_t p0, p1;
+    e4m3x4_to_f16x4(h[i], p0, p1);
+    const float2 p = f16x2_to_float2(p0), q = f16x2_to_float2(p1);
+    l[i] = f32x4_to_e5m2x4(x[0] - p.x, x[1] - p.y, x[2] - q.x, x[3] - q.y);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  return exp2_int(k);
+}
+
 // ---------------------------------------------------------------- the kernel
 
 __global__ void __launch_bounds__(kFtThreads, 1)
@@ -562,54 +594,38 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           sh->nan_key[ct] = INT32_MAX;
           if (ct == 0) sh->nan_any = 0;
           const int c = ct & 7;  // dims 16 c .. 16 c + 15 of rows ct / 8, + 16, ...
-          for (int rr = ct >> 3; rr < t.width * kFtRows; rr += 16) {
-            const int row = t.row0 + rr;
-            const bool valid = rr < t.rows;
-            const int64_t at = (static_cast<int64_t>(t.b) * T + row / Hg) * a.q_stride + (g * Hg + row % Hg) * kDim + 16 * c;
-            uint8_t* dst = q_tile + (rr >> 7) * (kFtRows * 128) + sw128(rr & 127, c);
-            float fac = 1.f;
-            if (!a.q_bf16) {
-              const uint4 u = valid ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(dst) = u;
-            } else {
-              float v[16];
-              float m = 0.f;
+          for (int r0 = ct >> 3; r0 < t.width * kFtRows; r0 += 64) {  // four rows' loads at once
+            uint4 u[4][2];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint4 u = valid ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[i]
-                                      : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-                  v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            for (int i = 0; i < 4; ++i) {
+              const int rr = r0 + 16 * i, row = t.row0 + rr;
+              u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+              if (rr < t.rows) {
+                const int64_t at = (static_cast<int64_t>(t.b) * T + row / Hg) * a.q_stride + (g * Hg + row % Hg) * kDim + 16 * c;
+                if (a.q_bf16) {
+                  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+                  u[i][0] = src[0];
+                  u[i][1] = src[1];
+                } else {
+                  u[i][0] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at);
                 }
               }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
-#pragma unroll
-              for (int s = 1; s < 8; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-              // the largest value of the row into [2^7, 2^8)
-              const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -100), 112);
-              fac = exp2_int(k);
-              const float inv = exp2_int(-k);
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = v[4 * i + j] * inv;
-                hi[i] = f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]);
-                uint32_t h0, h1;
-                e4m3x4_to_f16x4(hi[i], h0, h1);
-                const float2 p = f16x2_to_float2(h0), s = f16x2_to_float2(h1);
-                lo[i] = f32x4_to_e5m2x4(x[0] - p.x, x[1] - p.y, x[2] - s.x, x[3] - s.y);
-              }
-              *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(dst + 2 * kFtRows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
-            if (c == 0) sh->q_fac[rr] = fac;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = r0 + 16 * i;
+              uint8_t* dst = q_tile + (rr >> 7) * (kFtRows * 128) + sw128(rr & 127, c);
+              float fac = 1.f;
+              if (!a.q_bf16) {
+                *reinterpret_cast<uint4*>(dst) = u[i][0];
+              } else {
+                uint4 hi, lo;
+                fac = ft_split_bf16(u[i][0], u[i][1], hi, lo);
+                *reinterpret_cast<uint4*>(dst) = hi;
+                *reinterpret_cast<uint4*>(dst + 2 * kFtRows * 128) = lo;
+              }
+              if (c == 0) sh->q_fac[rr] = fac;
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
