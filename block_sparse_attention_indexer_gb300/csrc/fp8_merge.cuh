@@ -1,8 +1,8 @@
 // The last step of units whose pages the split gave to several teams or CTAs: each left a partial
 // state (O, M, l) of every row, added here.
 //
-// A warp takes a row, or with many parts per unit (kSplit) the eight warps of a CTA share one: a
-// lane holds four dims, eight parts' states are loaded before any is used.  Bound by latency: one
+// A thread takes four dims (a chunk) of a row.  A CTA has eight rows, or with many parts per unit
+// (kSplit) one that its eight warps share; eight parts' states are loaded before any is used.  Bound by latency: one
 // round of loads for each eight parts of a warp.
 #pragma once
 
@@ -28,11 +28,11 @@ struct Fp8MergeShared {
   float m[8], l[8];
 };
 
-// Adds the states of places sh.list[0 .. n) for row `row` (states of `rows` rows); on return the
-// row's sum is in o, M, l of the row's (first) warp.
+// Adds the states of places sh.list[0 .. n) for the thread's chunk of row `row`, float4 number `at` of a
+// state of `rows` rows (O, then M, then l of the rows); with kSplit the sum is warp 0's.
 template <bool kSplit>
-__device__ __forceinline__ void fp8_merge_row(const float* partial, int rows, int row, Fp8MergeShared& sh, float4& o,
-                                              float& M, float& l) {
+__device__ __forceinline__ void fp8_merge_row(const float* partial, int rows, int row, int at, Fp8MergeShared& sh,
+                                              float4& o, float& M, float& l) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = sh.n, first = kSplit ? warp : 0, step = kSplit ? 8 : 1;
   M = -INFINITY;
@@ -51,7 +51,7 @@ __device__ __forceinline__ void fp8_merge_row(const float* partial, int rows, in
         const float* part = partial + static_cast<int64_t>(sh.list[k]) * rows * (kDim + 2);
         ms[i] = __ldcg(part + rows * kDim + row);
         ls[i] = __ldcg(part + rows * (kDim + 1) + row);
-        os[i] = __ldcg(reinterpret_cast<const float4*>(part + row * kDim) + lane);
+        os[i] = __ldcg(reinterpret_cast<const float4*>(part) + at);
       }
     }
     float mb = M;
@@ -98,15 +98,15 @@ __device__ __forceinline__ void fp8_merge_row(const float* partial, int rows, in
   }
 }
 
-// The row's output (head row hr), lse and statistics (index si), from its state; a whole warp.
-__device__ __forceinline__ void fp8_write_row(const Fp8AttnArgs& a, int64_t hr, int64_t si, const float4& o, float M, float l) {
-  const int lane = threadIdx.x & 31;
+// A chunk of the row's output (head row hr) and, by chunk 0, its lse and statistics (index si).
+__device__ __forceinline__ void fp8_write_row(const Fp8AttnArgs& a, int64_t hr, int64_t si, int chunk, const float4& o,
+                                              float M, float l) {
   const bool any = l != 0.f;  // (NaN counts as any)
   const float inv = any ? 1.f / l : 0.f;
   const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), h1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(a.out + hr * kDim)[lane] =
+  reinterpret_cast<uint2*>(a.out + hr * kDim)[chunk] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-  if (lane == 0) {
+  if (chunk == 0) {
     if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * kLn2F : -INFINITY;
     if (a.weight_out != nullptr) a.row_stat[si] = make_float2(any ? M : 0.f, inv);
   }

@@ -773,10 +773,11 @@ __global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(cons
   if (r >= rows) return;
   float4 o;
   float M, l;
-  fp8_merge_row<kSplit>(a.partial, FsShape<NT>::kRows, r, sh, o, M, l);
+  const int chunk = threadIdx.x & 31;
+  fp8_merge_row<kSplit>(a.partial, FsShape<NT>::kRows, r, r * 32 + chunk, sh, o, M, l);
   if (kSplit && threadIdx.x >= 32) return;
   const int64_t token = sparse ? unit / a.groups : static_cast<int64_t>(unit / a.groups) * a.q_len + r / Hg;
-  fp8_write_row(a, token * a.groups * Hg + unit % a.groups * Hg + r % Hg, static_cast<int64_t>(unit) * rows + r, o, M, l);
+  fp8_write_row(a, token * a.groups * Hg + unit % a.groups * Hg + r % Hg, static_cast<int64_t>(unit) * rows + r, chunk, o, M, l);
 }
 
 size_t fp8_stream_partial_bytes() {

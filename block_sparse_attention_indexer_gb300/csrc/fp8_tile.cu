@@ -58,17 +58,19 @@ struct FtShared {
   uint64_t k_full[kFtK], k_empty[kFtK], raw_full[kFtRaw], raw_empty[kFtRaw], v_full[kFtV], v_empty[kFtV];
   uint64_t item_full[kFtItems], item_empty[kFtItems];
   uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [slot], [slot][half of the page's keys]
-  uint64_t q_full, fin, other;  // Q of a unit loaded; a unit written; slot 1's statistics left
+  uint64_t q_full[2], fin[2];   // Q of a unit loaded; a unit written (by the unit's parity on this CTA)
+  uint64_t other;               // slot 1's statistics of a one-tile unit left
   uint64_t drain[2];             // every product issued has ended (after a wait that gave up)
   uint32_t tmem;
-  int nan_any;
+  int nan_any[2];
   FtItem item[kFtItems];
-  float q_fac[2 * kFtRows];     // the power of two taken out of each row (bf16)
+  float q_fac[2][2 * kFtRows];  // the power of two taken out of each row (bf16)
   float other_m[kFtRows], other_l[kFtRows];
-  int nan_key[kDim];            // first key of the unit's edge pages with a NaN code in V, per dim
+  int nan_key[2][kDim];         // first key of the unit's edge pages with a NaN code in V, per dim
 };
 
-constexpr size_t kFtQ = 4 * kFtRows * 128;   // [part hi / lo][tile]
+constexpr int kFtQHalf = 2 * kFtRows * 128;   // two tiles of E4M3 rows
+constexpr size_t kFtQ = 2 * kFtQHalf;         // bf16: the parts hi and lo; E4M3: this unit's and the next one's
 constexpr size_t kFtSmem = 1024 + kFtQ + kFtK * kFp8PageBytes + kFtRaw * kFp8PageBytes + kFtV * kFtVBytes + sizeof(FtShared);
 static_assert(kFtSmem <= 232448, "227 KB of shared memory per CTA");
 
@@ -134,13 +136,16 @@ __global__ void __launch_bounds__(kFtPlanThreads) fp8_tile_plan_kernel(const Fp8
 // First step of CTA c of n.
 __device__ __forceinline__ int ft_lo(int64_t E, int c, int n) { return static_cast<int>(E * c / n); }
 
-// The last unit u with prefix[u] * G <= x.
+// The last unit u with prefix[u] * G <= x, by a whole warp: 32 places a round.
 __device__ __forceinline__ int ft_find(const int32_t* prefix, int units, int groups, int x) {
-  int lo = 0, hi = units;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(prefix[mid]) * groups <= x) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = units;  // it is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool below = at < lo + n && static_cast<int64_t>(prefix[at]) * groups <= x;
+    const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // (the first place always is)
+    n = min(step, lo + n - (lo + k * step));
+    lo += k * step;
   }
   return lo;
 }
@@ -294,8 +299,10 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         mbar_init(&sh->pv_done[i][h], 1);
       }
     }
-    mbar_init(&sh->q_full, 4);
-    mbar_init(&sh->fin, 9);  // eight softmax warps, the issuer of S
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->q_full[i], 4);
+      mbar_init(&sh->fin[i], 9);  // eight softmax warps, the issuer of S
+    }
     mbar_init(&sh->drain[0], 1);
     mbar_init(&sh->drain[1], 1);
     mbar_init(&sh->other, 4);
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kFtO + slot * 128 + lane_base;
     // steps of this slot and of the other one so far, and at the unit's start
-    int unit = -1, g = 0, done = 0, done_o = 0, pages = 0, valid_pages = 0, loads = 0, others = 0;
+    int unit = -1, g = 0, done = 0, done_o = 0, pages = 0, valid_pages = 0, uc = -1, others = 0;  // uc: units before this one
     int place = -1, start = 0, start_o = 0;
     FtUnit t{};
     int row = 0, pos = 0, pos_first = 0, pos0 = 0;  // pos0: of the sequence's first query token
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       const int pr = row - t.row0;  // row of the partial state
       float* part = place < 0 ? nullptr
                               : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kFtPlaceFloats;
-      const bool poison = sh->nan_any != 0;
+      const bool poison = sh->nan_any[uc & 1] != 0;
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {  // 16 columns = dims of two groups of 8
         uint32_t x[16];
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          if (poison && pos >= sh->nan_key[8 * ft_dim8(2 * c + (i >> 3)) + (i & 7)]) v[i] = NAN;
+          if (poison && pos >= sh->nan_key[uc & 1][8 * ft_dim8(2 * c + (i >> 3)) + (i & 7)]) v[i] = NAN;
           v[i] *= out_f;
         }
 #pragma unroll
@@ -406,9 +413,10 @@ __global__ void __launch_bounds__(kFtThreads, 1)
             }
             *reinterpret_cast<uint4*>(a.out + hr * kDim + d) = make_uint4(w[0], w[1], w[2], w[3]);
           } else {
-            float4* dst = reinterpret_cast<float4*>(part + pr * kDim + d);
+            // four dims of all rows together: the lanes of a store are neighbouring rows
+            float4* dst = reinterpret_cast<float4*>(part) + (d / 4) * (2 * kFtRows) + pr;
             dst[0] = make_float4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
-            dst[1] = make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+            dst[2 * kFtRows] = make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
           }
         }
         __syncwarp();
@@ -441,11 +449,18 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           }
           if (t.width == 1) ++others;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->fin);
+          if (lane == 0) mbar_arrive(&sh->fin[uc & 1]);
         }
+        const bool shared_o = unit >= 0 && t.width == 1;
         unit = it.unit;
         g = it.g;
         if (unit < 0) break;
+        ++uc;
+        // slot 0 reads slot 1's O and statistics of a one-tile unit: slot 1 goes on when it has
+        if (slot == 1 && shared_o && !mbar_wait_warp(&sh->fin[(uc - 1) & 1], ((uc - 1) >> 1) & 1)) {
+          failed = true;
+          break;
+        }
         t = ft_unit(a, unit, per_seq);
         place = it.place;
         pages = 0;
@@ -457,12 +472,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         pos_first = pos0 + (t.row0 + (t.width == 2 ? slot * kFtRows : 0)) / Hg;
         M = -INFINITY;
         l = 0.f;
-        if (!mbar_wait_warp(&sh->q_full, loads & 1)) {
+        if (!mbar_wait_warp(&sh->q_full[uc & 1], (uc >> 1) & 1)) {
           failed = true;
           break;
         }
-        ++loads;
-        q_fac = sh->q_fac[row - t.row0];
+        q_fac = sh->q_fac[uc & 1][row - t.row0];
       }
       if (it.block < 0) continue;
       // the page's V stage, and whether its step is this slot's
@@ -570,7 +584,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     if (warp < 12) {
       // ---- Q tiles, V conversion
       const int ct = tid - 256;
-      int unit = -1, g = 0, page = 0, units_done = 0;
+      int unit = -1, g = 0, page = 0, uc = -1;
       FtUnit t{};
       int L = 0;
       for (int n = 0; !failed; ++n) {
@@ -583,21 +597,23 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           unit = it.unit;
           g = it.g;
           if (unit < 0) break;
-          // the unit before is written: its products are done, its factors and NaN marks read
-          if (units_done > 0 && !mbar_wait_warp(&sh->fin, (units_done - 1) & 1)) {
+          ++uc;
+          // the unit that used this one's half of Q (bf16: both halves), factors and NaN marks is written
+          const int back = a.q_bf16 ? 1 : 2;
+          if (uc >= back && !mbar_wait_warp(&sh->fin[(uc - back) & 1], ((uc - back) >> 1) & 1)) {
             failed = true;
             break;
           }
-          ++units_done;
           t = ft_unit(a, unit, per_seq);
           L = a.seq_lens[t.b];
-          sh->nan_key[ct] = INT32_MAX;
-          if (ct == 0) sh->nan_any = 0;
+          sh->nan_key[uc & 1][ct] = INT32_MAX;
+          if (ct == 0) sh->nan_any[uc & 1] = 0;
+          uint8_t* q_half = q_tile + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf);
           const int c = ct & 7;  // dims 16 c .. 16 c + 15 of rows ct / 8, + 16, ...
-          for (int r0 = ct >> 3; r0 < t.width * kFtRows; r0 += 64) {  // four rows' loads at once
-            uint4 u[4][2];
+          for (int r0 = ct >> 3; r0 < t.width * kFtRows; r0 += 128) {  // eight rows' loads at once
+            uint4 u[8][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const int rr = r0 + 16 * i, row = t.row0 + rr;
               u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
               if (rr < t.rows) {
@@ -612,9 +628,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const int rr = r0 + 16 * i;
-              uint8_t* dst = q_tile + (rr >> 7) * (kFtRows * 128) + sw128(rr & 127, c);
+              uint8_t* dst = q_half + (rr >> 7) * (kFtRows * 128) + sw128(rr & 127, c);
               float fac = 1.f;
               if (!a.q_bf16) {
                 *reinterpret_cast<uint4*>(dst) = u[i][0];
@@ -622,16 +638,16 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                 uint4 hi, lo;
                 fac = ft_split_bf16(u[i][0], u[i][1], hi, lo);
                 *reinterpret_cast<uint4*>(dst) = hi;
-                *reinterpret_cast<uint4*>(dst + 2 * kFtRows * 128) = lo;
+                *reinterpret_cast<uint4*>(dst + kFtQHalf) = lo;
               }
-              if (c == 0) sh->q_fac[rr] = fac;
+              if (c == 0) sh->q_fac[uc & 1][rr] = fac;
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->q_full);
+          if (lane == 0) mbar_arrive(&sh->q_full[uc & 1]);
           // every converter has reset its marks before any page sets one
-          if (!mbar_wait_warp(&sh->q_full, (units_done - 1) & 1)) {
+          if (!mbar_wait_warp(&sh->q_full[uc & 1], (uc >> 1) & 1)) {
             failed = true;
             break;
           }
@@ -661,9 +677,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               const uint32_t nan = __vcmpeq4(w[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
               w[j] &= ~nan;
               if (nan != 0u && key < L) {
-                sh->nan_any = 1;
+                sh->nan_any[uc & 1] = 1;
                 for (int q = 0; q < 4; ++q)
-                  if (nan >> (8 * q) & 1u) atomicMin(&sh->nan_key[16 * c + 4 * j + q], key);
+                  if (nan >> (8 * q) & 1u) atomicMin(&sh->nan_key[uc & 1][16 * c + 4 * j + q], key);
               }
             }
           }
@@ -780,7 +796,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       const uint32_t id_lo = id_s | (1u << 7);                           // A is E5M2
       const uint32_t id_o = umma_idesc_f16(kFtRows, kDim) | (1u << 16);  // B MN-major
       const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
-      int unit = -1, g = 0, width = 1, pages = 0, page = 0, loads = 0;
+      int unit = -1, g = 0, width = 1, pages = 0, page = 0, uc = -1;
       int done0 = 0, done1 = 0, start0 = 0, start1 = 0;  // steps of the slots so far, and at the unit's start
       for (int n = 0; !failed; ++n) {
         FtItem it;
@@ -789,7 +805,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           break;
         }
         if (it.unit < 0 || it.unit != unit || it.g != g) {
-          if (scores && unit >= 0 && lane == 0) mbar_arrive(&sh->fin);
+          if (scores && unit >= 0 && lane == 0) mbar_arrive(&sh->fin[uc & 1]);
           unit = it.unit;
           g = it.g;
           if (unit < 0) break;
@@ -797,11 +813,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           pages = 0;
           start0 = done0;
           start1 = done1;
-          if (scores && !mbar_wait_warp(&sh->q_full, loads & 1)) {
+          ++uc;
+          if (scores && !mbar_wait_warp(&sh->q_full[uc & 1], (uc >> 1) & 1)) {
             failed = true;
             break;
           }
-          ++loads;
         }
         if (it.block < 0) continue;
         const int ks = page % kFtK, vs = page % kFtV;
@@ -822,11 +838,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
             }
             tc_fence_after();
             if (lane == 0) {
-              const uint32_t qt = qb + (width == 2 ? s : 0) * (kFtRows * 128), kt = kb + ks * kFp8PageBytes;
+              const uint32_t qt = qb + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf) + (width == 2 ? s : 0) * (kFtRows * 128), kt = kb + ks * kFp8PageBytes;
               for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // 32 dims a step
-                  umma_f8(tmem + s * 128, umma_desc(qt + part * (2 * kFtRows * 128) + 32 * kk), umma_desc(kt + 32 * kk),
+                  umma_f8(tmem + s * 128, umma_desc(qt + part * kFtQHalf + 32 * kk), umma_desc(kt + 32 * kk),
                           part > 0 ? id_lo : id_s, part > 0 || kk > 0 ? 1u : 0u);
               umma_commit(&sh->s_full[s]);
               if (last) umma_commit(&sh->k_empty[ks]);
@@ -913,15 +929,17 @@ __global__ void __launch_bounds__(kFp8MergeThreads) fp8_tile_merge_kernel(const 
   }
   __syncthreads();
   if (sh.n < 2) return;  // one CTA's: written by it
-  const int pr = kSplit ? blockIdx.y : blockIdx.y * 8 + (threadIdx.x >> 5);
+  // states lie by chunks of four dims: without kSplit a CTA's eight rows of a chunk are one 128-byte line
+  const int pr = kSplit ? blockIdx.y : blockIdx.y * 8 + (threadIdx.x & 7);
+  const int chunk = kSplit ? threadIdx.x & 31 : threadIdx.x >> 3;
   if (pr >= t.rows) return;
   float4 o;
   float M, l;
-  fp8_merge_row<kSplit>(a.partial, 2 * kFtRows, pr, sh, o, M, l);
+  fp8_merge_row<kSplit>(a.partial, 2 * kFtRows, pr, chunk * 2 * kFtRows + pr, sh, o, M, l);
   if (kSplit && threadIdx.x >= 32) return;
   const int row = t.row0 + pr;
   fp8_write_row(a, (static_cast<int64_t>(t.b) * T + row / Hg) * G * Hg + g * Hg + row % Hg,
-                (static_cast<int64_t>(t.b) * G + g) * T * Hg + row, o, M, l);
+                (static_cast<int64_t>(t.b) * G + g) * T * Hg + row, chunk, o, M, l);
 }
 
 int fp8_tile_units_per_seq(int64_t rows) { return static_cast<int>((rows + 2 * kFtRows - 1) / (2 * kFtRows)); }
