@@ -210,6 +210,13 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One lane of the warp (a form that leaves the issue of the products in uniform control flow)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // (a.x, a.y) * f + c and (a.x, a.y) + (b.x, b.y): two floats an instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 f, float2 c) {
   float2 d;
@@ -837,7 +844,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               break;
             }
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
               const uint32_t qt = qb + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf) + (width == 2 ? s : 0) * (kFtRows * 128), kt = kb + ks * kFp8PageBytes;
               for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
 #pragma unroll
@@ -855,7 +862,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                 break;
               }
               tc_fence_after();
-              if (lane == 0) {
+              if (elect_one()) {
                 const bool add = h > 0 || d > (s ? start1 : start0);
                 const uint32_t vt = vb + vs * kFtVBytes + h * 64 * 128;
 #pragma unroll
