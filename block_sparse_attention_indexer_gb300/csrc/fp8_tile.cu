@@ -845,11 +845,12 @@ __global__ void __launch_bounds__(kFtThreads, 1)
             }
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t qt = qb + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf) + (width == 2 ? s : 0) * (kFtRows * 128), kt = kb + ks * kFp8PageBytes;
+              const uint64_t qd = umma_desc(qb + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf) + (width == 2 ? s : 0) * (kFtRows * 128));
+              const uint64_t kd = umma_desc(kb + ks * kFp8PageBytes);
               for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // 32 dims a step
-                  umma_f8(tmem + s * 128, umma_desc(qt + part * kFtQHalf + 32 * kk), umma_desc(kt + 32 * kk),
+                  umma_f8(tmem + s * 128, qd + ((part * kFtQHalf + 32 * kk) >> 4), kd + ((32 * kk) >> 4),
                           part > 0 ? id_lo : id_s, part > 0 || kk > 0 ? 1u : 0u);
               umma_commit(&sh->s_full[s]);
               if (last) umma_commit(&sh->k_empty[ks]);
@@ -864,11 +865,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               tc_fence_after();
               if (elect_one()) {
                 const bool add = h > 0 || d > (s ? start1 : start0);
-                const uint32_t vt = vb + vs * kFtVBytes + h * 64 * 128;
+                const uint64_t vd = umma_desc_mn(vb + vs * kFtVBytes + h * 64 * 128, kFtVBytes / 2);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
                   umma_f16_tmem_a(tmem + kFtO + s * 128, tmem + s * 128 + h * 64 + 8 * kk,
-                                  umma_desc_mn(vt + kk * 2048, kFtVBytes / 2), id_o, add || kk > 0 ? 1u : 0u);
+                                  vd + ((kk * 2048) >> 4), id_o, add || kk > 0 ? 1u : 0u);
                 umma_commit(&sh->pv_done[s][h]);
                 if (last && h == 1) umma_commit(&sh->v_empty[vs]);
               }
