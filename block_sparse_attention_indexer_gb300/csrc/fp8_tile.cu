@@ -799,52 +799,54 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       // ---- product issuers: warp 13 S, warp 14 P V.  Two warps, because issuing blocks while the tensor
       // pipe is full: each waits for its operands while the other's products run.
       const bool scores = warp == 13;
-      const uint32_t id_s = umma_idesc_f16(kFtRows, kBlock);             // (E4M3 has format code 0 too)
-      const uint32_t id_lo = id_s | (1u << 7);                           // A is E5M2
-      const uint32_t id_o = umma_idesc_f16(kFtRows, kDim) | (1u << 16);  // B MN-major
-      const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
-      int unit = -1, g = 0, width = 1, pages = 0, page = 0, uc = -1;
-      int done0 = 0, done1 = 0, start0 = 0, start1 = 0;  // steps of the slots so far, and at the unit's start
-      for (int n = 0; !failed; ++n) {
-        FtItem it;
-        if (!take_item(n, it)) {
-          failed = true;
-          break;
-        }
-        if (it.unit < 0 || it.unit != unit || it.g != g) {
-          if (scores && unit >= 0 && lane == 0) mbar_arrive(&sh->fin[uc & 1]);
-          unit = it.unit;
-          g = it.g;
-          if (unit < 0) break;
-          width = ft_unit(a, unit, per_seq).width;
-          pages = 0;
-          start0 = done0;
-          start1 = done1;
-          ++uc;
-          if (scores && !mbar_wait_warp(&sh->q_full[uc & 1], (uc >> 1) & 1)) {
-            failed = true;
+      if (elect_one()) {
+        const uint32_t id_s = umma_idesc_f16(kFtRows, kBlock);             // (E4M3 has format code 0 too)
+        const uint32_t id_lo = id_s | (1u << 7);                           // A is E5M2
+        const uint32_t id_o = umma_idesc_f16(kFtRows, kDim) | (1u << 16);  // B MN-major
+        const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
+        int unit = -1, g = 0, width = 1, pages = 0, page = 0, uc = -1;
+        int done0 = 0, done1 = 0, start0 = 0, start1 = 0;  // steps of the slots so far, and at the unit's start
+        bool bad = false;
+        for (int n = 0; !bad; ++n) {
+          if (!mbar_wait(&sh->item_full[n % kFtItems], (n / kFtItems) & 1)) {
+            bad = true;
             break;
           }
-        }
-        if (it.block < 0) continue;
-        const int ks = page % kFtK, vs = page % kFtV;
-        if (scores ? !mbar_wait_warp(&sh->k_full[ks], (page / kFtK) & 1)
-                   : !mbar_wait_warp(&sh->v_full[vs], (page / kFtV) & 1)) {
-          failed = true;
-          break;
-        }
-        for (int i = 0; i < width && !failed; ++i) {
-          const int s = width == 2 ? i : pages & 1;
-          const int d = s ? done1 : done0;
-          const bool last = i == width - 1;
-          if (scores) {
-            // S overwrites the slot's P: it waits until that has been multiplied
-            if (d > 0 && !mbar_wait_warp(&sh->pv_done[s][1], (d - 1) & 1)) {
-              failed = true;
+          const int it_unit = sh->item[n % kFtItems].unit, it_g = sh->item[n % kFtItems].g;
+          const bool empty = sh->item[n % kFtItems].block < 0;
+          mbar_arrive(&sh->item_empty[n % kFtItems]);
+          if (it_unit < 0 || it_unit != unit || it_g != g) {
+            if (scores && unit >= 0) mbar_arrive(&sh->fin[uc & 1]);
+            unit = it_unit;
+            g = it_g;
+            if (unit < 0) break;
+            width = ft_unit(a, unit, per_seq).width;
+            pages = 0;
+            start0 = done0;
+            start1 = done1;
+            ++uc;
+            if (scores && !mbar_wait(&sh->q_full[uc & 1], (uc >> 1) & 1)) {
+              bad = true;
               break;
             }
-            tc_fence_after();
-            if (elect_one()) {
+          }
+          if (empty) continue;
+          const int ks = page % kFtK, vs = page % kFtV;
+          if (scores ? !mbar_wait(&sh->k_full[ks], (page / kFtK) & 1) : !mbar_wait(&sh->v_full[vs], (page / kFtV) & 1)) {
+            bad = true;
+            break;
+          }
+          for (int i = 0; i < width && !bad; ++i) {
+            const int s = width == 2 ? i : pages & 1;
+            const int d = s ? done1 : done0;
+            const bool last = i == width - 1;
+            if (scores) {
+              // S overwrites the slot's P: it waits until that has been multiplied
+              if (d > 0 && !mbar_wait(&sh->pv_done[s][1], (d - 1) & 1)) {
+                bad = true;
+                break;
+              }
+              tc_fence_after();
               const uint64_t qd = umma_desc(qb + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf) + (width == 2 ? s : 0) * (kFtRows * 128));
               const uint64_t kd = umma_desc(kb + ks * kFp8PageBytes);
               for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
@@ -854,16 +856,13 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                           part > 0 ? id_lo : id_s, part > 0 || kk > 0 ? 1u : 0u);
               umma_commit(&sh->s_full[s]);
               if (last) umma_commit(&sh->k_empty[ks]);
-            }
-            __syncwarp();
-          } else {
-            for (int h = 0; h < 2; ++h) {  // 64 keys: the products of the first half run beside the softmax of the second
-              if (!mbar_wait_warp(&sh->p_full[s][h], d & 1)) {
-                failed = true;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
+            } else {
+              for (int h = 0; h < 2; ++h) {  // 64 keys: the products of the first half run beside the softmax of the second
+                if (!mbar_wait(&sh->p_full[s][h], d & 1)) {
+                  bad = true;
+                  break;
+                }
+                tc_fence_after();
                 const bool add = h > 0 || d > (s ? start1 : start0);
                 const uint64_t vd = umma_desc_mn(vb + vs * kFtVBytes + h * 64 * 128, kFtVBytes / 2);
 #pragma unroll
@@ -873,19 +872,19 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                 umma_commit(&sh->pv_done[s][h]);
                 if (last && h == 1) umma_commit(&sh->v_empty[vs]);
               }
-              __syncwarp();
             }
+            s ? ++done1 : ++done0;
           }
-          s ? ++done1 : ++done0;
+          ++pages;
+          ++page;
         }
-        ++pages;
-        ++page;
+        if (bad) {  // the products still running end before TMEM is freed
+          flag_error(a.err, MSA_DEVERR_TIMEOUT);
+          umma_commit(&sh->drain[scores]);
+          mbar_wait(&sh->drain[scores], 0);
+        }
       }
-      if (failed) {  // the products still running end before TMEM is freed
-        if (lane == 0) umma_commit(&sh->drain[scores]);
-        __syncwarp();
-        mbar_wait_warp(&sh->drain[scores], 0);
-      }
+      __syncwarp();
     }
   }
   if (failed && lane == 0) flag_error(a.err, MSA_DEVERR_TIMEOUT);
