@@ -58,23 +58,19 @@ __global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const Fp8AttnArg
   if (tid == 0) a.weight_out[idx] = decayed(a, idx) + sum;
 }
 
-// Sparse: each (row of the selection, slot) adds its share to its block as a fixed-point number
+// Sparse: each entry (row of the selection, slot) adds its share to its block as a fixed-point number
 // with 40 fraction bits, so that the sum does not depend on the order (a sequence collects at
-// most T * H < 2^22: it fits bit 62; bit 63 marks a NaN).  Eight lanes take one entry, a head each.
-__global__ void __launch_bounds__(256) fp8_weights_scatter_kernel(const Fp8AttnArgs a) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int64_t units = static_cast<int64_t>(a.batch) * a.q_len * a.groups;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 8;
-  const int h = threadIdx.x & 7;
-  const int Hg = a.heads_per_group;
-  float sum = 0.f;
-  int b = 0, n = -1;
-  if (i < units * kTopK) {
+// most T * H < 2^22: it fits bit 62; bit 63 marks a NaN).  Eight lanes take an entry, a head each.
+constexpr float kMassOne = 1099511627776.f;  // 2^40
+
+// The block that entry i = (b, t, g, slot) adds to (-1: none), and in its first lane what it adds.
+__device__ __forceinline__ int entry_share(const Fp8AttnArgs& a, int64_t i, bool in, float& sum) {
+  const int h = threadIdx.x & 7, Hg = a.heads_per_group;
+  int n = -1;
+  sum = 0.f;
+  if (in) {
     const int64_t unit = i / kTopK;
-    const int bt = static_cast<int>(unit / a.groups);
-    b = bt / a.q_len;
-    const int L = a.seq_lens[b];
+    const int bt = static_cast<int>(unit / a.groups), b = bt / a.q_len, L = a.seq_lens[b];
     n = a.selection[i];
     if (!length_ok(a, L) || n > (L - a.q_len + bt - b * a.q_len) / kBlock) n = -1;
     if (n >= 0 && h < Hg) {
@@ -88,22 +84,57 @@ __global__ void __launch_bounds__(256) fp8_weights_scatter_kernel(const Fp8AttnA
   }
 #pragma unroll
   for (int s = 4; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-  if (h != 0 || n < 0) return;
-  unsigned long long* m = a.mass + static_cast<int64_t>(b) * a.max_blocks + n;
+  return h == 0 ? n : -1;
+}
+__device__ __forceinline__ void add_mass(unsigned long long* m, float sum) {
   if (sum != sum)
     atomicOr(m, 1ull << 63);
   else if (sum > 0.f)
-    atomicAdd(m, static_cast<unsigned long long>(static_cast<double>(sum) * 1099511627776.0 + 0.5));
+    atomicAdd(m, static_cast<unsigned long long>(static_cast<double>(sum) * static_cast<double>(kMassOne) + 0.5));
+}
+__device__ __forceinline__ float mass_value(unsigned long long m) {
+  return (m >> 63) ? NAN : static_cast<float>(static_cast<double>(m) * (1.0 / static_cast<double>(kMassOne)));
 }
 
+// Few entries per sequence: a CTA per (sequence, 2,048 blocks) goes through all of them and keeps its
+// blocks' sums in shared memory.
+constexpr int kMassBlocks = 2048, kMassEntries = 2048, kMassThreads = 512;
+__global__ void __launch_bounds__(kMassThreads) fp8_weights_sequence_kernel(const Fp8AttnArgs a) {
+  __shared__ unsigned long long s_mass[kMassBlocks];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int b = blockIdx.y, n0 = blockIdx.x * kMassBlocks, n1 = min(n0 + kMassBlocks, a.max_blocks);
+  for (int n = threadIdx.x; n < kMassBlocks; n += kMassThreads) s_mass[n] = 0ull;
+  __syncthreads();
+  const int entries = a.q_len * a.groups * kTopK;
+  for (int e0 = 0; e0 < entries; e0 += kMassThreads / 8) {
+    const int e = e0 + threadIdx.x / 8;
+    float sum;
+    const int n = entry_share(a, static_cast<int64_t>(b) * entries + e, e < entries, sum);
+    if (n >= n0 && n < n1) add_mass(&s_mass[n - n0], sum);
+  }
+  __syncthreads();
+  for (int n = n0 + threadIdx.x; n < n1; n += kMassThreads) {
+    const int64_t i = static_cast<int64_t>(b) * a.max_blocks + n;
+    a.weight_out[i] = decayed(a, i) + mass_value(s_mass[n - n0]);
+  }
+}
+
+// Many: the entries of all sequences over the grid, into sums in the workspace that a second kernel reads.
+__global__ void __launch_bounds__(256) fp8_weights_scatter_kernel(const Fp8AttnArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t all = static_cast<int64_t>(a.batch) * a.q_len * a.groups * kTopK;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 8;
+  float sum;
+  const int n = entry_share(a, i, i < all, sum);
+  if (n >= 0) add_mass(a.mass + i / (static_cast<int64_t>(a.q_len) * a.groups * kTopK) * a.max_blocks + n, sum);
+}
 __global__ void __launch_bounds__(256) fp8_weights_sparse_kernel(const Fp8AttnArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.batch) * a.max_blocks) return;
-  const unsigned long long m = a.mass[i];
-  const float sum = (m >> 63) ? NAN : static_cast<float>(static_cast<double>(m) * (1.0 / 1099511627776.0));
-  a.weight_out[i] = decayed(a, i) + sum;
+  if (i < static_cast<int64_t>(a.batch) * a.max_blocks) a.weight_out[i] = decayed(a, i) + mass_value(a.mass[i]);
 }
 
 // ---------------------------------------------------------------- tensor maps and dispatch
@@ -147,9 +178,16 @@ cudaError_t launch_fp8_attn(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
   const int64_t units = static_cast<int64_t>(a.batch) * a.q_len * a.groups;
   const bool stream = sparse || a.q_len * a.heads_per_group <= kFp8StreamRows;
   const int parts = stream ? kFp8StreamParts : 1;
-  if (sparse && weights && (e = cudaMemsetAsync(a.mass, 0, blocks * sizeof(*a.mass), s)) != cudaSuccess) return e;
+  // one launch while a sequence's entries are few (64 sequences of 64 entries: 36 us with the attention as
+  // XXX, against YYY with three)
+  const bool few = a.q_len * a.groups * kTopK <= kMassEntries;
+  if (sparse && weights && !few && (e = cudaMemsetAsync(a.mass, 0, blocks * sizeof(*a.mass), s)) != cudaSuccess) return e;
   e = stream ? launch_fp8_stream(a, num_sms, s) : launch_fp8_tile(a, num_sms, s);
   if (e != cudaSuccess || !weights) return e;
+  if (sparse && few)
+    return launch_dependent(fp8_weights_sequence_kernel,
+                            dim3(static_cast<unsigned>((a.max_blocks + kMassBlocks - 1) / kMassBlocks),
+                                 static_cast<unsigned>(a.batch)), kMassThreads, 0, s, a);
   if (sparse) {
     e = launch_dependent(fp8_weights_scatter_kernel, dim3(static_cast<unsigned>((units * kTopK + 31) / 32)), 256, 0, s, a);
     if (e != cudaSuccess) return e;

@@ -53,6 +53,7 @@ struct FsItem {
   int place;      // block (dense) or selection slot (sparse)
   int block;      // logical block
   int page;       // -1: nothing to attend to in this range of the unit
+  int pos;        // position of the unit's first query token
   float k_scale;  // 2^a * softmax_scale * log2(e)
   float v_exp;    // b
 };
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
   if (tid < S::kTeams) {
     FsTeam<NT>* tm = &sh->team[tid];
     for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(&tm->full[i], 1);
+      mbar_init(&tm->full[i], 2);  // the copy (its bytes too), the item's record
       mbar_init(&tm->empty[i], kFsWarps);
     }
     mbar_init(&tm->pair, 2);
@@ -269,19 +270,19 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
   if (warp >= S::kTeams * kFsWarps) {
     // ---- producer
     const uint64_t policy = sparse && T > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
-    int items = 0;
+    int copied = 0, items = 0;  // items whose copies are issued, whose records are written
     bool ok = true;
-    auto send = [&](const FsItem& it, int row) {
-      // slots 2 i, 2 i + 1 of the ring for item i's K and V
+    // Slots 2 i, 2 i + 1 of the ring hold item i's K and V.  A slot is full when its copy and the item's
+    // record are there, so that the first copies can start before the pages' scales are known.
+    auto copy = [&](int page, int row) {
       for (int kv = 0; kv < 2 && ok; ++kv) {
-        const int use = 2 * items + kv, slot = use % S::kSlots;
+        const int use = 2 * copied + kv, slot = use % S::kSlots;
         if (use >= S::kSlots && !mbar_wait_warp(&tm->empty[slot], (use / S::kSlots - 1) & 1)) {
           ok = false;
           break;
         }
         if (lane == 0) {
-          if (kv == 0) tm->item[items % kFsMeta] = it;
-          if (it.page >= 0) {
+          if (page >= 0) {
             fence_proxy_async_smem();
             mbar_arrive_expect_tx(&tm->full[slot], kFp8PageBytes);
             tma_page(my_slots + slot * kFp8PageBytes, kv ? &maps.v : &maps.k, row, &tm->full[slot], policy);
@@ -290,75 +291,95 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
           }
         }
       }
+      ++copied;
+    };
+    auto record = [&](const FsItem& it) {
+      if (lane == 0) {
+        tm->item[items % kFsMeta] = it;
+        mbar_arrive(&tm->full[2 * items % S::kSlots]);
+        mbar_arrive(&tm->full[(2 * items + 1) % S::kSlots]);
+      }
       ++items;
+    };
+    auto send = [&](const FsItem& it, int row) {
+      if (copied == items) copy(it.page, row);
+      if (ok) record(it);
     };
     int open = -1;      // the unit that the last item belongs to
     bool sent = false;  // whether it has an item
     for (int xb = x0; xb < x1 && ok; xb += 32) {
       const int x = xb + lane;
-      FsEntry en{-1, 0, 0};
-      FsItem it{-1, 0, -1, -1, 0.f, 0.f};
-      int row = 0;
+      FsItem it{-1, 0, -1, -1, 0, 0.f, 0.f};
+      int ph = -1;
       if (x < x1) {
-        en = fs_entry(a, sh->prefix, x);
+        const FsEntry en = fs_entry(a, sh->prefix, x);
         it.unit = en.unit;
         it.place = en.place;
         const int L = a.seq_lens[en.b];
+        const int n = sparse ? a.selection[x] : en.place;
+        // (the table entry is read before the length is known; its place in the table is in range)
+        const int page = a.block_table[static_cast<int64_t>(en.b) * a.max_blocks + (n >= 0 && n < a.max_blocks ? n : 0)];
         const bool live = length_ok(a, L);
         if (sparse && !live && L != 0 && en.place == 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
-        const int t = sparse ? (en.unit / a.groups) % T : T - 1;
-        const int n = sparse ? a.selection[x] : en.place;
-        if (live && n >= 0 && n <= (L - T + t) / kBlock) {
+        it.pos = L - T + (sparse ? (en.unit / a.groups) % T : 0);
+        if (live && n >= 0 && n <= (sparse ? it.pos : L - 1) / kBlock) {
           it.block = n;
-          const int page = a.block_table[static_cast<int64_t>(en.b) * a.max_blocks + n];
           if (page >= 0 && page < a.num_pages) {
-            const int ph = page * a.groups + en.unit % a.groups;
-            const int ks = a.k_scale[ph], vs = a.v_scale[ph];
-            if (e8m0_ok(ks) && e8m0_ok(vs)) {
-              it.page = page;
-              row = ph * kBlock;
-              it.k_scale = exp2_int(ks - kE8m0One) * a.scale_log2;
-              it.v_exp = static_cast<float>(vs - kE8m0One);
-            } else {
-              flag_error(a.err, MSA_DEVERR_BAD_SCALE);
-            }
+            it.page = page;
+            ph = page * a.groups + en.unit % a.groups;
           } else {
             flag_error(a.err, MSA_DEVERR_BAD_PAGE);
-          }
-          if (it.page < 0 && a.weight_out != nullptr) {  // a skipped page collects nothing
-            float2* share = a.share + (static_cast<int64_t>(en.unit) * (sparse ? kTopK : a.max_blocks) + en.place) *
-                                          kFp8StreamParts * rows;
-            for (int i = 0; i < kFp8StreamParts * rows; ++i) share[i] = make_float2(0.f, 0.f);
           }
         }
       }
       const int count = min(x1 - xb, 32);
+      const int ks = ph >= 0 ? a.k_scale[ph] : kE8m0One, vs = ph >= 0 ? a.v_scale[ph] : kE8m0One;
+      if (xb == x0) {  // the first pages' copies, while the scales are on their way
+        const unsigned have = __ballot_sync(0xffffffffu, ph >= 0);
+        const int j0 = __ffs(have) - 1;
+        // (only where the first item sent is this page: no marker of an empty unit comes before it)
+        const int u0 = __shfl_sync(0xffffffffu, it.unit, 0), uj = __shfl_sync(0xffffffffu, it.unit, max(j0, 0));
+        if (j0 >= 0 && uj == u0) copy(0, __shfl_sync(0xffffffffu, ph, j0) * kBlock);
+      }
+      if (it.page >= 0 && !(e8m0_ok(ks) && e8m0_ok(vs))) {
+        flag_error(a.err, MSA_DEVERR_BAD_SCALE);
+        it.page = -1;
+      }
+      it.k_scale = exp2_int(ks - kE8m0One) * a.scale_log2;
+      it.v_exp = static_cast<float>(vs - kE8m0One);
+      if (it.block >= 0 && it.page < 0 && a.weight_out != nullptr) {  // a skipped page collects nothing
+        float2* share = a.share + (static_cast<int64_t>(it.unit) * (sparse ? kTopK : a.max_blocks) + it.place) *
+                                      kFp8StreamParts * rows;
+        for (int i = 0; i < kFp8StreamParts * rows; ++i) share[i] = make_float2(0.f, 0.f);
+      }
       for (int j = 0; j < count && ok; ++j) {
         FsItem s;
         s.unit = __shfl_sync(0xffffffffu, it.unit, j);
         s.place = __shfl_sync(0xffffffffu, it.place, j);
         s.block = __shfl_sync(0xffffffffu, it.block, j);
         s.page = __shfl_sync(0xffffffffu, it.page, j);
+        s.pos = __shfl_sync(0xffffffffu, it.pos, j);
         s.k_scale = __shfl_sync(0xffffffffu, it.k_scale, j);
         s.v_exp = __shfl_sync(0xffffffffu, it.v_exp, j);
-        const int r = __shfl_sync(0xffffffffu, row, j);
+        const int pj = __shfl_sync(0xffffffffu, ph, j);
         if (s.unit != open) {
-          if (open >= 0 && !sent) send(FsItem{open, 0, -1, -1, 0.f, 0.f}, 0);
+          if (open >= 0 && !sent) send(FsItem{open, 0, -1, -1, 0, 0.f, 0.f}, 0);
           open = s.unit;
           sent = false;
         }
-        if (s.page >= 0 && ok) {
-          send(s, r);
+        // (a page with a bad scale whose copy is on its way goes as an item without a page)
+        if (ok && (s.page >= 0 || (pj >= 0 && copied > items))) {
+          send(s, pj * kBlock);
           sent = true;
         }
       }
     }
-    if (ok && open >= 0 && !sent) send(FsItem{open, 0, -1, -1, 0.f, 0.f}, 0);
-    if (ok) send(FsItem{-1, 0, -1, -1, 0.f, 0.f}, 0);
+    if (ok && open >= 0 && !sent) send(FsItem{open, 0, -1, -1, 0, 0.f, 0.f}, 0);
+    if (ok) send(FsItem{-1, 0, -1, -1, 0, 0.f, 0.f}, 0);
     if (!ok) {
       if (lane == 0) flag_error(a.err, MSA_DEVERR_TIMEOUT);
       // wait (bounded) for the copies still in flight before leaving
-      for (int use = max(0, 2 * items - S::kSlots); use < 2 * items; ++use)
+      for (int use = max(0, 2 * copied - S::kSlots); use < 2 * copied; ++use)
         mbar_wait(&tm->full[use % S::kSlots], (use / S::kSlots) & 1);
     }
     return;
@@ -372,6 +393,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
   int pos[NT][2];  // positions of this lane's accumulator columns
   int unit = -1, units_done = 0, pos_min = 0;
   const int first_unit = x0 < x1 ? fs_entry(a, sh->prefix, x0).unit : -1;
+  if (first_unit >= 0) fs_load_q<NT>(a, first_unit, rows, gq, t4, bq, fac);  // while the first pages come
   bool failed = false;
 
   // adds the state in a merge area to this warp's
@@ -511,17 +533,15 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
       }
       unit = it.unit;
       if (unit >= 0) {
-        fs_load_q<NT>(a, unit, rows, gq, t4, bq, fac);
-        const int b = sparse ? unit / (a.groups * T) : unit / a.groups;
-        const int p0 = a.seq_lens[b] - T;
-        pos_min = sparse ? p0 + unit / a.groups % T : p0;
+        if (unit != first_unit) fs_load_q<NT>(a, unit, rows, gq, t4, bq, fac);
+        pos_min = it.pos;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             m_run[nt][e] = -INFINITY;
             l_run[nt][e] = 0.f;
-            pos[nt][e] = sparse ? pos_min : p0 + min((8 * nt + 2 * t4 + e) / Hg, T - 1);
+            pos[nt][e] = sparse ? pos_min : pos_min + min((8 * nt + 2 * t4 + e) / Hg, T - 1);
           }
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
