@@ -101,7 +101,12 @@ __global__ void __launch_bounds__(kThreads, kBins ? 2048 / kThreads : 4) evict_k
       page[j] = i < nb ? table[i] : -1;
     }
   };
+  // whether this warp has blocks of a step (ragged batches leave many warps none)
+  auto busy = [&](int base) { return base + mine - lane < nb; };
   auto load = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < kEvItems; ++j) order[j] = 0u;
+    if (!busy(base)) return;
     float x[kEvItems];
 #pragma unroll
     for (int j = 0; j < kEvItems; ++j) {
@@ -123,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, kBins ? 2048 / kThreads : 4) evict_k
       int n[3] = {0, 0, 0};
       for (int base = 0; base < nb; base += kStep) {
         if (!once) load(base);
+        if (!busy(base)) continue;
 #pragma unroll
         for (int j = 0; j < kEvItems; ++j)
 #pragma unroll
@@ -159,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, kBins ? 2048 / kThreads : 4) evict_k
       __syncthreads();
       for (int base = 0; base < nb; base += kStep) {
         if (!once || base == 0) load(base);
+        if (!busy(base)) continue;
 #pragma unroll
         for (int j = 0; j < kEvItems; ++j) {
           const uint32_t o = order[j];
@@ -214,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, kBins ? 2048 / kThreads : 4) evict_k
       } else if (sh.bins[bin] <= kEvListed) {
         for (int base = 0; base < nb; base += kStep) {
           if (!once) load(base);
+          if (!busy(base)) continue;
 #pragma unroll
           for (int j = 0; j < kEvItems; ++j)
             if (order[j] >> 20 == static_cast<uint32_t>(bin) && order[j] != 0u) sh.list[atomicAdd(&sh.listed, 1)] = order[j];
@@ -257,48 +265,59 @@ __global__ void __launch_bounds__(kThreads, kBins ? 2048 / kThreads : 4) evict_k
 
   int stayed = 0, gone = 0, ties = 0;
   for (int base = 0; base < nb; base += kStep) {
-    if (!held) fetch(base);
+    const bool some = busy(base);
     uint32_t stay = 0, tie = 0;  // bit j: block j of this thread
     int tie_here = 0;            // of the warp
+    if (some) {
+      if (!held) fetch(base);
 #pragma unroll
-    for (int j = 0; j < kEvItems; ++j) {
-      const int i = base + mine + 32 * j;
-      const bool in = i < nb, forced = !cut || i < c0 || i >= c1;
-      const uint32_t o = score_order(w[j]);
-      if (in && (forced || (k > 0 && o > kth))) stay |= 1u << j;
-      const bool t = in && !forced && k > 0 && o == kth;
-      if (t) tie |= 1u << j;
-      tie_here += __popc(__ballot_sync(0xffffffffu, t));
+      for (int j = 0; j < kEvItems; ++j) {
+        const int i = base + mine + 32 * j;
+        const bool in = i < nb, forced = !cut || i < c0 || i >= c1;
+        const uint32_t o = score_order(w[j]);
+        if (in && (forced || (k > 0 && o > kth))) stay |= 1u << j;
+        if (in && !forced && k > 0 && o == kth) tie |= 1u << j;
+      }
+      tie_here = __reduce_add_sync(0xffffffffu, __popc(tie));
     }
     int total;
     int before = ties + cta_before<kThreads>(tie_here, sh.count, turn, total);  // (and: every block of the step is read)
     ties += total;
     int stay_here = 0;
+    if (some) {
+      if (tie_here > 0 && before < equal) {
 #pragma unroll
-    for (int j = 0; j < kEvItems; ++j) {
-      const bool t = tie >> j & 1u;
-      const unsigned m = __ballot_sync(0xffffffffu, t);
-      if (t && before + __popc(m & ((1u << lane) - 1u)) < equal) stay |= 1u << j;
-      before += __popc(m);
-      stay_here += __popc(__ballot_sync(0xffffffffu, stay >> j & 1u));
+        for (int j = 0; j < kEvItems; ++j) {
+          const bool t = tie >> j & 1u;
+          const unsigned m = __ballot_sync(0xffffffffu, t);
+          if (t && before + __popc(m & ((1u << lane) - 1u)) < equal) stay |= 1u << j;
+          before += __popc(m);
+        }
+      }
+      stay_here = __reduce_add_sync(0xffffffffu, __popc(stay));
     }
     int place = stayed + cta_before<kThreads>(stay_here, sh.count, turn, total);
     int left = gone + (mine - lane) - (place - stayed);  // blocks of the step before this warp that go
     stayed += total;
     gone += min(nb - base, kStep) - total;
-#pragma unroll
-    for (int j = 0; j < kEvItems; ++j) {
-      const bool in = base + mine + 32 * j < nb, s = stay >> j & 1u;
-      const unsigned ms = __ballot_sync(0xffffffffu, s), mg = __ballot_sync(0xffffffffu, in && !s);
+    if (some) {
       const unsigned below = (1u << lane) - 1u;
-      if (s) {
-        a.table_out[at + place + __popc(ms & below)] = page[j];
-        a.weight_out[at + place + __popc(ms & below)] = w[j];
-      } else if (in) {
-        a.freed[at + left + __popc(mg & below)] = page[j];
+      int32_t* table_out = a.table_out + at;
+      float* weight_out = a.weight_out + at;
+      int32_t* freed = a.freed + at;
+#pragma unroll
+      for (int j = 0; j < kEvItems; ++j) {
+        const bool in = base + mine + 32 * j < nb, s = stay >> j & 1u;
+        const unsigned ms = __ballot_sync(0xffffffffu, s), mi = __ballot_sync(0xffffffffu, in);
+        if (s) {
+          table_out[place + __popc(ms & below)] = page[j];
+          weight_out[place + __popc(ms & below)] = w[j];
+        } else if (in) {
+          freed[left + __popc(mi & ~ms & below)] = page[j];
+        }
+        place += __popc(ms);
+        left += __popc(mi & ~ms);
       }
-      place += __popc(ms);
-      left += __popc(mg);
     }
   }
   for (int i = stayed + tid; i < MB; i += kThreads) {
