@@ -153,7 +153,11 @@ msa_status_t msa_fp8_attn(const msa_config_t* cfg, const msa_fp8_cache_t* cache,
     a.row_stat = reinterpret_cast<float2*>(ws + w.stat);
     a.mass = reinterpret_cast<unsigned long long*>(ws + w.mass);
   }
-  return status_of(launch_fp8_attn(a, sms, static_cast<cudaStream_t>(stream)));
+  try {  // (the launch's bookkeeping allocates host memory: nothing may leave a C entry)
+    return status_of(launch_fp8_attn(a, sms, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return MSA_ERR_CUDA;
+  }
 }
 
 msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int32_t budget, int32_t keep_first,

@@ -207,7 +207,7 @@ __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int ro
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 112);
-      f = exp2_int(k);
+      f = m < INFINITY ? exp2_int(k) : NAN;  // (a row with an infinity gives NaN)
       const float inv = exp2_int(-k);
       if (r < rows) {
 #pragma unroll

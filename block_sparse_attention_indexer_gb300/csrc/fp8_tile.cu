@@ -238,7 +238,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ int ft_dim8(int group) { return group < 8 ? group : group ^ 1; }
 
 // A lane's 16 bf16 dims of a row (eight lanes hold the row) as the E4M3 and E5M2 parts hi + lo = q 2^-k;
-// returns 2^k, which puts the row's largest value into [2^7, 2^8).
+// returns 2^k, which puts the row's largest value into [2^7, 2^8); NaN for a row with an infinity.
 __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, uint4& hi, uint4& lo) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float v[16], m = 0.f;
@@ -266,7 +266,7 @@ __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, u
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
-  return exp2_int(k);
+  return m < INFINITY ? exp2_int(k) : NAN;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -505,7 +505,8 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         break;
       }
       tc_fence_after();
-      const float f = fmaxf(it.k_scale * q_fac, 1.2e-38f);  // (positive: -inf times it stays -inf)
+      // positive, so that -inf times it stays -inf; NaN (a row with an infinity) stays NaN
+      const float f = it.k_scale * q_fac < 1.2e-38f ? 1.2e-38f : it.k_scale * q_fac;
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {

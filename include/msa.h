@@ -321,9 +321,9 @@ msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cach
  *                              + sum over t, h and the keys j of block n of e^{z_j - lse}
  *           for every n in 0 .. max_blocks - 1 (a missing weight_in counts as 0).  weight_in may be
  *           weight_out, but not overlap it otherwise.  weight_decay in 0..1.
- * K and V codes must be finite where they are visible to some row of the call, else that
- * row's results are NaN as the formula has it; codes past seq_lens[b] may be anything, and a
- * NaN code reaches only rows that see its key.  A page whose table entry or scale is bad is skipped
+ * A NaN code in K or V makes the results of the rows that see its key NaN (of V: in its dim),
+ * and of no other row; codes past seq_lens[b] may be anything.  A query row with a NaN or an
+ * infinity gives NaN.  A page whose table entry or scale is bad is skipped
  * (MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SCALE), a sequence whose length is bad gives empty rows
  * (MSA_DEVERR_BAD_SEQLEN).
  * Results do not depend on how the work is split beyond rounding, and are the same bits in

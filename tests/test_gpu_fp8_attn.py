@@ -15,7 +15,7 @@ SHAPES = [
     ([300, 7, 0, 129], 2, 2, 8), ([256, 20], 16, 1, 1), ([130, 3], 3, 4, 5),
     ([300, 17, 0], 17, 2, 1), ([700, 130], 8, 2, 8), ([1500, 11, 600], 11, 1, 8), ([260, 128], 128, 1, 1),
     ([129, 140], 129, 2, 1), ([500], 40, 2, 7), ([400, 300], 300, 1, 1), ([300], 100, 1, 4), ([390], 129, 1, 8),
-    ([2100], 70, 1, 8),
+    ([2100], 70, 1, 8), ([300, 500], 17, 8, 8), ([20000], 1, 1, 3), ([9000], 20, 1, 1), ([1300, 900], 700, 1, 1),
 ]
 
 
@@ -31,7 +31,8 @@ def test_dense_matches_the_oracle(lens, T, G, Hg, q_type):
 
 @pytest.mark.parametrize("q_type", ["e4m3", "bf16"])
 @pytest.mark.parametrize("lens,T,G,Hg", [
-    ([1], 1, 1, 1), ([5000, 129, 0, 2100], 1, 4, 8), ([3000, 40], 5, 2, 5), ([2500], 70, 1, 3), ([4000, 200], 3, 8, 8)])
+    ([1], 1, 1, 1), ([5000, 129, 0, 2100], 1, 4, 8), ([3000, 40], 5, 2, 5), ([2500], 70, 1, 3), ([4000, 200], 3, 8, 8),
+    ([900, 3000], 40, 4, 2)])
 def test_sparse_matches_the_oracle(lens, T, G, Hg, q_type):
     need_gpu()
     c = Case(300 + T, lens, T, G, Hg, q_type).upload()
@@ -39,6 +40,44 @@ def test_sparse_matches_the_oracle(lens, T, G, Hg, q_type):
     w_in = c.rng.random((c.B, c.max_blocks)).astype(np.float32)
     ref = c.oracle(selection=sel, weight_in=w_in, decay=0.25)
     assert_attention(c, c.run(selection=sel, weight_in=w_in, weights=True, decay=0.25), ref, weights=True)
+
+
+@pytest.mark.parametrize("B,T,G,Hg,most", [(33, 1, 2, 4, 400), (200, 1, 1, 8, 300), (2048, 1, 1, 1, 200), (70, 5, 1, 8, 200),
+                                           (40, 2, 1, 3, 500), (600, 17, 1, 1, 150)])
+def test_many_sequences(B, T, G, Hg, most):
+    need_gpu()
+    rng = np.random.default_rng(B)
+    lens = rng.integers(T, most, B)
+    lens[rng.integers(0, B, B // 8)] = 0
+    c = Case(400 + B, lens.tolist(), T, G, Hg).upload()
+    assert_attention(c, c.run(weights=True), c.oracle(), weights=True)
+
+
+def test_tables_far_wider_than_the_sequences():
+    need_gpu()
+    for T in (1, 30):
+        c = Case(31 + T, [300, 0, 129, 64], T, 1, 2, max_blocks=5000).upload()
+        w_in = c.rng.random((4, 5000)).astype(np.float32)
+        ref = c.oracle(weight_in=w_in, decay=1.0)
+        assert_attention(c, c.run(weight_in=w_in, weights=True), ref, weights=True)
+        if T == 1:
+            sel = c.selection()
+            ref = c.oracle(selection=sel, weight_in=w_in, decay=0.0)
+            assert_attention(c, c.run(selection=sel, weight_in=w_in, weights=True, decay=0.0), ref, weights=True)
+
+
+@pytest.mark.parametrize("T,Hg", [(1, 8), (2, 8), (40, 4)])
+def test_an_infinite_or_nan_query_makes_its_row_nan(T, Hg):
+    need_gpu()
+    c = Case(32, [300, 200], T, 1, Hg, "bf16").upload()
+    want = c.run()
+    for h, value in ((0, float("inf")), (Hg - 1, float("-inf")), (1, float("nan"))):
+        c.dq[1, T - 1, h, 77] = value
+    out, lse, _, err = c.run()
+    hit = np.zeros(lse.shape, bool)
+    hit[1, T - 1, [0, Hg - 1, 1]] = True
+    assert err == 0 and np.isnan(out[hit]).all() and np.isnan(lse[hit]).all()
+    assert np.array_equal(out[~hit], want[0][~hit]) and np.array_equal(lse[~hit], want[1][~hit])
 
 
 def test_a_selection_in_any_order_with_gaps():
