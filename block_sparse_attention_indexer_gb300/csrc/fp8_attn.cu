@@ -178,8 +178,9 @@ cudaError_t launch_fp8_attn(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
   const int64_t units = static_cast<int64_t>(a.batch) * a.q_len * a.groups;
   const bool stream = sparse || a.q_len * a.heads_per_group <= kFp8StreamRows;
   const int parts = stream ? kFp8StreamParts : 1;
-  // one launch while a sequence's entries are few (64 sequences of 64 entries: 36 us with the attention as
-  // XXX, against YYY with three)
+  // one launch while a sequence's entries are few (64 sequences of 64 entries over 1,024 blocks: 35.1 us with
+  // the attention, against 36.8 with the three of many; a CTA's 512 threads take 2,048 entries in 32 rounds,
+  // where many CTAs would share them)
   const bool few = a.q_len * a.groups * kTopK <= kMassEntries;
   if (sparse && weights && !few && (e = cudaMemsetAsync(a.mass, 0, blocks * sizeof(*a.mass), s)) != cudaSuccess) return e;
   e = stream ? launch_fp8_stream(a, num_sms, s) : launch_fp8_tile(a, num_sms, s);
@@ -193,8 +194,11 @@ cudaError_t launch_fp8_attn(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     return launch_dependent(fp8_weights_sparse_kernel, dim3(static_cast<unsigned>((blocks + 255) / 256)), 256, 0, s, a);
   }
+  // a warp a block up to 128 entries (64 sequences of 4K, one token: 43.6 us with the attention, 44.5 with a
+  // CTA a block; 8 of 32K: 39.6 and 40.1), a CTA from there (256 entries, 16 sequences of 16K: 61.4 us, 65.5 with
+  // a warp; 1,152 entries, 46 sequences of 6 blocks: 95 and 112)
   const int64_t each = static_cast<int64_t>(a.groups) * parts * a.q_len * a.heads_per_group;
-  return each <= 2048 ? launch_dependent(fp8_weights_dense_kernel<32>, dim3(static_cast<unsigned>((blocks + 7) / 8)), 256, 0,
+  return each <= 128 ? launch_dependent(fp8_weights_dense_kernel<32>, dim3(static_cast<unsigned>((blocks + 7) / 8)), 256, 0,
                                          s, a, parts)
                       : launch_dependent(fp8_weights_dense_kernel<256>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, a,
                                          parts);

@@ -16,9 +16,8 @@ namespace msa {
 constexpr int kFp8MergeThreads = 256;
 constexpr float kLn2F = 0.6931471805599453f;
 
-// Parts per unit from which a CTA's warps share a row (measured on one sequence of 4,096 tokens, 32
-// parts a unit: 12.9 us with one warp per row, 4 us with eight; with two or three parts the extra warps
-// only wait).
+// Parts per unit from which a CTA's warps share a row (one sequence of 4,096 tokens, 32 parts a unit:
+// 12.9 us with one warp per row, 6.2 with eight; with two or three parts the extra warps only wait).
 constexpr int kFp8MergeSplitParts = 12;
 
 struct Fp8MergeShared {

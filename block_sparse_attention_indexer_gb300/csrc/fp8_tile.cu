@@ -7,8 +7,7 @@
 // Work.  A unit is 256 query rows (token, head) of a (sequence, group), as two tiles of 128, or the
 // at most 128 rows of a last one, as one tile.  A unit's products are counted in (tile, page) steps;
 // the units of the call, in order, are one flat list of steps that a persistent grid (one CTA an SM)
-// cuts into equal ranges (fp8_tile_plan_kernel has the units' prefix sums; causal units differ in
-// length).  Two accumulator slots work in turn: with two tiles each page is used by slot 0 (tile 0)
+// cuts into equal ranges by the units' prefix sums (causal units differ in length).  Two accumulator slots work in turn: with two tiles each page is used by slot 0 (tile 0)
 // and slot 1 (tile 1), so a page is loaded and its V converted once for 256 rows; with one tile the
 // pages alternate between the slots and the two states are added at the end.
 //   * S = Q K^T: kind::f8f6f4, E4M3 from the page as it is (a tensor copy lands the 128-byte key rows
@@ -20,13 +19,21 @@
 //     exactly to fp16 as the MN-major B operand (keys as K rows, as the page has them: no transpose).
 // TMEM: S of the two slots, then O of the two slots: 4 x 128 columns, all of it.
 //
-// Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread, its 128 scores in registers), 8-11
-// load Q and convert V, 12 resolves pages and issues the copies, 13 issues S, 14 issues P V.
+// Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread, 64 scores at a time in registers), 8-11
+// load Q and convert V, 12 resolves pages and issues the copies, 13 issues S, 14 issues P V.  Two issuers,
+// because an issue blocks while the tensor queue is full: each waits for its operands while the other's products
+// run (one warp for both: 4.12 ms against 3.41).  An issuer is one elected lane, waits included (3.41 -> 3.06 ms).
+// P goes over in halves of 64 keys, so that the first half's product runs beside the second half's softmax.
+// Queries lie twice, so that the next unit's are loaded beside this one's pages.
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
 //
-// Bound by the tensor pipe for prompt chunks (768 cycles of products per step), by the page stream
-// for a few draft tokens.
+// Measured: 4,096 tokens on 64K, 64 E4M3 heads, 3.01 ms = 1.51 PFLOP/s of the products, tensor pipe 38%
+// active: a slot's chain (S, softmax, P V, rescale) is longer than the other slot's products.  8 draft tokens of
+// 4 sequences of 512K: 335 us = 4.6 TB/s of pages; the same chain, the pages' stream would allow 230.
+// More V stages, polling waits, S in halves of 64 keys and register shares between the warps changed nothing
+// or lost.  Short contexts (a few pages a unit) wait for latencies: lengths, table, scales, queries, first pages,
+// then a unit's rows written before the next begin, some 10 us in all.
 #include <cuda_bf16.h>
 
 #include "fp8_device.cuh"
@@ -66,6 +73,7 @@ struct FtShared {
   FtItem item[kFtItems];
   float q_fac[2][2 * kFtRows];  // the power of two taken out of each row (bf16)
   float other_m[kFtRows], other_l[kFtRows];
+  int32_t prefix[1024 + 1];     // the units' prefix sums, where the CTA makes them itself
   int nan_key[2][kDim];         // first key of the unit's edge pages with a NaN code in V, per dim
 };
 
@@ -94,22 +102,19 @@ __device__ __forceinline__ FtUnit ft_unit(const Fp8AttnArgs& a, int u, int per_s
   return t;
 }
 
-// prefix[u]: steps (per group) of the units before u; one CTA.
-constexpr int kFtPlanThreads = 1024;
-__global__ void __launch_bounds__(kFtPlanThreads) fp8_tile_plan_kernel(const Fp8AttnArgs a, int per_seq) {
-  __shared__ int s_warp[32];
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// out[u]: steps (per group) of the units before u, u = 0..units; every thread of the CTA (a whole number of
+// warps, at most 32) calls it.  `flag`: report bad lengths.
+__device__ __forceinline__ void ft_prefix(const Fp8AttnArgs& a, int per_seq, int32_t* out, int* warp_sum, bool flag) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const int units = a.batch * per_seq;
   int base = 0;
-  for (int u0 = 0; u0 < units; u0 += kFtPlanThreads) {
+  for (int u0 = 0; u0 < units; u0 += threads) {
     const int u = u0 + tid;
     int v = 0;
     if (u < units) {
       const FtUnit t = ft_unit(a, u, per_seq);
       v = t.width * t.pages;
-      if (t.row0 == 0 && !t.live && a.seq_lens[t.b] != 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
+      if (flag && t.row0 == 0 && !t.live && a.seq_lens[t.b] != 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
     }
     int x = v;
 #pragma unroll
@@ -117,20 +122,28 @@ __global__ void __launch_bounds__(kFtPlanThreads) fp8_tile_plan_kernel(const Fp8
       const int y = __shfl_up_sync(0xffffffffu, x, s);
       if (lane >= s) x += y;
     }
-    if (lane == 31) s_warp[warp] = x;
+    if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    int w = s_warp[lane];
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, s);
-      if (lane >= s) w += y;
-    }
-    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-    if (u < units) a.block_prefix[u] = base + x - v + (warp > 0 ? before : 0);
-    base += __shfl_sync(0xffffffffu, w, 31);
+    const int w = lane < threads / 32 ? warp_sum[lane] : 0;
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    if (u < units) out[u] = base + x - v + before;
+    base += __reduce_add_sync(0xffffffffu, w);
     __syncthreads();
   }
-  if (tid == 0) a.block_prefix[units] = base;
+  if (tid == 0) out[units] = base;
+}
+
+// Units up to which every CTA of the attention sums for itself (as many as a CTA sums in three rounds: 32.6 ->
+// 31.6 us for one prompt of 512, 58.3 -> 58.1 for 23 short sequences); more are summed by a launch before it, which
+// is then little beside the units' own time.
+constexpr int kFtOwnUnits = 1024;
+
+constexpr int kFtPlanThreads = 1024;
+__global__ void __launch_bounds__(kFtPlanThreads) fp8_tile_plan_kernel(const Fp8AttnArgs a, int per_seq) {
+  __shared__ int s_warp[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  ft_prefix(a, per_seq, a.block_prefix, s_warp, true);
 }
 
 // First step of CTA c of n.
@@ -321,14 +334,24 @@ __global__ void __launch_bounds__(kFtThreads, 1)
   }
   grid_dependency_wait();
   grid_dependents_launch();
+  const int units = a.batch * per_seq;
+  const int32_t* prefix = a.block_prefix;
+  if (units <= kFtOwnUnits) {
+    ft_prefix(a, per_seq, sh->prefix, sh->nan_key[0], blockIdx.x == 0);
+    prefix = sh->prefix;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (units <= kFtOwnUnits && blockIdx.x == 0)  // for the merge
+    for (int u = tid; u <= units; u += kFtThreads) a.block_prefix[u] = sh->prefix[u];
   const uint32_t tmem = sh->tmem;
-  const int units = a.batch * per_seq;
+  // Two units' queries fit by turns, but for two tiles of bf16 rows: where the odd units' lie
+  const bool q_by_turns = !a.q_bf16 || T * Hg <= kFtRows;
+  const int q_turn = !q_by_turns ? 0 : a.q_bf16 ? kFtRows * 128 : kFtQHalf;
   bool failed = false;
 
-  // The next page record, for a whole warp; `n` counts records.  free_item: this warp is done with it.
+  // The next page record, for a whole warp; `n` counts records.
   auto take_item = [&](int n, FtItem& it) -> bool {
     if (!mbar_wait_warp(&sh->item_full[n % kFtItems], (n / kFtItems) & 1)) return false;
     it = sh->item[n % kFtItems];
@@ -607,7 +630,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           if (unit < 0) break;
           ++uc;
           // the unit that used this one's half of Q (bf16: both halves), factors and NaN marks is written
-          const int back = a.q_bf16 ? 1 : 2;
+          const int back = a.q_bf16 && !q_by_turns ? 1 : 2;
           if (uc >= back && !mbar_wait_warp(&sh->fin[(uc - back) & 1], ((uc - back) >> 1) & 1)) {
             failed = true;
             break;
@@ -616,7 +639,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           L = a.seq_lens[t.b];
           sh->nan_key[uc & 1][ct] = INT32_MAX;
           if (ct == 0) sh->nan_any[uc & 1] = 0;
-          uint8_t* q_half = q_tile + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf);
+          uint8_t* q_half = q_tile + (uc & 1) * q_turn;
           const int c = ct & 7;  // dims 16 c .. 16 c + 15 of rows ct / 8, + 16, ...
           for (int r0 = ct >> 3; r0 < t.width * kFtRows; r0 += 128) {  // eight rows' loads at once
             uint4 u[8][2];
@@ -707,7 +730,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       }
     } else if (warp == 12) {
       // ---- producer: page records and copies
-      const int64_t E = static_cast<int64_t>(a.block_prefix[units]) * G;
+      const int64_t E = static_cast<int64_t>(prefix[units]) * G;
       const int x0 = ft_lo(E, blockIdx.x, gridDim.x), x1 = ft_lo(E, blockIdx.x + 1, gridDim.x);
       // every sequence's tiles read its pages again: keep them in L2, unless one tile has them all
       const uint64_t policy = per_seq > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
@@ -721,9 +744,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         ++n;
         return true;
       };
-      int u = x0 < x1 ? ft_find(a.block_prefix, units, G, x0) : units;
+      int u = x0 < x1 ? ft_find(prefix, units, G, x0) : units;
       for (; u < units && !failed; ++u) {
-        const int64_t first = static_cast<int64_t>(a.block_prefix[u]) * G;
+        const int64_t first = static_cast<int64_t>(prefix[u]) * G;
         if (first >= x1) break;
         const FtUnit t = ft_unit(a, u, per_seq);
         const int steps = t.width * t.pages;
@@ -848,7 +871,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                 break;
               }
               tc_fence_after();
-              const uint64_t qd = umma_desc(qb + (a.q_bf16 ? 0 : (uc & 1) * kFtQHalf) + (width == 2 ? s : 0) * (kFtRows * 128));
+              const uint64_t qd = umma_desc(qb + (uc & 1) * q_turn + (width == 2 ? s : 0) * (kFtRows * 128));
               const uint64_t kd = umma_desc(kb + ks * kFp8PageBytes);
               for (int part = 0; part < (a.q_bf16 ? 2 : 1); ++part)
 #pragma unroll
@@ -961,7 +984,9 @@ cudaError_t launch_fp8_tile(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
   const int per_seq = fp8_tile_units_per_seq(static_cast<int64_t>(a.q_len) * a.heads_per_group);
   const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas;
   if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(fp8_tile_kernel), kFtSmem)) != cudaSuccess) return e;
-  if ((e = launch_dependent(fp8_tile_plan_kernel, dim3(1), kFtPlanThreads, 0, s, a, per_seq)) != cudaSuccess) return e;
+  if (static_cast<int64_t>(a.batch) * per_seq > kFtOwnUnits &&
+      (e = launch_dependent(fp8_tile_plan_kernel, dim3(1), kFtPlanThreads, 0, s, a, per_seq)) != cudaSuccess)
+    return e;
   if ((e = launch_dependent(fp8_tile_kernel, dim3(ctas), kFtThreads, kFtSmem, s, a, maps, per_seq)) != cudaSuccess)
     return e;
   if (ctas == 1) return cudaSuccess;

@@ -43,7 +43,7 @@ def test_sparse_matches_the_oracle(lens, T, G, Hg, q_type):
 
 
 @pytest.mark.parametrize("B,T,G,Hg,most", [(33, 1, 2, 4, 400), (200, 1, 1, 8, 300), (2048, 1, 1, 1, 200), (70, 5, 1, 8, 200),
-                                           (40, 2, 1, 3, 500), (600, 17, 1, 1, 150)])
+                                           (40, 2, 1, 3, 500), (600, 17, 1, 1, 150), (1100, 17, 1, 1, 60)])
 def test_many_sequences(B, T, G, Hg, most):
     need_gpu()
     rng = np.random.default_rng(B)
