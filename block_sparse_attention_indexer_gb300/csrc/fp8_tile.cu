@@ -685,47 +685,57 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         }
         if (it.block < 0) continue;
         const int rs = page % kFtRaw, vs = page % kFtV;
-        if (!mbar_wait_warp(&sh->raw_full[rs], (page / kFtRaw) & 1) ||
-            (page >= kFtV && !mbar_wait_warp(&sh->v_empty[vs], (page / kFtV - 1) & 1))) {
+        if (!mbar_wait_warp(&sh->raw_full[rs], (page / kFtRaw) & 1)) {
           failed = true;
           break;
         }
+        // all of the page's loads first: the raw stage is free again before the fp16 stage is waited for
         const uint8_t* src = raw_ring + rs * kFp8PageBytes;
-        uint8_t* dst = v_ring + vs * kFtVBytes;
-        const bool edge = it.block * kBlock + kBlock - 1 > L - T;  // hidden from some row of the sequence
         const int c = ct & 7;
-        const int h0 = c < 4 ? 2 * c : 2 * (c & 3) + 1;  // chunk of the first 8 dims within its half
-        uint8_t* half = dst + (c < 4 ? 0 : kFtVBytes / 2);
-#pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
-          const int r = 16 * i + (ct >> 3);
-          const uint4 u = lds128(src + page_chunk(r, c));
-          uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          if (edge) {
-            const int key = it.block * kBlock + r;
+        uint4 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = lds128(src + page_chunk(16 * i + (ct >> 3), c));
+        if (it.block * kBlock + kBlock - 1 > L - T) {  // hidden from some row of the sequence
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = it.block * kBlock + 16 * i + (ct >> 3);
+            uint32_t* w[4] = {&u[i].x, &u[i].y, &u[i].z, &u[i].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t nan = __vcmpeq4(w[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              w[j] &= ~nan;
+              const uint32_t nan = __vcmpeq4(*w[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              *w[j] &= ~nan;
               if (nan != 0u && key < L) {
                 sh->nan_any[uc & 1] = 1;
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q)
                   if (nan >> (8 * q) & 1u) atomicMin(&sh->nan_key[uc & 1][16 * c + 4 * j + q], key);
               }
             }
           }
-          uint32_t x[8];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->raw_empty[rs]);
+        if (page >= kFtV && !mbar_wait_warp(&sh->v_empty[vs], (page / kFtV - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        uint8_t* dst = v_ring + vs * kFtVBytes;
+        const int h0 = c < 4 ? 2 * c : 2 * (c & 3) + 1;  // chunk of the first 8 dims within its half
+        uint8_t* half = dst + (c < 4 ? 0 : kFtVBytes / 2);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) e4m3x4_to_f16x4(w[j], x[2 * j], x[2 * j + 1]);
+        for (int i = 0; i < 8; ++i) {
+          const int r = 16 * i + (ct >> 3);
+          uint32_t x[8];
+          e4m3x4_to_f16x4(u[i].x, x[0], x[1]);
+          e4m3x4_to_f16x4(u[i].y, x[2], x[3]);
+          e4m3x4_to_f16x4(u[i].z, x[4], x[5]);
+          e4m3x4_to_f16x4(u[i].w, x[6], x[7]);
           *reinterpret_cast<uint4*>(half + sw128(r, h0)) = make_uint4(x[0], x[1], x[2], x[3]);
           *reinterpret_cast<uint4*>(half + sw128(r, h0 ^ 1)) = make_uint4(x[4], x[5], x[6], x[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh->v_full[vs]);
-          mbar_arrive(&sh->raw_empty[rs]);
-        }
+        if (lane == 0) mbar_arrive(&sh->v_full[vs]);
         ++page;
       }
     } else if (warp == 12) {
