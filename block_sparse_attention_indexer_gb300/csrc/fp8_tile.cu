@@ -28,11 +28,11 @@
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
 //
-// Measured: 4,096 tokens on 64K, 64 E4M3 heads, 3.01 ms = 1.51 PFLOP/s of the products, tensor pipe 38%
-// active: a slot's chain (S, softmax, P V, rescale) is longer than the other slot's products.  8 draft tokens of
-// 4 sequences of 512K: 335 us = 4.6 TB/s of pages; the same chain, the pages' stream would allow 230.
-// More V stages, polling waits, S in halves of 64 keys and register shares between the warps changed nothing
-// or lost.  Short contexts (a few pages a unit) wait for latencies: lengths, table, scales, queries, first pages,
+// Measured: 4,096 tokens on 64K, 64 E4M3 heads, 2.93 ms = 1.55 PFLOP/s of the products: a slot's chain (S,
+// softmax, P V, rescale) is longer than the other slot's products.  8 draft tokens of 4 sequences of 512K:
+// 301 us = 5.1 TB/s of pages; the same chain, the pages' stream alone would take 230.
+// More stages of K, raw V or fp16 V, polling waits, S in halves of 64 keys and register shares between the warps
+// changed nothing or lost.  Short contexts (a few pages a unit) wait for latencies: lengths, table, scales, queries, first pages,
 // then a unit's rows written before the next begin, some 10 us in all.
 #include <cuda_bf16.h>
 
