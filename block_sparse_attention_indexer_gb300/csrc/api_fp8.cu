@@ -44,9 +44,12 @@ AttnLayout attn_layout(const msa_config_t* c, const msa_batch_t* b, bool weights
   w.total = w.partial + align_up(fp8_attn_partial_bytes(rows));
   if (!weights) return w;
   const size_t all = static_cast<size_t>(b->batch) * c->num_kv_groups * rows;
-  const size_t places = b->max_blocks > kSelTopK ? b->max_blocks : kSelTopK;
+  // shares of a row: the streaming form keeps the parts of a page apart (dense, or of the 16 selected ones), the
+  // tile form does not
+  const size_t dense = static_cast<size_t>(b->max_blocks) * (rows <= kFp8StreamRows ? kFp8StreamParts : 1);
+  const size_t sparse = static_cast<size_t>(kSelTopK) * kFp8StreamParts;
   w.share = w.total;
-  w.stat = w.share + align_up(all * places * kFp8StreamParts * sizeof(float2));
+  w.stat = w.share + align_up(all * (dense > sparse ? dense : sparse) * sizeof(float2));
   w.mass = w.stat + align_up(all * sizeof(float2));
   w.total = w.mass + align_up(static_cast<size_t>(b->batch) * b->max_blocks * sizeof(unsigned long long));
   return w;

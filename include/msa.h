@@ -294,8 +294,8 @@ msa_status_t msa_decode(const msa_config_t* cfg, const msa_cache_t* cache, const
  * times 2^(e_old - e) rounded to E4M3 once more.  Codes: x * 2^-e rounded to nearest even, saturating at
  * +-448 (infinities too), the sign of zero kept, NaN as a NaN code.  Rows of the page at
  * seq_lens[b] and beyond are left as they are, and so is every other page.
- * A page is written by one sequence per call: two sequences whose tables give one page to
- * written blocks leave its contents unspecified.  Sequences of length 0 write nothing; an old scale
+ * A page is written once per call: tables that give one page to two written blocks, of one
+ * sequence or of two, leave its contents unspecified.  Sequences of length 0 write nothing; an old scale
  * outside MSA_E8M0_MIN..MAX sets MSA_DEVERR_BAD_SCALE and leaves the page head alone.
  * workspace: msa_workspace_bytes(MSA_OP_FP8_APPEND, ...) (the error word). */
 msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cache, const msa_batch_t* batch,
