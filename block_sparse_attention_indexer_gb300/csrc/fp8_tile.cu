@@ -696,20 +696,36 @@ __global__ void __launch_bounds__(kFtThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] = lds128(src + page_chunk(16 * i + (ct >> 3), c));
         if (it.block * kBlock + kBlock - 1 > L - T) {  // hidden from some row of the sequence
+          auto nans = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };  // a bit per code
+          uint32_t any = 0u;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int key = it.block * kBlock + 16 * i + (ct >> 3);
-            uint32_t* w[4] = {&u[i].x, &u[i].y, &u[i].z, &u[i].w};
+          for (int i = 0; i < 8; ++i) any |= nans(u[i].x) | nans(u[i].y) | nans(u[i].z) | nans(u[i].w);
+          if (any != 0u) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const int r = 16 * i + (ct >> 3), key = it.block * kBlock + r;
+              const uint4 x = lds128(src + page_chunk(r, c));
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t nan = __vcmpeq4(*w[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              *w[j] &= ~nan;
-              if (nan != 0u && key < L) {
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t nan = nans(w[j]);
+                if (nan == 0u || key >= L) continue;
                 sh->nan_any[uc & 1] = 1;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q)
-                  if (nan >> (8 * q) & 1u) atomicMin(&sh->nan_key[uc & 1][16 * c + 4 * j + q], key);
+                  if (nan >> (8 * q + 7) & 1u) atomicMin(&sh->nan_key[uc & 1][16 * c + 4 * j + q], key);
               }
+            }
+            auto clear = [&](uint32_t& w) {
+              const uint32_t m = nans(w);
+              w &= ~(m | (m - (m >> 7)));
+            };
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              clear(u[i].x);
+              clear(u[i].y);
+              clear(u[i].z);
+              clear(u[i].w);
             }
           }
         }
