@@ -59,7 +59,12 @@ struct alignas(16) FtItem {
   int place;      // partial-state place of a cut unit; -1: the whole unit is this CTA's
   float k_scale;  // 2^a * softmax_scale * log2(e)
   float v_exp;    // b
+  int seq;        // sequence
+  int flags;      // kFtEdge ...
 };
+// Flags of a record: some row of the sequence must not see all of the page; some row of slot s's tile must not
+// see all of its half h (bit kFtHide + 2 s + h); the unit has two tiles.
+constexpr int kFtEdge = 1, kFtTwo = 2, kFtHide = 2;
 
 struct FtShared {
   uint64_t k_full[kFtK], k_empty[kFtK], raw_full[kFtRaw], raw_empty[kFtRaw], v_full[kFtV], v_empty[kFtV];
@@ -74,6 +79,7 @@ struct FtShared {
   float q_fac[2][2 * kFtRows];  // the power of two taken out of each row (bf16)
   float other_m[kFtRows], other_l[kFtRows];
   int32_t prefix[1024 + 1];     // the units' prefix sums, where the CTA makes them itself
+  int pos[2 * kFtRows];         // positions of the rows of the slots' tiles: read by the thread that wrote it
   int nan_key[2][kDim];         // first key of the unit's edge pages with a NaN code in V, per dim
 };
 
@@ -165,6 +171,14 @@ __device__ __forceinline__ int ft_find(const int32_t* prefix, int units, int gro
 
 // ---------------------------------------------------------------- tcgen05 forms used here only
 
+// n / d for 0 <= n < 2^29 and 1 <= d <= 8: with m = ceil(2^32 / d), n m / 2^32 exceeds n / d by less than
+// n d / (2^32 d) < 1 / d.
+struct FtDiv {
+  uint32_t m;
+  __device__ __forceinline__ explicit FtDiv(int d) : m(d > 1 ? 0xFFFFFFFFu / static_cast<uint32_t>(d) + 1u : 0u) {}
+  __device__ __forceinline__ int operator()(int n) const { return m != 0u ? static_cast<int>(__umulhi(n, m)) : n; }
+};
+
 // kind::f8f6f4, both operands in shared memory
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -180,6 +194,12 @@ __device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
+
+// 16 bytes (or, with bytes = 0, as many zeros) global -> shared by this thread's own queue
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Four floats as E5M2 codes, the first in the low byte
 __device__ __forceinline__ uint32_t f32x4_to_e5m2x4(float a, float b, float c, float d) {
@@ -352,6 +372,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
   bool failed = false;
 
   // The next page record, for a whole warp; `n` counts records.
+  const FtDiv by_hg(Hg);
   auto take_item = [&](int n, FtItem& it) -> bool {
     if (!mbar_wait_warp(&sh->item_full[n % kFtItems], (n / kFtItems) & 1)) return false;
     it = sh->item[n % kFtItems];
@@ -365,18 +386,23 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     const int slot = warp >> 2, r = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kFtO + slot * 128 + lane_base;
-    // steps of this slot and of the other one so far, and at the unit's start
-    int unit = -1, g = 0, done = 0, done_o = 0, pages = 0, valid_pages = 0, uc = -1, others = 0;  // uc: units before this one
-    int place = -1, start = 0, start_o = 0;
-    FtUnit t{};
-    int row = 0, pos = 0, pos_first = 0, pos0 = 0;  // pos0: of the sequence's first query token
+    // What the steps need stays in registers, the rest is made again where a unit ends.  Steps of this slot and of
+    // the other one so far, pages, units before this one:
+    int unit = -1, g = 0, done = 0, done_o = 0, valid_pages = 0, uc = -1;
+    // bits: steps of this slot, of the other one in the unit; slot of a one-tile unit's next page; parity of the
+    // one-tile units so far; two tiles; place + 1 (two bits)
+    constexpr int kMine = 1, kOther = 2, kTurn = 4, kShared = 8, kTwo = 16, kPlace = 32;
+    int st = 0;
     float M = -INFINITY, l = 0.f, q_fac = 1.f;
+    const int row_of_slot = r + ((warp >> 2) << 7);
 
     // writes the unit's rows (or its partial state)
     auto finish = [&]() -> bool {
-      const bool mine = done > start;
+      const bool mine = st & kMine;
       if (mine && !mbar_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) return false;
-      if (t.width == 1) {
+      const int place = st / kPlace - 1, b = unit / per_seq, row0 = (unit - b * per_seq) * 2 * kFtRows;
+      const int row = row0 + (st & kTwo ? row_of_slot : r), row_end = min(row0 + 2 * kFtRows, T * Hg);
+      if (!(st & kTwo)) {
         if (slot == 1) {
           sh->other_m[r] = M;
           sh->other_l[r] = l;
@@ -384,13 +410,13 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           if (lane == 0) mbar_arrive(&sh->other);
           return true;
         }
-        if (!mbar_wait_warp(&sh->other, others & 1)) return false;
-        if (done_o > start_o && !mbar_wait_warp(&sh->pv_done[1][1], (done_o - 1) & 1)) return false;
+        if (!mbar_wait_warp(&sh->other, (st & kShared) != 0)) return false;
+        if (st & kOther && !mbar_wait_warp(&sh->pv_done[1][1], (done_o - 1) & 1)) return false;
       }
       tc_fence_after();
       // state of the row = fa * own O + fb * the other slot's O
       float fa = mine ? 1.f : 0.f, fb = 0.f;
-      const bool both = t.width == 1 && done_o > start_o;
+      const bool both = (st & (kTwo | kOther)) == kOther;
       if (both) {
         const float mo = sh->other_m[r], lo = sh->other_l[r];
         const float mn = fmaxf(M, mo);
@@ -399,16 +425,17 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         l = l * fa + lo * fb;
         M = mn;
       }
-      const bool valid = row < t.row0 + t.rows;
+      const bool valid = row < row_end;
       const bool any = l != 0.f;  // (NaN counts as any)
       const float inv = any ? 1.f / l : 0.f;
       const float out_f = place < 0 ? inv : 1.f;
-      const int64_t token = static_cast<int64_t>(t.b) * T + row / Hg;
-      const int64_t hr = token * G * Hg + g * Hg + row % Hg;
-      const int pr = row - t.row0;  // row of the partial state
+      const int64_t token = static_cast<int64_t>(b) * T + by_hg(row);
+      const int64_t hr = token * G * Hg + g * Hg + (row - by_hg(row) * Hg);
+      const int pr = row - row0;  // row of the partial state
       float* part = place < 0 ? nullptr
                               : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kFtPlaceFloats;
       const bool poison = sh->nan_any[uc & 1] != 0;
+      const int pos = sh->pos[row_of_slot];
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {  // 16 columns = dims of two groups of 8
         uint32_t x[16];
@@ -455,7 +482,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         if (place < 0) {
           if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * kLn2F : -INFINITY;
           if (a.weight_out != nullptr)
-            a.row_stat[(static_cast<int64_t>(t.b) * G + g) * T * Hg + row] = make_float2(any ? M : 0.f, inv);
+            a.row_stat[(static_cast<int64_t>(b) * G + g) * T * Hg + row] = make_float2(any ? M : 0.f, inv);
         } else {
           part[2 * kFtRows * kDim + pr] = M;
           part[2 * kFtRows * (kDim + 1) + pr] = l;
@@ -477,11 +504,11 @@ __global__ void __launch_bounds__(kFtThreads, 1)
             failed = true;
             break;
           }
-          if (t.width == 1) ++others;
+          if (!(st & kTwo)) st ^= kShared;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->fin[uc & 1]);
         }
-        const bool shared_o = unit >= 0 && t.width == 1;
+        const bool shared_o = unit >= 0 && !(st & kTwo);
         unit = it.unit;
         g = it.g;
         if (unit < 0) break;
@@ -491,39 +518,34 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           failed = true;
           break;
         }
-        t = ft_unit(a, unit, per_seq);
-        place = it.place;
-        pages = 0;
-        start = done;
-        start_o = done_o;
-        row = t.row0 + (t.width == 2 ? slot * kFtRows : 0) + r;
-        pos0 = a.seq_lens[t.b] - T;
-        pos = pos0 + min(row, T * Hg - 1) / Hg;
-        pos_first = pos0 + (t.row0 + (t.width == 2 ? slot * kFtRows : 0)) / Hg;
+        st = (st & kShared) | (it.flags & kFtTwo ? kTwo : 0) | (it.place + 1) * kPlace;
+        const int row = (unit - it.seq * per_seq) * 2 * kFtRows + (st & kTwo ? row_of_slot : r);
+        sh->pos[row_of_slot] = a.seq_lens[it.seq] - T + by_hg(min(row, T * Hg - 1));
         M = -INFINITY;
         l = 0.f;
         if (!mbar_wait_warp(&sh->q_full[uc & 1], (uc >> 1) & 1)) {
           failed = true;
           break;
         }
-        q_fac = sh->q_fac[uc & 1][row - t.row0];
+        if (a.q_bf16) q_fac = sh->q_fac[uc & 1][st & kTwo ? row_of_slot : r];
       }
       if (it.block < 0) continue;
       // the page's V stage, and whether its step is this slot's
       const int vstage = valid_pages % kFtV, vphase = (valid_pages / kFtV) & 1;
       ++valid_pages;
-      const int turn = pages & 1;
-      ++pages;
-      if (t.width == 1 && turn != slot) {
-        ++done_o;
-        continue;
+      if (!(st & kTwo)) {
+        st ^= kTurn;
+        if ((st & kTurn) == (slot ? kTurn : 0)) {  // (toggled already)
+          ++done_o;
+          st |= kOther;
+          continue;
+        }
       }
-      const bool had = done > start;
       // the converters' NaN marks of a page that some row of the sequence does not see whole are read
       // when the unit is written: seeing the page's stage full orders them before that (the stage
       // is not used again before this step's P)
       if (!mbar_wait_warp(&sh->s_full[slot], done & 1) ||
-          (it.block * kBlock + kBlock - 1 > pos0 && !mbar_wait_warp(&sh->v_full[vstage], vphase))) {
+          (it.flags & kFtEdge && !mbar_wait_warp(&sh->v_full[vstage], vphase))) {
         failed = true;
         break;
       }
@@ -534,25 +556,21 @@ __global__ void __launch_bounds__(kFtThreads, 1)
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const uint32_t tH = tS + 64 * h;
-        if (it.block * kBlock + 64 * h + 63 > pos_first) {
-          // some row of the tile must not see one of these keys: -inf over those scores, in place
-          const int vis = pos - it.block * kBlock - 64 * h + 1;  // visible columns
-#pragma unroll 1
-          for (int c = 0; c < 64; c += 16) {
-            uint32_t y[16];
-            tmem_ld16(tH + c, y);
-            tmem_wait_ld(y);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = c + j < vis ? y[j] : 0xff800000u;
-            tmem_st16(tH + c, y);
-          }
-          tmem_wait_st();
-        }
         uint32_t v[64];
         float mx;
         tmem_ld64_max(tH, v, mx);
         tmem_wait_ld(v);
         asm volatile("" : "+f"(mx));
+        if (it.flags >> (kFtHide + 2 * slot + h) & 1) {
+          // some row of the tile must not see one of these keys: -inf over its scores, and the maximum again
+          const int vis = sh->pos[row_of_slot] - it.block * kBlock - 64 * h + 1;  // visible columns
+          mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            v[j] = j < vis ? v[j] : 0xff800000u;
+            mx = fmaxf(mx, __uint_as_float(v[j]));
+          }
+        }
         mx = fmaf(mx, f, it.v_exp);
         if (__any_sync(0xffffffffu, mx > M + 8.f)) {
           float alpha = 1.f;
@@ -564,7 +582,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
             sum.x *= alpha;
             sum.y *= alpha;
           }
-          if (had || h > 0) {  // O as the products issued so far leave it, rescaled
+          if (st & kMine || h > 0) {  // O as the products issued so far leave it, rescaled
             if (!mbar_wait_warp(&sh->pv_done[slot][h ^ 1], (h ? done : done - 1) & 1)) {
               failed = true;
               break;
@@ -604,12 +622,16 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       }
       if (failed) break;
       ++done;
-      if (t.width == 2) ++done_o;
+      st |= kMine;
+      if (st & kTwo) ++done_o;
       const float total = sum.x + sum.y;
       l = fmaf(total, ex2(-it.v_exp), l);
-      if (a.weight_out != nullptr && row < t.row0 + t.rows)
-        a.share[((static_cast<int64_t>(t.b) * G + g) * a.max_blocks + it.block) * T * Hg + row] =
-            make_float2(total, (M == -INFINITY ? 0.f : M) - it.v_exp);
+      if (a.weight_out != nullptr) {
+        const int row = (unit - it.seq * per_seq) * 2 * kFtRows + (st & kTwo ? row_of_slot : r);
+        if (row < T * Hg)
+          a.share[((static_cast<int64_t>(it.seq) * G + g) * a.max_blocks + it.block) * T * Hg + row] =
+              make_float2(total, (M == -INFINITY ? 0.f : M) - it.v_exp);
+      }
     }
   } else {
     if (warp < 12) {
@@ -641,36 +663,37 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           if (ct == 0) sh->nan_any[uc & 1] = 0;
           uint8_t* q_half = q_tile + (uc & 1) * q_turn;
           const int c = ct & 7;  // dims 16 c .. 16 c + 15 of rows ct / 8, + 16, ...
-          for (int r0 = ct >> 3; r0 < t.width * kFtRows; r0 += 128) {  // eight rows' loads at once
-            uint4 u[8][2];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = r0 + 16 * i, row = t.row0 + rr;
-              u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
-              if (rr < t.rows) {
-                const int64_t at = (static_cast<int64_t>(t.b) * T + row / Hg) * a.q_stride + (g * Hg + row % Hg) * kDim + 16 * c;
-                if (a.q_bf16) {
-                  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-                  u[i][0] = src[0];
-                  u[i][1] = src[1];
-                } else {
-                  u[i][0] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at);
-                }
-              }
+          // Rows behind the unit's are zeros.  bf16 rows are copied as they are first, their first 64 dims into
+          // the place of the row's hi part and the others into that of its lo part, and split there.
+          const int rows = t.width * kFtRows;
+          const int64_t at0 = static_cast<int64_t>(t.b) * T * a.q_stride + g * Hg * kDim;
+#pragma unroll 2
+          for (int rr = ct >> 3; rr < rows; rr += 16) {
+            const int row = t.row0 + rr, token = by_hg(row);
+            const int64_t at = rr < t.rows ? at0 + token * a.q_stride + (row - token * Hg) * kDim : 0;
+            const uint32_t bytes = rr < t.rows ? 16u : 0u;
+            uint8_t* tile = q_half + (rr >> 7) * (kFtRows * 128);
+            if (a.q_bf16) {
+              const uint8_t* src = static_cast<const uint8_t*>(a.q) + 2 * at + 32 * c;
+              uint8_t* raw = tile + (c >> 2) * kFtQHalf + (rr & 127) * 128 + (c & 3) * 32;
+              cp_async16(raw, src, bytes);
+              cp_async16(raw + 16, src + 16, bytes);
+            } else {
+              cp_async16(tile + sw128(rr & 127, c), static_cast<const uint8_t*>(a.q) + at + 16 * c, bytes);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = r0 + 16 * i;
-              uint8_t* dst = q_half + (rr >> 7) * (kFtRows * 128) + sw128(rr & 127, c);
-              float fac = 1.f;
-              if (!a.q_bf16) {
-                *reinterpret_cast<uint4*>(dst) = u[i][0];
-              } else {
-                uint4 hi, lo;
-                fac = ft_split_bf16(u[i][0], u[i][1], hi, lo);
-                *reinterpret_cast<uint4*>(dst) = hi;
-                *reinterpret_cast<uint4*>(dst + kFtQHalf) = lo;
-              }
+          }
+          cp_async_wait_all();
+          if (a.q_bf16) {
+#pragma unroll 1
+            for (int rr = ct >> 3; rr < rows; rr += 16) {
+              uint8_t* tile = q_half + (rr >> 7) * (kFtRows * 128);
+              const uint8_t* raw = tile + (c >> 2) * kFtQHalf + (rr & 127) * 128 + (c & 3) * 32;
+              uint4 hi, lo;
+              const float fac = ft_split_bf16(lds128(raw), lds128(raw + 16), hi, lo);
+              __syncwarp();  // the lanes of a row have read it
+              uint8_t* dst = tile + sw128(rr & 127, c);
+              *reinterpret_cast<uint4*>(dst) = hi;
+              *reinterpret_cast<uint4*>(dst + kFtQHalf) = lo;
               if (c == 0) sh->q_fac[uc & 1][rr] = fac;
             }
           }
@@ -775,7 +798,10 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         const int64_t first = static_cast<int64_t>(prefix[u]) * G;
         if (first >= x1) break;
         const FtUnit t = ft_unit(a, u, per_seq);
-        const int steps = t.width * t.pages;
+        const int steps = t.width * t.pages, two = t.width == 2 ? kFtTwo : 0;
+        // positions of the sequence's first token and of the first row of each slot's tile
+        const int pos0 = t.live ? a.seq_lens[t.b] - T : 0, pos1 = pos0 + t.row0 / Hg;
+        const int pos2 = two ? pos0 + (t.row0 + kFtRows) / Hg : pos1;
         for (int g = 0; g < G && !failed; ++g) {
           const int64_t u0 = first + static_cast<int64_t>(g) * steps;
           if (u0 >= x1) break;
@@ -783,7 +809,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           const int hi = min(static_cast<int>((x1 - u0) / t.width), t.pages);
           if (lo >= hi) continue;
           const int place = lo == 0 && hi == t.pages ? -1 : lo == 0 ? 1 : 0;
-          FtItem it{u, g, -1, place, 0.f, 0.f};
+          FtItem it{u, g, -1, place, 0.f, 0.f, t.b, two};
           bool any = false;
           for (int p0 = lo; p0 < hi && !failed; p0 += 32) {
             const int p = p0 + lane;
@@ -817,6 +843,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               if (y < 0) continue;
               any = true;
               it.block = p0 + j;
+              const int half = it.block * kBlock + 63, last = half + 64;  // last keys of the page's halves
+              it.flags = two | (last > pos0 ? kFtEdge : 0) | (half > pos1 ? 1 : 0) << kFtHide |
+                         (last > pos1 ? 2 : 0) << kFtHide | (half > pos2 ? 4 : 0) << kFtHide | (last > pos2 ? 8 : 0) << kFtHide;
               const int ksl = page_n % kFtK, rsl = page_n % kFtRaw;
               if (!record(it) || (page_n >= kFtK && !mbar_wait_warp(&sh->k_empty[ksl], (page_n / kFtK - 1) & 1)) ||
                   (page_n >= kFtRaw && !mbar_wait_warp(&sh->raw_empty[rsl], (page_n / kFtRaw - 1) & 1))) {
@@ -839,7 +868,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           }
         }
       }
-      if (!failed) failed = !record(FtItem{-1, 0, -1, -1, 0.f, 0.f});
+      if (!failed) failed = !record(FtItem{-1, 0, -1, -1, 0.f, 0.f, 0, 0});
       if (failed) {
         // wait (bounded) for the copies still in flight
         for (int k = max(0, page_n - kFtK); k < page_n; ++k) mbar_wait(&sh->k_full[k % kFtK], (k / kFtK) & 1);
