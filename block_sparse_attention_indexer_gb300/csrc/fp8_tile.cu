@@ -28,12 +28,13 @@
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
 //
-// Measured: 4,096 tokens on 64K, 64 E4M3 heads, 2.93 ms = 1.55 PFLOP/s of the products: a slot's chain (S,
+// Measured: 4,096 tokens on 64K, 64 E4M3 heads, 2.69 ms = 1.69 PFLOP/s of the products: a slot's chain (S,
 // softmax, P V, rescale) is longer than the other slot's products.  8 draft tokens of 4 sequences of 512K:
-// 301 us = 5.1 TB/s of pages; the same chain, the pages' stream alone would take 230.
+// 303 us = 5.1 TB/s of pages; the same chain, the pages' stream alone would take 230.
 // More stages of K, raw V or fp16 V, polling waits, S in halves of 64 keys and register shares between the warps
-// changed nothing or lost.  Short contexts (a few pages a unit) wait for latencies: lengths, table, scales, queries, first pages,
-// then a unit's rows written before the next begin, some 10 us in all.
+// changed nothing or lost.  Registers spilled in the softmax's steps cost 10 % and more, so what they do not need
+// is kept in shared memory or made again where a unit ends.  Short contexts (a few pages a unit) wait for
+// latencies: lengths, table, scales, queries, first pages, then a unit's rows written before the next begin.
 #include <cuda_bf16.h>
 
 #include "fp8_device.cuh"
@@ -171,6 +172,17 @@ __device__ __forceinline__ int ft_find(const int32_t* prefix, int units, int gro
 
 // ---------------------------------------------------------------- tcgen05 forms used here only
 
+// First step of CTA c of n as it is taken: a cut inside a unit that stays whole goes to the nearer of its ends.  A
+// whole warp calls it.
+__device__ __forceinline__ int ft_cut(const int32_t* prefix, int units, int G, int64_t E, int c, int n, int whole) {
+  const int x = ft_lo(E, c, n);
+  if (c == 0 || x >= E) return x;
+  const int u = ft_find(prefix, units, G, x), steps = prefix[u + 1] - prefix[u];
+  if (steps > whole) return x;
+  const int off = (x - prefix[u] * G) % steps;
+  return x - off + (2 * off < steps ? 0 : steps);
+}
+
 // n / d for 0 <= n < 2^29 and 1 <= d <= 8: with m = ceil(2^32 / d), n m / 2^32 exceeds n / d by less than
 // n d / (2^32 d) < 1 / d.
 struct FtDiv {
@@ -305,7 +317,7 @@ __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, u
 // ---------------------------------------------------------------- the kernel
 
 __global__ void __launch_bounds__(kFtThreads, 1)
-    fp8_tile_kernel(const Fp8AttnArgs a, const __grid_constant__ Fp8Maps maps, int per_seq) {
+    fp8_tile_kernel(const Fp8AttnArgs a, const __grid_constant__ Fp8Maps maps, int per_seq, int whole) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* q_tile = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* k_ring = q_tile + kFtQ;
@@ -780,7 +792,12 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     } else if (warp == 12) {
       // ---- producer: page records and copies
       const int64_t E = static_cast<int64_t>(prefix[units]) * G;
-      const int x0 = ft_lo(E, blockIdx.x, gridDim.x), x1 = ft_lo(E, blockIdx.x + 1, gridDim.x);
+      int x0 = 0, x1 = 0;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        x0 = x1;
+        x1 = ft_cut(prefix, units, G, E, blockIdx.x + i, gridDim.x, whole);
+      }
       // every sequence's tiles read its pages again: keep them in L2, unless one tile has them all
       const uint64_t policy = per_seq > 1 ? l2_evict_normal_policy() : l2_evict_first_policy();
       int n = 0, page_n = 0;
@@ -977,7 +994,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
 // blockIdx.x is the unit (by_unit) or the boundary whose unit the CTA takes if it is the unit's first
 // cut, whichever is fewer; blockIdx.y the row (kSplit) or eight of them.
 template <bool kSplit>
-__global__ void __launch_bounds__(kFp8MergeThreads) fp8_tile_merge_kernel(const Fp8AttnArgs a, int per_seq, int ctas, int by_unit) {
+__global__ void __launch_bounds__(kFp8MergeThreads) fp8_tile_merge_kernel(const Fp8AttnArgs a, int per_seq, int ctas, int by_unit, int whole) {
   __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -990,6 +1007,7 @@ __global__ void __launch_bounds__(kFp8MergeThreads) fp8_tile_merge_kernel(const 
     if (xb >= E) return;
     u = ft_find(a.block_prefix, units, G, xb);
   }
+  if (a.block_prefix[u + 1] - a.block_prefix[u] <= whole) return;  // not cut
   const FtUnit t = ft_unit(a, u, per_seq);
   const int steps = t.width * t.pages;
   const int64_t first = static_cast<int64_t>(a.block_prefix[u]) * G;
@@ -1032,27 +1050,41 @@ int fp8_tile_units_per_seq(int64_t rows) { return static_cast<int>((rows + 2 * k
 
 size_t fp8_tile_partial_bytes() { return static_cast<size_t>(2) * kFp8MaxCtas * kFtPlaceFloats * sizeof(float); }
 
+// Steps of a unit up to which it is not cut (ft_cut).  A cut costs two partial states and a merge, about as
+// much as kFtCutSteps steps; not cutting leaves CTAs idle: of `all` units (with groups) on n CTAs some take
+// ceil(all / n), so that a unit of S steps costs idle * S / n more than its share.  46 sequences of 144 rows and up to 6
+// pages take 60 us whole and 76 cut, one prompt of 2,048 tokens 162 and 197, 23 sequences of 75 rows 28 and 44; 12
+// sequences of 64 rows and up to 16 pages (48 units) 29 whole and 24 cut.  Above 64 steps a unit is cut in any case,
+// so that the long sequences of a ragged batch do not wait for a CTA of their own.
+static int ft_whole(const Fp8AttnArgs& a, int per_seq, int n) {
+  constexpr int kFtWhole = 64, kFtCutSteps[2] = {6, 11};  // one tile of rows, two
+  const int64_t all = static_cast<int64_t>(a.batch) * per_seq * a.groups, idle = n - 1 - (all - 1) % n;
+  const int64_t most = static_cast<int64_t>(kFtCutSteps[a.q_len * a.heads_per_group > kFtRows]) * n;
+  return idle * kFtWhole <= most ? kFtWhole : static_cast<int>(most / idle);
+}
+
 cudaError_t launch_fp8_tile(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
   Fp8Maps maps;
   cudaError_t e = fp8_page_maps(a, &maps);
   if (e != cudaSuccess) return e;
   const int per_seq = fp8_tile_units_per_seq(static_cast<int64_t>(a.q_len) * a.heads_per_group);
   const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas;
+  const int whole = ft_whole(a, per_seq, ctas);
   if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(fp8_tile_kernel), kFtSmem)) != cudaSuccess) return e;
   if (static_cast<int64_t>(a.batch) * per_seq > kFtOwnUnits &&
       (e = launch_dependent(fp8_tile_plan_kernel, dim3(1), kFtPlanThreads, 0, s, a, per_seq)) != cudaSuccess)
     return e;
-  if ((e = launch_dependent(fp8_tile_kernel, dim3(ctas), kFtThreads, kFtSmem, s, a, maps, per_seq)) != cudaSuccess)
+  if ((e = launch_dependent(fp8_tile_kernel, dim3(ctas), kFtThreads, kFtSmem, s, a, maps, per_seq, whole)) != cudaSuccess)
     return e;
-  if (ctas == 1) return cudaSuccess;
   const int rows = a.q_len * a.heads_per_group < 2 * kFtRows ? a.q_len * a.heads_per_group : 2 * kFtRows;
+  if (ctas == 1 || static_cast<int64_t>(a.max_blocks) * (rows > kFtRows ? 2 : 1) <= whole) return cudaSuccess;  // no cut
   const int64_t units = static_cast<int64_t>(a.batch) * per_seq * a.groups;
   const int by_unit = units < ctas - 1 ? 1 : 0;
   const unsigned grid = by_unit ? static_cast<unsigned>(units) : static_cast<unsigned>(ctas - 1);
   return ctas / units >= kFp8MergeSplitParts
-             ? launch_dependent(fp8_tile_merge_kernel<true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, per_seq, ctas, by_unit)
+             ? launch_dependent(fp8_tile_merge_kernel<true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, per_seq, ctas, by_unit, whole)
              : launch_dependent(fp8_tile_merge_kernel<false>, dim3(grid, (rows + 7) / 8), kFp8MergeThreads, 0, s, a, per_seq,
-                                ctas, by_unit);
+                                ctas, by_unit, whole);
 }
 
 }  // namespace msa

@@ -53,6 +53,20 @@ def test_many_sequences(B, T, G, Hg, most):
     assert_attention(c, c.run(weights=True), c.oracle(), weights=True)
 
 
+@pytest.mark.parametrize("B,T,G,Hg,q_type", [(40, 17, 4, 8, "e4m3"), (39, 17, 4, 8, "bf16"), (50, 9, 4, 4, "bf16"), (20, 150, 8, 1, "e4m3")])
+def test_long_units_cut_beside_short_whole_ones(B, T, G, Hg, q_type):
+    # the split of the work leaves short units to one CTA each: one and two tiles of rows, a row of long
+    # sequences between short ones, empty sequences at cuts
+    need_gpu()
+    rng = np.random.default_rng(B)
+    lens = rng.integers(T, 600, B)
+    lens[[0, B // 2, B - 1]] = [4000, 3001, 4097]
+    lens[rng.integers(1, B // 2, 3)] = 0
+    c = Case(500 + B, lens.tolist(), T, G, Hg, q_type).upload()
+    w_in = c.rng.random((B, c.max_blocks)).astype(np.float32)
+    assert_attention(c, c.run(weight_in=w_in, weights=True, decay=0.5), c.oracle(weight_in=w_in, decay=0.5), weights=True)
+
+
 def test_tables_far_wider_than_the_sequences():
     need_gpu()
     for T in (1, 30):
