@@ -307,7 +307,7 @@ msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cach
  * Query row (b, t, h), position pos = seq_lens[b] - q_len + t, attends with logits
  * z_j = (q . k_j) * softmax_scale to the keys j <= pos (selection NULL: dense causal), or to
  * those of them in the blocks selection[b][t][h / Hg][:] (the layout of msa_select_blocks, -1
- * for an empty place, a block listed once):
+ * for an empty place, in any order; a block listed twice counts twice):
  *   out  = sum_j e^{z_j - lse} v_j   bfloat16 [batch][q_len][G*Hg][D]
  *   lse  = ln sum_j e^{z_j}          float [batch][q_len][G*Hg], may be NULL
  * A row with no key (padding, an empty selection, only bad pages) gives out 0 and lse -inf.
