@@ -65,6 +65,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The top bits of the bytes of w that are NaN codes (0x7f, 0xff; no byte's sum carries), and such bits as whole bytes.
+__device__ __forceinline__ uint32_t e4m3_nans(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t whole_bytes(uint32_t m) { return m | (m - (m >> 7)); }
+
 // One 2-D tiled tensor copy global -> shared completing on `bar`, with an L2 policy (x, the byte
 // offset within a key row, is always 0 here: 16-byte aligned).
 __device__ __forceinline__ void tma_page(void* dst, const void* map, int y, uint64_t* bar, uint64_t policy) {

@@ -43,7 +43,7 @@ constexpr int kFsMaxBatch = 2048; // host bound on the batch
 template <int NT>
 struct FsShape {
   static constexpr int kTeams = NT == 1 ? 3 : 2;
-  static constexpr int kSlots = NT == 1 ? 4 : 5;
+  static constexpr int kSlots = 4;
   static constexpr int kThreads = kTeams * (kFsWarps + 1) * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kMergeFloats = NT * 8 * 4 * 32 + 2 * kRows;  // fragments, M, l
@@ -73,6 +73,7 @@ template <int NT>
 struct FsShared {
   FsTeam<NT> team[FsShape<NT>::kTeams];
   float merge[FsShape<NT>::kTeams][2][FsShape<NT>::kMergeFloats];
+  uint4 q[NT == 1 ? 1 : FsShape<NT>::kTeams * kFsWarps * 8][NT == 1 ? 1 : 32];  // two n-tiles: each warp's B fragments
   int prefix[kFsMaxBatch + 1];
   int chunk[kFsMaxBatch / 32];
 };
@@ -158,69 +159,65 @@ __device__ __forceinline__ FsEntry fs_entry(const Fp8AttnArgs& a, const int* pre
   return e;
 }
 
-// Query rows of a unit as B fragments (f16), and the power of two taken out of each (bf16).
-template <int NT>
-__device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int rows, int gq, int t4,
-                                          uint32_t (&bq)[NT][8][2], float (&fac)[NT][2]) {
+// Eight query rows of a unit, from r0, as B fragments (f16), and the power of two taken out of each (bf16).
+__device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int rows, int r0, int gq, int t4,
+                                          uint32_t (&bq)[8][2], float (&fac)[2]) {
   const bool sparse = a.selection != nullptr;
   const int Hg = a.heads_per_group;
   const int g = unit % a.groups, bt = unit / a.groups;  // dense: bt = b
+  const int r = r0 + gq;
+  float f = 1.f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + gq;
-    float f = 1.f;
+  for (int i = 0; i < 8; ++i) bq[i][0] = bq[i][1] = 0u;
+  uint4 v[4] = {};  // 32 bf16 dims
+  if (r < rows) {
+    const int64_t token = sparse ? bt : static_cast<int64_t>(bt) * a.q_len + r / Hg;
+    const int64_t at = token * a.q_stride + (g * Hg + r % Hg) * kDim + 32 * t4;
+    if (!a.q_bf16) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bq[nt][i][0] = bq[nt][i][1] = 0u;
-    uint4 v[4] = {};  // 32 bf16 dims
-    if (r < rows) {
-      const int64_t token = sparse ? bt : static_cast<int64_t>(bt) * a.q_len + r / Hg;
-      const int64_t at = token * a.q_stride + (g * Hg + r % Hg) * kDim + 32 * t4;
-      if (!a.q_bf16) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at);
+      for (int h = 0; h < 2; ++h) {
+        const uint4 u = src[h];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 u = src[h];
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], bq[nt][4 * h + i][0], bq[nt][4 * h + i][1]);
-        }
-      } else {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = src[i];
+        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(w[i], bq[4 * h + i][0], bq[4 * h + i][1]);
       }
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = src[i];
     }
-    if (a.q_bf16) {
-      // the row times 2^-k, its largest value in [2^14, 2^15): the 8 significant bits of a bf16 value
-      // stay exact in f16 down to 2^-31 of that
-      float m = 0.f;
-      if (r < rows) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
-        }
-      }
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 112);
-      f = m < INFINITY ? exp2_int(k) : NAN;  // (a row with an infinity gives NaN)
-      const float inv = exp2_int(-k);
-      if (r < rows) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w0 = i & 1 ? v[i >> 1].z : v[i >> 1].x, w1 = i & 1 ? v[i >> 1].w : v[i >> 1].y;
-          bq[nt][i][0] = pack_f16x2(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv);
-          bq[nt][i][1] = pack_f16x2(__uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv);
-        }
-      }
-    }
-    // accumulator columns of this lane: rows 8 nt + 2 t4, + 1
-    fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
-    fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
   }
+  if (a.q_bf16) {
+    // the row times 2^-k, its largest value in [2^14, 2^15): the 8 significant bits of a bf16 value
+    // stay exact in f16 down to 2^-31 of that
+    float m = 0.f;
+    if (r < rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+      }
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 112);
+    f = m < INFINITY ? exp2_int(k) : NAN;  // (a row with an infinity gives NaN)
+    const float inv = exp2_int(-k);
+    if (r < rows) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w0 = i & 1 ? v[i >> 1].z : v[i >> 1].x, w1 = i & 1 ? v[i >> 1].w : v[i >> 1].y;
+        bq[i][0] = pack_f16x2(__uint_as_float(w0 << 16) * inv, __uint_as_float(w0 & 0xFFFF0000u) * inv);
+        bq[i][1] = pack_f16x2(__uint_as_float(w1 << 16) * inv, __uint_as_float(w1 & 0xFFFF0000u) * inv);
+      }
+    }
+  }
+  // accumulator columns of this lane: rows r0 + 2 t4, + 1
+  fac[0] = __shfl_sync(0xffffffffu, f, 8 * t4);
+  fac[1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
 }
 
 template <int NT>
@@ -387,13 +384,25 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
 
   // ---- consumers: warp wt of the team, keys 32 wt .. 32 wt + 31 of every page
   const int wt = warp % kFsWarps;
-  uint32_t bq[NT][8][2];
+  uint32_t bq[8][2];  // the queries' fragments, of one n-tile
   float fac[NT][2], m_run[NT][2], l_run[NT][2];
   float o[NT][8][4];
   int pos[NT][2];  // positions of this lane's accumulator columns
   int unit = -1, units_done = 0, pos_min = 0;
   const int first_unit = x0 < x1 ? fs_entry(a, sh->prefix, x0).unit : -1;
-  if (first_unit >= 0) fs_load_q<NT>(a, first_unit, rows, gq, t4, bq, fac);  // while the first pages come
+  auto* my_q = sh->q + (NT == 1 ? 0 : 8 * warp);
+  auto load_q = [&](int u) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      fs_load_q(a, u, rows, 8 * nt, gq, t4, bq, fac[nt]);
+      if constexpr (NT == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) reinterpret_cast<uint2*>(&my_q[i][lane])[nt] = make_uint2(bq[i][0], bq[i][1]);
+      }
+    }
+    __syncwarp();
+  };
+  if (first_unit >= 0) load_q(first_unit);  // while the first pages come
   bool failed = false;
 
   // adds the state in a merge area to this warp's
@@ -533,7 +542,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
       }
       unit = it.unit;
       if (unit >= 0) {
-        if (unit != first_unit) fs_load_q<NT>(a, unit, rows, gq, t4, bq, fac);
+        if (unit != first_unit) load_q(unit);
         pos_min = it.pos;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -570,22 +579,49 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
     // ---- S^T = K Q^T
     float s[2][NT][4];
 #pragma unroll
-    for (int mq = 0; mq < 2; ++mq) {
+    for (int mq = 0; mq < 2; ++mq)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[mq][nt][0] = s[mq][nt][1] = s[mq][nt][2] = s[mq][nt][3] = 0.f;
-      const int r = 32 * wt + 16 * mq + gq;
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int mq = 0; mq < 2; ++mq) {
+        const int r = 32 * wt + 16 * mq + gq;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 u0 = lds128(kd + page_chunk(r, 2 * t4 + h)), u1 = lds128(kd + page_chunk(r + 8, 2 * t4 + h));
+          const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(w0[i], a0, a2);
+            e4m3x4_to_f16x4(w1[i], a1, a3);
+            mma_f16_16816(s[mq][0], a0, a1, a2, a3, bq[4 * h + i][0], bq[4 * h + i][1]);
+          }
+        }
+      }
+    } else {
+      // the queries' fragments from shared memory, each for both groups of 16 keys: as registers they would
+      // not fit beside O
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 u0 = lds128(kd + page_chunk(r, 2 * t4 + h)), u1 = lds128(kd + page_chunk(r + 8, 2 * t4 + h));
-        const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+        uint4 u[2][2];
+#pragma unroll
+        for (int mq = 0; mq < 2; ++mq)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) u[mq][e] = lds128(kd + page_chunk(32 * wt + 16 * mq + gq + 8 * e, 2 * t4 + h));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(w0[i], a0, a2);
-          e4m3x4_to_f16x4(w1[i], a1, a3);
+          const uint4 q = lds128(&my_q[4 * h + i][lane]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16_16816(s[mq][nt], a0, a1, a2, a3, bq[nt][4 * h + i][0], bq[nt][4 * h + i][1]);
+          for (int mq = 0; mq < 2; ++mq) {
+            const uint32_t w0[4] = {u[mq][0].x, u[mq][0].y, u[mq][0].z, u[mq][0].w};
+            const uint32_t w1[4] = {u[mq][1].x, u[mq][1].y, u[mq][1].z, u[mq][1].w};
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(w0[i], a0, a2);
+            e4m3x4_to_f16x4(w1[i], a1, a3);
+            mma_f16_16816(s[mq][0], a0, a1, a2, a3, q.x, q.y);
+            mma_f16_16816(s[mq][NT - 1], a0, a1, a2, a3, q.z, q.w);
+          }
         }
       }
     }
@@ -828,7 +864,8 @@ static cudaError_t launch_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t
 }
 
 cudaError_t launch_fp8_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
-  // 9 to 16 rows as two n-tiles: 64 sequences of 32K with 16 rows take 269 us, with 128-row tiles 290
+  // 9 to 16 rows as two n-tiles: 64 sequences of 32K with 16 rows take 213 us, with 128-row tiles 254 (200 of 500
+  // tokens 77 and 71)
   const int rows = a.selection != nullptr ? a.heads_per_group : a.q_len * a.heads_per_group;
   return rows <= 8 ? launch_stream<1>(a, num_sms, s) : launch_stream<2>(a, num_sms, s);
 }

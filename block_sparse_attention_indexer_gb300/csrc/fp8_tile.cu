@@ -731,10 +731,9 @@ __global__ void __launch_bounds__(kFtThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] = lds128(src + page_chunk(16 * i + (ct >> 3), c));
         if (it.block * kBlock + kBlock - 1 > L - T) {  // hidden from some row of the sequence
-          auto nans = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };  // a bit per code
           uint32_t any = 0u;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) any |= nans(u[i].x) | nans(u[i].y) | nans(u[i].z) | nans(u[i].w);
+          for (int i = 0; i < 8; ++i) any |= e4m3_nans(u[i].x) | e4m3_nans(u[i].y) | e4m3_nans(u[i].z) | e4m3_nans(u[i].w);
           if (any != 0u) {
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
@@ -743,7 +742,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint32_t nan = nans(w[j]);
+                const uint32_t nan = e4m3_nans(w[j]);
                 if (nan == 0u || key >= L) continue;
                 sh->nan_any[uc & 1] = 1;
 #pragma unroll 1
@@ -751,10 +750,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                   if (nan >> (8 * q + 7) & 1u) atomicMin(&sh->nan_key[uc & 1][16 * c + 4 * j + q], key);
               }
             }
-            auto clear = [&](uint32_t& w) {
-              const uint32_t m = nans(w);
-              w &= ~(m | (m - (m >> 7)));
-            };
+            auto clear = [](uint32_t& w) { w &= ~whole_bytes(e4m3_nans(w)); };
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               clear(u[i].x);
