@@ -23,8 +23,8 @@
 // unit the four warps' states are added through shared memory in two steps; a unit that the split
 // cut leaves partial states, which fp8_stream_merge_kernel adds.
 //
-// Bound by the page stream (256 B per token and KV head, read once): 64 sequences of up to 128K 704 us =
-// 6.8 TB/s; 8 of 32K 38 us with their weights (24 at the stream's rate: start, merge and weights are the rest);
+// Bound by the page stream (256 B per token and KV head, read once): 64 sequences of up to 128K 700 us =
+// 6.9 TB/s; 8 of 32K 38 us with their weights (24 at the stream's rate: start, merge and weights are the rest);
 // one token of one sequence of 4,096 12 us, all of it latency.
 #include <cuda_bf16.h>
 
@@ -72,7 +72,7 @@ struct FsTeam {
 template <int NT>
 struct FsShared {
   FsTeam<NT> team[FsShape<NT>::kTeams];
-  float merge[FsShape<NT>::kTeams][2][FsShape<NT>::kMergeFloats];
+  alignas(16) float merge[FsShape<NT>::kTeams][2][FsShape<NT>::kMergeFloats];
   uint4 q[NT == 1 ? 1 : FsShape<NT>::kTeams * kFsWarps * 8][NT == 1 ? 1 : 32];  // two n-tiles: each warp's B fragments
   int prefix[kFsMaxBatch + 1];
   int chunk[kFsMaxBatch / 32];
@@ -405,32 +405,40 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
   if (first_unit >= 0) load_q(first_unit);  // while the first pages come
   bool failed = false;
 
-  // adds the state in a merge area to this warp's
+  // Adds the state in a merge area to this warp's.  An area has O's fragments, four floats a lane, then M and l
+  // of the rows.
   auto absorb = [&](const float* area) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float fa[2], fb[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * nt + 2 * t4 + e;
         const float mo = area[NT * 1024 + r], lo = area[NT * 1024 + S::kRows + r];
         const float mn = fmaxf(m_run[nt][e], mo);
-        const float fa = mn == -INFINITY ? 1.f : ex2(m_run[nt][e] - mn), fb = mn == -INFINITY ? 1.f : ex2(mo - mn);
+        fa[e] = mn == -INFINITY ? 1.f : ex2(m_run[nt][e] - mn);
+        fb[e] = mn == -INFINITY ? 1.f : ex2(mo - mn);
         m_run[nt][e] = mn;
-        l_run[nt][e] = l_run[nt][e] * fa + lo * fb;
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          o[nt][mt][e] = o[nt][mt][e] * fa + area[((nt * 8 + mt) * 4 + e) * 32 + lane] * fb;
-          o[nt][mt][2 + e] = o[nt][mt][2 + e] * fa + area[((nt * 8 + mt) * 4 + 2 + e) * 32 + lane] * fb;
-        }
+        l_run[nt][e] = l_run[nt][e] * fa[e] + lo * fb[e];
       }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        const float4 v = reinterpret_cast<const float4*>(area)[(nt * 8 + mt) * 32 + lane];
+        o[nt][mt][0] = o[nt][mt][0] * fa[0] + v.x * fb[0];
+        o[nt][mt][1] = o[nt][mt][1] * fa[1] + v.y * fb[1];
+        o[nt][mt][2] = o[nt][mt][2] * fa[0] + v.z * fb[0];
+        o[nt][mt][3] = o[nt][mt][3] * fa[1] + v.w * fb[1];
+      }
+    }
+    __syncwarp();
   };
   auto leave = [&](float* area) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) area[((nt * 8 + mt) * 4 + i) * 32 + lane] = o[nt][mt][i];
+        reinterpret_cast<float4*>(area)[(nt * 8 + mt) * 32 + lane] =
+            make_float4(o[nt][mt][0], o[nt][mt][1], o[nt][mt][2], o[nt][mt][3]);
       if (gq == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -455,24 +463,17 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
         l_run[nt][e] = v;
       }
     const uint32_t parity = units_done & 1;
-    float* area = sh->merge[team][wt & 1];
-    if (wt >= 2) {
-      if (units_done > 0 && !mbar_wait_warp(&tm->freed, parity ^ 1)) return false;
-      leave(area);
-      if (lane == 0) mbar_arrive(&tm->pair);
+    if (wt >= 2 && units_done > 0 && !mbar_wait_warp(&tm->freed, parity ^ 1)) return false;
+#pragma unroll 1
+    for (int k = wt; k < 2; ++k) {  // warp 0: of warps 2 and 1; warp 1: of warp 3
+      if (!mbar_wait_warp(k == wt ? &tm->pair : &tm->last, parity)) return false;
+      absorb(sh->merge[team][k]);
+    }
+    if (wt != 0) {
+      leave(sh->merge[team][wt & 1]);
+      if (lane == 0) mbar_arrive(wt == 1 ? &tm->last : &tm->pair);
       return true;
     }
-    if (!mbar_wait_warp(&tm->pair, parity)) return false;
-    absorb(area);
-    __syncwarp();
-    if (wt == 1) {
-      leave(area);
-      if (lane == 0) mbar_arrive(&tm->last);
-      return true;
-    }
-    if (!mbar_wait_warp(&tm->last, parity)) return false;
-    absorb(sh->merge[team][1]);
-    __syncwarp();
     if (lane == 0) mbar_arrive(&tm->freed);
     // whole, or cut by a range boundary?
     int64_t u0, u1;
@@ -864,8 +865,8 @@ static cudaError_t launch_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t
 }
 
 cudaError_t launch_fp8_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
-  // 9 to 16 rows as two n-tiles: 64 sequences of 32K with 16 rows take 213 us, with 128-row tiles 254 (200 of 500
-  // tokens 77 and 71)
+  // 9 to 16 rows as two n-tiles: 64 sequences of 32K with 16 rows take 194 us, with 128-row tiles 254 (200 of 500
+  // tokens 62 and 71)
   const int rows = a.selection != nullptr ? a.heads_per_group : a.q_len * a.heads_per_group;
   return rows <= 8 ? launch_stream<1>(a, num_sms, s) : launch_stream<2>(a, num_sms, s);
 }
