@@ -159,6 +159,17 @@ __device__ __forceinline__ FsEntry fs_entry(const Fp8AttnArgs& a, const int* pre
   return e;
 }
 
+// First entry of team c of n as it is taken: a cut inside a unit of at most `whole` pages goes to the nearer of the
+// unit's ends (fs_whole).
+__device__ __forceinline__ int fs_cut(const Fp8AttnArgs& a, const int* prefix, int64_t E, int c, int n, int whole) {
+  const int x = fs_lo(E, c, n);
+  if (whole == 0 || c == 0 || x >= E) return x;
+  const FsEntry e = fs_entry(a, prefix, x);
+  const int pages = a.selection != nullptr ? kTopK : prefix[e.b + 1] - prefix[e.b];
+  if (pages > whole) return x;
+  return x - e.place + (2 * e.place < pages ? 0 : pages);
+}
+
 // Eight query rows of a unit, from r0, as B fragments (f16), and the power of two taken out of each (bf16).
 __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int rows, int r0, int gq, int t4,
                                           uint32_t (&bq)[8][2], float (&fac)[2]) {
@@ -222,7 +233,7 @@ __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int ro
 
 template <int NT>
 __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
-    fp8_stream_kernel(const Fp8AttnArgs a, const __grid_constant__ Fp8Maps maps) {
+    fp8_stream_kernel(const Fp8AttnArgs a, const __grid_constant__ Fp8Maps maps, int whole) {
   using S = FsShape<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);  // the swizzle counts from 1 KB
@@ -260,7 +271,8 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
   const int tt = blockIdx.x * S::kTeams + team, teams = gridDim.x * S::kTeams;
   const int64_t E = sparse ? static_cast<int64_t>(a.batch) * T * a.groups * kTopK
                            : static_cast<int64_t>(sh->prefix[a.batch]) * a.groups;
-  const int x0 = fs_lo(E, tt, teams), x1 = fs_lo(E, tt + 1, teams);
+  const int cut = fs_cut(a, sh->prefix, E, tt + (lane & 1), teams, whole);  // both at once
+  const int x0 = __shfl_sync(0xffffffffu, cut, 0), x1 = __shfl_sync(0xffffffffu, cut, 1);
   uint8_t* my_slots = slots + team * S::kSlots * kFp8PageBytes;
   FsTeam<NT>* tm = &sh->team[team];
 
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
       u1 = u0 + nb;
     }
     const bool whole = u0 >= x0 && u1 <= x1;
-    float* part = a.partial + (2 * static_cast<int64_t>(tt) + (unit == first_unit ? 0 : 1)) * S::kSlotFloats;
+    float* part = a.partial + (2 * static_cast<int64_t>(tt) + (x0 > u0 ? 0 : 1)) * S::kSlotFloats;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -787,7 +799,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
 // blockIdx.x is the unit (by_unit) or the boundary whose unit the CTA takes if it is the unit's
 // first, whichever is fewer; blockIdx.y the row (kSplit) or eight of them.
 template <int NT, bool kSplit>
-__global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(const Fp8AttnArgs a, int teams, int by_unit) {
+__global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(const Fp8AttnArgs a, int teams, int by_unit, int whole) {
   __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -809,6 +821,7 @@ __global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(cons
     u0 = static_cast<int64_t>(p) * a.groups + static_cast<int64_t>(unit % a.groups) * nb;
     u1 = u0 + nb;
   }
+  if (u1 - u0 <= whole) return;  // not cut
   const int ca = fs_owner(E, u0, teams), cb = fs_owner(E, u1 - 1, teams);
   if (ca == cb || (!by_unit && static_cast<int>(blockIdx.x) != ca)) return;  // whole, or another boundary's
   if (threadIdx.x < 32) {  // the teams ca .. cb with a range, in order
@@ -818,8 +831,8 @@ __global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(cons
       const int lo = fs_lo(E, c, teams);
       const bool some = c <= cb && lo < fs_lo(E, c + 1, teams);
       const unsigned m = __ballot_sync(0xffffffffu, some);
-      // the state is in the team's first place if the unit is the first of its range
-      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * c + (lo >= u0 ? 0 : 1);
+      // the state is in the team's first place if its range begins inside the unit
+      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * c + (lo > u0 ? 0 : 1);
       n += __popc(m);
     }
     if (threadIdx.x == 0) sh.n = n;
@@ -843,6 +856,17 @@ size_t fp8_stream_partial_bytes() {
   return 2 * kFp8MaxCtas * (one > two ? one : two) * sizeof(float);
 }
 
+// Pages of a unit up to which it is not cut: a cut costs a merge, about as much as kFsCutPages pages; not cutting
+// leaves teams idle, as `all` units on n teams give some ceil(all / n), which for a unit of S pages is idle * S / n
+// more than its share.  200 sequences of up to 500 tokens, 4 groups: 29 us whole and 34 cut, with two new tokens (16
+// rows) 54 and 63.
+static int fs_whole(int64_t all, int n) {
+  constexpr int kFsWhole = 32, kFsCutPages = 3;
+  const int64_t idle = n - 1 - (all - 1) % n, most = kFsCutPages * static_cast<int64_t>(n);
+  const int whole = idle * kFsWhole <= most ? kFsWhole : static_cast<int>(most / idle);
+  return whole > kFsCutPages ? whole : 0;
+}
+
 template <int NT>
 static cudaError_t launch_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
   Fp8Maps maps;
@@ -851,17 +875,20 @@ static cudaError_t launch_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t
   const size_t smem = fs_smem_bytes<NT>();
   if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(fp8_stream_kernel<NT>), smem)) != cudaSuccess) return e;
   const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas, teams = ctas * FsShape<NT>::kTeams;
-  if ((e = launch_dependent(fp8_stream_kernel<NT>, dim3(ctas), FsShape<NT>::kThreads, smem, s, a, maps)) != cudaSuccess)
-    return e;
   const bool sparse = a.selection != nullptr;
   const int64_t units = static_cast<int64_t>(a.batch) * a.groups * (sparse ? a.q_len : 1);
+  // (tables of much longer sequences: no search for units to leave whole)
+  const int limit = fs_whole(units, teams), whole = (sparse ? kTopK : a.max_blocks) <= 2 * limit ? limit : 0;
+  if ((e = launch_dependent(fp8_stream_kernel<NT>, dim3(ctas), FsShape<NT>::kThreads, smem, s, a, maps, whole)) != cudaSuccess)
+    return e;
+  if ((sparse ? kTopK : a.max_blocks) <= whole) return cudaSuccess;  // no unit is cut
   const int rows = sparse ? a.heads_per_group : a.q_len * a.heads_per_group;
   const int by_unit = units < teams - 1 ? 1 : 0;
   const unsigned grid = by_unit ? static_cast<unsigned>(units) : static_cast<unsigned>(teams - 1);
   return teams / units >= kFp8MergeSplitParts
-             ? launch_dependent(fp8_stream_merge_kernel<NT, true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, teams, by_unit)
+             ? launch_dependent(fp8_stream_merge_kernel<NT, true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, teams, by_unit, whole)
              : launch_dependent(fp8_stream_merge_kernel<NT, false>, dim3(grid, (rows + 7) / 8), kFp8MergeThreads, 0, s, a,
-                                teams, by_unit);
+                                teams, by_unit, whole);
 }
 
 cudaError_t launch_fp8_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {

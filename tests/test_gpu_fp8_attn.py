@@ -67,6 +67,19 @@ def test_long_units_cut_beside_short_whole_ones(B, T, G, Hg, q_type):
     assert_attention(c, c.run(weight_in=w_in, weights=True, decay=0.5), c.oracle(weight_in=w_in, decay=0.5), weights=True)
 
 
+@pytest.mark.parametrize("B,T,Hg", [(225, 1, 2), (75, 9, 1)])
+def test_few_rows_of_long_sequences_beside_short_ones(B, T, Hg):
+    need_gpu()
+    rng = np.random.default_rng(B)
+    lens = rng.integers(T, 400, B)
+    lens[[0, B // 3, B - 1]] = [5000, 4737, 4224]
+    lens[rng.integers(1, B // 3, 3)] = 0
+    c = Case(550 + B, lens.tolist(), T, 4, Hg, "bf16").upload()
+    assert_attention(c, c.run(weights=True), c.oracle(), weights=True)
+    sel = c.selection()
+    assert_attention(c, c.run(selection=sel, weights=True), c.oracle(selection=sel), weights=True)
+
+
 def test_tables_far_wider_than_the_sequences():
     need_gpu()
     for T in (1, 30):
