@@ -12,7 +12,7 @@
 //
 // Work.  A unit is the rows that share a page list; the (unit, page) pairs of the call are one
 // flat list, cut into equal ranges, one for each of the teams of a persistent grid (one CTA an
-// SM).  A team is a producer warp and four consuming warps: the producer resolves 32 entries at a
+// SM), short units staying whole (fs_cut).  A team is a producer warp and four consuming warps: the producer resolves 32 entries at a
 // time (table -> page -> scales) and streams K and V pages (16 KB each) through a ring of slots
 // with tensor copies that land the 128-byte rows swizzled; consumer w takes keys 32w..32w+31 of
 // every page: S^T = K Q^T on mma.sync (keys as M, 8 or 16 rows as N; a lane's 16 bytes of a key
@@ -799,7 +799,8 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
 // blockIdx.x is the unit (by_unit) or the boundary whose unit the CTA takes if it is the unit's
 // first, whichever is fewer; blockIdx.y the row (kSplit) or eight of them.
 template <int NT, bool kSplit>
-__global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(const Fp8AttnArgs a, int teams, int by_unit, int whole) {
+__global__ void __launch_bounds__(kFp8MergeThreads)
+    fp8_stream_merge_kernel(const Fp8AttnArgs a, int teams, int by_unit, int whole) {
   __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -847,7 +848,8 @@ __global__ void __launch_bounds__(kFp8MergeThreads) fp8_stream_merge_kernel(cons
   fp8_merge_row<kSplit>(a.partial, FsShape<NT>::kRows, r, r * 32 + chunk, sh, o, M, l);
   if (kSplit && threadIdx.x >= 32) return;
   const int64_t token = sparse ? unit / a.groups : static_cast<int64_t>(unit / a.groups) * a.q_len + r / Hg;
-  fp8_write_row(a, token * a.groups * Hg + unit % a.groups * Hg + r % Hg, static_cast<int64_t>(unit) * rows + r, chunk, o, M, l);
+  fp8_write_row(a, token * a.groups * Hg + unit % a.groups * Hg + r % Hg, static_cast<int64_t>(unit) * rows + r, chunk, o,
+                M, l);
 }
 
 size_t fp8_stream_partial_bytes() {
@@ -879,14 +881,16 @@ static cudaError_t launch_stream(const Fp8AttnArgs& a, int num_sms, cudaStream_t
   const int64_t units = static_cast<int64_t>(a.batch) * a.groups * (sparse ? a.q_len : 1);
   // (tables of much longer sequences: no search for units to leave whole)
   const int limit = fs_whole(units, teams), whole = (sparse ? kTopK : a.max_blocks) <= 2 * limit ? limit : 0;
-  if ((e = launch_dependent(fp8_stream_kernel<NT>, dim3(ctas), FsShape<NT>::kThreads, smem, s, a, maps, whole)) != cudaSuccess)
+  if ((e = launch_dependent(fp8_stream_kernel<NT>, dim3(ctas), FsShape<NT>::kThreads, smem, s, a, maps, whole)) !=
+      cudaSuccess)
     return e;
   if ((sparse ? kTopK : a.max_blocks) <= whole) return cudaSuccess;  // no unit is cut
   const int rows = sparse ? a.heads_per_group : a.q_len * a.heads_per_group;
   const int by_unit = units < teams - 1 ? 1 : 0;
   const unsigned grid = by_unit ? static_cast<unsigned>(units) : static_cast<unsigned>(teams - 1);
   return teams / units >= kFp8MergeSplitParts
-             ? launch_dependent(fp8_stream_merge_kernel<NT, true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, teams, by_unit, whole)
+             ? launch_dependent(fp8_stream_merge_kernel<NT, true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a,
+                                teams, by_unit, whole)
              : launch_dependent(fp8_stream_merge_kernel<NT, false>, dim3(grid, (rows + 7) / 8), kFp8MergeThreads, 0, s, a,
                                 teams, by_unit, whole);
 }

@@ -7,9 +7,10 @@
 // Work.  A unit is 256 query rows (token, head) of a (sequence, group), as two tiles of 128, or the
 // at most 128 rows of a last one, as one tile.  A unit's products are counted in (tile, page) steps;
 // the units of the call, in order, are one flat list of steps that a persistent grid (one CTA an SM)
-// cuts into equal ranges by the units' prefix sums (causal units differ in length).  Two accumulator slots work in turn: with two tiles each page is used by slot 0 (tile 0)
-// and slot 1 (tile 1), so a page is loaded and its V converted once for 256 rows; with one tile the
-// pages alternate between the slots and the two states are added at the end.
+// cuts into equal ranges by the units' prefix sums (causal units differ in length), short units
+// staying whole (ft_cut).  Two accumulator slots work in turn: with two tiles each page is used by
+// slot 0 (tile 0) and slot 1 (tile 1), so a page is loaded and its V converted once for 256 rows;
+// with one tile the pages alternate between the slots and the two states are added at the end.
 //   * S = Q K^T: kind::f8f6f4, E4M3 from the page as it is (a tensor copy lands the 128-byte key rows
 //     in the operand's 128-byte swizzle), exact products, float32 sums.  bf16 queries are split into
 //     two parts, q = 2^k (hi + lo) with the row's largest value in [2^7, 2^8): hi is q 2^-k rounded to
@@ -24,11 +25,11 @@
 // because an issue blocks while the tensor queue is full: each waits for its operands while the other's products
 // run (one warp for both: 4.12 ms against 3.41).  An issuer is one elected lane, waits included (3.41 -> 3.06 ms).
 // P goes over in halves of 64 keys, so that the first half's product runs beside the second half's softmax.
-// Queries lie twice, so that the next unit's are loaded beside this one's pages.
+// Queries lie twice (but two tiles of bf16 rows), so that the next unit's are loaded beside this one's pages.
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
 //
-// Measured: 4,096 tokens on 64K, 64 E4M3 heads, 2.69 ms = 1.69 PFLOP/s of the products: a slot's chain (S,
+// Measured: 4,096 tokens on 64K, 32 heads of E4M3 queries, 2.69 ms = 1.69 PFLOP/s of the products: a slot's chain (S,
 // softmax, P V, rescale) is longer than the other slot's products.  8 draft tokens of 4 sequences of 512K:
 // 303 us = 5.1 TB/s of pages; the same chain, the pages' stream alone would take 230.
 // More stages of K, raw V or fp16 V, polling waits, S in halves of 64 keys and register shares between the warps
@@ -858,7 +859,8 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               it.block = p0 + j;
               const int half = it.block * kBlock + 63, last = half + 64;  // last keys of the page's halves
               it.flags = two | (last > pos0 ? kFtEdge : 0) | (half > pos1 ? 1 : 0) << kFtHide |
-                         (last > pos1 ? 2 : 0) << kFtHide | (half > pos2 ? 4 : 0) << kFtHide | (last > pos2 ? 8 : 0) << kFtHide;
+                         (last > pos1 ? 2 : 0) << kFtHide | (half > pos2 ? 4 : 0) << kFtHide |
+                         (last > pos2 ? 8 : 0) << kFtHide;
               const int ksl = page_n % kFtK, rsl = page_n % kFtRaw;
               if (!record(it) || (page_n >= kFtK && !mbar_wait_warp(&sh->k_empty[ksl], (page_n / kFtK - 1) & 1)) ||
                   (page_n >= kFtRaw && !mbar_wait_warp(&sh->raw_empty[rsl], (page_n / kFtRaw - 1) & 1))) {
@@ -990,7 +992,8 @@ __global__ void __launch_bounds__(kFtThreads, 1)
 // blockIdx.x is the unit (by_unit) or the boundary whose unit the CTA takes if it is the unit's first
 // cut, whichever is fewer; blockIdx.y the row (kSplit) or eight of them.
 template <bool kSplit>
-__global__ void __launch_bounds__(kFp8MergeThreads) fp8_tile_merge_kernel(const Fp8AttnArgs a, int per_seq, int ctas, int by_unit, int whole) {
+__global__ void __launch_bounds__(kFp8MergeThreads)
+    fp8_tile_merge_kernel(const Fp8AttnArgs a, int per_seq, int ctas, int by_unit, int whole) {
   __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -1015,7 +1018,8 @@ __global__ void __launch_bounds__(kFp8MergeThreads) fp8_tile_merge_kernel(const 
   }
   if (threadIdx.x < 32) {  // the CTAs with pages of the unit, in order
     int n = 0;
-    for (int c0 = by_unit ? static_cast<int>(((u0 + 1) * ctas - 1) / E) : x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + steps; c0 += 32) {
+    for (int c0 = by_unit ? static_cast<int>(((u0 + 1) * ctas - 1) / E) : x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + steps;
+         c0 += 32) {
       const int c = c0 + threadIdx.x;
       const int64_t a0 = ft_lo(E, c, ctas) - u0, a1 = ft_lo(E, c + 1, ctas) - u0;
       const int lo = static_cast<int>(max(a0, int64_t{0}) / t.width);
@@ -1078,7 +1082,8 @@ cudaError_t launch_fp8_tile(const Fp8AttnArgs& a, int num_sms, cudaStream_t s) {
   const int by_unit = units < ctas - 1 ? 1 : 0;
   const unsigned grid = by_unit ? static_cast<unsigned>(units) : static_cast<unsigned>(ctas - 1);
   return ctas / units >= kFp8MergeSplitParts
-             ? launch_dependent(fp8_tile_merge_kernel<true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, per_seq, ctas, by_unit, whole)
+             ? launch_dependent(fp8_tile_merge_kernel<true>, dim3(grid, rows), kFp8MergeThreads, 0, s, a, per_seq,
+                                ctas, by_unit, whole)
              : launch_dependent(fp8_tile_merge_kernel<false>, dim3(grid, (rows + 7) / 8), kFp8MergeThreads, 0, s, a, per_seq,
                                 ctas, by_unit, whole);
 }

@@ -331,8 +331,8 @@ msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cach
  * workspace: msa_workspace_bytes(MSA_OP_FP8_ATTN_WEIGHTS, ...) with weight_out, else
  * MSA_OP_FP8_ATTN; calls that can overlap need a workspace each.
  * Errors: MSA_ERR_UNSUPPORTED for num_pages * G > 2^24 (a tensor map's row coordinate) or
- * 2 * batch * ceil(q_len * Hg / 256) * max_blocks * G > 2^31 - 1 (the pages to visit); MSA_ERR_CUDA also when the driver's tensor-map encoder is
- * not available. */
+ * 2 * batch * ceil(q_len * Hg / 256) * max_blocks * G > 2^31 - 1 (the pages to visit);
+ * MSA_ERR_CUDA also when the driver's tensor-map encoder is not available. */
 msa_status_t msa_fp8_attn(const msa_config_t* cfg, const msa_fp8_cache_t* cache, const msa_batch_t* batch,
                           const void* q, int32_t q_type, int64_t q_stride, const int32_t* selection, uint16_t* out,
                           float* lse, const float* weight_in, float weight_decay, float* weight_out, void* workspace,
