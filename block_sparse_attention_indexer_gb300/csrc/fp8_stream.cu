@@ -4,11 +4,10 @@
 // Mathematics.  For row r and key j of a page with scales 2^a (K) and 2^b (V) the kernel works in
 // the log2 domain on e_j = z_j log2(e) + b, the size of the key's term of the output sum:
 //   P_j = 2^(e_j - M) in fp16,  O = sum P_j code(v_j),  l = sum over pages of 2^-b sum P_j,
-// out = O / l, lse = ln 2 (M + log2 l).  So the V scale costs no multiply per element, and the
-// fp16 rounding of P_j (relative 2^-11) is relative to what the key adds to the output.  M is an
-// integer, raised only when some e_j exceeds it by more than 8 (P_j <= 2^8 cannot overflow, and
-// below fp16's normal range P_j is 2^-14 of something at least 1/2): rescaling is exact and rare,
-// and differences of M's (shares of the blocks, merges) are exact.  Sums are float32.
+// out = O / l, lse = ln 2 (M + log2 l).  So the V scale costs no multiply per element.  M is an integer that
+// keeps P inside fp16's range and moves rarely (kFsRefSet below): P is rounded by 2^-11 of itself, or by 2^-33 of the
+// row's sum where it is small beside that.  Rescaling and differences of M's (shares of the
+// blocks, merges) are exact.  Sums are float32.
 //
 // Work.  A unit is the rows that share a page list; the (unit, page) pairs of the call are one
 // flat list, cut into equal ranges, one for each of the teams of a persistent grid (one CTA an
@@ -38,6 +37,10 @@ namespace msa {
 constexpr int kFsWarps = 4;       // consuming warps per team
 constexpr int kFsMeta = 4;        // item records (more items than the ring can hold)
 constexpr int kFsMaxBatch = 2048; // host bound on the batch
+// The reference's rule (fp8_device.cuh has what it must hold).  t is the larger of the page's largest e and the row's
+// largest z so far at the page's scale: M moves to ceil(t) - kFsRefSet when t leaves M + kFsRefMin .. M + kFp8RefMax.
+// With equal scales t only grows: M moves up only.
+constexpr float kFsRefSet = 11.f, kFsRefMin = 8.f;
 
 // NT n-tiles of 8 rows.  Teams and ring slots per team are what fits 227 KB with the merge areas.
 template <int NT>
@@ -398,6 +401,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
   const int wt = warp % kFsWarps;
   uint32_t bq[8][2];  // the queries' fragments, of one n-tile
   float fac[NT][2], m_run[NT][2], l_run[NT][2];
+  float z_top[NT][2];  // largest z of the row's keys so far, times log2(e)
   float o[NT][8][4];
   int pos[NT][2];  // positions of this lane's accumulator columns
   int unit = -1, units_done = 0, pos_min = 0;
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            m_run[nt][e] = -INFINITY;
+            m_run[nt][e] = z_top[nt][e] = -INFINITY;
             l_run[nt][e] = 0.f;
             pos[nt][e] = sparse ? pos_min : pos_min + min((8 * nt + 2 * t4 + e) / Hg, T - 1);
           }
@@ -642,8 +646,8 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
     if (lane == 0) mbar_arrive(&tm->empty[kslot]);
 
     // ---- online softmax on e = s * scale + b
-    bool grow = false;
-    float mx[NT][2];
+    bool move = false;
+    float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -662,16 +666,17 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        mx[nt][e] = m;
-        grow |= m > m_run[nt][e] + 8.f;
+        z_top[nt][e] = fmaxf(z_top[nt][e], m - it.v_exp);
+        top[nt][e] = z_top[nt][e] + it.v_exp;  // >= m
+        move |= top[nt][e] > m_run[nt][e] + kFp8RefMax || top[nt][e] < m_run[nt][e] + kFsRefMin;
       }
-    if (__any_sync(0xffffffffu, grow)) {
+    if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          if (mx[nt][e] > m_run[nt][e] + 8.f) {
-            const float mn = ceilf(mx[nt][e]), alpha = ex2(m_run[nt][e] - mn);
+          if (top[nt][e] > m_run[nt][e] + kFp8RefMax || top[nt][e] < m_run[nt][e] + kFsRefMin) {
+            const float mn = ceilf(top[nt][e]) - kFsRefSet, alpha = ex2(m_run[nt][e] - mn);
             m_run[nt][e] = mn;
             l_run[nt][e] *= alpha;
 #pragma unroll

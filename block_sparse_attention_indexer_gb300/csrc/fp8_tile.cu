@@ -2,7 +2,7 @@
 // draft tokens and prompt chunks, on the tcgen05 tensor cores.
 //
 // Mathematics: as fp8_stream.cu has it, P_j = 2^(e_j - M) with e_j = z_j log2(e) + b (2^b the page's V scale)
-// and an integer reference M that is raised only when some e_j exceeds it by more than 8.
+// and an integer reference M that keeps P inside fp16's range (kFtRefSet below).
 //
 // Work.  A unit is 256 query rows (token, head) of a (sequence, group), as two tiles of 128, or the
 // at most 128 rows of a last one, as one tile.  A unit's products are counted in (tile, page) steps;
@@ -65,8 +65,16 @@ struct alignas(16) FtItem {
   int flags;      // kFtEdge ...
 };
 // Flags of a record: some row of the sequence must not see all of the page; some row of slot s's tile must not
-// see all of its half h (bit kFtHide + 2 s + h); the unit has two tiles.
-constexpr int kFtEdge = 1, kFtTwo = 2, kFtHide = 2;
+// see all of its half h (bit kFtHide + 2 s + h); the unit has two tiles; the page's V scale is more than 2^kFtRefSlack
+// below that of an earlier page of the unit.
+constexpr int kFtEdge = 1, kFtTwo = 2, kFtHide = 2, kFtLow = 64;
+
+// The reference's rule (fp8_device.cuh has what it must hold): it goes up as in the streaming form, and down only at pages
+// marked kFtLow, where the row's sum so far at the page's scale is below 2^kFtRefMin.  So that sum is at least 2^4 wherever
+// P is rounded, and 2^6 where the row's pages have one scale: 2^-29 and 2^-31 of the row's sum.  A first place four higher,
+// as the streaming form has it, moves more references early: a prompt chunk took 2.77 ms instead of 2.69.  The mark and
+// the way down cost 1 to 2 % (121.8 -> 125.0 us for 4 drafts on 128K); asking every page 5 %.
+constexpr float kFtRefSet = 7.f, kFtRefMin = 4.f, kFtRefSlack = 2.f;
 
 struct FtShared {
   uint64_t k_full[kFtK], k_empty[kFtK], raw_full[kFtRaw], raw_empty[kFtRaw], v_full[kFtV], v_empty[kFtV];
@@ -81,6 +89,8 @@ struct FtShared {
   float q_fac[2][2 * kFtRows];  // the power of two taken out of each row (bf16)
   float other_m[kFtRows], other_l[kFtRows];
   int32_t prefix[1024 + 1];     // the units' prefix sums, where the CTA makes them itself
+  float2 ref[2 * kFtRows];      // of a row whose reference is to go down (M is -inf meanwhile): the old one, and the
+                                // row's sum at the page's scale (log2)
   int pos[2 * kFtRows];         // positions of the rows of the slots' tiles: read by the thread that wrote it
   int nan_key[2][kDim];         // first key of the unit's edge pages with a NaN code in V, per dim
 };
@@ -412,6 +422,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     // writes the unit's rows (or its partial state)
     auto finish = [&]() -> bool {
       const bool mine = st & kMine;
+      if (M == -INFINITY) M = sh->ref[row_of_slot].x;  // (a way down that no key followed)
       if (mine && !mbar_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) return false;
       const int place = st / kPlace - 1, b = unit / per_seq, row0 = (unit - b * per_seq) * 2 * kFtRows;
       const int row = row0 + (st & kTwo ? row_of_slot : r), row_end = min(row0 + 2 * kFtRows, T * Hg);
@@ -535,6 +546,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         const int row = (unit - it.seq * per_seq) * 2 * kFtRows + (st & kTwo ? row_of_slot : r);
         sh->pos[row_of_slot] = a.seq_lens[it.seq] - T + by_hg(min(row, T * Hg - 1));
         M = -INFINITY;
+        sh->ref[row_of_slot] = make_float2(M, M);
         l = 0.f;
         if (!mbar_wait_warp(&sh->q_full[uc & 1], (uc >> 1) & 1)) {
           failed = true;
@@ -552,6 +564,13 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           ++done_o;
           st |= kOther;
           continue;
+        }
+      }
+      if (it.flags & kFtLow) {
+        const float t = M + __log2f(l) + it.v_exp;
+        if (t < M + kFtRefMin) {
+          sh->ref[row_of_slot] = make_float2(M, t);
+          M = -INFINITY;
         }
       }
       // the converters' NaN marks of a page that some row of the sequence does not see whole are read
@@ -585,10 +604,15 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           }
         }
         mx = fmaf(mx, f, it.v_exp);
-        if (__any_sync(0xffffffffu, mx > M + 8.f)) {
+        if (__any_sync(0xffffffffu, mx > M + kFp8RefMax)) {
           float alpha = 1.f;
-          if (mx > M + 8.f) {
-            const float mn = ceilf(mx);
+          if (mx > M + kFp8RefMax) {
+            if (M == -INFINITY) {  // the row's first key, or the reference goes down
+              const float2 ref = sh->ref[row_of_slot];
+              M = ref.x;
+              mx = fmaxf(mx, ref.y);
+            }
+            const float mn = ceilf(mx) - kFtRefSet;
             alpha = ex2(M - mn);
             M = mn;
             l *= alpha;
@@ -825,6 +849,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           const int place = lo == 0 && hi == t.pages ? -1 : lo == 0 ? 1 : 0;
           FtItem it{u, g, -1, place, 0.f, 0.f, t.b, two};
           bool any = false;
+          float top_exp = -INFINITY;  // largest V scale of the unit's pages so far
           for (int p0 = lo; p0 < hi && !failed; p0 += 32) {
             const int p = p0 + lane;
             int row = -1;
@@ -860,7 +885,8 @@ __global__ void __launch_bounds__(kFtThreads, 1)
               const int half = it.block * kBlock + 63, last = half + 64;  // last keys of the page's halves
               it.flags = two | (last > pos0 ? kFtEdge : 0) | (half > pos1 ? 1 : 0) << kFtHide |
                          (last > pos1 ? 2 : 0) << kFtHide | (half > pos2 ? 4 : 0) << kFtHide |
-                         (last > pos2 ? 8 : 0) << kFtHide;
+                         (last > pos2 ? 8 : 0) << kFtHide | (it.v_exp < top_exp - kFtRefSlack ? kFtLow : 0);
+              top_exp = fmaxf(top_exp, it.v_exp);
               const int ksl = page_n % kFtK, rsl = page_n % kFtRaw;
               if (!record(it) || (page_n >= kFtK && !mbar_wait_warp(&sh->k_empty[ksl], (page_n / kFtK - 1) & 1)) ||
                   (page_n >= kFtRaw && !mbar_wait_warp(&sh->raw_empty[rsl], (page_n / kFtRaw - 1) & 1))) {

@@ -152,3 +152,17 @@ def _close(name, got, want, bound):
     bad = err > np.where(special, 0.0, bound)
     assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:4].tolist(),
                            float((err / np.maximum(np.where(special, 1, bound), 1e-300)).max()))
+
+
+def run_repeated(c, n, selection=None):
+    """c.run with c's sequences n times over, on the same pages (so many units that a CTA or team has all pages of
+    one): the results of the first copy and of the last."""
+    queries = "q_codes" if c.q_type == "e4m3" else "q_bf16"
+    was = {name: getattr(c, name) for name in ("B", "table", "lens", queries)}
+    c.B, c.table, c.lens = n * c.B, np.tile(c.table, (n, 1)), np.tile(c.lens, n)
+    setattr(c, queries, was[queries].repeat(n, 1, 1, 1) if queries == "q_bf16" else np.tile(was[queries], (n, 1, 1, 1)))
+    out, lse, w, err = c.upload().run(selection=None if selection is None else np.tile(selection, (n, 1, 1, 1)), weights=True)
+    for name, value in was.items():
+        setattr(c, name, value)
+    c.upload()
+    return [(out[s], lse[s], w[s], err) for s in (slice(0, c.B), slice(-c.B, None))]
