@@ -59,7 +59,7 @@ struct FsItem {
   int block;      // logical block
   int page;       // -1: nothing to attend to in this range of the unit
   int pos;        // position of the unit's first query token
-  float k_scale;  // 2^a * softmax_scale * log2(e)
+  float k_scale;  // 2^a
   float v_exp;    // b
 };
 
@@ -173,7 +173,8 @@ __device__ __forceinline__ int fs_cut(const Fp8AttnArgs& a, const int* prefix, i
   return x - e.place + (2 * e.place < pages ? 0 : pages);
 }
 
-// Eight query rows of a unit, from r0, as B fragments (f16), and the power of two taken out of each (bf16).
+// Eight query rows of a unit, from r0, as B fragments (f16), and each row's factor: softmax_scale * log2(e) times the
+// power of two taken out of it (bf16).
 __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int rows, int r0, int gq, int t4,
                                           uint32_t (&bq)[8][2], float (&fac)[2]) {
   const bool sparse = a.selection != nullptr;
@@ -230,6 +231,7 @@ __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int ro
     }
   }
   // accumulator columns of this lane: rows r0 + 2 t4, + 1
+  f *= a.scale_log2;  // (before the page's 2^a: a large and a small one of the three then meet)
   fac[0] = __shfl_sync(0xffffffffu, f, 8 * t4);
   fac[1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
 }
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
         flag_error(a.err, MSA_DEVERR_BAD_SCALE);
         it.page = -1;
       }
-      it.k_scale = exp2_int(ks - kE8m0One) * a.scale_log2;
+      it.k_scale = exp2_int(ks - kE8m0One);
       it.v_exp = static_cast<float>(vs - kE8m0One);
       if (it.block >= 0 && it.page < 0 && a.weight_out != nullptr) {  // a skipped page collects nothing
         float2* share = a.share + (static_cast<int64_t>(it.unit) * (sparse ? kTopK : a.max_blocks) + it.place) *
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float f = it.k_scale * fac[nt][e];
+        const float f = finite_factor(it.k_scale * fac[nt][e]);
         float m = -INFINITY;
 #pragma unroll
         for (int mq = 0; mq < 2; ++mq)

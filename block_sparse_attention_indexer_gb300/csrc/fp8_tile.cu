@@ -59,7 +59,7 @@ struct alignas(16) FtItem {
   int g;
   int block;      // -1: a unit (or a part of one) with no page
   int place;      // partial-state place of a cut unit; -1: the whole unit is this CTA's
-  float k_scale;  // 2^a * softmax_scale * log2(e)
+  float k_scale;  // 2^a
   float v_exp;    // b
   int seq;        // sequence
   int flags;      // kFtEdge ...
@@ -325,6 +325,12 @@ __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, u
   return m < INFINITY ? exp2_int(k) : NAN;
 }
 
+// A row's factor f, at least 2^-86: times any page's 2^a it is then a normal number (-inf, a hidden key's score, times it
+// stays -inf), and a score, at most 2^25, times 2^-86 2^40 is less than 2^-20, whatever smaller f it had.  NaN stays NaN.
+__device__ __forceinline__ float ft_factor(float f) {
+  return __uint_as_float(max(__float_as_uint(f), static_cast<uint32_t>(127 - 86) << 23));
+}
+
 // ---------------------------------------------------------------- the kernel
 
 __global__ void __launch_bounds__(kFtThreads, 1)
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
     // one-tile units so far; two tiles; place + 1 (two bits)
     constexpr int kMine = 1, kOther = 2, kTurn = 4, kShared = 8, kTwo = 16, kPlace = 32;
     int st = 0;
-    float M = -INFINITY, l = 0.f, q_fac = 1.f;
+    float M = -INFINITY, l = 0.f, q_fac = ft_factor(a.scale_log2);
     const int row_of_slot = r + ((warp >> 2) << 7);
 
     // writes the unit's rows (or its partial state)
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           failed = true;
           break;
         }
-        if (a.q_bf16) q_fac = sh->q_fac[uc & 1][st & kTwo ? row_of_slot : r];
+        if (a.q_bf16) q_fac = ft_factor(a.scale_log2 * sh->q_fac[uc & 1][st & kTwo ? row_of_slot : r]);
       }
       if (it.block < 0) continue;
       // the page's V stage, and whether its step is this slot's
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       }
       tc_fence_after();
       // positive, so that -inf times it stays -inf; NaN (a row with an infinity) stays NaN
-      const float f = it.k_scale * q_fac < 1.2e-38f ? 1.2e-38f : it.k_scale * q_fac;
+      const float f = finite_factor(it.k_scale * q_fac);
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -861,7 +867,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
                 const int kb = a.k_scale[ph], vb = a.v_scale[ph];
                 if (e8m0_ok(kb) && e8m0_ok(vb)) {
                   row = ph * kBlock;
-                  ks = exp2_int(kb - kE8m0One) * a.scale_log2;
+                  ks = exp2_int(kb - kE8m0One);
                   ve = static_cast<float>(vb - kE8m0One);
                 } else {
                   flag_error(a.err, MSA_DEVERR_BAD_SCALE);

@@ -20,7 +20,7 @@ def _bounds(case, ref, one_scale=False):
     _, lse, weight = attention_bounds(case, ref)
     dz = lse - 2.0 ** -20 - 2.0 ** -22 * np.abs(np.where(np.isfinite(ref["lse"]), ref["lse"], 0.0))
     rel = 2 * dz + 2.0 ** -20 + 2.0 ** -11
-    tiles = case.T * case.Hg > 16 and not ref["sparse"]
+    tiles = case.T * case.Hg > 16 and not ref.get("sparse")
     flush = 2.0 ** -33 if not tiles else 2.0 ** -31 if one_scale else 2.0 ** -29
     out = 2.0 ** -8 * np.abs(ref["out"]) + rel[..., None] * ref["spread"] \
         + flush * ref["keys"][..., None] * ref["v_abs"] + 1e-30
@@ -113,3 +113,14 @@ def test_many_small_probabilities_beside_one_large(T, Hg, q_type, gap):
         c.q_bf16.zero_()
         c.q_bf16[..., 0] = 1.0
     _check_repeated(c, 70, one_scale=True)
+
+
+@pytest.mark.parametrize("T,Hg", FORMS)
+def test_zero_keys_under_the_largest_scale(T, Hg):
+    need_gpu()
+    # every logit is 0, whatever the factors before it
+    c = Case(750 + T, [600, 260], T, 1, Hg, "bf16", q_scale=1e36)
+    c.k[c.k != 0x7F] = 0
+    c.ks[c.ks != 255] = 167
+    c.upload()
+    _check(c, c.run(weights=True), c.oracle())
