@@ -218,7 +218,8 @@ __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int ro
     }
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -100), 112);
+    // (at 112 the largest bf16 value becomes 2^16 - 2^8, which f16 holds)
+    const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -126), 112);
     f = m < INFINITY ? exp2_int(k) : NAN;  // (a row with an infinity gives NaN)
     const float inv = exp2_int(-k);
     if (r < rows) {

@@ -294,7 +294,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ int ft_dim8(int group) { return group < 8 ? group : group ^ 1; }
 
 // A lane's 16 bf16 dims of a row (eight lanes hold the row) as the E4M3 and E5M2 parts hi + lo = q 2^-k;
-// returns 2^k, which puts the row's largest value into [2^7, 2^8); NaN for a row with an infinity.
+// returns 2^k, which puts the row's largest value into [2^7, 2^8) (below that for rows of at most 2^-119, whose 2^-k float32
+// would not hold); NaN for a row with an infinity.
 __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, uint4& hi, uint4& lo) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float v[16], m = 0.f;
@@ -306,7 +307,7 @@ __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, u
   }
 #pragma unroll
   for (int s = 1; s < 8; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-  const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -100), 112);
+  const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -126), 120);
   const float inv = exp2_int(-k);
   uint32_t h[4], l[4];
 #pragma unroll

@@ -315,7 +315,7 @@ msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cach
  *           the heads of a token are contiguous, tokens are q_stride elements apart; pointer
  *           and stride in bytes multiples of 16, q_stride >= G * Hg * D.  bfloat16 values more
  *           than 2^13 below the largest of their row may be rounded, by at most 2^-21 of that
- *           largest value.
+ *           largest value (or by 2^-143, if that is more).
  *   weight_out  float [batch][max_blocks] or NULL: how much attention each block collected,
  *           weight_out[b][n] = weight_decay * weight_in[b][n]
  *                              + sum over t, h and the keys j of block n of e^{z_j - lse}

@@ -124,3 +124,13 @@ def test_zero_keys_under_the_largest_scale(T, Hg):
     c.ks[c.ks != 255] = 167
     c.upload()
     _check(c, c.run(weights=True), c.oracle())
+
+
+@pytest.mark.parametrize("T,Hg", FORMS)
+@pytest.mark.parametrize("size,scales", [(4e37, (99, 104)), (3e-37, (139, 144))])
+def test_bf16_queries_at_the_ends_of_their_range(T, Hg, size, scales):
+    need_gpu()
+    a = 2.0 ** (121.5 - np.mean(scales))         # K's values times this are those of the other tests
+    c = Case(760 + T, [600, 260], T, 1, Hg, "bf16", scales=scales, q_scale=size, softmax_scale=float(np.float32(0.05 / size * a)))
+    c.upload()
+    _check(c, c.run(weights=True), c.oracle())
