@@ -18,11 +18,21 @@ __device__ __forceinline__ float decayed(const Fp8AttnArgs& a, int64_t i) {
   return a.weight_in != nullptr ? a.weight_decay * a.weight_in[i] : 0.f;
 }
 
+// A row whose sum is NaN collects NaN in every block with a key that it sees, also where the share is 0, but not in a page
+// that was skipped.  Whether a 0 is such a share, and whether block n's page of KV head g is one:
+__device__ __forceinline__ bool zero_of_nan(float2 s, float2 st) { return s.x == 0.f && st.y != st.y; }
+__device__ __noinline__ bool page_counts(const Fp8AttnArgs& a, int b, int n, int g) {
+  const int page = a.block_table[static_cast<int64_t>(b) * a.max_blocks + n];
+  if (page < 0 || page >= a.num_pages) return false;
+  const int64_t ph = static_cast<int64_t>(page) * a.groups + g;
+  return e8m0_ok(a.k_scale[ph]) && e8m0_ok(a.v_scale[ph]);
+}
+
 // Dense: one warp per (sequence, block) for few shares, else one CTA of 256 threads; each thread
 // takes every 32nd (256th) of the block's shares (group, part, row), then a tree: a fixed order.
 // Rows before the block's first key have no share there.
 template <int kTeam>
-__global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const Fp8AttnArgs a, int parts) {
+__global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const __grid_constant__ Fp8AttnArgs a, int parts) {
   __shared__ float s_sum[8];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -38,13 +48,17 @@ __global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const Fp8AttnArg
     // first row that sees the block: token t with L - T + t >= 128 n
     const int r0 = max(n * kBlock - (L - T), 0) * a.heads_per_group, seen = rows - r0;
     const int all = a.groups * parts * seen;
+    unsigned nan = 0u;  // bit g: a zero of a NaN row in KV head g (at most 8)
 #pragma unroll 4
     for (int i = tid; i < all; i += kTeam) {
       const int gp = i / seen, r = r0 + i - gp * seen, g = gp / parts, p = gp - g * parts;
       const int64_t unit = static_cast<int64_t>(b) * a.groups + g;
       const float2 s = a.share[((unit * a.max_blocks + n) * parts + p) * rows + r], st = a.row_stat[unit * rows + r];
       sum += s.x != 0.f ? s.x * exp2f(s.y - st.x) * st.y : 0.f;
+      nan |= static_cast<unsigned>(zero_of_nan(s, st)) << g;
     }
+    for (; nan != 0u; nan &= nan - 1u)
+      if (page_counts(a, b, n, __ffs(nan) - 1)) sum = NAN;
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
@@ -63,8 +77,9 @@ __global__ void __launch_bounds__(256) fp8_weights_dense_kernel(const Fp8AttnArg
 // most T * H < 2^22: it fits bit 62; bit 63 marks a NaN).  Eight lanes take an entry, a head each.
 constexpr float kMassOne = 1099511627776.f;  // 2^40
 
-// The block that entry i = (b, t, g, slot) adds to (-1: none), and in its first lane what it adds.
-__device__ __forceinline__ int entry_share(const Fp8AttnArgs& a, int64_t i, bool in, float& sum) {
+// The block that entry i = (b, t, g, slot) adds to (-1: none), and in its first lane what it adds.  `nan` is set where
+// the lane's head has a zero of a NaN row (page_counts has then the last word).
+__device__ __forceinline__ int entry_share(const Fp8AttnArgs& a, int64_t i, bool in, float& sum, bool& nan) {
   const int h = threadIdx.x & 7, Hg = a.heads_per_group;
   int n = -1;
   sum = 0.f;
@@ -80,11 +95,24 @@ __device__ __forceinline__ int entry_share(const Fp8AttnArgs& a, int64_t i, bool
       for (int p = 0; p < kFp8StreamParts; ++p) s[p] = a.share[(i * kFp8StreamParts + p) * Hg + h];
 #pragma unroll
       for (int p = 0; p < kFp8StreamParts; ++p) sum += s[p].x != 0.f ? s[p].x * exp2f(s[p].y - st.x) * st.y : 0.f;
+#pragma unroll
+      for (int p = 0; p < kFp8StreamParts; ++p) nan |= zero_of_nan(s[p], st);
     }
   }
 #pragma unroll
   for (int s = 4; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
   return h == 0 ? n : -1;
+}
+// Whether entry i, which has block n, is in this thread's head a zero of a NaN row that counts as NaN.
+__device__ __noinline__ bool nan_entry(const Fp8AttnArgs& a, int64_t i, int n) {
+  const int h = threadIdx.x & 7, Hg = a.heads_per_group;
+  const int64_t unit = i / kTopK;
+  const int bt = static_cast<int>(unit / a.groups), b = bt / a.q_len, L = a.seq_lens[b];
+  if (h >= Hg || n < 0 || !length_ok(a, L) || n > (L - a.q_len + bt - b * a.q_len) / kBlock) return false;
+  bool nan = false;
+  for (int p = 0; p < kFp8StreamParts; ++p)
+    nan |= zero_of_nan(a.share[(i * kFp8StreamParts + p) * Hg + h], a.row_stat[unit * Hg + h]);
+  return nan && page_counts(a, b, n, static_cast<int>(unit % a.groups));
 }
 __device__ __forceinline__ void add_mass(unsigned long long* m, float sum) {
   if (sum != sum)
@@ -99,7 +127,7 @@ __device__ __forceinline__ float mass_value(unsigned long long m) {
 // Few entries per sequence: a CTA per (sequence, 2,048 blocks) goes through all of them and keeps its
 // blocks' sums in shared memory.
 constexpr int kMassBlocks = 2048, kMassEntries = 2048, kMassThreads = 512;
-__global__ void __launch_bounds__(kMassThreads) fp8_weights_sequence_kernel(const Fp8AttnArgs a) {
+__global__ void __launch_bounds__(kMassThreads) fp8_weights_sequence_kernel(const __grid_constant__ Fp8AttnArgs a) {
   __shared__ unsigned long long s_mass[kMassBlocks];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -107,12 +135,19 @@ __global__ void __launch_bounds__(kMassThreads) fp8_weights_sequence_kernel(cons
   for (int n = threadIdx.x; n < kMassBlocks; n += kMassThreads) s_mass[n] = 0ull;
   __syncthreads();
   const int entries = a.q_len * a.groups * kTopK;
+  bool nan = false;
   for (int e0 = 0; e0 < entries; e0 += kMassThreads / 8) {
     const int e = e0 + threadIdx.x / 8;
     float sum;
-    const int n = entry_share(a, static_cast<int64_t>(b) * entries + e, e < entries, sum);
+    const int n = entry_share(a, static_cast<int64_t>(b) * entries + e, e < entries, sum, nan);
     if (n >= n0 && n < n1) add_mass(&s_mass[n - n0], sum);
   }
+  if (nan)  // this thread's head of its entries, the zeros of NaN rows among them
+    for (int e = threadIdx.x / 8; e < entries; e += kMassThreads / 8) {
+      const int64_t i = static_cast<int64_t>(b) * entries + e;
+      const int n = a.selection[i];
+      if (n >= n0 && n < n1 && nan_entry(a, i, n)) add_mass(&s_mass[n - n0], NAN);
+    }
   __syncthreads();
   for (int n = n0 + threadIdx.x; n < n1; n += kMassThreads) {
     const int64_t i = static_cast<int64_t>(b) * a.max_blocks + n;
@@ -121,13 +156,16 @@ __global__ void __launch_bounds__(kMassThreads) fp8_weights_sequence_kernel(cons
 }
 
 // Many: the entries of all sequences over the grid, into sums in the workspace that a second kernel reads.
-__global__ void __launch_bounds__(256) fp8_weights_scatter_kernel(const Fp8AttnArgs a) {
+__global__ void __launch_bounds__(256) fp8_weights_scatter_kernel(const __grid_constant__ Fp8AttnArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t all = static_cast<int64_t>(a.batch) * a.q_len * a.groups * kTopK;
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 8;
   float sum;
-  const int n = entry_share(a, i, i < all, sum);
+  bool nan = false;
+  const int n = entry_share(a, i, i < all, sum, nan);
+  if (nan && nan_entry(a, i, a.selection[i]))
+    add_mass(a.mass + i / (static_cast<int64_t>(a.q_len) * a.groups * kTopK) * a.max_blocks + a.selection[i], NAN);
   if (n >= 0) add_mass(a.mass + i / (static_cast<int64_t>(a.q_len) * a.groups * kTopK) * a.max_blocks + n, sum);
 }
 __global__ void __launch_bounds__(256) fp8_weights_sparse_kernel(const Fp8AttnArgs a) {
