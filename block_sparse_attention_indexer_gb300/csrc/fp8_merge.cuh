@@ -14,7 +14,12 @@
 namespace msa {
 
 constexpr int kFp8MergeThreads = 256;
-constexpr float kLn2F = 0.6931471805599453f;
+
+// ln(2^M l); -inf for l = 0.  The powers of two meet first: M and log2 l alone may be far larger than their sum (V scales are in M).
+__device__ __forceinline__ float fp8_lse(float M, float l) {
+  const int e = min(static_cast<int>(__float_as_uint(l) >> 23) - 127, 127);
+  return (M + static_cast<float>(e) + log2f(l * exp2_int(-e))) * 0.6931471805599453f;
+}
 
 // Parts per unit from which a CTA's warps share a row (one sequence of 4,096 tokens, 32 parts a unit:
 // 12.9 us with one warp per row, 6.2 with eight; with two or three parts the extra warps only wait).
@@ -106,7 +111,7 @@ __device__ __forceinline__ void fp8_write_row(const Fp8AttnArgs& a, int64_t hr, 
   reinterpret_cast<uint2*>(a.out + hr * kDim)[chunk] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
   if (chunk == 0) {
-    if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * kLn2F : -INFINITY;
+    if (a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
     if (a.weight_out != nullptr) a.row_stat[si] = make_float2(any ? M : 0.f, inv);
   }
 }

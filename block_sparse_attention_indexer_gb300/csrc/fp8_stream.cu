@@ -232,7 +232,9 @@ __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int ro
     }
   }
   // accumulator columns of this lane: rows r0 + 2 t4, + 1
-  f *= a.scale_log2;  // (before the page's 2^a: a large and a small one of the three then meet)
+  // softmax_scale before the page's 2^a: a large and a small one of the three then meet.  At least 2^-100: times 2^a it is
+  // not 0 (-inf, a hidden key's score, stays -inf), and a score, at most 2^32, times 2^-100 2^40 is less than 2^-20.
+  f = __uint_as_float(max(__float_as_uint(f * a.scale_log2), static_cast<uint32_t>(127 - 100) << 23));
   fac[0] = __shfl_sync(0xffffffffu, f, 8 * t4);
   fac[1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
 }
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
           dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
           dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
           if (gq == 0) {
-            if (a.lse != nullptr) a.lse[hr] = any ? (m + log2f(l)) * kLn2F : -INFINITY;
+            if (a.lse != nullptr) a.lse[hr] = fp8_lse(m, l);
             if (a.weight_out != nullptr) a.row_stat[static_cast<int64_t>(unit) * rows + r] = make_float2(any ? m : 0.f, inv);
           }
         } else {
@@ -648,7 +650,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&tm->empty[kslot]);
 
-    // ---- online softmax on e = s * scale + b
+    // ---- online softmax on e = s * f + b (the difference with M is taken in one rounding: b and M may be large)
     bool move = false;
     float top[NT][2];
 #pragma unroll
@@ -662,13 +664,13 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             float& z = s[mq][nt][2 * half + e];
-            z = fmaf(z, f, it.v_exp);
             if (edge && key0 + 16 * mq + 8 * half + gq > pos[nt][e]) z = -INFINITY;
             m = fmaxf(m, z);
           }
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        m = fmaf(m, f, it.v_exp);  // (f is positive, or NaN)
         z_top[nt][e] = fmaxf(z_top[nt][e], m - it.v_exp);
         top[nt][e] = z_top[nt][e] + it.v_exp;  // >= m
         move |= top[nt][e] > m_run[nt][e] + kFp8RefMax || top[nt][e] < m_run[nt][e] + kFsRefMin;
@@ -696,14 +698,15 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
       float sum[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ref = m_run[nt][e] == -INFINITY ? 0.f : m_run[nt][e];
+        const float f = finite_factor(it.k_scale * fac[nt][e]);
+        const float c0 = it.v_exp - (m_run[nt][e] == -INFINITY ? 0.f : m_run[nt][e]);
         sum[e] = 0.f;
 #pragma unroll
         for (int mq = 0; mq < 2; ++mq)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             float& z = s[mq][nt][2 * half + e];
-            z = ex2(z - ref);
+            z = ex2(fmaf(z, f, c0));
             sum[e] += z;
           }
         l_run[nt][e] = fmaf(sum[e], inv_v, l_run[nt][e]);

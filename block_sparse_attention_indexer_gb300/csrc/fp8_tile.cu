@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
       }
       if (valid) {
         if (place < 0) {
-          if (a.lse != nullptr) a.lse[hr] = any ? (M + log2f(l)) * kLn2F : -INFINITY;
+          if (a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
           if (a.weight_out != nullptr)
             a.row_stat[(static_cast<int64_t>(b) * G + g) * T * Hg + row] = make_float2(any ? M : 0.f, inv);
         } else {

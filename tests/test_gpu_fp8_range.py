@@ -134,3 +134,14 @@ def test_bf16_queries_at_the_ends_of_their_range(T, Hg, size, scales):
     c = Case(760 + T, [600, 260], T, 1, Hg, "bf16", scales=scales, q_scale=size, softmax_scale=float(np.float32(0.05 / size * a)))
     c.upload()
     _check(c, c.run(weights=True), c.oracle())
+
+
+@pytest.mark.parametrize("byte", [87, 107, 147, 167])
+@pytest.mark.parametrize("T,Hg", FORMS)
+def test_lse_of_few_keys_under_any_v_scale(T, Hg, byte):
+    need_gpu()
+    # rows of 1 to some keys with logits near 0: the V scale must not show in the sum's logarithm
+    c = Case(770 + T, [T, T + 2, T + 7, T + 40], T, 4, Hg, "bf16", softmax_scale=1e-6)
+    c.vs[c.vs <= 167] = byte
+    c.upload()
+    _check(c, c.run(weights=True), c.oracle())
