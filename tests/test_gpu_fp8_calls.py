@@ -105,3 +105,31 @@ def test_append_attend_and_evict_in_one_graph(T, Hg):
         assert torch.equal(x, y)
     assert sc["count"].tolist() == [7, 1, 0, 0]
     assert all(msa.msa_read_device_error(w) == 0 for w in sc["ws"] + sd["ws"])
+
+
+@pytest.mark.parametrize("T", [40, 100])
+def test_a_long_selection_with_weights_in_a_graph(T):
+    # 1,280 and 3,200 entries a sequence: the weights in one launch, and in three behind a memset
+    need_gpu()
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+    c = Case(640 + T, [2000, 900, 0, 300], T, 2, 8).upload()
+    sel = c.selection()
+    want = c.run(selection=sel, weights=True)
+    assert_attention(c, want, c.oracle(selection=sel), weights=True)
+    sel = torch.from_numpy(sel).cuda()
+    ws = msa.alloc_workspace(msa.MSA_OP_FP8_ATTN_WEIGHTS, c.cfg, c.batch)
+    out, lse = c.buffers()
+    w = torch.zeros(c.B, c.max_blocks, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):               # (one call behind the other: the second clears what the first has read)
+            msa.msa_fp8_attn(c.cfg, c.cache, c.batch, c.dq, out, lse, ws, selection=sel, weight_out=w)
+    for _ in range(3):
+        for t in (out, lse, w):
+            t.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip((out, lse, w), want):
+            assert np.array_equal(got.double().cpu().numpy(), ref)
+    assert msa.msa_read_device_error(ws) == 0
