@@ -14,8 +14,8 @@ constexpr int kE8m0One = 127;  // the byte of scale 1
 
 __device__ __forceinline__ bool e8m0_ok(int byte) { return byte >= MSA_E8M0_MIN && byte <= MSA_E8M0_MAX; }
 
-// A factor of the scores that float32 does not hold as its largest value: a score of 0 stays 0.  (A NaN stays NaN; with
-// any other score the logit itself is beyond float32, or further from all others than the softmax can tell.)
+// A factor of the scores that float32 does not hold as its largest value: a score of 0 stays 0.  (With any other score the
+// logit itself is beyond float32, or further from all others than the softmax can tell.)
 __device__ __forceinline__ float finite_factor(float f) { return f == INFINITY ? 3.402823466e38f : f; }
 
 // The reference M of the attention kernels, in P_j = 2^(e_j - M) with e_j = z_j log2(e) + b (2^b the V scale of the

@@ -220,8 +220,8 @@ __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int ro
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     // (at 112 the largest bf16 value becomes 2^16 - 2^8, which f16 holds)
     const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14, -126), 112);
-    f = m < INFINITY ? exp2_int(k) : NAN;  // (a row with an infinity gives NaN)
-    const float inv = exp2_int(-k);
+    f = exp2_int(k);
+    const float inv = m < INFINITY ? exp2_int(-k) : NAN;  // (a row with an infinity gives NaN: its elements are)
     if (r < rows) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(FsShape<NT>::kThreads, 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        m = fmaf(m, f, it.v_exp);  // (f is positive, or NaN)
+        m = fmaf(m, f, it.v_exp);  // (f is positive)
         z_top[nt][e] = fmaxf(z_top[nt][e], m - it.v_exp);
         top[nt][e] = z_top[nt][e] + it.v_exp;  // >= m
         move |= top[nt][e] > m_run[nt][e] + kFp8RefMax || top[nt][e] < m_run[nt][e] + kFsRefMin;

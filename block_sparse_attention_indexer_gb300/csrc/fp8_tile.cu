@@ -295,7 +295,7 @@ __device__ __forceinline__ int ft_dim8(int group) { return group < 8 ? group : g
 
 // A lane's 16 bf16 dims of a row (eight lanes hold the row) as the E4M3 and E5M2 parts hi + lo = q 2^-k;
 // returns 2^k, which puts the row's largest value into [2^7, 2^8) (below that for rows of at most 2^-119, whose 2^-k float32
-// would not hold); NaN for a row with an infinity.
+// would not hold).  A row with an infinity becomes NaN.
 __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, uint4& hi, uint4& lo) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float v[16], m = 0.f;
@@ -308,7 +308,7 @@ __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, u
 #pragma unroll
   for (int s = 1; s < 8; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
   const int k = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127 - 7, -126), 120);
-  const float inv = exp2_int(-k);
+  const float inv = m < INFINITY ? exp2_int(-k) : NAN;
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -323,11 +323,11 @@ __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, u
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
-  return m < INFINITY ? exp2_int(k) : NAN;
+  return exp2_int(k);
 }
 
 // A row's factor f, at least 2^-86: times any page's 2^a it is then a normal number (-inf, a hidden key's score, times it
-// stays -inf), and a score, at most 2^25, times 2^-86 2^40 is less than 2^-20, whatever smaller f it had.  NaN stays NaN.
+// stays -inf), and a score, at most 2^25, times 2^-86 2^40 is less than 2^-20, whatever smaller f it had.
 __device__ __forceinline__ float ft_factor(float f) {
   return __uint_as_float(max(__float_as_uint(f), static_cast<uint32_t>(127 - 86) << 23));
 }
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
         break;
       }
       tc_fence_after();
-      // positive, so that -inf times it stays -inf; NaN (a row with an infinity) stays NaN
+      // positive, so that -inf times it stays -inf
       const float f = finite_factor(it.k_scale * q_fac);
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1

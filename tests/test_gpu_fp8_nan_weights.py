@@ -91,3 +91,23 @@ def test_blocks_that_underflow_collect_nan_too(T, Hg, sparse):
         for _, _, part, err in run_repeated(c, n, sel):
             assert err == msa.MSA_DEVERR_BAD_SCALE
             assert np.array_equal(np.isnan(part), np.isnan(want)) and part[0, 3] == 0
+
+
+@pytest.mark.parametrize("T,Hg", [(3, 2), (4, 4), (40, 3), (100, 3)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_nan_query_that_sees_only_a_skipped_page_is_an_empty_row(value, T, Hg):
+    need_gpu()
+    import block_sparse_attention_indexer_gb300 as msa
+    c = Case(820 + T, [129 + T // 2], T, 1, Hg, "bf16")  # the first half of the tokens sees page 0 alone
+    c.table[0, 0] = -1
+    c.q_bf16[0, 0, 0, 5] = value
+    c.q_bf16[0, T - 1, Hg - 1, 5] = value
+    c.q = c.q_bf16.double().numpy()
+    c.upload()
+    out, lse, w, err = c.run(weights=True)
+    assert err == msa.MSA_DEVERR_BAD_PAGE
+    assert not out[0, 0].any() and np.isneginf(lse[0, 0]).all()
+    assert np.isnan(out[0, T - 1, Hg - 1]).all() and np.isnan(lse[0, T - 1, Hg - 1]) and np.isnan(w[0, 1]) and w[0, 0] == 0
+    hit = np.zeros((T, Hg), bool)
+    hit[T - 1, Hg - 1] = True
+    assert np.isfinite(out[0][~hit]).all()
