@@ -11,8 +11,8 @@
 // read once into registers (four 16-element units a thread), reduced to the maximum, encoded
 // and stored as 16-byte units, so that the bytes moved are the input once and the codes once.
 // Bound by memory for prompt chunks, by one round of dependent loads (length -> table ->
-// scale) for decode steps: 65,520 tokens of 4 heads in float32 63 us = 5.3 TB/s, a decode step of 64
-// sequences 4.4 us.  Three CTAs an SM (80 registers) keep that many tiles' loads in flight; two took 76 us.
+// scale) for decode steps: 65,520 tokens of 4 heads in float32 64 us = 5.2 TB/s, a decode step of 64
+// sequences 4.3 us.  Three CTAs an SM (80 registers) keep that many tiles' loads in flight; two took 76 us.
 #include <cuda_bf16.h>
 
 #include "fp8_device.cuh"

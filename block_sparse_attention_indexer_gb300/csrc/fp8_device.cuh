@@ -25,10 +25,10 @@ __device__ __forceinline__ float finite_factor(float f) { return f == INFINITY ?
 //   * the row's sum so far at this page's scale, sum e^z 2^(b - M), may not be small while the page's keys are rounded:
 //     M moves down first.  With that sum at least 2^s, a P below fp16's normal range is off by at most 2^-25 / 2^s
 //     of the row's sum, whatever the scales of the row's other pages are (s: fp8_stream.cu, fp8_tile.cu).
-// M is an integer: moves are exact.  With Z the largest z log2(e) of the row's keys in the part of it that has its own
-// state, Z - 51 <= M <= Z + 34 for b in -40..40, hence
-//   |O| <= 2^22 keys * 448 * 2^(Z + 40 - M) < 2^122 and l <= 2^73 do not overflow, and
-//   a state whose weight 2^(M_i - M_k) underflows beside another one has less than 2^-40 of that one's sum.
+// M is an integer: moves are exact.  With Z the largest z log2(e) so far of the row's keys in the part of it that has its
+// own state, Z - 55 <= M <= Z + 34 for b in -40..40 (no P passes 2^15, and M moves to a place below the largest e), hence
+//   |O| <= 2^22 keys * 448 * 2^(Z + 40 - M) < 2^126 and l <= 2^77 do not overflow, and
+//   a state whose weight 2^(M_i - M_k) underflows beside another one has no key above 2^-37 of that one's largest.
 constexpr float kFp8RefMax = 15.f;
 
 // 2^e for -126 <= e <= 127, exact

@@ -22,9 +22,9 @@
 // unit the four warps' states are added through shared memory in two steps; a unit that the split
 // cut leaves partial states, which fp8_stream_merge_kernel adds.
 //
-// Bound by the page stream (256 B per token and KV head, read once): 64 sequences of up to 128K 700 us =
-// 6.9 TB/s; 8 of 32K 38 us with their weights (24 at the stream's rate: start, merge and weights are the rest);
-// one token of one sequence of 4,096 12 us, all of it latency.
+// Bound by the page stream (256 B per token and KV head, read once): 64 sequences of up to 128K 705 us =
+// 6.8 TB/s; 8 of up to 32K 39 us with their weights (24 at the stream's rate: start, merge and weights are the rest);
+// one token of one sequence of 4,096 11 us, all of it latency.
 #include <cuda_bf16.h>
 
 #include "fp8_device.cuh"

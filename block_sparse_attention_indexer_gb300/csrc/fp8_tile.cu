@@ -29,9 +29,9 @@
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
 //
-// Measured: 4,096 tokens on 64K, 32 heads of E4M3 queries, 2.69 ms = 1.69 PFLOP/s of the products: a slot's chain (S,
+// Measured: 4,096 tokens on 64K, 32 heads of E4M3 queries, 2.74 ms = 1.65 PFLOP/s of the products: a slot's chain (S,
 // softmax, P V, rescale) is longer than the other slot's products.  8 draft tokens of 4 sequences of 512K:
-// 303 us = 5.1 TB/s of pages; the same chain, the pages' stream alone would take 230.
+// 306 us = 5.0 TB/s of pages; the same chain, the pages' stream alone would take 230.
 // More stages of K, raw V or fp16 V, polling waits, S in halves of 64 keys and register shares between the warps
 // changed nothing or lost.  Registers spilled in the softmax's steps cost 10 % and more, so what they do not need
 // is kept in shared memory or made again where a unit ends.  Short contexts (a few pages a unit) wait for

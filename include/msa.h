@@ -328,8 +328,18 @@ msa_status_t msa_fp8_append(const msa_config_t* cfg, const msa_fp8_cache_t* cach
  * (MSA_DEVERR_BAD_SEQLEN).
  * Results do not depend on how the work is split beyond rounding, and are the same bits in
  * every call with the same arguments on one GPU.
+ * Rounding: logits, sums and lse are float32 (a logit is to stay inside its range).  A probability
+ * meets its V row in fp16: it is rounded by 2^-11 of itself or, where it is small, by at most 2^-29
+ * of its row's sum, whatever the page scales: before its rounding to bfloat16 out[d] is off by at most
+ *   (2^-11 + twice the largest error of a logit) * sum_j p_j |v_jd| + keys * 2^-29 * max_j |v_jd|.
+ * With a selection the collected weights of a sequence are summed in units of 2^-40.
  * workspace: msa_workspace_bytes(MSA_OP_FP8_ATTN_WEIGHTS, ...) with weight_out, else
- * MSA_OP_FP8_ATTN; calls that can overlap need a workspace each.
+ * MSA_OP_FP8_ATTN; calls that can overlap need a workspace each.  The first holds 8 bytes for every
+ * query row (token, head) and place: max_blocks places (the table's width, not the lengths) for
+ * dense rows, four times as many up to 16 rows of a group, or 64 for a selection, whichever is
+ * more, as the operation's size does not say which it is: 0.6 GB for 4,096 tokens of 32 heads on
+ * 544 blocks, 8.6 GB for 16,384 tokens of 64 heads on 1,024.  A long prompt collects its weights in
+ * calls of some thousand tokens each, weight_in = weight_out and weight_decay 1.
  * Errors: MSA_ERR_UNSUPPORTED for num_pages * G > 2^24 (a tensor map's row coordinate) or
  * 2 * batch * ceil(q_len * Hg / 256) * max_blocks * G > 2^31 - 1 (the pages to visit);
  * MSA_ERR_CUDA also when the driver's tensor-map encoder is not available. */
