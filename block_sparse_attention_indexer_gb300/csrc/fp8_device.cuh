@@ -14,19 +14,20 @@ constexpr int kE8m0One = 127;  // the byte of scale 1
 
 __device__ __forceinline__ bool e8m0_ok(int byte) { return byte >= MSA_E8M0_MIN && byte <= MSA_E8M0_MAX; }
 
-// A factor of the scores that float32 does not hold as its largest value: a score of 0 stays 0.  (With any other score the
-// logit itself is beyond float32, or further from all others than the softmax can tell.)
+// A factor of the scores that float32 does not hold as its largest value: a score of 0 stays 0.  (With any other
+// score the logit itself is beyond float32, or further from all others than the softmax can tell.)
 __device__ __forceinline__ float finite_factor(float f) { return f == INFINITY ? 3.402823466e38f : f; }
 
-// The reference M of the attention kernels, in P_j = 2^(e_j - M) with e_j = z_j log2(e) + b (2^b the V scale of the
-// key's page).  fp16 holds P to 11 bits from 2^-14 up and to multiples of 2^-24 below, while the sum l counts the
-// unrounded P, so M is kept where P uses that range, and follows the pages' V scales down as well as up:
+// The reference M of the attention kernels, in P_j = 2^(e_j - M) with e_j = z_j log2(e) + b (2^b the V scale of
+// the key's page).  fp16 holds P to 11 bits from 2^-14 up and to multiples of 2^-24 below, while the sum l counts
+// the unrounded P, so M is kept where P uses that range, and follows the pages' V scales down as well as up:
 //   * a P that would pass 2^kFp8RefMax moves M up;
-//   * the row's sum so far at this page's scale, sum e^z 2^(b - M), may not be small while the page's keys are rounded:
-//     M moves down first.  With that sum at least 2^s, a P below fp16's normal range is off by at most 2^-25 / 2^s
-//     of the row's sum, whatever the scales of the row's other pages are (s: fp8_stream.cu, fp8_tile.cu).
-// M is an integer: moves are exact.  With Z the largest z log2(e) so far of the row's keys in the part of it that has its
-// own state, Z - 55 <= M <= Z + 34 for b in -40..40 (no P passes 2^15, and M moves to a place below the largest e), hence
+//   * the row's sum so far at this page's scale, sum e^z 2^(b - M), may not be small while the page's keys are
+//     rounded: M moves down first.  With that sum at least 2^s, a P below fp16's normal range is off by at most
+//     2^-25 / 2^s of the row's sum, whatever the scales of its other pages are (s: fp8_stream.cu, fp8_tile.cu).
+// M is an integer: moves are exact.  With Z the largest z log2(e) so far of the row's keys in the part of it that
+// has its own state, Z - 55 <= M <= Z + 34 for b in -40..40 (no P passes 2^15, and M moves to a place below the
+// largest e), hence
 //   |O| <= 2^22 keys * 448 * 2^(Z + 40 - M) < 2^126 and l <= 2^77 do not overflow, and
 //   a state whose weight 2^(M_i - M_k) underflows beside another one has no key above 2^-37 of that one's largest.
 constexpr float kFp8RefMax = 15.f;

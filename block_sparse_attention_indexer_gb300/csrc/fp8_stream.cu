@@ -4,10 +4,10 @@
 // Mathematics.  For row r and key j of a page with scales 2^a (K) and 2^b (V) the kernel works in
 // the log2 domain on e_j = z_j log2(e) + b, the size of the key's term of the output sum:
 //   P_j = 2^(e_j - M) in fp16,  O = sum P_j code(v_j),  l = sum over pages of 2^-b sum P_j,
-// out = O / l, lse = ln 2 (M + log2 l).  So the V scale costs no multiply per element.  M is an integer that
-// keeps P inside fp16's range and moves rarely (kFsRefSet below): P is rounded by 2^-11 of itself, or by 2^-33 of the
-// row's sum where it is small beside that.  Rescaling and differences of M's (shares of the
-// blocks, merges) are exact.  Sums are float32.
+// out = O / l, lse = ln 2 (M + log2 l).  So the V scale costs no multiply per element.  M is an
+// integer that keeps P inside fp16's range and moves rarely (kFsRefSet below): P is rounded by 2^-11
+// of itself, or by 2^-33 of the row's sum where it is small beside that.  Rescaling and differences
+// of M's (shares of the blocks, merges) are exact.  Sums are float32.
 //
 // Work.  A unit is the rows that share a page list; the (unit, page) pairs of the call are one
 // flat list, cut into equal ranges, one for each of the teams of a persistent grid (one CTA an
@@ -231,10 +231,10 @@ __device__ __forceinline__ void fs_load_q(const Fp8AttnArgs& a, int unit, int ro
       }
     }
   }
-  // accumulator columns of this lane: rows r0 + 2 t4, + 1
-  // softmax_scale before the page's 2^a: a large and a small one of the three then meet.  At least 2^-100: times 2^a it is
-  // not 0 (-inf, a hidden key's score, stays -inf), and a score, at most 2^32, times 2^-100 2^40 is less than 2^-20.
+  // softmax_scale before the page's 2^a: a large and a small one of the three then meet.  At least 2^-100: times 2^a it
+  // is not 0 (-inf, a hidden key's score, stays -inf), and a score, at most 2^32, times 2^-100 2^40 is below 2^-20.
   f = __uint_as_float(max(__float_as_uint(f * a.scale_log2), static_cast<uint32_t>(127 - 100) << 23));
+  // accumulator columns of this lane: rows r0 + 2 t4, + 1
   fac[0] = __shfl_sync(0xffffffffu, f, 8 * t4);
   fac[1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
 }

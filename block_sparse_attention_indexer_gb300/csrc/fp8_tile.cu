@@ -69,11 +69,12 @@ struct alignas(16) FtItem {
 // below that of an earlier page of the unit.
 constexpr int kFtEdge = 1, kFtTwo = 2, kFtHide = 2, kFtLow = 64;
 
-// The reference's rule (fp8_device.cuh has what it must hold): it goes up as in the streaming form, and down only at pages
-// marked kFtLow, where the row's sum so far at the page's scale is below 2^kFtRefMin.  So that sum is at least 2^4 wherever
-// P is rounded, and 2^6 where the row's pages have one scale: 2^-29 and 2^-31 of the row's sum.  A first place four higher,
-// as the streaming form has it, moves more references early: a prompt chunk took 2.77 ms instead of 2.69.  The mark and
-// the way down cost 1 to 2 % (121.8 -> 125.0 us for 4 drafts on 128K); asking every page 5 %.
+// The reference's rule (fp8_device.cuh has what it must hold): it goes up where a P would pass 2^kFp8RefMax, and down
+// only at pages marked kFtLow, where the row's sum so far at the page's scale is below 2^kFtRefMin.  So that sum is at
+// least 2^4 wherever P is rounded, and 2^6 where the row's pages have one scale: 2^-29 and 2^-31 of the row's sum.  A
+// first place four higher, as the streaming form has it, moves more references early: a prompt chunk took 2.77 ms
+// instead of 2.69.  The mark and the way down cost 1 to 2 % (4 x 128K with 8 draft tokens 121.8 -> 124.5 us); asking
+// every page 5 %.
 constexpr float kFtRefSet = 7.f, kFtRefMin = 4.f, kFtRefSlack = 2.f;
 
 struct FtShared {
@@ -294,8 +295,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ int ft_dim8(int group) { return group < 8 ? group : group ^ 1; }
 
 // A lane's 16 bf16 dims of a row (eight lanes hold the row) as the E4M3 and E5M2 parts hi + lo = q 2^-k;
-// returns 2^k, which puts the row's largest value into [2^7, 2^8) (below that for rows of at most 2^-119, whose 2^-k float32
-// would not hold).  A row with an infinity becomes NaN.
+// returns 2^k, which puts the row's largest value into [2^7, 2^8) (below that for rows of at most 2^-119, whose
+// 2^-k float32 would not hold).  A row with an infinity becomes NaN.
 __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, uint4& hi, uint4& lo) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float v[16], m = 0.f;
@@ -326,8 +327,8 @@ __device__ __forceinline__ float ft_split_bf16(const uint4& a, const uint4& b, u
   return exp2_int(k);
 }
 
-// A row's factor f, at least 2^-86: times any page's 2^a it is then a normal number (-inf, a hidden key's score, times it
-// stays -inf), and a score, at most 2^25, times 2^-86 2^40 is less than 2^-20, whatever smaller f it had.
+// A row's factor f, at least 2^-86: times any page's 2^a it is then a normal number (-inf, a hidden key's score,
+// times it stays -inf), and a score, at most 2^25, times 2^-86 2^40 is below 2^-20, whatever smaller f it had.
 __device__ __forceinline__ float ft_factor(float f) {
   return __uint_as_float(max(__float_as_uint(f), static_cast<uint32_t>(127 - 86) << 23));
 }
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kFtThreads, 1)
           continue;
         }
       }
-      if (it.flags & kFtLow) {
+      if (it.flags & kFtLow) {  // (a row sets its reference aside here; it goes down with the row's next score)
         const float t = M + __log2f(l) + it.v_exp;
         if (t < M + kFtRefMin) {
           sh->ref[row_of_slot] = make_float2(M, t);
