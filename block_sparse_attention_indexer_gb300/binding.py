@@ -29,7 +29,9 @@ _lib = ctypes.CDLL(LIB_PATH)
 MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_CUDA = range(5)
 MSA_OP_INDEXER_SCORES, MSA_OP_SELECT_BLOCKS, MSA_OP_SPARSE_ATTN, MSA_OP_DECODE = range(4)
 MSA_OP_FP8_APPEND, MSA_OP_FP8_ATTN, MSA_OP_FP8_ATTN_WEIGHTS, MSA_OP_EVICT = range(4, 8)
+MSA_OP_PROMPT_ATTN = 8
 MSA_DEVERR_BAD_PAGE, MSA_DEVERR_BAD_SEQLEN, MSA_DEVERR_TIMEOUT, MSA_DEVERR_BAD_SCALE = 0x1, 0x2, 0x4, 0x8
+MSA_DEVERR_NO_PAGE, MSA_DEVERR_BAD_PARENT = 0x10, 0x20
 MSA_SCORE_MAX, MSA_SCORE_LSE = 0, 1
 MSA_TYPE_F32, MSA_TYPE_BF16, MSA_TYPE_E4M3 = range(3)
 MSA_E8M0_MIN, MSA_E8M0_MAX = 87, 167
@@ -58,9 +60,24 @@ class _Batch(ctypes.Structure):
                 ("max_blocks", ctypes.c_int32), ("q_len", ctypes.c_int32)]
 
 
+class _Packed(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("q_tokens", ctypes.c_int64), ("k_tokens", ctypes.c_int64)]
+
+
+class _PageBuffer(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("token_bytes", ctypes.c_int32)]
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("refs_out", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("buffers", ctypes.POINTER(_PageBuffer)), ("num_buffers", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _CP, _CC, _CB = ctypes.POINTER(_Config), ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
 _CF = ctypes.POINTER(_Fp8Cache)
+_CK, _CG = ctypes.POINTER(_Packed), ctypes.POINTER(_PagePool)
 _SIGS = {
     "msa_abi_version": (ctypes.c_int32, []),
     "msa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -81,6 +98,14 @@ _SIGS = {
                                     _P, _P, ctypes.c_size_t, _P]),
     "msa_evict_blocks": (ctypes.c_int, [_CB, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P,
                                         _P, ctypes.c_size_t, _P]),
+    "msa_prompt_workspace_bytes": (ctypes.c_size_t, [_CP, _CK]),
+    "msa_prompt_attn": (ctypes.c_int, [_CP, _CK, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P,
+                                       ctypes.c_size_t, _P]),
+    "msa_page_workspace_bytes": (ctypes.c_size_t, [_CG, ctypes.c_int32]),
+    "msa_extend_pages": (ctypes.c_int, [_CG, _CB, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "msa_fork_pages": (ctypes.c_int, [_CG, _CB, _P, ctypes.c_int32, _P, _P, _P, ctypes.c_size_t, _P]),
+    "msa_free_pages": (ctypes.c_int, [_CG, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "msa_compact_pages": (ctypes.c_int, [_CG, _CB, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "msa_sparse_attn_decode_noalloc": (ctypes.c_int, [_CP, _CC, _CB, _P, _P, _P, _P, _P]),
     "msa_noalloc_read_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _P]),
     "msa_test_indexer_stall": (ctypes.c_int, [_CP, _CC, _CB, _P, _P, _P, ctypes.c_size_t, ctypes.c_uint32, _P]),
@@ -330,6 +355,73 @@ class Batch:
         return self.block_table.shape[1]
 
 
+@dataclasses.dataclass
+class Packed:
+    """Packed prompts: sequence b's query tokens are cu_q[b] .. cu_q[b + 1] - 1 of a list of q_tokens, its keys
+    cu_k[b] .. cu_k[b + 1] - 1 of one of k_tokens."""
+    cu_q: torch.Tensor            # int32 [B + 1] on the device
+    cu_k: torch.Tensor            # int32 [B + 1] on the device (cu_q itself where every token is both)
+    q_tokens: int
+    k_tokens: int
+
+    def c(self):
+        n = self.cu_q.numel()
+        if self.cu_q.dim() != 1 or n < 1:
+            raise ValueError(f"cu_q must be [batch + 1], got {tuple(self.cu_q.shape)}")
+        dev = _on(self.cu_q, "cu_q")
+        return ctypes.byref(_Packed(_at(self.cu_q, (n,), torch.int32, dev, "cu_q"),
+                                    _at(self.cu_k, (n,), torch.int32, dev, "cu_k"), n - 1, self.q_tokens, self.k_tokens))
+
+    @property
+    def batch(self):
+        return self.cu_q.numel() - 1
+
+
+class PagePool:
+    """A pool of pages: refs (int32 [num_pages] on the device, 0 for a free page), and the caches
+    whose pools hold the pages (of every layer that goes by the same block table)."""
+
+    def __init__(self, caches=(), refs: Optional[torch.Tensor] = None, num_pages: Optional[int] = None, device=None):
+        self.caches = tuple(caches)
+        counts = {c.num_pages for c in self.caches} | ({int(num_pages)} if num_pages is not None else set())
+        if refs is None:
+            if len(counts) != 1:
+                raise ValueError(f"the pool needs one number of pages, got {sorted(counts)}")
+            where = self.caches[0].tensors()[0].device if device is None and self.caches else device or "cuda"
+            refs = torch.zeros(counts.pop(), dtype=torch.int32, device=where)
+        elif counts - {refs.numel()}:
+            raise ValueError(f"refs counts {refs.numel()} pages, the caches have {sorted(counts)}")
+        if refs.dim() != 1:
+            raise ValueError(f"refs must be [num_pages], got {tuple(refs.shape)}")
+        self.refs, self.num_pages, self.device_index = refs, refs.numel(), _on(refs, "refs")
+        _at(refs, (self.num_pages,), torch.int32, self.device_index, "refs")
+        buffers = []
+        for c in self.caches:
+            for t in c.tensors():
+                if t.dtype != torch.uint8 or t.get_device() != self.device_index or not t.is_contiguous():
+                    raise ValueError("the caches' pools must be contiguous uint8 tensors on the device of refs")
+                page = t.numel() // self.num_pages if self.num_pages else 0
+                # [P, groups, block, bytes] or [P, block, bytes]; FP8 scales [P, groups] belong to whole pages
+                buffers.append(_PageBuffer(t.data_ptr(), page, t.shape[-1] if t.dim() > 2 else 0))
+        self._buffers = (_PageBuffer * max(1, len(buffers)))(*buffers)
+        self._count = len(buffers)
+        self._c = _PagePool(refs.data_ptr(), refs.data_ptr(), self.num_pages, self._buffers, self._count)
+
+    def c(self, refs_out: Optional[torch.Tensor] = None):
+        """The C struct for a call that leaves the new counts in refs_out (None: in refs)."""
+        if refs_out is None:
+            return ctypes.byref(self._c)
+        out = _at(refs_out, (self.num_pages,), torch.int32, self.device_index, "refs_out")
+        return ctypes.byref(_PagePool(self._c.refs, out, self.num_pages, self._buffers, self._count))
+
+
+def _pool_batch(pool: PagePool, batch: Batch) -> int:
+    dev = _batch_device(batch)
+    if pool.device_index != dev:
+        raise ValueError(f"the page pool is on CUDA device {pool.device_index}, the block table on {dev}")
+    return dev
+
+
 # ---------------------------------------------------------------------------- entry points
 def msa_abi_version() -> int:
     return _lib.msa_abi_version()
@@ -339,10 +431,24 @@ def msa_workspace_bytes(op: int, cfg: Config, batch: Batch) -> int:
     return int(_lib.msa_workspace_bytes(op, cfg.c(), batch.c()))
 
 
-def alloc_workspace(op: int, cfg: Config, batch: Batch, device="cuda") -> torch.Tensor:
-    """Zero-filled workspace of the size `op` needs (the zero fill clears the error word)."""
-    n = max(msa_workspace_bytes(op, cfg, batch), 256)
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+def alloc_workspace(op: int, cfg: Config, batch, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of the size `op` needs (the zero fill clears the error word).
+    `batch` is a Batch, or for MSA_OP_PROMPT_ATTN a Packed."""
+    size = msa_prompt_workspace_bytes(cfg, batch) if isinstance(batch, Packed) else msa_workspace_bytes(op, cfg, batch)
+    return torch.zeros(max(size, 256), dtype=torch.uint8, device=device)
+
+
+def msa_prompt_workspace_bytes(cfg: Config, packed: Packed) -> int:
+    return int(_lib.msa_prompt_workspace_bytes(cfg.c(), packed.c()))
+
+
+def msa_page_workspace_bytes(pool: PagePool, rows: int) -> int:
+    return int(_lib.msa_page_workspace_bytes(pool.c(), rows))
+
+
+def alloc_page_workspace(pool: PagePool, rows: int) -> torch.Tensor:
+    """Zero-filled workspace of the page operators for calls of up to `rows` sequences (or children)."""
+    return torch.zeros(max(msa_page_workspace_bytes(pool, rows), 256), dtype=torch.uint8, device=pool.refs.device)
 
 
 def msa_nvfp4_insert(x: torch.Tensor, slots: torch.Tensor, data: torch.Tensor, scale: torch.Tensor,
@@ -509,6 +615,93 @@ def msa_evict_blocks(batch: Batch, weight: torch.Tensor, budget: int, keep_first
             budget, keep_first, keep_last, _at(table_out, table, i32, dev, "table_out"),
             _at(seq_lens_out, rows, i32, dev, "seq_lens_out"), _at(weight_out, table, f32, dev, "weight_out"),
             _at(freed, table, i32, dev, "freed"), _at(freed_count, rows, i32, dev, "freed_count"),
+            *_space(workspace, dev))
+
+
+def _flat_rows(t: torch.Tensor, shape, dev: int, name: str):
+    """(pointer, token stride in elements) of a bfloat16 [tokens, heads, dim] tensor whose heads are contiguous
+    within a token (a slice of the heads of wider rows is: no copy is made)."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on CUDA device {dev} like cu_q, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    tokens, heads, dim = shape
+    st, sh, sd = t.stride()
+    if tokens and (sd != 1 or (heads > 1 and sh != dim)):
+        raise ValueError(f"{name} must hold each token's heads contiguously, got strides {t.stride()}")
+    return t.data_ptr(), st if tokens > 1 else heads * dim
+
+
+def msa_prompt_attn(cfg: Config, packed: Packed, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                    lse: Optional[torch.Tensor], workspace: torch.Tensor, stream=None):
+    """Causal attention of packed prompts over their own keys and values (include/msa.h).
+    q: bfloat16 [q_tokens, H, 128]; k, v: bfloat16 [k_tokens, G, 128]; each contiguous or a slice of
+    the heads of a fused projection's rows; out: bfloat16 [q_tokens, H, 128]; lse: float32
+    [q_tokens, H] or None.  workspace: alloc_workspace(MSA_OP_PROMPT_ATTN, cfg, packed)."""
+    dev = _on(packed.cu_q, "cu_q")
+    rows = (packed.q_tokens, cfg.num_heads, cfg.head_dim)
+    keys = (packed.k_tokens, cfg.num_kv_groups, cfg.head_dim)
+    _launch("msa_prompt_attn", _lib.msa_prompt_attn, dev, stream, cfg.c(), packed.c(), *_flat_rows(q, rows, dev, "q"),
+            *_flat_rows(k, keys, dev, "k"), *_flat_rows(v, keys, dev, "v"), _at(out, rows, torch.bfloat16, dev, "out"),
+            _at(lse, rows[:2], torch.float32, dev, "lse"), *_space(workspace, dev))
+
+
+def msa_extend_pages(pool: PagePool, batch: Batch, workspace: torch.Tensor, new_tokens: Optional[torch.Tensor] = None,
+                     table_out: Optional[torch.Tensor] = None, seq_lens_out: Optional[torch.Tensor] = None,
+                     refs_out: Optional[torch.Tensor] = None, stream=None):
+    """Pages for the next new_tokens (int32 [B]; None: batch.q_len for every sequence that has tokens) of
+    every sequence (include/msa.h), in place unless other outputs are given.  workspace:
+    alloc_page_workspace(pool, B)."""
+    dev = _pool_batch(pool, batch)
+    table, i32 = batch.block_table.shape, torch.int32
+    to = batch.block_table if table_out is None else table_out
+    lens = batch.seq_lens if seq_lens_out is None else seq_lens_out
+    _launch("msa_extend_pages", _lib.msa_extend_pages, dev, stream, pool.c(refs_out), batch.c(),
+            _at(new_tokens, table[:1], i32, dev, "new_tokens"), _at(to, table, i32, dev, "table_out"),
+            _at(lens, table[:1], i32, dev, "seq_lens_out"), *_space(workspace, dev))
+
+
+def msa_fork_pages(pool: PagePool, batch: Batch, parents: torch.Tensor, table_out: torch.Tensor,
+                   seq_lens_out: torch.Tensor, workspace: torch.Tensor, refs_out: Optional[torch.Tensor] = None,
+                   stream=None):
+    """Sequences that go on from batch's sequences parents (int32 [children]; -1: empty): table_out [children,
+    max_blocks] and seq_lens_out [children] (include/msa.h).  workspace: alloc_page_workspace(pool, children)."""
+    dev = _pool_batch(pool, batch)
+    if parents.dim() != 1:
+        raise ValueError(f"parents must be [children], got {tuple(parents.shape)}")
+    n, i32 = parents.shape[0], torch.int32
+    _launch("msa_fork_pages", _lib.msa_fork_pages, dev, stream, pool.c(refs_out), batch.c(),
+            _at(parents, (n,), i32, dev, "parents"), n, _at(table_out, (n, batch.max_blocks), i32, dev, "table_out"),
+            _at(seq_lens_out, (n,), i32, dev, "seq_lens_out"), *_space(workspace, dev))
+
+
+def msa_free_pages(pool: PagePool, pages: torch.Tensor, workspace: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                   refs_out: Optional[torch.Tensor] = None, stream=None):
+    """One reference to every listed page given back (include/msa.h): the first counts[r] entries of each
+    row of pages (int32 [rows, width]; counts int32 [rows], None: all), msa_evict_blocks' freed and
+    freed_count for example.  workspace: alloc_page_workspace(pool, 0)."""
+    dev = pool.device_index
+    if pages.dim() != 2:
+        raise ValueError(f"pages must be [rows, width], got {tuple(pages.shape)}")
+    rows, width = pages.shape
+    _launch("msa_free_pages", _lib.msa_free_pages, dev, stream, pool.c(refs_out),
+            _at(pages, (rows, width), torch.int32, dev, "pages"), _at(counts, (rows,), torch.int32, dev, "counts"), rows,
+            width, *_space(workspace, dev))
+
+
+def msa_compact_pages(pool: PagePool, batch: Batch, page_map: torch.Tensor, live_count: torch.Tensor,
+                      workspace: torch.Tensor, table_out: Optional[torch.Tensor] = None,
+                      refs_out: Optional[torch.Tensor] = None, stream=None):
+    """The pages in use moved to the lowest numbers, the block table renamed in place or into table_out
+    (include/msa.h).  page_map: int32 [num_pages], every page's new number; live_count: int32 [1].
+    workspace: alloc_page_workspace(pool, 0)."""
+    dev = _pool_batch(pool, batch)
+    to, i32 = batch.block_table if table_out is None else table_out, torch.int32
+    _launch("msa_compact_pages", _lib.msa_compact_pages, dev, stream, pool.c(refs_out), batch.c(),
+            _at(to, batch.block_table.shape, i32, dev, "table_out"),
+            _at(page_map, (pool.num_pages,), i32, dev, "page_map"), _at(live_count, (1,), i32, dev, "live_count"),
             *_space(workspace, dev))
 
 

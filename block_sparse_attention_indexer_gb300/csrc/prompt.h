@@ -1,0 +1,26 @@
+// Kernel arguments and launcher of the packed prompt attention, shared between the C-ABI layer
+// (api_prompt.cu) and prompt_attn.cu.  Every pointer is device memory.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace msa {
+
+struct PromptArgs {
+  const int32_t* cu_q;  // [batch + 1]
+  const int32_t* cu_k;
+  int32_t batch, q_tokens, k_tokens, groups, heads_per_group;
+  const uint16_t* q;    // bf16 [q_tokens][G * Hg][128], tokens q_stride elements apart
+  const uint16_t* k;    // bf16 [k_tokens][G][128]
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride;
+  uint16_t* out;        // bf16 [q_tokens][G * Hg][128]
+  float* lse;           // [q_tokens][G * Hg] or null
+  float scale_log2;     // softmax_scale * log2(e)
+  uint32_t* err;
+};
+
+cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s);
+
+}  // namespace msa

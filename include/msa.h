@@ -72,6 +72,8 @@ typedef enum {
 #define MSA_DEVERR_BAD_SEQLEN 0x2u  /* seq_len < q_len (but > 0), or > max_blocks*128 */
 #define MSA_DEVERR_TIMEOUT 0x4u     /* a bounded wait inside a kernel gave up */
 #define MSA_DEVERR_BAD_SCALE 0x8u   /* an FP8 page scale outside MSA_E8M0_MIN..MSA_E8M0_MAX */
+#define MSA_DEVERR_NO_PAGE 0x10u    /* the page pool has fewer free pages than a call needs */
+#define MSA_DEVERR_BAD_PARENT 0x20u /* msa_fork_pages: a parent outside [-1, batch) */
 
 /* Block-score reduction over the visible keys of a block ("MiniMax M3 x vLLM：百万 token
  * 多模态推理的 Day-0 部署", §Prefill 执行 step 2: a block-level rule such as max or
@@ -130,7 +132,8 @@ typedef enum {
   MSA_OP_FP8_APPEND = 4,
   MSA_OP_FP8_ATTN = 5,          /* msa_fp8_attn without weight_out */
   MSA_OP_FP8_ATTN_WEIGHTS = 6,  /* msa_fp8_attn with weight_out (or without) */
-  MSA_OP_EVICT = 7
+  MSA_OP_EVICT = 7,
+  MSA_OP_PROMPT_ATTN = 8        /* sized by msa_prompt_workspace_bytes, not by msa_workspace_bytes */
 } msa_op_t;
 
 /* Element types of the arguments that come in more than one. */
@@ -157,6 +160,38 @@ typedef struct {
   uint8_t* v_scale;
   int64_t num_pages;
 } msa_fp8_cache_t;
+
+/* Packed prompts: the query tokens of all sequences in one list and their keys in another
+ * (device pointers; sizes on the host).  Sequence b has the query tokens cu_q[b] ..
+ * cu_q[b + 1] - 1 and the keys cu_k[b] .. cu_k[b + 1] - 1. */
+typedef struct {
+  const int32_t* cu_q; /* [batch + 1] */
+  const int32_t* cu_k; /* [batch + 1] */
+  int32_t batch;       /* 0..2048 */
+  int64_t q_tokens;    /* tokens of the query list (those behind the last sequence belong to none) */
+  int64_t k_tokens;    /* tokens of the key list */
+} msa_packed_t;
+
+/* One buffer of a page pool (device): page p's bytes start at data + p * page_bytes.  With
+ * token_bytes > 0 a page is page_bytes / (128 * token_bytes) runs of 128 tokens of token_bytes
+ * each (a run is a KV head); with token_bytes = 0 nothing in it belongs to single tokens. */
+typedef struct {
+  void* data;
+  int64_t page_bytes;
+  int32_t token_bytes;
+} msa_page_buffer_t;
+
+/* A pool of pages that block tables share: how many references each page has (0: free), and
+ * the buffers that hold the pages, of as many caches (layers, K and V, codes and scales) as go
+ * by the same page numbers.  An operation reads refs and leaves the new counts in refs_out,
+ * which may be refs. */
+typedef struct {
+  const int32_t* refs;             /* device int32 [num_pages], 16-byte aligned */
+  int32_t* refs_out;               /* device int32 [num_pages], 16-byte aligned */
+  int64_t num_pages;               /* 1 .. 2^27 */
+  const msa_page_buffer_t* buffers; /* HOST array, read during the call */
+  int32_t num_buffers;             /* 0 .. 4096 */
+} msa_page_pool_t;
 
 /* ABI version of the loaded library (MSA_ABI_VERSION). */
 int32_t msa_abi_version(void);
@@ -370,6 +405,101 @@ msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int
                               int32_t keep_last, int32_t* table_out, int32_t* seq_lens_out, float* weight_out,
                               int32_t* freed, int32_t* freed_count, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/* Causal attention of packed prompts over their own bfloat16 keys and values, before (or
+ * without) their way into pages: whole prompts, chunks of them behind keys that are still at
+ * hand (cu_k longer than cu_q), single new tokens.
+ * Query token t of sequence b, of Lq = cu_q[b+1] - cu_q[b], sits at position Lk - Lq + t of its
+ * Lk = cu_k[b+1] - cu_k[b] keys, and head h attends to the keys j <= that position of KV head
+ * h / Hg with logits z_j = (q . k_j) * softmax_scale:
+ *   out  = sum_j e^{z_j - lse} v_j   bfloat16 [q_tokens][G*Hg][D]
+ *   lse  = ln sum_j e^{z_j}          float [q_tokens][G*Hg], may be NULL
+ * A row with no key (Lk < Lq: the first Lq - Lk tokens) gives out 0 and lse -inf.  Rows of
+ * tokens that belong to no sequence are left as they are.
+ *   q        bfloat16 [q_tokens][G*Hg][D], k, v bfloat16 [k_tokens][G][D]: the heads of a token are
+ *            contiguous, tokens are q_stride (k_stride, v_stride) elements apart, so that slices of
+ *            one fused projection's rows need no copy.  Pointers and strides in bytes are multiples
+ *            of 16, strides at least a token's elements.  out may not overlap an input.
+ * Keys that a row does not see (later ones, other sequences') do not touch it, whatever they
+ * hold.  A NaN or an infinity in q or k makes the rows whose logits it reaches what float
+ * arithmetic makes of them; one in v the results of the rows that see it, in its dim.
+ * cu_q and cu_k must not decrease, start below 0 or end past q_tokens and k_tokens: otherwise
+ * MSA_DEVERR_BAD_SEQLEN is set and nothing is written.
+ * Rounding: logits, sums and lse are float32; a probability meets its V row as bfloat16 (rounded by
+ * at most 2^-8 of itself, the sum of the probabilities is taken before that).  The same arguments give the
+ * same bits in every call on one GPU.
+ * workspace: msa_prompt_workspace_bytes(...); calls that can overlap need one each.
+ * Errors: MSA_ERR_UNSUPPORTED for q_tokens or k_tokens above 2^28, or where the call's pairs of
+ * 128 query rows and 128 keys cannot be counted in 31 bits: 2 * (q_tokens / (2 * floor(128 / Hg)) + batch) *
+ * ceil(k_tokens / 128) > 2^31 - 1.  MSA_ERR_CUDA also when the driver's tensor-map encoder is
+ * not available. */
+size_t msa_prompt_workspace_bytes(const msa_config_t* cfg, const msa_packed_t* packed);
+msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride, uint16_t* out,
+                             float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The life of a pool's pages, on the device and without a look at them by the host: sequences
+ * take pages for new tokens, go on from one another, give pages back, and the pages in use move
+ * together.  Whoever holds a page of a block table holds a reference to it; a page is free when
+ * its count is 0.  Pages are handed out from the lowest free number up, so that every result
+ * is determined by the arguments.  A last block that is not full belongs to one sequence.
+ * Overlapping arrays are MSA_ERR_INVALID_ARG, except an output that is its own input; the
+ * buffers of a pool may not overlap.  A pool's calls change it one after another: on one
+ * stream, or ordered by events.
+ * workspace: msa_page_workspace_bytes(pool, rows), rows being the batch of the call (the
+ * children of a fork); calls that can overlap need one each. */
+size_t msa_page_workspace_bytes(const msa_page_pool_t* pool, int32_t rows);
+
+/* Pages for new tokens.  Sequence b grows from L = seq_lens[b] by n = new_tokens[b] tokens
+ * (new_tokens NULL: by batch->q_len, sequences of length 0 by none):
+ *   seq_lens_out[b]  L + n
+ *   table_out[b]     the row of block_table; blocks ceil(L/128) .. ceil((L+n)/128) - 1 get free pages,
+ *                    which then have one reference
+ * The i-th new block of the call, by sequence and then by block, gets the i-th free page.  When
+ * the blocks that the sequences 0 .. b need are more than the free pages there are, a sequence b that needs
+ * any stays as it was (MSA_DEVERR_NO_PAGE), and so does one with n < 0, L < 0 or L + n > max_blocks * 128
+ * (MSA_DEVERR_BAD_SEQLEN).  table_out and seq_lens_out may be the inputs. */
+msa_status_t msa_extend_pages(const msa_page_pool_t* pool, const msa_batch_t* batch, const int32_t* new_tokens,
+                              int32_t* table_out, int32_t* seq_lens_out, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Sequences that go on from others (samples of one prompt, beams).  Child i gets the length
+ * of sequence parents[i] (int32 [children], 0..2048 of them; -1: an empty child, length 0), and
+ *   table_out     int32 [children][max_blocks]: the parent's full blocks, whose pages have one reference
+ *                 more per child, then, if the parent's last block is not full, a free page with one
+ *                 reference and a copy of that block's tokens in every buffer of the pool (of a buffer
+ *                 without tokens the whole page); -1 behind
+ *   seq_lens_out  int32 [children]
+ * The i-th child that needs a page gets the i-th free one; one that finds none is cut to its
+ * full blocks (MSA_DEVERR_NO_PAGE).  Rows of the new pages behind the parent's tokens are left as they are.
+ * A parent out of range (MSA_DEVERR_BAD_PARENT) or with a length below 0 or above max_blocks * 128
+ * (MSA_DEVERR_BAD_SEQLEN) gives an empty child; a table entry outside the pool (MSA_DEVERR_BAD_PAGE)
+ * becomes -1.  table_out and seq_lens_out may not overlap the inputs. */
+msa_status_t msa_fork_pages(const msa_page_pool_t* pool, const msa_batch_t* batch, const int32_t* parents,
+                            int32_t children, int32_t* table_out, int32_t* seq_lens_out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* References given back: one for every entry of pages (int32 [rows][width]; the first counts[r]
+ * entries of row r, all with counts NULL), msa_evict_blocks' freed and freed_count for example, or the
+ * blocks of finished sequences.  Entries of -1 are passed over.  An entry outside the pool, or
+ * one reference more than a page has (its count stays 0), sets MSA_DEVERR_BAD_PAGE; a count
+ * below 0 or above width sets MSA_DEVERR_BAD_SEQLEN and its row is passed over. */
+msa_status_t msa_free_pages(const msa_page_pool_t* pool, const int32_t* pages, const int32_t* counts, int32_t rows,
+                            int32_t width, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Pages in use moved to the lowest numbers.  With n pages in use (count not 0), the i-th of them
+ * that is numbered n or higher moves, in every buffer, to the i-th free number below n:
+ *   refs_out    counts under the new numbers; 0 from n on
+ *   page_map    int32 [num_pages]: the new number of every page, -1 for a free one
+ *   live_count  int32 [1]: n
+ *   table_out   int32 [batch][max_blocks] (may be the block table): the ceil(seq_lens[b] / 128) entries of
+ *               every row under their new numbers, -1 behind; an entry of a free page or outside
+ *               the pool becomes -1 (MSA_DEVERR_BAD_PAGE), unless it is -1 already.  A length
+ *               below 0 or above max_blocks * 128 sets MSA_DEVERR_BAD_SEQLEN: all of the row counts.
+ * Other holders of page numbers take theirs through page_map. */
+msa_status_t msa_compact_pages(const msa_page_pool_t* pool, const msa_batch_t* batch, int32_t* table_out,
+                               int32_t* page_map, int32_t* live_count, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /* The stage-3 sparse attention of msa_sparse_attn_decode for callers that cannot allocate
  * device memory, or cannot hand the library a workspace: for example a plugin inside a host

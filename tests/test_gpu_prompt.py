@@ -1,0 +1,192 @@
+"""msa_prompt_attn against its definition in 64 bits: lengths around the tiles' edges, every number of heads,
+empty rows and sequences, strides, what masked places hold, captured calls."""
+import numpy as np
+import pytest
+
+from gpu_util import need_gpu
+from prompt_util import Prompts, close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def run(p):
+    p.upload().call()
+    return p.results()
+
+
+@pytest.mark.parametrize("Hg", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_heads(Hg):
+    p = Prompts(10 + Hg, [1, 37, 200, 0, 129], G=2, Hg=Hg, before=3, behind=5, fused=Hg % 2 == 1)
+    p.check(run(p))
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+def test_lengths(n):
+    p = Prompts(n, [n], G=1, Hg=8)
+    p.check(run(p))
+    p = Prompts(n + 1, [n, n], G=1, Hg=1, fused=True)
+    p.check(run(p))
+
+
+@pytest.mark.parametrize("Lq,Lk", [(1, 1000), (1, 128), (1, 129), (5, 640), (40, 41), (100, 513), (130, 1029), (257, 700)])
+def test_keys_before_the_queries(Lq, Lk):
+    p = Prompts(Lq * 7 + Lk, [Lq, 3, Lq], [Lk, 3, Lk + 1], G=2, Hg=4)
+    p.check(run(p))
+
+
+@pytest.mark.parametrize("Hg", [1, 5, 8])
+def test_rows_without_keys(Hg):
+    # more queries than keys: the first ones see nothing; sequences without keys; without queries
+    p = Prompts(77, [200, 10, 300, 5, 0, 1], [150, 0, 1, 0, 40, 0], G=2, Hg=Hg, behind=2)
+    got = run(p)
+    p.check(got)
+    assert (got[0][:50] == 0).all() and (got[1][:50] == -np.inf).all()
+
+
+def test_no_keys_at_all():
+    p = Prompts(78, [20, 5], [0, 0], G=2, Hg=3)
+    assert p.Nk == 0
+    got = run(p)
+    assert (got[0] == 0).all() and (got[1] == -np.inf).all() and got[2] == 0
+
+
+def test_nothing_to_do():
+    p = Prompts(79, [0, 0], [4, 0], G=1, Hg=2, behind=3)
+    p.check(run(p))
+    p = Prompts(80, [], G=1, Hg=2, behind=3)
+    p.check(run(p))
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 20, 700).tolist()
+    p = Prompts(81, lens, G=1, Hg=2, before=1)
+    p.check(run(p))
+    p = Prompts(82, [1] * 2048, G=1, Hg=1)
+    p.check(run(p))
+
+
+def test_ragged_batch():
+    p = Prompts(83, [400, 1, 77, 513, 128, 250], G=2, Hg=4, fused=True)
+    p.check(run(p))
+
+
+def test_one_long_prompt():
+    p = Prompts(84, [2500], G=1, Hg=2)
+    p.check(run(p))
+
+
+@pytest.mark.parametrize("scale,dev", [(0.5, 1.5), (1e-3, 1.5), (1.0, 20.0), (1e-30, 1.0), (0.08, 1e-20)])
+def test_scales(scale, dev):
+    p = Prompts(85, [150, 33], G=1, Hg=4, scale=scale, dev=dev)
+    p.check(run(p))
+
+
+def test_rising_and_falling_logits():
+    # the running maximum moves at nearly every key, or never again after the first
+    for sign in (1.0, -1.0):
+        p = Prompts(86, [700], G=1, Hg=2)
+        ramp = (np.arange(700) * 0.25 * sign).astype(np.float32)
+        p.q[:], p.k[:] = 0.0, 0.0
+        p.q[:, :, 0] = 11.3125
+        import torch
+        p.k[:, :, 0] = torch.from_numpy(ramp)[:, None].to(torch.bfloat16)
+        p.check(run(p))
+
+
+@pytest.mark.parametrize("what", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("Hg", [2, 8])
+def test_values_of_later_keys(what, Hg):
+    """A special value in one dim of v at a key touches the rows that see the key, in that dim, and no others; in k,
+    rows that do not see it stay as they are."""
+    p = Prompts(87, [300, 150], G=2, Hg=Hg)
+    for key, dim in ((130, 5), (140, 127), (299, 64), (300, 0), (449, 1)):
+        p.v[key, 0, dim] = what
+    p.v[135, 0, 5] = np.inf        # meets -inf or NaN of key 130
+    p.v[128, 1, 7], p.v[129, 1, 7] = -np.inf, what
+    ref = p.oracle()
+    # the definition over infinities: numpy's 0 weights do not occur here (every probability is above 0)
+    got = run(p)
+    special = ~np.isfinite(ref["out"])
+    assert special.any()
+    ref["spread"] = np.where(special, 0.0, ref["spread"])
+    p.check(got, ref)
+
+
+def test_special_values_in_keys_and_queries():
+    p = Prompts(88, [300], G=1, Hg=4)
+    p.k[200, 0, 3] = np.nan
+    p.k[290, 0, 3] = np.inf
+    p.q[20, 1, 0] = np.nan
+    got = run(p)
+    ref = p.oracle()
+    clean = np.isfinite(ref["lse"])
+    assert not clean[200:].any() and not clean[20, 1] and clean[:200].sum() == 200 * 4 - 1
+    assert np.isnan(got[0][200:]).all() and np.isnan(got[0][20, 1]).all()
+    for r in (ref, ):
+        r["out"][~clean], r["lse"][~clean] = 0, 0
+        r["spread"][~clean], r["logit"][~clean] = 0, 0
+    got[0][~clean], got[1][~clean] = 0, 0
+    p.check(got, ref)
+
+
+@pytest.mark.parametrize("cu_q,cu_k", [([0, 50, 40, 80], [0, 50, 60, 80]), ([0, 50, 60, 80], [0, 50, 60, 81]),
+                                       ([-1, 50, 60, 80], [0, 50, 60, 80]), ([0, 50, 60, 80], [0, 20, 10, 80])])
+def test_bad_offsets(cu_q, cu_k):
+    import block_sparse_attention_indexer_gb300 as msa
+    p = Prompts(89, [50, 10, 20], G=1, Hg=2)
+    p.cu_q, p.cu_k = np.array(cu_q, np.int32), np.array(cu_k, np.int32)
+    out, lse, err = run(p)
+    assert err == msa.MSA_DEVERR_BAD_SEQLEN and (out == 7).all() and (lse == 7).all()
+
+
+def test_without_lse_same_bits():
+    p = Prompts(90, [513, 64, 900], G=2, Hg=5)
+    first = run(p)
+    for _ in range(3):
+        p.out.fill_(7.0)
+        p.call(lse=False)
+        again = p.results()
+        assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+def test_captured_and_on_another_stream():
+    import torch
+    p = Prompts(91, [300, 20, 1], G=2, Hg=8)
+    ref = p.oracle()
+    p.upload()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    p.call(stream=s)
+    s.synchronize()
+    p.check(p.results(), ref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.call()
+    for lens in ([300, 20, 1], [1, 319, 1], [0, 0, 321]):     # new lengths under the same graph
+        cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        p.packed.cu_q.copy_(torch.from_numpy(cu))
+        p.packed.cu_k.copy_(torch.from_numpy(cu))
+        p.cu_q = p.cu_k = cu
+        p.out.fill_(7.0)
+        p.lse.fill_(7.0)
+        g.replay()
+        p.check(p.results())
+
+
+def test_single_token_agrees_with_the_prompt():
+    """The last row of a prompt is the single-token call over the same keys."""
+    p = Prompts(92, [700], G=2, Hg=4)
+    out, lse, _ = run(p)
+    one = Prompts(92, [700], G=2, Hg=4)
+    one.cu_q, one.Nq, one.q = np.array([0, 1], np.int32), 1, p.q[-1:]
+    one.used_q = np.ones(1, bool)
+    o1, l1, err = run(one)
+    assert err == 0
+    close("out", o1[0], out[-1], np.abs(out[-1]) * 2.0 ** -7 + 2.0 ** -8)
+    close("lse", l1[0], lse[-1], np.full(l1[0].shape, 1e-4))
