@@ -22,7 +22,7 @@ SOURCES = ["api.cu", "quant.cu", "indexer.cu", "prefill.cu", "select.cu", "atten
            "fp8_tile.cu", "evict.cu", "api_prompt.cu", "prompt_attn.cu", "api_pages.cu", "pages.cu"]
 HEADERS = ["msa_device.cuh", "msa_kernels.h", "api_internal.h", "select_row.cuh", "umma.cuh", "indexer_tile.cuh",
            "attention_tile.cuh", "attention_team.cuh", "fp8_device.cuh", "fp8_kernels.h", "fp8_merge.cuh",
-           "prompt.h", "pages.h"]
+           "prompt.h", "pages.h", "tile_split.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

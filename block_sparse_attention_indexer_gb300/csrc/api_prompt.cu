@@ -18,9 +18,24 @@ msa_status_t check_packed(const msa_config_t* c, const msa_packed_t* p) {
   if (p->batch > 0 && (p->cu_q == nullptr || p->cu_k == nullptr)) return MSA_ERR_INVALID_ARG;
   if (p->batch > kMaxBatchSmem || p->q_tokens > kMaxTokens || p->k_tokens > kMaxTokens) return MSA_ERR_UNSUPPORTED;
   // the flat list of (tile of 128 rows, 128 keys) steps is counted in 32 bits
-  const int64_t tile = 128 / c->heads_per_group, units = p->q_tokens / (2 * tile) + p->batch;
-  if (2 * units * ((p->k_tokens + 127) / 128) > INT32_MAX) return MSA_ERR_UNSUPPORTED;
+  const int64_t blocks = (p->k_tokens + 127) / 128;
+  if (2 * prompt_max_units(p->q_tokens, p->batch, c->heads_per_group) * (blocks > 1 ? blocks : 1) >
+      INT32_MAX / c->num_kv_groups)
+    return MSA_ERR_UNSUPPORTED;
   return MSA_OK;
+}
+
+struct PromptLayout {
+  size_t plan, base, prefix, partial, total;
+};
+PromptLayout prompt_layout(const msa_config_t* c, const msa_packed_t* p) {
+  PromptLayout w;
+  w.plan = kErrBytes;
+  w.base = w.plan + kWsAlign;
+  w.prefix = w.base + align_up((static_cast<size_t>(p->batch) + 1) * sizeof(int32_t));
+  w.partial = w.prefix + align_up((prompt_max_units(p->q_tokens, p->batch, c->heads_per_group) + 1) * sizeof(int32_t));
+  w.total = w.partial + align_up(prompt_partial_bytes());
+  return w;
 }
 
 // token-strided bf16 rows: pointer and stride on 16-byte boundaries, tokens not overlapping
@@ -39,7 +54,7 @@ extern "C" {
 
 size_t msa_prompt_workspace_bytes(const msa_config_t* cfg, const msa_packed_t* packed) {
   if (check_config(cfg) != MSA_OK || check_packed(cfg, packed) != MSA_OK) return 0;
-  return kErrBytes;
+  return prompt_layout(cfg, packed).total;
 }
 
 msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed, const void* q, int64_t q_stride,
@@ -61,8 +76,8 @@ msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed
   for (const auto& x : in)
     if (overlap(out, size, x.p, x.n) || overlap(lse, stats, x.p, x.n)) return MSA_ERR_INVALID_ARG;
   if (overlap(out, size, lse, stats)) return MSA_ERR_INVALID_ARG;
-  if (workspace == nullptr || workspace_bytes < msa_prompt_workspace_bytes(cfg, packed) || !aligned16(workspace))
-    return MSA_ERR_WORKSPACE;
+  const PromptLayout w = prompt_layout(cfg, packed);
+  if (workspace == nullptr || workspace_bytes < w.total || !aligned16(workspace)) return MSA_ERR_WORKSPACE;
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return MSA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -84,6 +99,10 @@ msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed
   a.lse = lse;
   a.scale_log2 = scale_log2(cfg);
   a.err = reinterpret_cast<uint32_t*>(ws);
+  a.plan = reinterpret_cast<int32_t*>(ws + w.plan);
+  a.base = reinterpret_cast<int32_t*>(ws + w.base);
+  a.prefix = reinterpret_cast<int32_t*>(ws + w.prefix);
+  a.partial = reinterpret_cast<float*>(ws + w.partial);
   try {  // (the launch's bookkeeping allocates host memory: nothing may leave a C entry)
     return launch_prompt_attn(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
   } catch (...) {

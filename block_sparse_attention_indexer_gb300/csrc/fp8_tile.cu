@@ -42,6 +42,7 @@
 #include "fp8_kernels.h"
 #include "fp8_merge.cuh"
 #include "msa_device.cuh"
+#include "tile_split.cuh"
 #include "umma.cuh"
 
 namespace msa {
@@ -165,43 +166,7 @@ __global__ void __launch_bounds__(kFtPlanThreads) fp8_tile_plan_kernel(const Fp8
   ft_prefix(a, per_seq, a.block_prefix, s_warp, true);
 }
 
-// First step of CTA c of n.
-__device__ __forceinline__ int ft_lo(int64_t E, int c, int n) { return static_cast<int>(E * c / n); }
-
-// The last unit u with prefix[u] * G <= x, by a whole warp: 32 places a round.
-__device__ __forceinline__ int ft_find(const int32_t* prefix, int units, int groups, int x) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = units;  // it is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32, at = lo + lane * step;
-    const bool below = at < lo + n && static_cast<int64_t>(prefix[at]) * groups <= x;
-    const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // (the first place always is)
-    n = min(step, lo + n - (lo + k * step));
-    lo += k * step;
-  }
-  return lo;
-}
-
 // ---------------------------------------------------------------- tcgen05 forms used here only
-
-// First step of CTA c of n as it is taken: a cut inside a unit that stays whole goes to the nearer of its ends.  A
-// whole warp calls it.
-__device__ __forceinline__ int ft_cut(const int32_t* prefix, int units, int G, int64_t E, int c, int n, int whole) {
-  const int x = ft_lo(E, c, n);
-  if (c == 0 || x >= E) return x;
-  const int u = ft_find(prefix, units, G, x), steps = prefix[u + 1] - prefix[u];
-  if (steps > whole) return x;
-  const int off = (x - prefix[u] * G) % steps;
-  return x - off + (2 * off < steps ? 0 : steps);
-}
-
-// n / d for 0 <= n < 2^29 and 1 <= d <= 8: with m = ceil(2^32 / d), n m / 2^32 exceeds n / d by less than
-// n d / (2^32 d) < 1 / d.
-struct FtDiv {
-  uint32_t m;
-  __device__ __forceinline__ explicit FtDiv(int d) : m(d > 1 ? 0xFFFFFFFFu / static_cast<uint32_t>(d) + 1u : 0u) {}
-  __device__ __forceinline__ int operator()(int n) const { return m != 0u ? static_cast<int>(__umulhi(n, m)) : n; }
-};
 
 // kind::f8f6f4, both operands in shared memory
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -209,14 +174,6 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-
-// kind::f16 with A in tensor memory
-__device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
 
 // 16 bytes (or, with bytes = 0, as many zeros) global -> shared by this thread's own queue
@@ -237,57 +194,6 @@ __device__ __forceinline__ uint32_t f32x4_to_e5m2x4(float a, float b, float c, f
       : "=r"(w)
       : "f"(a), "f"(b), "f"(c), "f"(d));
   return w;
-}
-
-// Descriptor of an MN-major operand tile with the 128-byte swizzle: 64 fp16 of N per 128-byte row,
-// one row per k; 8-row groups 1024 bytes apart along k, the next 64 of N `next` bytes on.
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t next) {
-  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(next >> 4) << 16;  // leading byte offset
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;  // stride byte offset
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-
-// Waits for the warp's TMEM loads; the registers given are not used before it.
-template <int N>
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// One lane of the warp (a form that leaves the issue of the products in uniform control flow)
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
-// (a.x, a.y) * f + c and (a.x, a.y) + (b.x, b.y): two floats an instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 f, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(f)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
 }
 
 // Output dim of accumulator column n: the upper 64 dims' 16-byte chunks are stored in swapped

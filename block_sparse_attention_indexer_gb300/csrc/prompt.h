@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace msa {
@@ -19,8 +20,20 @@ struct PromptArgs {
   float* lse;           // [q_tokens][G * Hg] or null
   float scale_log2;     // softmax_scale * log2(e)
   uint32_t* err;
+  // scratch
+  int32_t* plan;        // [0]: units; [1]: steps up to which a unit is not cut
+  int32_t* base;        // [batch + 1]: units of the sequences before each
+  int32_t* prefix;      // [units + 1]: steps (per KV head) of the units before each
+  float* partial;       // partial softmax states of units cut by the split of the work
 };
 
+// Query tokens of a tile of 128 rows (token, head), and of a unit of two tiles.
+inline int prompt_tile_tokens(int heads_per_group) { return 128 / heads_per_group; }
+// At least as many units as the packed sequences have.
+inline int64_t prompt_max_units(int64_t q_tokens, int batch, int heads_per_group) {
+  return q_tokens / (2 * prompt_tile_tokens(heads_per_group)) + batch;
+}
+size_t prompt_partial_bytes();
 cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace msa

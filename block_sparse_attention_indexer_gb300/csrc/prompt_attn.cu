@@ -1,76 +1,882 @@
-// Causal attention of packed bf16 prompts: one warp per query row (token, head), the keys one
-// after another with a running maximum and sum.  A lane holds four dims.
+// Causal attention of packed bf16 prompts on the tcgen05 tensor cores.
+//
+// Mathematics: P_j = 2^(e_j - M) with e_j = (q . k_j) softmax_scale log2(e), O = sum P_j v_j, l = sum P_j;
+// out = O / l, lse = ln 2 (M + log2 l).  M is an integer (rescaling O and l is exact) that is moved only where a
+// P would pass 1, to 2^8 above the largest so far, so that most pages move nothing.  P is rounded
+// to bf16 as the operand of P V: by 2^-8 of itself at most, whatever its size (bf16 has float32's range); l
+// adds what was before the rounding.  S, O, l and M are float32.
+//
+// Work.  A row is a (token, head) of a KV head; a tile is 128 rows, floor(128 / Hg) tokens with their Hg heads, a
+// unit two tiles (or one, of a sequence's last tokens) of a sequence and a KV head, so that keys loaded once meet
+// 256 rows and the causal border costs half a block of 128 keys for each tile, whatever Hg is.  A unit's
+// products are counted in (tile, 128 keys) steps; all units' steps are one flat list that a
+// persistent grid, one CTA an SM, cuts into equal ranges (tile_split.cuh).  Units that are cut leave partial
+// states, which a second kernel adds.  Two accumulator slots work in turn: with two tiles each block of keys
+// is used by slot 0 and slot 1, with one tile the blocks alternate between the slots.
+//   * S = Q K^T: Q and K by tensor copies in 128-byte swizzle (a Q tile is one box of Hg heads by tokens).
+//   * O += P V: P in tensor memory over S (the A operand), V as it lies, as the MN-major B operand.
+// TMEM: S of the two slots, then O of the two slots: 4 x 128 columns, all of it.
+//
+// Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread), 8-11 look through the V rows that not
+// every row of the unit sees, 12 issues the copies, 13 the products S, 14 P V.
+// What a row does not see cannot reach it: its S is replaced by -inf, and infinities and NaN in V are taken
+// out of the blocks where they could meet a P of 0; rows that do see them get them back at the end.
+// Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
+// the others at the end, where TMEM is freed.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include "fp8_device.cuh"
 #include "fp8_kernels.h"
+#include "fp8_merge.cuh"
 #include "msa_device.cuh"
 #include "prompt.h"
+#include "tile_split.cuh"
+#include "umma.cuh"
 
 namespace msa {
 
-__device__ __forceinline__ float4 bf16x4(const uint16_t* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
+constexpr int kPtRows = 128;  // rows per tile
+constexpr int kPtThreads = 480;
+constexpr int kPtK = 3, kPtV = 2;             // stages of 128 keys
+constexpr int kPtItems = 8;                   // records in flight
+constexpr int kPtTile = kPtRows * kDim * 2;   // bytes of a Q tile, and of a stage
+constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
+constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
+constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
+constexpr float kPtRefSet = 8.f;
+
+// A block of 128 keys of a unit (or a unit without keys), for the roles that work on it.
+struct alignas(16) PtItem {
+  int flags;   // kPtEnd ...; place + 1 from kPtPlace on
+  int block;   // -1: no keys
+  int token0;  // the unit's first query token, in the packed list
+  int tokens;  // of the unit
+  int pos0;    // the first one's position
+  int key0;    // the sequence's first key, in the packed list
+  int g;
+  int pad;
+};
+// Bits: no more items; first item of a unit, last one; the unit has two tiles; some row of it must not see all of the
+// block's keys; some row of slot s's tile must not see all of half h of them (bit kPtHide + 2 s + h).
+constexpr int kPtEnd = 1, kPtNew = 2, kPtLast = 4, kPtTwo = 8, kPtEdge = 16, kPtHide = 5, kPtPlace = 9;
+
+struct PtShared {
+  uint64_t k_full[kPtK], k_empty[kPtK], v_full[kPtV], v_ok[kPtV], v_empty[kPtV];
+  uint64_t item_full[kPtItems], item_empty[kPtItems];
+  uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [slot], [slot][half of the keys]
+  uint64_t q_full[2], q_empty[2];                   // [tile]
+  uint64_t fin[2];                                  // a unit written (by the unit's parity on this CTA)
+  uint64_t other;                                   // slot 1's statistics of a one-tile unit left
+  uint64_t drain[2];                                // every product issued has ended (after a wait that gave up)
+  uint32_t tmem;
+  alignas(16) int special[2][4];                    // a V row taken care of by warp 8 + i (by the unit's parity)
+  PtItem item[kPtItems];
+  float other_m[kPtRows], other_l[kPtRows];
+};
+constexpr size_t kPtSmem = 1024 + 2 * kPtTile + (kPtK + kPtV) * kPtTile + sizeof(PtShared);
+static_assert(kPtSmem <= 232448, "227 KB of shared memory per CTA");
+
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+
+// ---------------------------------------------------------------- the plan
+
+// Unit i of a sequence.
+struct PtUnit {
+  int tokens, pos0, width, pages;  // pages 0: no row has a key
+};
+__device__ __forceinline__ PtUnit pt_unit(int Lq, int Lk, int i, int tile_tokens) {
+  PtUnit t;
+  const int first = i * 2 * tile_tokens;
+  t.tokens = min(Lq - first, 2 * tile_tokens);
+  t.pos0 = Lk - Lq + first;
+  t.width = t.tokens > tile_tokens ? 2 : 1;
+  const int last = t.pos0 + t.tokens - 1;
+  t.pages = last < 0 ? 0 : last / kBlock + 1;
+  return t;
 }
 
-__global__ void __launch_bounds__(256) prompt_attn_kernel(const PromptArgs a) {
+constexpr int kPtPlanThreads = 1024;
+
+// Exclusive prefix sum of v over the CTA plus `carry`, which moves on by the sum.
+__device__ __forceinline__ int pt_prefix(int v, int& carry, int* warp_sum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int x = v;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, s);
+    if (lane >= s) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  const int w = warp_sum[lane];
+  const int at = carry + x - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  carry += __reduce_add_sync(0xffffffffu, w);
+  return at;
+}
+
+// Steps of a unit up to which it is not cut: a cut costs two partial states and a merge, about as much as
+// kPtCutSteps steps; of `all` units on n CTAs some take ceil(all / n), so that an uncut unit of S steps costs
+// idle * S / n more than its share.  Above 64 steps a unit is cut in any case.
+__device__ __forceinline__ int pt_whole(int64_t all, int n) {
+  constexpr int kPtWhole = 64, kPtCutSteps = 8;
+  if (all == 0) return kPtWhole;
+  const int64_t idle = n - 1 - (all - 1) % n;
+  const int64_t most = static_cast<int64_t>(kPtCutSteps) * n;
+  return idle * kPtWhole <= most ? kPtWhole : static_cast<int>(most / idle);
+}
+
+__global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const PromptArgs a, int ctas) {
+  __shared__ int s_base[2048 + 1], s_sum[32];
+  const int tid = threadIdx.x, tt = kPtRows / a.heads_per_group;
   grid_dependency_wait();
   grid_dependents_launch();
   bool bad = false;
-  for (int b = threadIdx.x; b < a.batch; b += 256)
-    bad |= a.cu_q[b] < 0 || a.cu_k[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_k[b + 1] < a.cu_k[b] ||
-           a.cu_q[b + 1] > a.q_tokens || a.cu_k[b + 1] > a.k_tokens;
-  if (__syncthreads_or(bad)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
+  int units = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kPtPlanThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < a.batch) {
+      const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+      bad |= q0 < 0 || k0 < 0 || q1 < q0 || k1 < k0 || q1 > a.q_tokens || k1 > a.k_tokens;
+      n = bad ? 0 : (q1 - q0 + 2 * tt - 1) / (2 * tt);
+    }
+    const int at = pt_prefix(n, units, s_sum);
+    if (b < a.batch) s_base[b] = at;
+  }
+  if (__syncthreads_or(bad)) {  // nothing is done
+    if (tid == 0) {
+      flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
+      a.plan[0] = 0;
+    }
     return;
   }
-  const int lane = threadIdx.x & 31, H = a.groups * a.heads_per_group;
-  const int q0 = a.cu_q[0];
-  const int64_t rows = static_cast<int64_t>(a.cu_q[a.batch] - q0) * H;
-  for (int64_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += static_cast<int64_t>(gridDim.x) * 8) {
-    const int token = q0 + static_cast<int>(r / H), h = static_cast<int>(r % H), g = h / a.heads_per_group;
-    int lo = 0, n = a.batch;  // the last sequence that starts at or before the token
-    while (n > 1) {
-      const int half = n / 2;
-      if (a.cu_q[lo + half] <= token) {
-        lo += half;
-        n -= half;
-      } else {
-        n = half;
+  if (tid == 0) {
+    s_base[a.batch] = units;
+    a.plan[0] = units;
+    a.plan[1] = pt_whole(static_cast<int64_t>(units) * a.groups, ctas);
+  }
+  __syncthreads();
+  for (int b = tid; b <= a.batch; b += kPtPlanThreads) a.base[b] = s_base[b];
+  int steps = 0;
+  for (int u0 = 0; u0 < units; u0 += kPtPlanThreads) {
+    const int u = u0 + tid;
+    int n = 0;
+    if (u < units) {
+      int b = 0, left = a.batch;  // the last sequence with base <= u
+      while (left > 1) {
+        const int h = left / 2;
+        if (s_base[b + h] <= u) {
+          b += h;
+          left -= h;
+        } else {
+          left = h;
+        }
+      }
+      const PtUnit t = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], u - s_base[b], tt);
+      n = t.width * max(t.pages, 1);
+    }
+    const int at = pt_prefix(n, steps, s_sum);
+    if (u < units) a.prefix[u] = at;
+  }
+  if (tid == 0) a.prefix[units] = steps;
+}
+
+// ---------------------------------------------------------------- bf16 forms
+
+// A box of a tensor of rank 3 (x: dims, y: heads, z: tokens)
+__device__ __forceinline__ void tma_box(void* dst, const void* map, int x, int y, int z, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+      "{%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// The top bits of the halves of w that are infinities or NaN (exponent all ones; no half's sum carries)
+__device__ __forceinline__ uint32_t bf16_special(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// ---------------------------------------------------------------- the kernel
+
+__global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* q_tile = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* k_ring = q_tile + 2 * kPtTile;
+  uint8_t* v_ring = k_ring + kPtK * kPtTile;
+  PtShared* sh = reinterpret_cast<PtShared*>(v_ring + kPtV * kPtTile);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hg = a.heads_per_group, G = a.groups, H = G * Hg, tt = kPtRows / Hg;
+
+  if (tid == 0) {
+    for (int i = 0; i < kPtK; ++i) {
+      mbar_init(&sh->k_full[i], 1);
+      mbar_init(&sh->k_empty[i], 1);
+    }
+    for (int i = 0; i < kPtV; ++i) {
+      mbar_init(&sh->v_full[i], 1);
+      mbar_init(&sh->v_ok[i], 4);
+      mbar_init(&sh->v_empty[i], 1);
+    }
+    for (int i = 0; i < kPtItems; ++i) {
+      mbar_init(&sh->item_full[i], 1);
+      mbar_init(&sh->item_empty[i], 14);  // eight softmax warps, four of V, two issuers
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh->p_full[i][h], 4);
+        mbar_init(&sh->pv_done[i][h], 1);
+      }
+      mbar_init(&sh->q_full[i], 1);
+      mbar_init(&sh->q_empty[i], 1);
+      mbar_init(&sh->fin[i], 8);
+      mbar_init(&sh->drain[i], 1);
+    }
+    mbar_init(&sh->other, 4);
+    fence_mbar_init();
+  }
+  // rows of a tile behind its tokens (Hg does not divide 128): no copy writes them
+  if (tt * Hg < kPtRows && tid < 2 * (kPtRows - tt * Hg) * 16) {
+    const int i = tid / 16, t = i & 1, r = tt * Hg + (i >> 1), c = tid & 15;
+    *reinterpret_cast<uint4*>(q_tile + t * kPtTile + (c >> 3) * kPtHalf + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const uint32_t tmem = sh->tmem;
+  bool failed = false;
+
+  // The next record, for a whole warp; `n` counts records.
+  auto take_item = [&](int n, PtItem& it) -> bool {
+    if (!mbar_wait_warp(&sh->item_full[n % kPtItems], (n / kPtItems) & 1)) return false;
+    it = sh->item[n % kPtItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_empty[n % kPtItems]);
+    return true;
+  };
+
+  if (warp < 8) {
+    // ---- softmax of slot `slot`: row r of its tile
+    const int slot = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kPtO + slot * 128 + lane_base;
+    const float f = finite_factor(a.scale_log2);
+    const int my_token = r / Hg, my_head = r - my_token * Hg;
+    // steps of this slot and of the other one so far, blocks, units
+    int done = 0, done_o = 0, blocks = 0, uc = -1;
+    bool mine = false, others = false, turn = false, shared_par = false, one_before = false;
+    float M = -INFINITY, l = 0.f;
+    int pos = 0, first_block = 0;
+
+    // writes the unit's rows (or its partial state); `it` is its last record
+    auto finish = [&](const PtItem& it) -> bool {
+      const bool two = it.flags & kPtTwo;
+      const int place = (it.flags >> kPtPlace) - 1;
+      if (mine && !mbar_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) return false;
+      if (!two) {
+        if (slot == 1) {
+          sh->other_m[r] = M;
+          sh->other_l[r] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->other);
+          return true;
+        }
+        if (!mbar_wait_warp(&sh->other, shared_par)) return false;
+        if (others && !mbar_wait_warp(&sh->pv_done[1][1], (done_o - 1) & 1)) return false;
+      }
+      tc_fence_after();
+      // state of the row = fa * own O + fb * the other slot's O
+      float fa = mine ? 1.f : 0.f, fb = 0.f;
+      const bool both = !two && others;
+      if (both) {
+        const float mo = sh->other_m[r], lo = sh->other_l[r];
+        const float mn = fmaxf(M, mo);
+        fa = mn == -INFINITY ? 1.f : ex2(M - mn);
+        fb = mn == -INFINITY ? 1.f : ex2(mo - mn);
+        l = l * fa + lo * fb;
+        M = mn;
+      }
+      const int t = my_token + (two && slot ? tt : 0);  // token of the unit
+      const bool valid = my_token < tt && t < it.tokens;
+      const float inv = l != 0.f ? 1.f / l : 0.f;       // (NaN counts as a sum)
+      const float out_f = place < 0 ? inv : 1.f;
+      const int64_t hr = static_cast<int64_t>(it.token0 + t) * H + it.g * Hg + my_head;
+      const int pr = r + (two && slot ? kPtRows : 0);   // row of the partial state
+      float* part = place < 0 ? nullptr : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats;
+      const int4 sp = *reinterpret_cast<const int4*>(sh->special[uc & 1]);
+      const bool special = first_block >= 0 && (sp.x | sp.y | sp.z | sp.w) != 0;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {  // 16 dims
+        uint32_t x[16];
+        float v[16];
+        if (mine) {
+          tmem_ld16(tO + 16 * c, x);
+          tmem_wait_ld(x);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = mine ? __uint_as_float(x[i]) * fa : 0.f;
+        if (both) {
+          tmem_ld16(tO + 128 + 16 * c, x);
+          tmem_wait_ld(x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(x[i]) * fb;
+        }
+        if (special) {
+          // what was taken out of V comes back for the rows that see its key
+          const int last = min(pos, it.block * kBlock + kBlock - 1);
+#pragma unroll 1
+          for (int j = max(it.pos0 + 1, first_block * kBlock); j <= last; ++j) {
+            const uint16_t* src = a.v + (it.key0 + j) * a.v_stride + it.g * kDim + 16 * c;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float y = __uint_as_float(static_cast<uint32_t>(src[i]) << 16);
+              if (!(fabsf(y) < INFINITY)) v[i] += y;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= out_f;
+        if (valid) {
+          if (place < 0) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            uint4* dst = reinterpret_cast<uint4*>(a.out + hr * kDim + 16 * c);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else {
+            // four dims of all rows together: the lanes of a store are neighbouring rows
+            float4* dst = reinterpret_cast<float4*>(part) + 4 * c * (2 * kPtRows) + pr;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[j * 2 * kPtRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        if (place < 0) {
+          if (a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
+        } else {
+          part[2 * kPtRows * kDim + pr] = M;
+          part[2 * kPtRows * (kDim + 1) + pr] = l;
+        }
+      }
+      tc_fence_before();
+      return true;
+    };
+
+    for (int n = 0;; ++n) {
+      PtItem it;
+      if (!take_item(n, it)) {
+        failed = true;
+        break;
+      }
+      if (it.flags & kPtEnd) break;
+      const bool two = it.flags & kPtTwo;
+      if (it.flags & kPtNew) {
+        ++uc;
+        // slot 0 reads slot 1's O and statistics of a one-tile unit: slot 1 goes on when it has
+        if (slot == 1 && one_before && !mbar_wait_warp(&sh->fin[(uc - 1) & 1], ((uc - 1) >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        mine = others = turn = false;
+        M = -INFINITY;
+        l = 0.f;
+        first_block = it.block;
+        pos = it.pos0 + min(min(my_token, tt - 1) + (two && slot ? tt : 0), it.tokens - 1);
+      }
+      bool step = it.block >= 0;
+      int vstage = 0, vphase = 0;
+      if (step) {
+        vstage = blocks % kPtV;
+        vphase = (blocks / kPtV) & 1;
+        ++blocks;
+        if (!two) {  // the blocks alternate between the slots
+          step = turn == (slot == 1);
+          turn = !turn;
+          if (!step) {
+            ++done_o;
+            others = true;
+          }
+        }
+      }
+      if (step) {
+        // what the V warps found in a block that not every row sees whole is read when the unit is written: seeing the
+        // stage ready orders it before that (the stage is not used again before this step's P)
+        if (!mbar_wait_warp(&sh->s_full[slot], done & 1) ||
+            (it.flags & kPtEdge && !mbar_wait_warp(&sh->v_ok[vstage], vphase))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t tH = tS + 64 * h;
+          uint32_t v[64];
+          float mx;
+          tmem_ld64_max(tH, v, mx);
+          tmem_wait_ld(v);
+          asm volatile("" : "+f"(mx));
+          if (it.flags >> (kPtHide + 2 * slot + h) & 1) {
+            // some row of the tile must not see one of these keys: -inf over its scores, and the maximum again
+            const int vis = pos - it.block * kBlock - 64 * h + 1;  // visible columns
+            mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+              v[j] = j < vis ? v[j] : 0xff800000u;
+              mx = fmaxf(mx, __uint_as_float(v[j]));
+            }
+          }
+          mx *= f;
+          if (__any_sync(0xffffffffu, mx > M)) {
+            float alpha = 1.f;
+            if (mx > M) {
+              const float mn = ceilf(mx) + kPtRefSet;
+              alpha = ex2(M - mn);
+              M = mn;
+              l *= alpha;
+              sum.x *= alpha;
+              sum.y *= alpha;
+            }
+            if (mine || h > 0) {  // O as the products issued so far leave it, rescaled
+              if (!mbar_wait_warp(&sh->pv_done[slot][h ^ 1], (h ? done : done - 1) & 1)) {
+                failed = true;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t y[16];
+                tmem_ld16(tO + 16 * c, y);
+                tmem_wait_ld(y);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * alpha);
+                tmem_st16(tO + 16 * c, y);
+              }
+            }
+          }
+          // P goes over the first 32 columns of S
+          const float c0 = M == -INFINITY ? 0.f : -M;
+          const float2 ff = make_float2(f, f), cc = make_float2(c0, c0);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int k = 32 * i + 2 * j;
+              const float2 e = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, cc);
+              const float2 p = make_float2(ex2(e.x), ex2(e.y));
+              sum = add2(sum, p);
+              pk[j] = pack_bf16x2(p.x, p.y);
+            }
+            tmem_st16(tH + 16 * i, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->p_full[slot][h]);
+        }
+        if (failed) break;
+        ++done;
+        mine = true;
+        if (two) ++done_o;
+        l += sum.x + sum.y;
+      }
+      if (it.flags & kPtLast) {
+        if (!finish(it)) {
+          failed = true;
+          break;
+        }
+        one_before = !two;
+        if (!two) shared_par = !shared_par;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->fin[uc & 1]);
       }
     }
-    const int Lq = a.cu_q[lo + 1] - a.cu_q[lo], Lk = a.cu_k[lo + 1] - a.cu_k[lo];
-    const int seen = Lk - Lq + (token - a.cu_q[lo]) + 1;
-    float4 q = bf16x4(a.q + token * a.q_stride + h * kDim + 4 * lane);
-    const int64_t key0 = a.cu_k[lo];
-    float M = -INFINITY, was = M, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < seen; ++j) {
-      const float4 k = bf16x4(a.k + (key0 + j) * a.k_stride + g * kDim + 4 * lane);
-      const float4 v = bf16x4(a.v + (key0 + j) * a.v_stride + g * kDim + 4 * lane);
-      float z = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+  } else if (warp < 12) {
+    // ---- V: infinities and NaN out of the rows that not every row of the unit sees
+    const int ct = tid - 256;
+    int blocks = 0, uc = -1;
+    for (int n = 0;; ++n) {
+      PtItem it;
+      if (!take_item(n, it)) {
+        failed = true;
+        break;
+      }
+      if (it.flags & kPtEnd) break;
+      if (it.flags & kPtNew) {
+        ++uc;
+        // the unit that used these marks is written
+        if (uc >= 2 && !mbar_wait_warp(&sh->fin[uc & 1], ((uc - 2) >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) sh->special[uc & 1][warp - 8] = 0;
+        __syncwarp();
+      }
+      if (it.block < 0) continue;
+      const int vs = blocks % kPtV;
+      if (!mbar_wait_warp(&sh->v_full[vs], (blocks / kPtV) & 1)) {
+        failed = true;
+        break;
+      }
+      ++blocks;
+      if (it.flags & kPtEdge) {
+        const int r0 = max(it.pos0 + 1 - it.block * kBlock, 0);  // first row to look at
+        uint8_t* stage = v_ring + vs * kPtTile + (ct & 7) * 16;
+        uint32_t any = 0u;
+#pragma unroll 2
+        for (int r = (r0 & ~15) + (ct >> 3); r < kBlock; r += 16) {
+          const uint4 x = lds128(stage + r * 128), y = lds128(stage + kPtHalf + r * 128);
+          const uint32_t s = bf16_special(x.x) | bf16_special(x.y) | bf16_special(x.z) | bf16_special(x.w) | bf16_special(y.x) |
+                             bf16_special(y.y) | bf16_special(y.z) | bf16_special(y.w);
+          any |= r >= r0 ? s : 0u;
+        }
+        if (any != 0u) {
+          sh->special[uc & 1][warp - 8] = 1;
+          auto clear = [](uint32_t w) {
+            const uint32_t s = bf16_special(w);
+            return w & ~(s | (s - (s >> 15)));  // (whole halves: the top bit and the 15 below it)
+          };
+#pragma unroll 1
+          for (int r = (r0 & ~15) + (ct >> 3); r < kBlock; r += 16) {
+            if (r < r0) continue;
 #pragma unroll
-      for (int s = 16; s; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-      z *= a.scale_log2;
-      M = fmaxf(M, z);  // (a NaN is left aside here and reaches the sums)
-      const float ref = M == -INFINITY ? 0.f : M, f = exp2f(was - ref), p = exp2f(z - ref);
-      was = M;
-      l = l * f + p;
-      o = make_float4(o.x * f + p * v.x, o.y * f + p * v.y, o.z * f + p * v.z, o.w * f + p * v.w);
+            for (int half = 0; half < 2; ++half) {
+              uint8_t* p = stage + half * kPtHalf + r * 128;
+              const uint4 x = lds128(p);
+              *reinterpret_cast<uint4*>(p) = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->v_ok[vs]);
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int64_t row = static_cast<int64_t>(token) * H + h;
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv), y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(a.out + row * kDim + 4 * lane) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    if (lane == 0 && a.lse != nullptr) a.lse[row] = (M + log2f(l)) * 0.6931471805599453f;
+  } else if (warp == 12) {
+    // ---- producer: records and copies
+    const int units = a.plan[0];
+    int x0 = 0, x1 = 0;
+    if (units > 0) {
+      const int whole = a.plan[1];
+      const int64_t E = static_cast<int64_t>(a.prefix[units]) * G;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        x0 = x1;
+        x1 = ft_cut(a.prefix, units, G, E, blockIdx.x + i, gridDim.x, whole);
+      }
+    }
+    const uint64_t keep = l2_evict_normal_policy(), once = l2_evict_first_policy();
+    const uint32_t q_bytes = static_cast<uint32_t>(tt) * Hg * 256;
+    int n = 0, blocks = 0, tiles0 = 0, tiles1 = 0;  // records, blocks, units that used tile 0 and tile 1
+    auto record = [&](const PtItem& it) -> bool {
+      if (n >= kPtItems && !mbar_wait_warp(&sh->item_empty[n % kPtItems], (n / kPtItems - 1) & 1)) return false;
+      if (lane == 0) {
+        sh->item[n % kPtItems] = it;
+        mbar_arrive(&sh->item_full[n % kPtItems]);
+      }
+      ++n;
+      return true;
+    };
+    int u = x0 < x1 ? ft_find(a.prefix, units, G, x0) : units;
+    for (; u < units && !failed; ++u) {
+      const int64_t first = static_cast<int64_t>(a.prefix[u]) * G;
+      if (first >= x1) break;
+      const int b = ft_find(a.base, a.batch, 1, u);
+      const int q0 = a.cu_q[b], key0 = a.cu_k[b], i = u - a.base[b];
+      const PtUnit t = pt_unit(a.cu_q[b + 1] - q0, a.cu_k[b + 1] - key0, i, tt);
+      const int pages = max(t.pages, 1), steps = t.width * pages, two = t.width == 2 ? kPtTwo : 0;
+      const int token0 = q0 + i * 2 * tt, pos1 = two ? t.pos0 + tt : t.pos0;  // of slot 1's first row
+      for (int g = 0; g < G && !failed; ++g) {
+        const int64_t u0 = first + static_cast<int64_t>(g) * steps;
+        if (u0 >= x1) break;
+        const int lo = static_cast<int>(max(x0 - u0, int64_t{0}) / t.width);
+        const int hi = min(static_cast<int>((x1 - u0) / t.width), pages);
+        if (lo >= hi) continue;
+        const int place = lo == 0 && hi == pages ? -1 : lo == 0 ? 1 : 0;
+        PtItem it{0, -1, token0, t.tokens, t.pos0, key0, g, 0};
+        for (int p = lo; p < hi && !failed; ++p) {
+          const int half = p * kBlock + 63, last = half + 64;  // last keys of the block's halves
+          it.flags = two | (p == lo ? kPtNew : 0) | (p == hi - 1 ? kPtLast : 0) | (last > t.pos0 ? kPtEdge : 0) |
+                     (half > t.pos0 ? 1 : 0) << kPtHide | (last > t.pos0 ? 2 : 0) << kPtHide |
+                     (half > pos1 ? 4 : 0) << kPtHide | (last > pos1 ? 8 : 0) << kPtHide | (place + 1) << kPtPlace;
+          it.block = t.pages > 0 ? p : -1;
+          if (!record(it)) {
+            failed = true;
+            break;
+          }
+          if (it.block < 0) continue;
+          if (p == lo) {  // the unit's queries
+            for (int k = 0; k < t.width && !failed; ++k) {
+              int& used = k ? tiles1 : tiles0;
+              if (used > 0 && !mbar_wait_warp(&sh->q_empty[k], (used - 1) & 1)) {
+                failed = true;
+                break;
+              }
+              ++used;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&sh->q_full[k], q_bytes);
+                tma_box(q_tile + k * kPtTile, &maps.q, 0, g * Hg, token0 + k * tt, &sh->q_full[k], once);
+                tma_box(q_tile + k * kPtTile + kPtHalf, &maps.q, 64, g * Hg, token0 + k * tt, &sh->q_full[k], once);
+              }
+            }
+            if (failed) break;
+          }
+          const int ks = blocks % kPtK, vs = blocks % kPtV;
+          if (blocks >= kPtK && !mbar_wait_warp(&sh->k_empty[ks], (blocks / kPtK - 1) & 1)) {
+            failed = true;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh->k_full[ks], kPtTile);
+            tma_box(k_ring + ks * kPtTile, &maps.k, 0, g, key0 + p * kBlock, &sh->k_full[ks], keep);
+            tma_box(k_ring + ks * kPtTile + kPtHalf, &maps.k, 64, g, key0 + p * kBlock, &sh->k_full[ks], keep);
+          }
+          if (blocks >= kPtV && !mbar_wait_warp(&sh->v_empty[vs], (blocks / kPtV - 1) & 1)) {
+            failed = true;
+            ++blocks;  // (its K is in flight; V of this stage is not)
+            break;
+          }
+          if (lane == 0) {
+            fence_proxy_async_smem();  // the V warps' stores to the stage are before the copy
+            mbar_arrive_expect_tx(&sh->v_full[vs], kPtTile);
+            tma_box(v_ring + vs * kPtTile, &maps.v, 0, g, key0 + p * kBlock, &sh->v_full[vs], keep);
+            tma_box(v_ring + vs * kPtTile + kPtHalf, &maps.v, 64, g, key0 + p * kBlock, &sh->v_full[vs], keep);
+          }
+          ++blocks;
+        }
+      }
+    }
+    if (!failed) failed = !record(PtItem{kPtEnd, -1, 0, 0, 0, 0, 0, 0});
+    if (failed) {
+      // wait (bounded) for the copies still in flight
+      for (int k = max(0, blocks - kPtK); k < blocks; ++k) mbar_wait(&sh->k_full[k % kPtK], (k / kPtK) & 1);
+      for (int k = max(0, blocks - kPtV); k < blocks; ++k) mbar_wait(&sh->v_full[k % kPtV], (k / kPtV) & 1);
+      if (tiles0 > 0) mbar_wait(&sh->q_full[0], (tiles0 - 1) & 1);
+      if (tiles1 > 0) mbar_wait(&sh->q_full[1], (tiles1 - 1) & 1);
+    }
+  } else {
+    // ---- product issuers: warp 13 S, warp 14 P V.  Two warps, because issuing blocks while the tensor
+    // pipe is full: each waits for its operands while the other's products run.
+    const bool scores = warp == 13;
+    if (elect_one()) {
+      constexpr uint32_t kBf16 = 1u << 7 | 1u << 10;  // A and B
+      const uint32_t id_s = umma_idesc_f16(kPtRows, kBlock) | kBf16;
+      const uint32_t id_o = umma_idesc_f16(kPtRows, kDim) | kBf16 | 1u << 16;  // B MN-major
+      const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
+      int blocks = 0, done0 = 0, done1 = 0;      // blocks, steps of the slots so far
+      int start0 = 0, start1 = 0, first = 0;     // at the unit's start
+      int tiles0 = 0, tiles1 = 0;                // units that used tile 0 and tile 1
+      bool bad = false;
+      for (int n = 0; !bad; ++n) {
+        if (!mbar_wait(&sh->item_full[n % kPtItems], (n / kPtItems) & 1)) {
+          bad = true;
+          break;
+        }
+        const int flags = sh->item[n % kPtItems].flags;
+        const bool empty = sh->item[n % kPtItems].block < 0;
+        mbar_arrive(&sh->item_empty[n % kPtItems]);
+        if (flags & kPtEnd) break;
+        if (empty) continue;
+        const int width = flags & kPtTwo ? 2 : 1;
+        if (flags & kPtNew) {
+          start0 = done0;
+          start1 = done1;
+          first = blocks;
+          ++tiles0;
+          if (width == 2) ++tiles1;
+        }
+        const int ks = blocks % kPtK, vs = blocks % kPtV;
+        if (scores ? !mbar_wait(&sh->k_full[ks], (blocks / kPtK) & 1) : !mbar_wait(&sh->v_ok[vs], (blocks / kPtV) & 1)) {
+          bad = true;
+          break;
+        }
+        for (int i = 0; i < width && !bad; ++i) {
+          const int s = width == 2 ? i : (blocks - first) & 1;
+          const int d = s ? done1 : done0;
+          const bool last = i == width - 1;
+          if (scores) {
+            // S overwrites the slot's P: it waits until that has been multiplied
+            if ((flags & kPtNew && !mbar_wait(&sh->q_full[i], ((i ? tiles1 : tiles0) - 1) & 1)) ||
+                (d > 0 && !mbar_wait(&sh->pv_done[s][1], (d - 1) & 1))) {
+              bad = true;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t qd = umma_desc(qb + i * kPtTile), kd = umma_desc(kb + ks * kPtTile);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {  // 16 dims a step
+              const uint32_t off = (kk >> 2) * kPtHalf + 32 * (kk & 3);
+              umma_f16(tmem + s * 128, qd + (off >> 4), kd + (off >> 4), id_s, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&sh->s_full[s]);
+            if (flags & kPtLast) umma_commit(&sh->q_empty[i]);
+            if (last) umma_commit(&sh->k_empty[ks]);
+          } else {
+            for (int h = 0; h < 2; ++h) {  // 64 keys: the products of the first half run beside the softmax of the second
+              if (!mbar_wait(&sh->p_full[s][h], d & 1)) {
+                bad = true;
+                break;
+              }
+              tc_fence_after();
+              const bool add = h > 0 || d > (s ? start1 : start0);
+              const uint64_t vd = umma_desc_mn(vb + vs * kPtTile + h * 64 * 128, kPtHalf);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
+                umma_f16_tmem_a(tmem + kPtO + s * 128, tmem + s * 128 + h * 64 + 8 * kk, vd + ((kk * 2048) >> 4), id_o,
+                                add || kk > 0 ? 1u : 0u);
+              umma_commit(&sh->pv_done[s][h]);
+              if (last && h == 1) umma_commit(&sh->v_empty[vs]);
+            }
+          }
+          s ? ++done1 : ++done0;
+        }
+        ++blocks;
+      }
+      if (bad) {  // the products still running end before TMEM is freed
+        flag_error(a.err, MSA_DEVERR_TIMEOUT);
+        umma_commit(&sh->drain[scores]);
+        mbar_wait(&sh->drain[scores], 0);
+      }
+    }
+    __syncwarp();
   }
+  if (failed && lane == 0) flag_error(a.err, MSA_DEVERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ---------------------------------------------------------------- units cut by range boundaries
+
+// The partial states that their CTAs left, added (fp8_merge.cuh).  blockIdx.x is the boundary whose unit
+// the CTA takes if it is the unit's first cut; blockIdx.y the row (kSplit) or eight of them.
+template <bool kSplit>
+__global__ void __launch_bounds__(kFp8MergeThreads) prompt_merge_kernel(const PromptArgs a, int ctas) {
+  __shared__ Fp8MergeShared sh;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int units = a.plan[0], G = a.groups, Hg = a.heads_per_group, tt = kPtRows / Hg;
+  if (units == 0) return;
+  const int whole = a.plan[1], x = blockIdx.x;
+  const int64_t E = static_cast<int64_t>(a.prefix[units]) * G;
+  const int xb = ft_lo(E, x + 1, ctas);
+  if (xb >= E) return;
+  const int u = ft_find(a.prefix, units, G, xb);
+  if (a.prefix[u + 1] - a.prefix[u] <= whole) return;  // not cut
+  const int b = ft_find(a.base, a.batch, 1, u), i = u - a.base[b];
+  const PtUnit t = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], i, tt);
+  const int pages = max(t.pages, 1), steps = t.width * pages;
+  const int64_t first = static_cast<int64_t>(a.prefix[u]) * G;
+  const int g = static_cast<int>((xb - first) / steps);
+  const int64_t u0 = first + static_cast<int64_t>(g) * steps;
+  const int xa = ft_lo(E, x, ctas);
+  if ((xb - u0) / t.width == 0 || (xa > u0 && (xa - u0) / t.width > 0)) return;  // no block before it, or not the first
+  if (threadIdx.x < 32) {  // the CTAs with blocks of the unit, in order
+    int n = 0;
+    for (int c0 = x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + steps; c0 += 32) {
+      const int c = c0 + threadIdx.x;
+      const int64_t a0 = ft_lo(E, c, ctas) - u0, a1 = ft_lo(E, c + 1, ctas) - u0;
+      const int lo = static_cast<int>(max(a0, int64_t{0}) / t.width);
+      const int hi = static_cast<int>(min(a1 / t.width, static_cast<int64_t>(pages)));
+      const bool some = c < ctas && a0 < steps && lo < hi;
+      const unsigned m = __ballot_sync(0xffffffffu, some);
+      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * c + (lo == 0 ? 1 : 0);
+      n += __popc(m);
+    }
+    if (threadIdx.x == 0) sh.n = n;
+  }
+  __syncthreads();
+  if (sh.n < 2) return;  // one CTA's: written by it
+  // states lie by chunks of four dims: without kSplit a CTA's eight rows of a chunk are one 128-byte line
+  const int pr = kSplit ? blockIdx.y : blockIdx.y * 8 + (threadIdx.x & 7);
+  const int chunk = kSplit ? threadIdx.x & 31 : threadIdx.x >> 3;
+  const int row = pr & (kPtRows - 1), token = row / Hg + (pr >= kPtRows ? tt : 0);
+  if (row / Hg >= tt || token >= t.tokens) return;
+  float4 o;
+  float M, l;
+  fp8_merge_row<kSplit>(a.partial, 2 * kPtRows, pr, chunk * 2 * kPtRows + pr, sh, o, M, l);
+  if (kSplit && threadIdx.x >= 32) return;
+  const int64_t hr = static_cast<int64_t>(a.cu_q[b] + i * 2 * tt + token) * G * Hg + g * Hg + row % Hg;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  reinterpret_cast<uint2*>(a.out + hr * kDim)[chunk] =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (chunk == 0 && a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
+}
+
+// ---------------------------------------------------------------- launch
+
+size_t prompt_partial_bytes() { return static_cast<size_t>(2) * kFp8MaxCtas * kPtPlaceFloats * sizeof(float); }
+
+static cudaError_t prompt_maps(const PromptArgs& a, PromptMaps* maps) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint32_t tt = static_cast<cuuint32_t>(prompt_tile_tokens(a.heads_per_group));
+  const struct {
+    CUtensorMap* map;
+    const uint16_t* data;
+    int64_t stride;
+    int heads, tokens;
+    cuuint32_t box_heads, box_tokens;
+  } x[3] = {{&maps->q, a.q, a.q_stride, a.groups * a.heads_per_group, a.q_tokens, static_cast<cuuint32_t>(a.heads_per_group), tt},
+            {&maps->k, a.k, a.k_stride, a.groups, a.k_tokens, 1, kBlock},
+            {&maps->v, a.v, a.v_stride, a.groups, a.k_tokens, 1, kBlock}};
+  for (const auto& t : x) {
+    // (without keys nothing is copied: any address)
+    const void* data = t.tokens > 0 ? t.data : a.q;
+    const cuuint64_t dims[3] = {kDim, static_cast<cuuint64_t>(t.heads), static_cast<cuuint64_t>(t.tokens > 0 ? t.tokens : 1)};
+    const cuuint64_t strides[2] = {kDim * 2, static_cast<cuuint64_t>(t.stride) * 2};
+    const cuuint32_t box[3] = {64, t.box_heads, t.box_tokens}, estr[3] = {1, 1, 1};
+    const CUresult r = encode(t.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(data), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s) {
-  return launch_dependent(prompt_attn_kernel, dim3(num_sms * 8), 256, 0, s, a);
+  PromptMaps maps;
+  cudaError_t e = prompt_maps(a, &maps);
+  if (e != cudaSuccess) return e;
+  const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas;
+  if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(prompt_attn_kernel), kPtSmem)) != cudaSuccess) return e;
+  if ((e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a, ctas)) != cudaSuccess) return e;
+  if ((e = launch_dependent(prompt_attn_kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps)) != cudaSuccess) return e;
+  if (ctas == 1) return cudaSuccess;
+  const int64_t units = prompt_max_units(a.q_tokens, a.batch, a.heads_per_group) * a.groups;
+  return ctas / units >= kFp8MergeSplitParts
+             ? launch_dependent(prompt_merge_kernel<true>, dim3(ctas - 1, 2 * kPtRows), kFp8MergeThreads, 0, s, a, ctas)
+             : launch_dependent(prompt_merge_kernel<false>, dim3(ctas - 1, 2 * kPtRows / 8), kFp8MergeThreads, 0, s, a, ctas);
 }
 
 }  // namespace msa
