@@ -38,32 +38,36 @@
 namespace msa {
 
 constexpr int kPtRows = 128;  // rows per tile
-constexpr int kPtThreads = 480;
+constexpr int kPtThreads = 512;
 constexpr int kPtK = 3, kPtV = 2;             // stages of 128 keys
-constexpr int kPtItems = 8;                   // records in flight
+constexpr int kPtItems = 2;                   // units known ahead
 constexpr int kPtTile = kPtRows * kDim * 2;   // bytes of a Q tile, and of a stage
 constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
 constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
+#ifndef PT_UNIT_COST
+#define PT_UNIT_COST 8
+#endif
+constexpr int kPtUnitCost = PT_UNIT_COST;
 
-// A block of 128 keys of a unit (or a unit without keys), for the roles that work on it.
+// A unit, or the part of it that this CTA has: blocks lo .. hi - 1 of 128 keys (none of a unit whose rows see no key).
 struct alignas(16) PtItem {
-  int flags;   // kPtEnd ...; place + 1 from kPtPlace on
-  int block;   // -1: no keys
+  int flags;   // kPtEnd: no more units; kPtTwo: two tiles; place of its partial state + 1 from kPtPlace on
+  int lo, hi;
   int token0;  // the unit's first query token, in the packed list
   int tokens;  // of the unit
   int pos0;    // the first one's position
   int key0;    // the sequence's first key, in the packed list
   int g;
-  int pad;
+  // the first of its blocks that some row of the unit does not see whole
+  __device__ __forceinline__ int edge() const { return min(max(lo, max(pos0 + 1, 0) / kBlock), hi); }
 };
-// Bits: no more items; first item of a unit, last one; the unit has two tiles; some row of it must not see all of the
-// block's keys; some row of slot s's tile must not see all of half h of them (bit kPtHide + 2 s + h).
-constexpr int kPtEnd = 1, kPtNew = 2, kPtLast = 4, kPtTwo = 8, kPtEdge = 16, kPtHide = 5, kPtPlace = 9;
+constexpr int kPtEnd = 1, kPtTwo = 2, kPtPlace = 2;
 
 struct PtShared {
-  uint64_t k_full[kPtK], k_empty[kPtK], v_full[kPtV], v_ok[kPtV], v_empty[kPtV];
+  uint64_t k_full[kPtK], k_empty[kPtK], v_empty[kPtV];
+  uint64_t v_full[kPtV], v_edge[kPtV], v_ok[kPtV];  // plain blocks by turns; edge blocks by turns: copied, looked through
   uint64_t item_full[kPtItems], item_empty[kPtItems];
   uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [slot], [slot][half of the keys]
   uint64_t q_full[2], q_empty[2];                   // [tile]
@@ -73,7 +77,7 @@ struct PtShared {
   uint32_t tmem;
   alignas(16) int special[2][4];                    // a V row taken care of by warp 8 + i (by the unit's parity)
   PtItem item[kPtItems];
-  float other_m[kPtRows], other_l[kPtRows];
+  float other_m[kPtRows], other_l[kPtRows], other_fix[kPtRows];
 };
 constexpr size_t kPtSmem = 1024 + 2 * kPtTile + (kPtK + kPtV) * kPtTile + sizeof(PtShared);
 static_assert(kPtSmem <= 232448, "227 KB of shared memory per CTA");
@@ -87,6 +91,11 @@ struct PromptMaps {
 // Unit i of a sequence.
 struct PtUnit {
   int tokens, pos0, width, pages;  // pages 0: no row has a key
+  // its share of the flat list, and the blocks before place y of that
+  __device__ __forceinline__ int cost() const { return width * max(pages, 1) + kPtUnitCost; }
+  __device__ __forceinline__ int block_at(int64_t y) const {
+    return static_cast<int>(max(min(y, static_cast<int64_t>(cost())) - kPtUnitCost, int64_t{0}) / width);
+  }
 };
 __device__ __forceinline__ PtUnit pt_unit(int Lq, int Lk, int i, int tile_tokens) {
   PtUnit t;
@@ -178,7 +187,7 @@ __global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const Promp
         }
       }
       const PtUnit t = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], u - s_base[b], tt);
-      n = t.width * max(t.pages, 1);
+      n = t.cost();
     }
     const int at = pt_prefix(n, steps, s_sum);
     if (u < units) a.prefix[u] = at;
@@ -197,10 +206,49 @@ __device__ __forceinline__ void tma_box(void* dst, const void* map, int x, int y
       : "memory");
 }
 
+// The warpgroup's registers from here on: a multiple of 8 a thread.  The four shares are 2 x 192 + 2 x 64, what the
+// 512 threads were launched with (128).
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
+}
+
+// a += the low half of w, b += the high half
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t w) {
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n add.rn.f32.bf16 %0, lo, %0;\n add.rn.f32.bf16 %1, hi, %1;\n}"
+      : "+f"(a), "+f"(b)
+      : "r"(w));
+}
+
+// Lane q of four has piece i of lane i's afterwards where it had its own piece i: w[i] of lane q <-> w[q] of lane i
+__device__ __forceinline__ void turn_pair(uint4& a, uint4& b, int bit) {  // (the lanes without the bit send b, the others a)
+  const bool odd = threadIdx.x & bit;
+  const uint4 give = odd ? a : b;
+  uint4 got;
+  got.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+  got.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+  got.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+  got.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+  if (odd)
+    a = got;
+  else
+    b = got;
+}
+__device__ __forceinline__ void turn_quad(uint4 (&w)[4]) {
+  turn_pair(w[0], w[1], 1);
+  turn_pair(w[2], w[3], 1);
+  turn_pair(w[0], w[2], 2);
+  turn_pair(w[1], w[3], 2);
 }
 
 // The top bits of the halves of w that are infinities or NaN (exponent all ones; no half's sum carries)
@@ -224,12 +272,13 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     }
     for (int i = 0; i < kPtV; ++i) {
       mbar_init(&sh->v_full[i], 1);
+      mbar_init(&sh->v_edge[i], 1);
       mbar_init(&sh->v_ok[i], 4);
       mbar_init(&sh->v_empty[i], 1);
     }
     for (int i = 0; i < kPtItems; ++i) {
       mbar_init(&sh->item_full[i], 1);
-      mbar_init(&sh->item_empty[i], 14);  // eight softmax warps, four of V, two issuers
+      mbar_init(&sh->item_empty[i], 15);  // eight softmax warps, four of V, two issuers, the loader of V
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
@@ -273,19 +322,19 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
   };
 
   if (warp < 8) {
+    registers_up<192>();
     // ---- softmax of slot `slot`: row r of its tile
     const int slot = warp >> 2, r = tid & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kPtO + slot * 128 + lane_base;
     const float f = finite_factor(a.scale_log2);
     const int my_token = r / Hg, my_head = r - my_token * Hg;
-    // steps of this slot and of the other one so far, blocks, units
-    int done = 0, done_o = 0, blocks = 0, uc = -1;
-    bool mine = false, others = false, turn = false, shared_par = false, one_before = false;
-    float M = -INFINITY, l = 0.f;
-    int pos = 0, first_block = 0;
+    int done = 0, done_o = 0, edges = 0, uc = -1;  // steps of this slot and of the other one, edge blocks, units so far
+    bool mine = false, others = false, shared_par = false, one_before = false;
+    float M = -INFINITY, l = 0.f, l_bf16 = 0.f;    // (l_bf16: of P as it is multiplied)
+    int pos = 0;
 
-    // writes the unit's rows (or its partial state); `it` is its last record
+    // writes the unit's rows (or its partial state)
     auto finish = [&](const PtItem& it) -> bool {
       const bool two = it.flags & kPtTwo;
       const int place = (it.flags >> kPtPlace) - 1;
@@ -294,6 +343,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         if (slot == 1) {
           sh->other_m[r] = M;
           sh->other_l[r] = l;
+          sh->other_fix[r] = l_bf16 != 0.f ? l / l_bf16 : 1.f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->other);
           return true;
@@ -302,78 +352,87 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         if (others && !mbar_wait_warp(&sh->pv_done[1][1], (done_o - 1) & 1)) return false;
       }
       tc_fence_after();
-      // state of the row = fa * own O + fb * the other slot's O
-      float fa = mine ? 1.f : 0.f, fb = 0.f;
+      // O is put right by the ratio of the sums of P before and after its rounding, the state of the row is
+      // then fa * own O + fb * the other slot's O
+      const float fix = mine && l_bf16 != 0.f ? l / l_bf16 : 1.f;
+      float fa = mine ? fix : 0.f, fb = 0.f;
       const bool both = !two && others;
       if (both) {
         const float mo = sh->other_m[r], lo = sh->other_l[r];
         const float mn = fmaxf(M, mo);
-        fa = mn == -INFINITY ? 1.f : ex2(M - mn);
-        fb = mn == -INFINITY ? 1.f : ex2(mo - mn);
-        l = l * fa + lo * fb;
+        const float wa = mn == -INFINITY ? 1.f : ex2(M - mn), wb = mn == -INFINITY ? 1.f : ex2(mo - mn);
+        fa *= wa;
+        fb = wb * sh->other_fix[r];
+        l = l * wa + lo * wb;
         M = mn;
       }
       const int t = my_token + (two && slot ? tt : 0);  // token of the unit
       const bool valid = my_token < tt && t < it.tokens;
       const float inv = l != 0.f ? 1.f / l : 0.f;       // (NaN counts as a sum)
-      const float out_f = place < 0 ? inv : 1.f;
-      const int64_t hr = static_cast<int64_t>(it.token0 + t) * H + it.g * Hg + my_head;
+      if (place < 0) {
+        fa *= inv;
+        fb *= inv;
+      }
+      const int64_t row0 = static_cast<int64_t>(it.token0) * H + it.g * Hg;  // row of the outputs of the unit's first one
+      const int off = t * H + my_head;
       const int pr = r + (two && slot ? kPtRows : 0);   // row of the partial state
       float* part = place < 0 ? nullptr : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats;
       const int4 sp = *reinterpret_cast<const int4*>(sh->special[uc & 1]);
-      const bool special = first_block >= 0 && (sp.x | sp.y | sp.z | sp.w) != 0;
+      const bool special = it.lo < it.hi && (sp.x | sp.y | sp.z | sp.w) != 0;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {  // 16 dims
-        uint32_t x[16];
-        float v[16];
+      for (int c = 0; c < 4; ++c) {  // 32 dims
+        uint32_t x[32];
+        float v[32];
         if (mine) {
-          tmem_ld16(tO + 16 * c, x);
+          tmem_ld32(tO + 32 * c, x);
           tmem_wait_ld(x);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = mine ? __uint_as_float(x[i]) * fa : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = mine ? __uint_as_float(x[i]) * fa : 0.f;
         if (both) {
-          tmem_ld16(tO + 128 + 16 * c, x);
+          tmem_ld32(tO + 128 + 32 * c, x);
           tmem_wait_ld(x);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(x[i]) * fb;
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), fb, v[i]);
         }
         if (special) {
           // what was taken out of V comes back for the rows that see its key
-          const int last = min(pos, it.block * kBlock + kBlock - 1);
+          const int last = min(pos, it.hi * kBlock - 1);
 #pragma unroll 1
-          for (int j = max(it.pos0 + 1, first_block * kBlock); j <= last; ++j) {
-            const uint16_t* src = a.v + (it.key0 + j) * a.v_stride + it.g * kDim + 16 * c;
+          for (int j = max(it.pos0 + 1, it.lo * kBlock); j <= last; ++j) {
+            const uint16_t* src = a.v + (it.key0 + j) * a.v_stride + it.g * kDim + 32 * c;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 32; ++i) {
               const float y = __uint_as_float(static_cast<uint32_t>(src[i]) << 16);
               if (!(fabsf(y) < INFINITY)) v[i] += y;
             }
           }
         }
+        if (place < 0) {
+          // pieces of 16 bytes turned among four lanes, so that these write a row's 64 bytes
+          uint4 w[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= out_f;
-        if (valid) {
-          if (place < 0) {
-            uint32_t w[8];
+          for (int j = 0; j < 4; ++j)
+            w[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                              pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          turn_quad(w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-            uint4* dst = reinterpret_cast<uint4*>(a.out + hr * kDim + 16 * c);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          } else {
-            // four dims of all rows together: the lanes of a store are neighbouring rows
-            float4* dst = reinterpret_cast<float4*>(part) + 4 * c * (2 * kPtRows) + pr;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              dst[j * 2 * kPtRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int i = 0; i < 4; ++i) {
+            const int to = __shfl_sync(0xffffffffu, valid ? off : -1, (lane & ~3) + i);
+            if (to >= 0) *reinterpret_cast<uint4*>(a.out + (row0 + to) * kDim + 32 * c + 8 * (lane & 3)) = w[i];
           }
+        } else if (valid) {
+          // four dims of all rows together: the lanes of a store are neighbouring rows
+          float4* dst = reinterpret_cast<float4*>(part) + 8 * c * (2 * kPtRows) + pr;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[j * 2 * kPtRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
         __syncwarp();
       }
       if (valid) {
         if (place < 0) {
-          if (a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
+          if (a.lse != nullptr) a.lse[row0 + off] = fp8_lse(M, l);
         } else {
           part[2 * kPtRows * kDim + pr] = M;
           part[2 * kPtRows * (kDim + 1) + pr] = l;
@@ -383,166 +442,151 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       return true;
     };
 
-    for (int n = 0;; ++n) {
+    for (;;) {
       PtItem it;
-      if (!take_item(n, it)) {
+      if (!take_item(++uc, it)) {
         failed = true;
         break;
       }
       if (it.flags & kPtEnd) break;
       const bool two = it.flags & kPtTwo;
-      if (it.flags & kPtNew) {
-        ++uc;
-        // slot 0 reads slot 1's O and statistics of a one-tile unit: slot 1 goes on when it has
-        if (slot == 1 && one_before && !mbar_wait_warp(&sh->fin[(uc - 1) & 1], ((uc - 1) >> 1) & 1)) {
-          failed = true;
-          break;
-        }
-        mine = others = turn = false;
-        M = -INFINITY;
-        l = 0.f;
-        first_block = it.block;
-        pos = it.pos0 + min(min(my_token, tt - 1) + (two && slot ? tt : 0), it.tokens - 1);
+      // slot 0 reads slot 1's O and statistics of a one-tile unit: slot 1 goes on when it has
+      if (slot == 1 && one_before && !mbar_wait_warp(&sh->fin[(uc - 1) & 1], ((uc - 1) >> 1) & 1)) {
+        failed = true;
+        break;
       }
-      bool step = it.block >= 0;
-      int vstage = 0, vphase = 0;
-      if (step) {
-        vstage = blocks % kPtV;
-        vphase = (blocks / kPtV) & 1;
-        ++blocks;
-        if (!two) {  // the blocks alternate between the slots
-          step = turn == (slot == 1);
-          turn = !turn;
-          if (!step) {
-            ++done_o;
-            others = true;
-          }
-        }
-      }
-      if (step) {
+      M = -INFINITY;
+      l = l_bf16 = 0.f;
+      pos = it.pos0 + min(min(my_token, tt - 1) + (two && slot ? tt : 0), it.tokens - 1);
+      // with one tile the blocks alternate between the slots
+      const int edge = it.edge(), step = two ? 1 : 2, first = it.lo + (two ? 0 : slot);
+      const int tile0 = it.pos0 + (two && slot ? tt : 0);  // position of the tile's first row
+      mine = first < it.hi;
+      others = two ? mine : it.lo + (slot ^ 1) < it.hi;
+      done_o += two ? it.hi - it.lo : (it.hi - it.lo + slot) / 2;
+#pragma unroll 1
+      for (int p = first; p < it.hi; p += step) {
         // what the V warps found in a block that not every row sees whole is read when the unit is written: seeing the
         // stage ready orders it before that (the stage is not used again before this step's P)
+        const int e = edges + p - edge;
         if (!mbar_wait_warp(&sh->s_full[slot], done & 1) ||
-            (it.flags & kPtEdge && !mbar_wait_warp(&sh->v_ok[vstage], vphase))) {
+            (p >= edge && !mbar_wait_warp(&sh->v_ok[e % kPtV], (e / kPtV) & 1))) {
           failed = true;
           break;
         }
         tc_fence_after();
+        uint32_t v[2][64];
+        float mx, mx1;
+        tmem_ld64_max(tS, v[0], mx);
+        tmem_ld64_max(tS + 64, v[1], mx1);
+        tmem_wait_ld(v[0]);
+        tmem_wait_ld(v[1]);
+        asm volatile("" : "+f"(mx), "+f"(mx1));
+        mx = fmaxf(mx, mx1);
+        if (p * kBlock + kBlock - 1 > tile0) {
+          // some row of the tile must not see one of these keys: -inf over its scores, and the maximum again
+          const int vis = pos - p * kBlock + 1;  // visible columns
+          mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 128; ++j) {
+            uint32_t& x = v[j >> 6][j & 63];
+            x = j < vis ? x : 0xff800000u;
+            mx = fmaxf(mx, __uint_as_float(x));
+          }
+        }
+        mx *= f;
+        if (__any_sync(0xffffffffu, mx > M)) {
+          float alpha = 1.f;
+          if (mx > M) {
+            const float mn = ceilf(mx) + kPtRefSet;
+            alpha = ex2(M - mn);
+            M = mn;
+            l *= alpha;
+            l_bf16 *= alpha;
+          }
+          if (p > first) {  // O as the products so far leave it, rescaled
+            if (!mbar_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t y[16];
+              tmem_ld16(tO + 16 * c, y);
+              tmem_wait_ld(y);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * alpha);
+              tmem_st16(tO + 16 * c, y);
+            }
+          }
+        }
+        // P goes over the first 32 columns of each half of S
+        const float c0 = M == -INFINITY ? 0.f : -M;
+        const float2 ff = make_float2(f, f), cc = make_float2(c0, c0);
         float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
+        float sum_bf16[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t tH = tS + 64 * h;
-          uint32_t v[64];
-          float mx;
-          tmem_ld64_max(tH, v, mx);
-          tmem_wait_ld(v);
-          asm volatile("" : "+f"(mx));
-          if (it.flags >> (kPtHide + 2 * slot + h) & 1) {
-            // some row of the tile must not see one of these keys: -inf over its scores, and the maximum again
-            const int vis = pos - it.block * kBlock - 64 * h + 1;  // visible columns
-            mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              v[j] = j < vis ? v[j] : 0xff800000u;
-              mx = fmaxf(mx, __uint_as_float(v[j]));
-            }
-          }
-          mx *= f;
-          if (__any_sync(0xffffffffu, mx > M)) {
-            float alpha = 1.f;
-            if (mx > M) {
-              const float mn = ceilf(mx) + kPtRefSet;
-              alpha = ex2(M - mn);
-              M = mn;
-              l *= alpha;
-              sum.x *= alpha;
-              sum.y *= alpha;
-            }
-            if (mine || h > 0) {  // O as the products issued so far leave it, rescaled
-              if (!mbar_wait_warp(&sh->pv_done[slot][h ^ 1], (h ? done : done - 1) & 1)) {
-                failed = true;
-                break;
-              }
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t y[16];
-                tmem_ld16(tO + 16 * c, y);
-                tmem_wait_ld(y);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * alpha);
-                tmem_st16(tO + 16 * c, y);
-              }
-            }
-          }
-          // P goes over the first 32 columns of S
-          const float c0 = M == -INFINITY ? 0.f : -M;
-          const float2 ff = make_float2(f, f), cc = make_float2(c0, c0);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const int k = 32 * i + 2 * j;
-              const float2 e = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, cc);
-              const float2 p = make_float2(ex2(e.x), ex2(e.y));
-              sum = add2(sum, p);
-              pk[j] = pack_bf16x2(p.x, p.y);
+              const float2 x = fma2(make_float2(__uint_as_float(v[h][k]), __uint_as_float(v[h][k + 1])), ff, cc);
+              const float2 y = make_float2(ex2(x.x), ex2(x.y));
+              sum = add2(sum, y);
+              pk[j] = pack_bf16x2(y.x, y.y);
+              add_bf16x2(sum_bf16[2 * (j & 1)], sum_bf16[2 * (j & 1) + 1], pk[j]);
             }
-            tmem_st16(tH + 16 * i, pk);
+            tmem_st16(tS + 64 * h + 16 * i, pk);
           }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->p_full[slot][h]);
         }
-        if (failed) break;
         ++done;
-        mine = true;
-        if (two) ++done_o;
         l += sum.x + sum.y;
+        l_bf16 += (sum_bf16[0] + sum_bf16[1]) + (sum_bf16[2] + sum_bf16[3]);
       }
-      if (it.flags & kPtLast) {
-        if (!finish(it)) {
-          failed = true;
-          break;
-        }
-        one_before = !two;
-        if (!two) shared_par = !shared_par;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->fin[uc & 1]);
+      if (failed || !finish(it)) {
+        failed = true;
+        break;
       }
+      edges += it.hi - edge;
+      one_before = !two;
+      if (!two) shared_par = !shared_par;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->fin[uc & 1]);
     }
   } else if (warp < 12) {
+    registers_down<64>();
     // ---- V: infinities and NaN out of the rows that not every row of the unit sees
     const int ct = tid - 256;
-    int blocks = 0, uc = -1;
-    for (int n = 0;; ++n) {
+    int blocks = 0, edges = 0;
+    for (int uc = 0; !failed; ++uc) {
       PtItem it;
-      if (!take_item(n, it)) {
+      if (!take_item(uc, it)) {
         failed = true;
         break;
       }
       if (it.flags & kPtEnd) break;
-      if (it.flags & kPtNew) {
-        ++uc;
-        // the unit that used these marks is written
-        if (uc >= 2 && !mbar_wait_warp(&sh->fin[uc & 1], ((uc - 2) >> 1) & 1)) {
-          failed = true;
-          break;
-        }
-        if (lane == 0) sh->special[uc & 1][warp - 8] = 0;
-        __syncwarp();
-      }
-      if (it.block < 0) continue;
-      const int vs = blocks % kPtV;
-      if (!mbar_wait_warp(&sh->v_full[vs], (blocks / kPtV) & 1)) {
+      // the unit that used these marks is written
+      if (uc >= 2 && !mbar_wait_warp(&sh->fin[uc & 1], ((uc - 2) >> 1) & 1)) {
         failed = true;
         break;
       }
-      ++blocks;
-      if (it.flags & kPtEdge) {
-        const int r0 = max(it.pos0 + 1 - it.block * kBlock, 0);  // first row to look at
+      if (lane == 0) sh->special[uc & 1][warp - 8] = 0;
+      __syncwarp();
+      for (int p = it.edge(); p < it.hi; ++p, ++edges) {
+        const int vs = (blocks + p - it.lo) % kPtV;
+        if (!mbar_wait_warp(&sh->v_edge[edges % kPtV], (edges / kPtV) & 1)) {
+          failed = true;
+          break;
+        }
+        const int r0 = max(it.pos0 + 1 - p * kBlock, 0);  // first row to look at
         uint8_t* stage = v_ring + vs * kPtTile + (ct & 7) * 16;
         uint32_t any = 0u;
 #pragma unroll 2
@@ -563,19 +607,22 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
             if (r < r0) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint8_t* p = stage + half * kPtHalf + r * 128;
-              const uint4 x = lds128(p);
-              *reinterpret_cast<uint4*>(p) = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
+              uint8_t* at = stage + half * kPtHalf + r * 128;
+              const uint4 x = lds128(at);
+              *reinterpret_cast<uint4*>(at) = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
             }
           }
         }
         fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->v_ok[edges % kPtV]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->v_ok[vs]);
+      blocks += it.hi - it.lo;
     }
-  } else if (warp == 12) {
-    // ---- producer: records and copies
+  } else {
+   registers_down<64>();
+   if (warp == 12) {
+    // ---- producer: units and the copies of Q and K
     const int units = a.plan[0];
     int x0 = 0, x1 = 0;
     if (units > 0) {
@@ -589,7 +636,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     }
     const uint64_t keep = l2_evict_normal_policy(), once = l2_evict_first_policy();
     const uint32_t q_bytes = static_cast<uint32_t>(tt) * Hg * 256;
-    int n = 0, blocks = 0, tiles0 = 0, tiles1 = 0;  // records, blocks, units that used tile 0 and tile 1
+    int n = 0, blocks = 0, tiles0 = 0, tiles1 = 0;  // units, blocks, units that used tile 0 and tile 1
     auto record = [&](const PtItem& it) -> bool {
       if (n >= kPtItems && !mbar_wait_warp(&sh->item_empty[n % kPtItems], (n / kPtItems - 1) & 1)) return false;
       if (lane == 0) {
@@ -606,44 +653,34 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       const int b = ft_find(a.base, a.batch, 1, u);
       const int q0 = a.cu_q[b], key0 = a.cu_k[b], i = u - a.base[b];
       const PtUnit t = pt_unit(a.cu_q[b + 1] - q0, a.cu_k[b + 1] - key0, i, tt);
-      const int pages = max(t.pages, 1), steps = t.width * pages, two = t.width == 2 ? kPtTwo : 0;
-      const int token0 = q0 + i * 2 * tt, pos1 = two ? t.pos0 + tt : t.pos0;  // of slot 1's first row
+      const int pages = max(t.pages, 1), cost = t.cost(), token0 = q0 + i * 2 * tt;
       for (int g = 0; g < G && !failed; ++g) {
-        const int64_t u0 = first + static_cast<int64_t>(g) * steps;
+        const int64_t u0 = first + static_cast<int64_t>(g) * cost;
         if (u0 >= x1) break;
-        const int lo = static_cast<int>(max(x0 - u0, int64_t{0}) / t.width);
-        const int hi = min(static_cast<int>((x1 - u0) / t.width), pages);
+        const int lo = t.block_at(x0 - u0), hi = t.block_at(x1 - u0);
         if (lo >= hi) continue;
         const int place = lo == 0 && hi == pages ? -1 : lo == 0 ? 1 : 0;
-        PtItem it{0, -1, token0, t.tokens, t.pos0, key0, g, 0};
-        for (int p = lo; p < hi && !failed; ++p) {
-          const int half = p * kBlock + 63, last = half + 64;  // last keys of the block's halves
-          it.flags = two | (p == lo ? kPtNew : 0) | (p == hi - 1 ? kPtLast : 0) | (last > t.pos0 ? kPtEdge : 0) |
-                     (half > t.pos0 ? 1 : 0) << kPtHide | (last > t.pos0 ? 2 : 0) << kPtHide |
-                     (half > pos1 ? 4 : 0) << kPtHide | (last > pos1 ? 8 : 0) << kPtHide | (place + 1) << kPtPlace;
-          it.block = t.pages > 0 ? p : -1;
-          if (!record(it)) {
+        if (!record(PtItem{(t.width == 2 ? kPtTwo : 0) | (place + 1) << kPtPlace, lo, t.pages > 0 ? hi : lo, token0, t.tokens,
+                           t.pos0, key0, g})) {
+          failed = true;
+          break;
+        }
+        if (t.pages == 0) continue;
+        for (int k = 0; k < t.width && !failed; ++k) {  // the unit's queries
+          int& used = k ? tiles1 : tiles0;
+          if (used > 0 && !mbar_wait_warp(&sh->q_empty[k], (used - 1) & 1)) {
             failed = true;
             break;
           }
-          if (it.block < 0) continue;
-          if (p == lo) {  // the unit's queries
-            for (int k = 0; k < t.width && !failed; ++k) {
-              int& used = k ? tiles1 : tiles0;
-              if (used > 0 && !mbar_wait_warp(&sh->q_empty[k], (used - 1) & 1)) {
-                failed = true;
-                break;
-              }
-              ++used;
-              if (lane == 0) {
-                mbar_arrive_expect_tx(&sh->q_full[k], q_bytes);
-                tma_box(q_tile + k * kPtTile, &maps.q, 0, g * Hg, token0 + k * tt, &sh->q_full[k], once);
-                tma_box(q_tile + k * kPtTile + kPtHalf, &maps.q, 64, g * Hg, token0 + k * tt, &sh->q_full[k], once);
-              }
-            }
-            if (failed) break;
+          ++used;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh->q_full[k], q_bytes);
+            tma_box(q_tile + k * kPtTile, &maps.q, 0, g * Hg, token0 + k * tt, &sh->q_full[k], once);
+            tma_box(q_tile + k * kPtTile + kPtHalf, &maps.q, 64, g * Hg, token0 + k * tt, &sh->q_full[k], once);
           }
-          const int ks = blocks % kPtK, vs = blocks % kPtV;
+        }
+        for (int p = lo; p < hi && !failed; ++p) {
+          const int ks = blocks % kPtK;
           if (blocks >= kPtK && !mbar_wait_warp(&sh->k_empty[ks], (blocks / kPtK - 1) & 1)) {
             failed = true;
             break;
@@ -653,30 +690,51 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
             tma_box(k_ring + ks * kPtTile, &maps.k, 0, g, key0 + p * kBlock, &sh->k_full[ks], keep);
             tma_box(k_ring + ks * kPtTile + kPtHalf, &maps.k, 64, g, key0 + p * kBlock, &sh->k_full[ks], keep);
           }
-          if (blocks >= kPtV && !mbar_wait_warp(&sh->v_empty[vs], (blocks / kPtV - 1) & 1)) {
-            failed = true;
-            ++blocks;  // (its K is in flight; V of this stage is not)
-            break;
-          }
-          if (lane == 0) {
-            fence_proxy_async_smem();  // the V warps' stores to the stage are before the copy
-            mbar_arrive_expect_tx(&sh->v_full[vs], kPtTile);
-            tma_box(v_ring + vs * kPtTile, &maps.v, 0, g, key0 + p * kBlock, &sh->v_full[vs], keep);
-            tma_box(v_ring + vs * kPtTile + kPtHalf, &maps.v, 64, g, key0 + p * kBlock, &sh->v_full[vs], keep);
-          }
           ++blocks;
         }
       }
     }
-    if (!failed) failed = !record(PtItem{kPtEnd, -1, 0, 0, 0, 0, 0, 0});
+    if (!failed) failed = !record(PtItem{kPtEnd, 0, 0, 0, 0, 0, 0, 0});
     if (failed) {
       // wait (bounded) for the copies still in flight
       for (int k = max(0, blocks - kPtK); k < blocks; ++k) mbar_wait(&sh->k_full[k % kPtK], (k / kPtK) & 1);
-      for (int k = max(0, blocks - kPtV); k < blocks; ++k) mbar_wait(&sh->v_full[k % kPtV], (k / kPtV) & 1);
       if (tiles0 > 0) mbar_wait(&sh->q_full[0], (tiles0 - 1) & 1);
       if (tiles1 > 0) mbar_wait(&sh->q_full[1], (tiles1 - 1) & 1);
     }
-  } else {
+   } else if (warp == 15) {
+    // ---- the copies of V
+    const uint64_t keep = l2_evict_normal_policy();
+    int blocks = 0, plain = 0, edges = 0;
+    for (int uc = 0; !failed; ++uc) {
+      PtItem it;
+      if (!take_item(uc, it)) {
+        failed = true;
+        break;
+      }
+      if (it.flags & kPtEnd) break;
+      const int edge = it.edge();
+      for (int p = it.lo; p < it.hi; ++p) {
+        const int vs = blocks % kPtV;
+        if (blocks >= kPtV && !mbar_wait_warp(&sh->v_empty[vs], (blocks / kPtV - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) {
+          fence_proxy_async_smem();  // the V warps' stores to the stage are before the copy
+          uint64_t* bar = p < edge ? &sh->v_full[plain % kPtV] : &sh->v_edge[edges % kPtV];
+          mbar_arrive_expect_tx(bar, kPtTile);
+          tma_box(v_ring + vs * kPtTile, &maps.v, 0, it.g, it.key0 + p * kBlock, bar, keep);
+          tma_box(v_ring + vs * kPtTile + kPtHalf, &maps.v, 64, it.g, it.key0 + p * kBlock, bar, keep);
+        }
+        ++blocks;
+        p < edge ? ++plain : ++edges;
+      }
+    }
+    if (failed) {  // wait (bounded) for the copies still in flight
+      for (int k = max(0, plain - kPtV); k < plain; ++k) mbar_wait(&sh->v_full[k % kPtV], (k / kPtV) & 1);
+      for (int k = max(0, edges - kPtV); k < edges; ++k) mbar_wait(&sh->v_edge[k % kPtV], (k / kPtV) & 1);
+    }
+   } else {
     // ---- product issuers: warp 13 S, warp 14 P V.  Two warps, because issuing blocks while the tensor
     // pipe is full: each waits for its operands while the other's products run.
     const bool scores = warp == 13;
@@ -685,74 +743,73 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       const uint32_t id_s = umma_idesc_f16(kPtRows, kBlock) | kBf16;
       const uint32_t id_o = umma_idesc_f16(kPtRows, kDim) | kBf16 | 1u << 16;  // B MN-major
       const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
-      int blocks = 0, done0 = 0, done1 = 0;      // blocks, steps of the slots so far
-      int start0 = 0, start1 = 0, first = 0;     // at the unit's start
-      int tiles0 = 0, tiles1 = 0;                // units that used tile 0 and tile 1
+      int blocks = 0, done0 = 0, done1 = 0;             // blocks, steps of the slots so far
+      int plain = 0, edges = 0;                         // blocks of the two kinds in the units before
+      int tiles1 = 0, tiles0 = 0;                       // units that used tile 1 and tile 0
       bool bad = false;
       for (int n = 0; !bad; ++n) {
         if (!mbar_wait(&sh->item_full[n % kPtItems], (n / kPtItems) & 1)) {
           bad = true;
           break;
         }
-        const int flags = sh->item[n % kPtItems].flags;
-        const bool empty = sh->item[n % kPtItems].block < 0;
+        const PtItem it = sh->item[n % kPtItems];
         mbar_arrive(&sh->item_empty[n % kPtItems]);
-        if (flags & kPtEnd) break;
-        if (empty) continue;
-        const int width = flags & kPtTwo ? 2 : 1;
-        if (flags & kPtNew) {
-          start0 = done0;
-          start1 = done1;
-          first = blocks;
-          ++tiles0;
-          if (width == 2) ++tiles1;
-        }
-        const int ks = blocks % kPtK, vs = blocks % kPtV;
-        if (scores ? !mbar_wait(&sh->k_full[ks], (blocks / kPtK) & 1) : !mbar_wait(&sh->v_ok[vs], (blocks / kPtV) & 1)) {
-          bad = true;
-          break;
-        }
-        for (int i = 0; i < width && !bad; ++i) {
-          const int s = width == 2 ? i : (blocks - first) & 1;
-          const int d = s ? done1 : done0;
-          const bool last = i == width - 1;
-          if (scores) {
-            // S overwrites the slot's P: it waits until that has been multiplied
-            if ((flags & kPtNew && !mbar_wait(&sh->q_full[i], ((i ? tiles1 : tiles0) - 1) & 1)) ||
-                (d > 0 && !mbar_wait(&sh->pv_done[s][1], (d - 1) & 1))) {
-              bad = true;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t qd = umma_desc(qb + i * kPtTile), kd = umma_desc(kb + ks * kPtTile);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {  // 16 dims a step
-              const uint32_t off = (kk >> 2) * kPtHalf + 32 * (kk & 3);
-              umma_f16(tmem + s * 128, qd + (off >> 4), kd + (off >> 4), id_s, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(&sh->s_full[s]);
-            if (flags & kPtLast) umma_commit(&sh->q_empty[i]);
-            if (last) umma_commit(&sh->k_empty[ks]);
-          } else {
-            for (int h = 0; h < 2; ++h) {  // 64 keys: the products of the first half run beside the softmax of the second
-              if (!mbar_wait(&sh->p_full[s][h], d & 1)) {
+        if (it.flags & kPtEnd) break;
+        if (it.lo >= it.hi) continue;
+        const int width = it.flags & kPtTwo ? 2 : 1, edge = it.edge();
+        ++tiles0;
+        if (width == 2) ++tiles1;
+        for (int p = it.lo; p < it.hi && !bad; ++p, ++blocks) {
+          const int ks = blocks % kPtK, vs = blocks % kPtV;
+          const int k = p < edge ? plain + p - it.lo : edges + p - edge;
+          if (scores ? !mbar_wait(&sh->k_full[ks], (blocks / kPtK) & 1)
+                     : !mbar_wait(p < edge ? &sh->v_full[k % kPtV] : &sh->v_ok[k % kPtV], (k / kPtV) & 1)) {
+            bad = true;
+            break;
+          }
+          for (int i = 0; i < width && !bad; ++i) {
+            const int s = width == 2 ? i : (p - it.lo) & 1;
+            const int d = s ? done1 : done0;
+            const bool last = i == width - 1;
+            if (scores) {
+              // S overwrites the slot's P: it waits until that has been multiplied
+              if ((p == it.lo && !mbar_wait(&sh->q_full[i], ((i ? tiles1 : tiles0) - 1) & 1)) ||
+                  (d > 0 && !mbar_wait(&sh->pv_done[s][1], (d - 1) & 1))) {
                 bad = true;
                 break;
               }
               tc_fence_after();
-              const bool add = h > 0 || d > (s ? start1 : start0);
-              const uint64_t vd = umma_desc_mn(vb + vs * kPtTile + h * 64 * 128, kPtHalf);
+              const uint64_t qd = umma_desc(qb + i * kPtTile), kd = umma_desc(kb + ks * kPtTile);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
-                umma_f16_tmem_a(tmem + kPtO + s * 128, tmem + s * 128 + h * 64 + 8 * kk, vd + ((kk * 2048) >> 4), id_o,
-                                add || kk > 0 ? 1u : 0u);
-              umma_commit(&sh->pv_done[s][h]);
-              if (last && h == 1) umma_commit(&sh->v_empty[vs]);
+              for (int kk = 0; kk < 8; ++kk) {  // 16 dims a step
+                const uint32_t off = (kk >> 2) * kPtHalf + 32 * (kk & 3);
+                umma_f16(tmem + s * 128, qd + (off >> 4), kd + (off >> 4), id_s, kk > 0 ? 1u : 0u);
+              }
+              umma_commit(&sh->s_full[s]);
+              if (p == it.hi - 1) umma_commit(&sh->q_empty[i]);
+              if (last) umma_commit(&sh->k_empty[ks]);
+            } else {
+              const bool first = p < it.lo + 2 && (width == 2 ? p == it.lo : true);  // of the slot in this unit
+              for (int h = 0; h < 2; ++h) {  // 64 keys: the products of the first half run beside the softmax of the second
+                if (!mbar_wait(&sh->p_full[s][h], d & 1)) {
+                  bad = true;
+                  break;
+                }
+                tc_fence_after();
+                const uint64_t vd = umma_desc_mn(vb + vs * kPtTile + h * 64 * 128, kPtHalf);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
+                  umma_f16_tmem_a(tmem + kPtO + s * 128, tmem + s * 128 + h * 64 + 8 * kk, vd + ((kk * 2048) >> 4), id_o,
+                                  !first || h > 0 || kk > 0 ? 1u : 0u);
+                umma_commit(&sh->pv_done[s][h]);
+                if (last && h == 1) umma_commit(&sh->v_empty[vs]);
+              }
             }
+            s ? ++done1 : ++done0;
           }
-          s ? ++done1 : ++done0;
         }
-        ++blocks;
+        plain += edge - it.lo;
+        edges += it.hi - edge;
       }
       if (bad) {  // the products still running end before TMEM is freed
         flag_error(a.err, MSA_DEVERR_TIMEOUT);
@@ -761,6 +818,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       }
     }
     __syncwarp();
+   }
   }
   if (failed && lane == 0) flag_error(a.err, MSA_DEVERR_TIMEOUT);
   tc_fence_before();
@@ -788,20 +846,17 @@ __global__ void __launch_bounds__(kFp8MergeThreads) prompt_merge_kernel(const Pr
   if (a.prefix[u + 1] - a.prefix[u] <= whole) return;  // not cut
   const int b = ft_find(a.base, a.batch, 1, u), i = u - a.base[b];
   const PtUnit t = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], i, tt);
-  const int pages = max(t.pages, 1), steps = t.width * pages;
+  const int cost = t.cost();
   const int64_t first = static_cast<int64_t>(a.prefix[u]) * G;
-  const int g = static_cast<int>((xb - first) / steps);
-  const int64_t u0 = first + static_cast<int64_t>(g) * steps;
-  const int xa = ft_lo(E, x, ctas);
-  if ((xb - u0) / t.width == 0 || (xa > u0 && (xa - u0) / t.width > 0)) return;  // no block before it, or not the first
+  const int g = static_cast<int>((xb - first) / cost);
+  const int64_t u0 = first + static_cast<int64_t>(g) * cost;
+  if (t.block_at(xb - u0) == 0 || t.block_at(ft_lo(E, x, ctas) - u0) > 0) return;  // no block before it, or not the first
   if (threadIdx.x < 32) {  // the CTAs with blocks of the unit, in order
     int n = 0;
-    for (int c0 = x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + steps; c0 += 32) {
+    for (int c0 = x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + cost; c0 += 32) {
       const int c = c0 + threadIdx.x;
-      const int64_t a0 = ft_lo(E, c, ctas) - u0, a1 = ft_lo(E, c + 1, ctas) - u0;
-      const int lo = static_cast<int>(max(a0, int64_t{0}) / t.width);
-      const int hi = static_cast<int>(min(a1 / t.width, static_cast<int64_t>(pages)));
-      const bool some = c < ctas && a0 < steps && lo < hi;
+      const int lo = t.block_at(ft_lo(E, c, ctas) - u0), hi = t.block_at(ft_lo(E, c + 1, ctas) - u0);
+      const bool some = c < ctas && lo < hi;
       const unsigned m = __ballot_sync(0xffffffffu, some);
       if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * c + (lo == 0 ? 1 : 0);
       n += __popc(m);

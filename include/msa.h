@@ -425,9 +425,10 @@ msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int
  * arithmetic makes of them; one in v the results of the rows that see it, in its dim.
  * cu_q and cu_k must not decrease, start below 0 or end past q_tokens and k_tokens: otherwise
  * MSA_DEVERR_BAD_SEQLEN is set and nothing is written.
- * Rounding: logits, sums and lse are float32; a probability meets its V row as bfloat16 (rounded by
- * at most 2^-8 of itself, the sum of the probabilities is taken before that).  The same arguments give the
- * same bits in every call on one GPU.
+ * Rounding: logits, sums and lse are float32.  A probability meets its V row as bfloat16, and out is divided
+ * by the sum of the rounded ones (lse has the sum before the rounding), so that before its own rounding
+ * out[d] is off by at most (2^-7 + 2^-14 + twice the largest error of a logit) * sum_j p_j |v_jd|, by nothing for a
+ * row of one key.  The same arguments give the same bits in every call on one GPU.
  * workspace: msa_prompt_workspace_bytes(...); calls that can overlap need one each.
  * Errors: MSA_ERR_UNSUPPORTED for q_tokens or k_tokens above 2^28, or where the call's pairs of
  * 128 query rows and 128 keys cannot be counted in 31 bits: 2 * G * (floor(q_tokens / (2 * floor(128 / Hg))) + batch)

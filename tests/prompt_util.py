@@ -65,8 +65,10 @@ class Prompts:
         """Against the 64-bit definition, element by element:
           * a logit: 128 exact products summed in float32 in any order, and the products with the scale and the
             subtraction of the reference: (128 + 4) * 2^-24 of sum |q k|;
-          * a probability: the logit's error twice (in it and in the sum), 2^-20 for exp2 and the sums, 2^-8 for its
-            rounding to bfloat16 (half a step);
+          * a probability: the logit's error twice (in it and in the sum), 2^-20 for exp2 and the sums;
+          * it is rounded to bfloat16, p (1 + d_j) with |d_j| <= 2^-8 (half a step), and the output divided by the sum of what
+            was rounded: sum p_j (1 + d_j) v_j / (1 + D) with D = sum p_j d_j is off by
+            sum p_j (d_j - D) v_j / (1 + D), at most 2 * 2^-8 / (1 - 2^-8) < 2^-7 + 2^-14 of sum p |v|;
           * the sum over keys in float32: one rounding for each key, 2^-24 of sum p |v|;
           * the output rounded to bfloat16: 2^-8 of it.
         Rows of no sequence keep what they held."""
@@ -77,7 +79,7 @@ class Prompts:
         assert (out[~self.used_q] == 7.0).all() and (lse[~self.used_q] == 7.0).all(), "rows of no sequence"
         u = self.used_q
         dz = scale * ref["logit"] * (128 + 4) * 2.0 ** -24
-        rel = 2 * dz + 2.0 ** -20 + ref["keys"] * 2.0 ** -24 + 2.0 ** -8
+        rel = 2 * dz + 2.0 ** -20 + ref["keys"] * 2.0 ** -24 + 2.0 ** -7 + 2.0 ** -14
         close("out", out[u], ref["out"][u], (2.0 ** -8 * np.abs(ref["out"]) + rel[..., None] * ref["spread"] + 1e-30)[u])
         at = np.where(np.isfinite(ref["lse"]), ref["lse"], 0.0)
         close("lse", lse[u], ref["lse"][u], (dz + 2.0 ** -20 + ref["keys"] * 2.0 ** -24 + 2.0 ** -22 * np.abs(at))[u])
