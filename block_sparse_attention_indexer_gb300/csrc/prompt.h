@@ -8,6 +8,8 @@
 
 namespace msa {
 
+struct PtCut;
+
 struct PromptArgs {
   const int32_t* cu_q;  // [batch + 1]
   const int32_t* cu_k;
@@ -21,9 +23,10 @@ struct PromptArgs {
   float scale_log2;     // softmax_scale * log2(e)
   uint32_t* err;
   // scratch
-  int32_t* plan;        // [0]: units; [1]: steps up to which a unit is not cut
+  int32_t* plan;        // [0]: units (where a launch of its own makes the plan)
   int32_t* base;        // [batch + 1]: units of the sequences before each
-  int32_t* prefix;      // [units + 1]: steps (per KV head) of the units before each
+  int32_t* prefix;      // [units + 1]: cost (per KV head) of the units before each
+  PtCut* cuts;   // [CTAs]: the unit inside which each CTA's range starts
   float* partial;       // partial softmax states of units cut by the split of the work
 };
 
@@ -33,6 +36,7 @@ inline int prompt_tile_tokens(int heads_per_group) { return 128 / heads_per_grou
 inline int64_t prompt_max_units(int64_t q_tokens, int batch, int heads_per_group) {
   return q_tokens / (2 * prompt_tile_tokens(heads_per_group)) + batch;
 }
+size_t prompt_cut_bytes();
 size_t prompt_partial_bytes();
 cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s);
 

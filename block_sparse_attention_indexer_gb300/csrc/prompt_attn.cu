@@ -43,11 +43,12 @@ constexpr int kPtK = 3, kPtV = 2;             // stages of 128 keys
 constexpr int kPtItems = 2;                   // units known ahead
 constexpr int kPtTile = kPtRows * kDim * 2;   // bytes of a Q tile, and of a stage
 constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
+constexpr int kPtMergeRows = 32;              // rows of a CTA of the merge
 constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
 #ifndef PT_UNIT_COST
-#define PT_UNIT_COST 8
+#define PT_UNIT_COST 6
 #endif
 constexpr int kPtUnitCost = PT_UNIT_COST;
 
@@ -75,7 +76,7 @@ struct PtShared {
   uint64_t other;                                   // slot 1's statistics of a one-tile unit left
   uint64_t drain[2];                                // every product issued has ended (after a wait that gave up)
   uint32_t tmem;
-  alignas(16) int special[2][4];                    // a V row taken care of by warp 8 + i (by the unit's parity)
+  int special[8][4];                                // the last unit (by turns) in whose V warp 8 + i found something
   PtItem item[kPtItems];
   float other_m[kPtRows], other_l[kPtRows], other_fix[kPtRows];
 };
@@ -108,11 +109,9 @@ __device__ __forceinline__ PtUnit pt_unit(int Lq, int Lk, int i, int tile_tokens
   return t;
 }
 
-constexpr int kPtPlanThreads = 1024;
-
 // Exclusive prefix sum of v over the CTA plus `carry`, which moves on by the sum.
 __device__ __forceinline__ int pt_prefix(int v, int& carry, int* warp_sum) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x / 32;
   int x = v;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
@@ -122,31 +121,30 @@ __device__ __forceinline__ int pt_prefix(int v, int& carry, int* warp_sum) {
   __syncthreads();
   if (lane == 31) warp_sum[warp] = x;
   __syncthreads();
-  const int w = warp_sum[lane];
+  const int w = lane < warps ? warp_sum[lane] : 0;
   const int at = carry + x - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
   carry += __reduce_add_sync(0xffffffffu, w);
   return at;
 }
 
-// Steps of a unit up to which it is not cut: a cut costs two partial states and a merge, about as much as
+// Cost of a unit up to which it is not cut: a cut costs two partial states and a merge, about as much as
 // kPtCutSteps steps; of `all` units on n CTAs some take ceil(all / n), so that an uncut unit of S steps costs
-// idle * S / n more than its share.  Above 64 steps a unit is cut in any case.
+// idle * S / n more than its share.  Above 64 a unit is cut in any case.
 __device__ __forceinline__ int pt_whole(int64_t all, int n) {
-  constexpr int kPtWhole = 64, kPtCutSteps = 8;
+  constexpr int kPtWhole = 64, kPtCutSteps = 16;
   if (all == 0) return kPtWhole;
   const int64_t idle = n - 1 - (all - 1) % n;
   const int64_t most = static_cast<int64_t>(kPtCutSteps) * n;
   return idle * kPtWhole <= most ? kPtWhole : static_cast<int>(most / idle);
 }
 
-__global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const PromptArgs a, int ctas) {
-  __shared__ int s_base[2048 + 1], s_sum[32];
-  const int tid = threadIdx.x, tt = kPtRows / a.heads_per_group;
-  grid_dependency_wait();
-  grid_dependents_launch();
+// The plan by a whole CTA: base[b], b = 0..batch: units of the sequences before b; prefix[u], u = 0..units: cost (per
+// KV head) of the units before u.  Returns the units; 0 where the offsets are bad, and `flag` reports them.
+__device__ __noinline__ int pt_plan(const PromptArgs& a, int* base, int32_t* prefix, int* warp_sum, bool flag) {
+  const int tid = threadIdx.x, threads = blockDim.x, tt = kPtRows / a.heads_per_group;
   bool bad = false;
   int units = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kPtPlanThreads) {
+  for (int b0 = 0; b0 < a.batch; b0 += threads) {
     const int b = b0 + tid;
     int n = 0;
     if (b < a.batch) {
@@ -154,46 +152,58 @@ __global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const Promp
       bad |= q0 < 0 || k0 < 0 || q1 < q0 || k1 < k0 || q1 > a.q_tokens || k1 > a.k_tokens;
       n = bad ? 0 : (q1 - q0 + 2 * tt - 1) / (2 * tt);
     }
-    const int at = pt_prefix(n, units, s_sum);
-    if (b < a.batch) s_base[b] = at;
+    const int at = pt_prefix(n, units, warp_sum);
+    if (b < a.batch) base[b] = at;
   }
   if (__syncthreads_or(bad)) {  // nothing is done
-    if (tid == 0) {
-      flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
-      a.plan[0] = 0;
-    }
-    return;
+    if (flag && tid == 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
+    return 0;
   }
-  if (tid == 0) {
-    s_base[a.batch] = units;
-    a.plan[0] = units;
-    a.plan[1] = pt_whole(static_cast<int64_t>(units) * a.groups, ctas);
-  }
+  if (tid == 0) base[a.batch] = units;
   __syncthreads();
-  for (int b = tid; b <= a.batch; b += kPtPlanThreads) a.base[b] = s_base[b];
-  int steps = 0;
-  for (int u0 = 0; u0 < units; u0 += kPtPlanThreads) {
+  int cost = 0;
+  for (int u0 = 0; u0 < units; u0 += threads) {
     const int u = u0 + tid;
     int n = 0;
     if (u < units) {
       int b = 0, left = a.batch;  // the last sequence with base <= u
       while (left > 1) {
         const int h = left / 2;
-        if (s_base[b + h] <= u) {
+        if (base[b + h] <= u) {
           b += h;
           left -= h;
         } else {
           left = h;
         }
       }
-      const PtUnit t = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], u - s_base[b], tt);
-      n = t.cost();
+      n = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], u - base[b], tt).cost();
     }
-    const int at = pt_prefix(n, steps, s_sum);
-    if (u < units) a.prefix[u] = at;
+    const int at = pt_prefix(n, cost, warp_sum);
+    if (u < units) prefix[u] = at;
   }
-  if (tid == 0) a.prefix[units] = steps;
+  if (tid == 0) prefix[units] = cost;
+  return units;
 }
+
+// Sequences and units up to which every CTA of the attention makes the plan for itself: one round of loads, a few of
+// sums.  More are planned by a launch before it.
+constexpr int kPtOwnBatch = kPtThreads, kPtOwnUnits = 2048;
+
+constexpr int kPtPlanThreads = 1024;
+__global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const PromptArgs a) {
+  __shared__ int s_base[2048 + 1], s_sum[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int units = pt_plan(a, s_base, a.prefix, s_sum, true);
+  if (threadIdx.x == 0) a.plan[0] = units;
+  for (int b = threadIdx.x; units > 0 && b <= a.batch; b += kPtPlanThreads) a.base[b] = s_base[b];
+}
+
+// The unit inside which a CTA's range starts (id -1: it starts with one), for the merge.
+struct alignas(16) PtCut {
+  int id, lo, hi;  // of the unit, with its KV head; blocks before the CTA's part of it, and at its end
+  int token0, tokens, g, pad[2];
+};
 
 // ---------------------------------------------------------------- bf16 forms
 
@@ -215,6 +225,13 @@ __device__ __forceinline__ void registers_up() {
 template <int N>
 __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 1 / x to one unit in the last place, for x from 2^-126 to 2^126
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -254,9 +271,37 @@ __device__ __forceinline__ void turn_quad(uint4 (&w)[4]) {
 // The top bits of the halves of w that are infinities or NaN (exponent all ones; no half's sum carries)
 __device__ __forceinline__ uint32_t bf16_special(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
+// What was taken out of V comes back to the rows that see its key: the infinities and NaN of the unit's keys that not
+// every row sees, added to its outputs or its partial state, a row at a time by each of the 128 threads that call it.
+// (Not inlined, and not the softmax warps' work: what stands beside their loop costs that loop instruction fetches
+// and registers, 1.43 -> 1.68 ms for a prompt of 16K.)
+__device__ __noinline__ void pt_put_back(const PromptArgs& a, const PtItem& it) {
+  const int Hg = a.heads_per_group, H = a.groups * Hg, tt = kPtRows / Hg, place = (it.flags >> kPtPlace) - 1;
+  const uint16_t* v = a.v + it.key0 * a.v_stride + it.g * kDim;
+  float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + max(place, 0)) * kPtPlaceFloats;
+  for (int pr = threadIdx.x & 127; pr < 2 * kPtRows; pr += 128) {
+    const int r = pr & (kPtRows - 1), t = r / Hg + (pr >= kPtRows ? tt : 0);
+    if (r / Hg >= tt || t >= it.tokens) continue;
+    uint16_t* out = a.out + (static_cast<int64_t>(it.token0 + t) * H + it.g * Hg + r % Hg) * kDim;
+    const int last = min(it.pos0 + t, it.hi * kBlock - 1);
+    for (int j = max(it.pos0 + 1, it.lo * kBlock); j <= last; ++j)
+      for (int d = 0; d < kDim; ++d) {
+        const float y = __uint_as_float(static_cast<uint32_t>(v[j * a.v_stride + d]) << 16);
+        if (fabsf(y) < INFINITY) continue;
+        if (place < 0) {
+          volatile uint16_t* dst = out + d;
+          *dst = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(static_cast<uint32_t>(*dst) << 16) + y, 0.f));
+        } else {
+          volatile float* dst = part + (d / 4) * (8 * kPtRows) + 4 * pr + (d & 3);
+          *dst += y;
+        }
+      }
+  }
+}
+
 // ---------------------------------------------------------------- the kernel
 
-__global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps) {
+__global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps, int own_plan) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* q_tile = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* k_ring = q_tile + 2 * kPtTile;
@@ -304,11 +349,21 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  grid_dependency_wait();
+  grid_dependents_launch();
+  // the plan, in what will be the stages of K
+  int* base = a.base;
+  int32_t* prefix = a.prefix;
+  int units = 0;
+  if (own_plan) {
+    base = reinterpret_cast<int*>(k_ring);
+    prefix = base + kPtOwnBatch + 1;
+    units = pt_plan(a, base, prefix, prefix + kPtOwnUnits + 1, blockIdx.x == 0);
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_dependency_wait();
-  grid_dependents_launch();
   const uint32_t tmem = sh->tmem;
   bool failed = false;
 
@@ -343,7 +398,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         if (slot == 1) {
           sh->other_m[r] = M;
           sh->other_l[r] = l;
-          sh->other_fix[r] = l_bf16 != 0.f ? l / l_bf16 : 1.f;
+          sh->other_fix[r] = l_bf16 != 0.f ? l * rcp(l_bf16) : 1.f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->other);
           return true;
@@ -354,7 +409,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       tc_fence_after();
       // O is put right by the ratio of the sums of P before and after its rounding, the state of the row is
       // then fa * own O + fb * the other slot's O
-      const float fix = mine && l_bf16 != 0.f ? l / l_bf16 : 1.f;
+      const float fix = mine && l_bf16 != 0.f ? l * rcp(l_bf16) : 1.f;
       float fa = mine ? fix : 0.f, fb = 0.f;
       const bool both = !two && others;
       if (both) {
@@ -368,7 +423,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       }
       const int t = my_token + (two && slot ? tt : 0);  // token of the unit
       const bool valid = my_token < tt && t < it.tokens;
-      const float inv = l != 0.f ? 1.f / l : 0.f;       // (NaN counts as a sum)
+      const float inv = l != 0.f ? rcp(l) : 0.f;        // (NaN counts as a sum)
       if (place < 0) {
         fa *= inv;
         fb *= inv;
@@ -377,8 +432,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       const int off = t * H + my_head;
       const int pr = r + (two && slot ? kPtRows : 0);   // row of the partial state
       float* part = place < 0 ? nullptr : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats;
-      const int4 sp = *reinterpret_cast<const int4*>(sh->special[uc & 1]);
-      const bool special = it.lo < it.hi && (sp.x | sp.y | sp.z | sp.w) != 0;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {  // 32 dims
         uint32_t x[32];
@@ -394,19 +447,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
           tmem_wait_ld(x);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), fb, v[i]);
-        }
-        if (special) {
-          // what was taken out of V comes back for the rows that see its key
-          const int last = min(pos, it.hi * kBlock - 1);
-#pragma unroll 1
-          for (int j = max(it.pos0 + 1, it.lo * kBlock); j <= last; ++j) {
-            const uint16_t* src = a.v + (it.key0 + j) * a.v_stride + it.g * kDim + 32 * c;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = __uint_as_float(static_cast<uint32_t>(src[i]) << 16);
-              if (!(fabsf(y) < INFINITY)) v[i] += y;
-            }
-          }
         }
         if (place < 0) {
           // pieces of 16 bytes turned among four lanes, so that these write a row's 64 bytes
@@ -466,8 +506,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       done_o += two ? it.hi - it.lo : (it.hi - it.lo + slot) / 2;
 #pragma unroll 1
       for (int p = first; p < it.hi; p += step) {
-        // what the V warps found in a block that not every row sees whole is read when the unit is written: seeing the
-        // stage ready orders it before that (the stage is not used again before this step's P)
+        // what the V warps found in a block that not every row sees whole they look up among themselves when the unit is
+        // written (fin): seeing the stage ready here orders it before that (it is not used again before this step's P)
         const int e = edges + p - edge;
         if (!mbar_wait_warp(&sh->s_full[slot], done & 1) ||
             (p >= edge && !mbar_wait_warp(&sh->v_ok[e % kPtV], (e / kPtV) & 1))) {
@@ -566,20 +606,28 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     // ---- V: infinities and NaN out of the rows that not every row of the unit sees
     const int ct = tid - 256;
     int blocks = 0, edges = 0;
+    if (lane < 8) sh->special[lane][warp - 8] = -1;
+    __syncwarp();
+    // unit n is written: its rows get back what was taken out
+    auto put_back = [&](int n, const PtItem& it) -> bool {
+      if (!mbar_wait_warp(&sh->fin[n & 1], (n >> 1) & 1)) return false;
+      const int* sp = sh->special[n & 7];
+      if (sp[0] == n || sp[1] == n || sp[2] == n || sp[3] == n) pt_put_back(a, it);
+      return true;
+    };
+    PtItem one{}, two{};  // the unit before, and the one before that
     for (int uc = 0; !failed; ++uc) {
       PtItem it;
-      if (!take_item(uc, it)) {
+      if (!take_item(uc, it) || (uc >= 2 && !put_back(uc - 2, two))) {
         failed = true;
         break;
       }
-      if (it.flags & kPtEnd) break;
-      // the unit that used these marks is written
-      if (uc >= 2 && !mbar_wait_warp(&sh->fin[uc & 1], ((uc - 2) >> 1) & 1)) {
-        failed = true;
+      if (it.flags & kPtEnd) {
+        failed = uc >= 1 && !put_back(uc - 1, one);
         break;
       }
-      if (lane == 0) sh->special[uc & 1][warp - 8] = 0;
-      __syncwarp();
+      two = one;
+      one = it;
       for (int p = it.edge(); p < it.hi; ++p, ++edges) {
         const int vs = (blocks + p - it.lo) % kPtV;
         if (!mbar_wait_warp(&sh->v_edge[edges % kPtV], (edges / kPtV) & 1)) {
@@ -597,7 +645,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
           any |= r >= r0 ? s : 0u;
         }
         if (any != 0u) {
-          sh->special[uc & 1][warp - 8] = 1;
+          sh->special[uc & 7][warp - 8] = uc;
           auto clear = [](uint32_t w) {
             const uint32_t s = bf16_special(w);
             return w & ~(s | (s - (s >> 15)));  // (whole halves: the top bit and the 15 below it)
@@ -623,16 +671,20 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
    registers_down<64>();
    if (warp == 12) {
     // ---- producer: units and the copies of Q and K
-    const int units = a.plan[0];
-    int x0 = 0, x1 = 0;
+    if (!own_plan) units = a.plan[0];
+    int x0 = 0, x1 = 0, u = 0, b = 0;
+    int64_t E = 0, first = 0;  // all cost, cost before unit u
     if (units > 0) {
-      const int whole = a.plan[1];
-      const int64_t E = static_cast<int64_t>(a.prefix[units]) * G;
+      const int whole = pt_whole(static_cast<int64_t>(units) * G, gridDim.x);
+      E = static_cast<int64_t>(prefix[units]) * G;
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
         x0 = x1;
-        x1 = ft_cut(a.prefix, units, G, E, blockIdx.x + i, gridDim.x, whole);
+        x1 = ft_cut(prefix, units, G, E, blockIdx.x + i, gridDim.x, whole);
       }
+      u = ft_find(prefix, units, G, static_cast<int>(min(static_cast<int64_t>(x0), E - 1)));
+      b = ft_find(base, a.batch, 1, u);
+      first = static_cast<int64_t>(prefix[u]) * G;
     }
     const uint64_t keep = l2_evict_normal_policy(), once = l2_evict_first_policy();
     const uint32_t q_bytes = static_cast<uint32_t>(tt) * Hg * 256;
@@ -646,18 +698,17 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       ++n;
       return true;
     };
-    int u = x0 < x1 ? ft_find(a.prefix, units, G, x0) : units;
-    for (; u < units && !failed; ++u) {
-      const int64_t first = static_cast<int64_t>(a.prefix[u]) * G;
-      if (first >= x1) break;
-      const int b = ft_find(a.base, a.batch, 1, u);
-      const int q0 = a.cu_q[b], key0 = a.cu_k[b], i = u - a.base[b];
-      const PtUnit t = pt_unit(a.cu_q[b + 1] - q0, a.cu_k[b + 1] - key0, i, tt);
+    PtCut cut{-1, 0, 0, 0, 0, 0, {0, 0}};
+    for (int i = units > 0 ? u - base[b] : 0; units > 0 && first <= x1 && !failed;) {  // unit i of sequence b
+      const int q0 = a.cu_q[b], key0 = a.cu_k[b], Lq = a.cu_q[b + 1] - q0;
+      const PtUnit t = pt_unit(Lq, a.cu_k[b + 1] - key0, i, tt);
       const int pages = max(t.pages, 1), cost = t.cost(), token0 = q0 + i * 2 * tt;
       for (int g = 0; g < G && !failed; ++g) {
         const int64_t u0 = first + static_cast<int64_t>(g) * cost;
-        if (u0 >= x1) break;
+        if (u0 + cost <= x0) continue;
         const int lo = t.block_at(x0 - u0), hi = t.block_at(x1 - u0);
+        if (u0 < x0 && x0 < E) cut = PtCut{u * G + g, lo, hi, token0, t.tokens, g, {0, 0}};
+        if (u0 >= x1) break;
         if (lo >= hi) continue;
         const int place = lo == 0 && hi == pages ? -1 : lo == 0 ? 1 : 0;
         if (!record(PtItem{(t.width == 2 ? kPtTwo : 0) | (place + 1) << kPtPlace, lo, t.pages > 0 ? hi : lo, token0, t.tokens,
@@ -693,7 +744,16 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
           ++blocks;
         }
       }
+      // the next unit: of this sequence, or the first one of the next sequence that has any
+      first += static_cast<int64_t>(cost) * G;
+      if (++u >= units) break;
+      if (++i * 2 * tt >= Lq) {
+        i = 0;
+        do ++b;
+        while (a.cu_q[b + 1] == a.cu_q[b]);
+      }
     }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
     if (!failed) failed = !record(PtItem{kPtEnd, 0, 0, 0, 0, 0, 0, 0});
     if (failed) {
       // wait (bounded) for the copies still in flight
@@ -829,60 +889,58 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
 
 // ---------------------------------------------------------------- units cut by range boundaries
 
-// The partial states that their CTAs left, added (fp8_merge.cuh).  blockIdx.x is the boundary whose unit
-// the CTA takes if it is the unit's first cut; blockIdx.y the row (kSplit) or eight of them.
+// The partial states that their CTAs left, added (fp8_merge.cuh).  blockIdx.x + 1 is a CTA that may have started inside a
+// unit: if it is the first one that did, its block here joins the unit.  blockIdx.y: the row (kSplit) or 32 rows.
 template <bool kSplit>
 __global__ void __launch_bounds__(kFp8MergeThreads) prompt_merge_kernel(const PromptArgs a, int ctas) {
   __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int units = a.plan[0], G = a.groups, Hg = a.heads_per_group, tt = kPtRows / Hg;
-  if (units == 0) return;
-  const int whole = a.plan[1], x = blockIdx.x;
-  const int64_t E = static_cast<int64_t>(a.prefix[units]) * G;
-  const int xb = ft_lo(E, x + 1, ctas);
-  if (xb >= E) return;
-  const int u = ft_find(a.prefix, units, G, xb);
-  if (a.prefix[u + 1] - a.prefix[u] <= whole) return;  // not cut
-  const int b = ft_find(a.base, a.batch, 1, u), i = u - a.base[b];
-  const PtUnit t = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], i, tt);
-  const int cost = t.cost();
-  const int64_t first = static_cast<int64_t>(a.prefix[u]) * G;
-  const int g = static_cast<int>((xb - first) / cost);
-  const int64_t u0 = first + static_cast<int64_t>(g) * cost;
-  if (t.block_at(xb - u0) == 0 || t.block_at(ft_lo(E, x, ctas) - u0) > 0) return;  // no block before it, or not the first
+  const int c = blockIdx.x + 1, G = a.groups, Hg = a.heads_per_group, tt = kPtRows / Hg;
+  const PtCut cut = a.cuts[c];
+  if (cut.id < 0 || a.cuts[c - 1].id == cut.id) return;
   if (threadIdx.x < 32) {  // the CTAs with blocks of the unit, in order
     int n = 0;
-    for (int c0 = x; c0 < ctas && ft_lo(E, c0, ctas) < u0 + cost; c0 += 32) {
-      const int c = c0 + threadIdx.x;
-      const int lo = t.block_at(ft_lo(E, c, ctas) - u0), hi = t.block_at(ft_lo(E, c + 1, ctas) - u0);
-      const bool some = c < ctas && lo < hi;
+    if (cut.lo > 0) {
+      if (threadIdx.x == 0) sh.list[0] = 2 * (c - 1) + 1;
+      n = 1;
+    }
+    for (int c0 = c;; c0 += 32) {
+      const int k = c0 + threadIdx.x;
+      const PtCut x = k < ctas ? a.cuts[k] : PtCut{-1, 0, 0, 0, 0, 0, {0, 0}};
+      const unsigned same = __ballot_sync(0xffffffffu, x.id == cut.id);
+      const bool some = x.id == cut.id && x.lo < x.hi;
       const unsigned m = __ballot_sync(0xffffffffu, some);
-      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * c + (lo == 0 ? 1 : 0);
+      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * k + (x.lo == 0 ? 1 : 0);
       n += __popc(m);
+      if (same != 0xffffffffu) break;
     }
     if (threadIdx.x == 0) sh.n = n;
   }
   __syncthreads();
   if (sh.n < 2) return;  // one CTA's: written by it
   // states lie by chunks of four dims: without kSplit a CTA's eight rows of a chunk are one 128-byte line
-  const int pr = kSplit ? blockIdx.y : blockIdx.y * 8 + (threadIdx.x & 7);
   const int chunk = kSplit ? threadIdx.x & 31 : threadIdx.x >> 3;
-  const int row = pr & (kPtRows - 1), token = row / Hg + (pr >= kPtRows ? tt : 0);
-  if (row / Hg >= tt || token >= t.tokens) return;
-  float4 o;
-  float M, l;
-  fp8_merge_row<kSplit>(a.partial, 2 * kPtRows, pr, chunk * 2 * kPtRows + pr, sh, o, M, l);
-  if (kSplit && threadIdx.x >= 32) return;
-  const int64_t hr = static_cast<int64_t>(a.cu_q[b] + i * 2 * tt + token) * G * Hg + g * Hg + row % Hg;
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  reinterpret_cast<uint2*>(a.out + hr * kDim)[chunk] =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (chunk == 0 && a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
+#pragma unroll 1
+  for (int i = 0; i < (kSplit ? 1 : kPtMergeRows / 8); ++i) {
+    const int pr = kSplit ? blockIdx.y : blockIdx.y * kPtMergeRows + 8 * i + (threadIdx.x & 7);
+    const int row = pr & (kPtRows - 1), token = row / Hg + (pr >= kPtRows ? tt : 0);
+    if (row / Hg >= tt || token >= cut.tokens) continue;
+    float4 o;
+    float M, l;
+    fp8_merge_row<kSplit>(a.partial, 2 * kPtRows, pr, chunk * 2 * kPtRows + pr, sh, o, M, l);
+    if (kSplit && threadIdx.x >= 32) return;
+    const int64_t hr = static_cast<int64_t>(cut.token0 + token) * G * Hg + cut.g * Hg + row % Hg;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    reinterpret_cast<uint2*>(a.out + hr * kDim)[chunk] =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (chunk == 0 && a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
+  }
 }
 
 // ---------------------------------------------------------------- launch
 
+size_t prompt_cut_bytes() { return kFp8MaxCtas * sizeof(PtCut); }
 size_t prompt_partial_bytes() { return static_cast<size_t>(2) * kFp8MaxCtas * kPtPlaceFloats * sizeof(float); }
 
 static cudaError_t prompt_maps(const PromptArgs& a, PromptMaps* maps) {
@@ -925,13 +983,14 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s)
   if (e != cudaSuccess) return e;
   const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas;
   if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(prompt_attn_kernel), kPtSmem)) != cudaSuccess) return e;
-  if ((e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a, ctas)) != cudaSuccess) return e;
-  if ((e = launch_dependent(prompt_attn_kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps)) != cudaSuccess) return e;
+  const int64_t most = prompt_max_units(a.q_tokens, a.batch, a.heads_per_group), units = most * a.groups;
+  const int own_plan = a.batch <= kPtOwnBatch && most <= kPtOwnUnits ? 1 : 0;
+  if (!own_plan && (e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a)) != cudaSuccess) return e;
+  if ((e = launch_dependent(prompt_attn_kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps, own_plan)) != cudaSuccess) return e;
   if (ctas == 1) return cudaSuccess;
-  const int64_t units = prompt_max_units(a.q_tokens, a.batch, a.heads_per_group) * a.groups;
   return ctas / units >= kFp8MergeSplitParts
              ? launch_dependent(prompt_merge_kernel<true>, dim3(ctas - 1, 2 * kPtRows), kFp8MergeThreads, 0, s, a, ctas)
-             : launch_dependent(prompt_merge_kernel<false>, dim3(ctas - 1, 2 * kPtRows / 8), kFp8MergeThreads, 0, s, a, ctas);
+             : launch_dependent(prompt_merge_kernel<false>, dim3(ctas - 1, 2 * kPtRows / kPtMergeRows), kFp8MergeThreads, 0, s, a, ctas);
 }
 
 }  // namespace msa
