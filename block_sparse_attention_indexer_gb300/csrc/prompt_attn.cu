@@ -345,6 +345,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     *reinterpret_cast<uint4*>(q_tile + t * kPtTile + (c >> 3) * kPtHalf + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
+  if (warp == 12 && lane < 3) {
+    const CUtensorMap* m = lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh->tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -410,65 +414,73 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       // O is put right by the ratio of the sums of P before and after its rounding, the state of the row is
       // then fa * own O + fb * the other slot's O
       const float fix = mine && l_bf16 != 0.f ? l * rcp(l_bf16) : 1.f;
-      float fa = mine ? fix : 0.f, fb = 0.f;
-      const bool both = !two && others;
-      if (both) {
+      float fa = fix;
+      if (!two && others) {  // (slot 1 had blocks, so this slot had the first one)
         const float mo = sh->other_m[r], lo = sh->other_l[r];
         const float mn = fmaxf(M, mo);
         const float wa = mn == -INFINITY ? 1.f : ex2(M - mn), wb = mn == -INFINITY ? 1.f : ex2(mo - mn);
+        const float fb = wb * sh->other_fix[r];
         fa *= wa;
-        fb = wb * sh->other_fix[r];
         l = l * wa + lo * wb;
         M = mn;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t x[16], y[16];
+          tmem_ld16(tO + 16 * c, x);
+          tmem_ld16(tO + 128 + 16 * c, y);
+          tmem_wait_ld(x);
+          tmem_wait_ld(y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), fb, __uint_as_float(x[i]) * fa));
+          tmem_st16(tO + 16 * c, x);
+        }
+        tmem_wait_st();
+        fa = 1.f;
       }
       const int t = my_token + (two && slot ? tt : 0);  // token of the unit
       const bool valid = my_token < tt && t < it.tokens;
       const float inv = l != 0.f ? rcp(l) : 0.f;        // (NaN counts as a sum)
-      if (place < 0) {
-        fa *= inv;
-        fb *= inv;
-      }
+      if (place < 0) fa *= inv;
       const int64_t row0 = static_cast<int64_t>(it.token0) * H + it.g * Hg;  // row of the outputs of the unit's first one
       const int off = t * H + my_head;
       const int pr = r + (two && slot ? kPtRows : 0);   // row of the partial state
       float* part = place < 0 ? nullptr : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats;
+      if (!mine) {  // no key
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (row0 + off) * kDim);
+        for (int c = 0; valid && c < kDim / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+      } else if (place < 0) {
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {  // 32 dims
-        uint32_t x[32];
-        float v[32];
-        if (mine) {
+        for (int c = 0; c < 4; ++c) {  // 32 dims
+          uint32_t x[32];
           tmem_ld32(tO + 32 * c, x);
           tmem_wait_ld(x);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = mine ? __uint_as_float(x[i]) * fa : 0.f;
-        if (both) {
-          tmem_ld32(tO + 128 + 32 * c, x);
-          tmem_wait_ld(x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), fb, v[i]);
-        }
-        if (place < 0) {
-          // pieces of 16 bytes turned among four lanes, so that these write a row's 64 bytes
           uint4 w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                              pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-          turn_quad(w);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(&w[j]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int to = __shfl_sync(0xffffffffu, valid ? off : -1, (lane & ~3) + i);
-            if (to >= 0) *reinterpret_cast<uint4*>(a.out + (row0 + to) * kDim + 32 * c + 8 * (lane & 3)) = w[i];
+            for (int i = 0; i < 4; ++i)
+              p[i] = pack_bf16x2(__uint_as_float(x[8 * j + 2 * i]) * fa, __uint_as_float(x[8 * j + 2 * i + 1]) * fa);
           }
-        } else if (valid) {
-          // four dims of all rows together: the lanes of a store are neighbouring rows
-          float4* dst = reinterpret_cast<float4*>(part) + 8 * c * (2 * kPtRows) + pr;
+          if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + (row0 + off) * kDim + 32 * c);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            dst[j * 2 * kPtRows] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            for (int j = 0; j < 4; ++j) dst[j] = w[j];
+          }
         }
-        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {  // 16 dims: four of all rows together, the lanes of a store are neighbouring rows
+          uint32_t x[16];
+          tmem_ld16(tO + 16 * c, x);
+          tmem_wait_ld(x);
+          float4* dst = reinterpret_cast<float4*>(part) + 4 * c * (2 * kPtRows) + pr;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (valid)
+              dst[j * 2 * kPtRows] = make_float4(__uint_as_float(x[4 * j]) * fa, __uint_as_float(x[4 * j + 1]) * fa,
+                                                 __uint_as_float(x[4 * j + 2]) * fa, __uint_as_float(x[4 * j + 3]) * fa);
+        }
       }
       if (valid) {
         if (place < 0) {
