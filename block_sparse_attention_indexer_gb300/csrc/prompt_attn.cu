@@ -227,6 +227,13 @@ __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The largest of three (a NaN is left aside)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 1 / x to one unit in the last place, for x from 2^-126 to 2^126
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -245,27 +252,6 @@ __device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t w) {
   asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n add.rn.f32.bf16 %0, lo, %0;\n add.rn.f32.bf16 %1, hi, %1;\n}"
       : "+f"(a), "+f"(b)
       : "r"(w));
-}
-
-// Lane q of four has piece i of lane i's afterwards where it had its own piece i: w[i] of lane q <-> w[q] of lane i
-__device__ __forceinline__ void turn_pair(uint4& a, uint4& b, int bit) {  // (the lanes without the bit send b, the others a)
-  const bool odd = threadIdx.x & bit;
-  const uint4 give = odd ? a : b;
-  uint4 got;
-  got.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
-  got.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
-  got.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
-  got.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
-  if (odd)
-    a = got;
-  else
-    b = got;
-}
-__device__ __forceinline__ void turn_quad(uint4 (&w)[4]) {
-  turn_pair(w[0], w[1], 1);
-  turn_pair(w[2], w[3], 1);
-  turn_pair(w[0], w[2], 2);
-  turn_pair(w[1], w[3], 2);
 }
 
 // The top bits of the halves of w that are infinities or NaN (exponent all ones; no half's sum carries)
@@ -535,19 +521,25 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         tmem_wait_ld(v[1]);
         asm volatile("" : "+f"(mx), "+f"(mx1));
         mx = fmaxf(mx, mx1);
-        if (p * kBlock + kBlock - 1 > tile0) {
+        if (__builtin_expect(p * kBlock + kBlock - 1 > tile0, 0)) {
           // some row of the tile must not see one of these keys: -inf over its scores, and the maximum again
           const int vis = pos - p * kBlock + 1;  // visible columns
+          const int least = __reduce_min_sync(0xffffffffu, vis);
           mx = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 128; ++j) {
-            uint32_t& x = v[j >> 6][j & 63];
-            x = j < vis ? x : 0xff800000u;
-            mx = fmaxf(mx, __uint_as_float(x));
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&x)[64] = v[c >> 1];
+            if (32 * c + 32 > least) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[32 * (c & 1) + j] = 32 * c + j < vis ? x[32 * (c & 1) + j] : 0xff800000u;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mx = max3(mx, __uint_as_float(x[32 * (c & 1) + j]), __uint_as_float(x[32 * (c & 1) + j + 1]));
           }
         }
         mx *= f;
-        if (__any_sync(0xffffffffu, mx > M)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, mx > M), 0)) {
           float alpha = 1.f;
           if (mx > M) {
             const float mn = ceilf(mx) + kPtRefSet;
