@@ -39,7 +39,7 @@ namespace msa {
 
 constexpr int kPtRows = 128;  // rows per tile
 constexpr int kPtThreads = 512;
-constexpr int kPtK = 3, kPtV = 2;             // stages of 128 keys
+constexpr int kPtK = 2, kPtV = 3;             // stages of 128 keys
 constexpr int kPtItems = 2;                   // units known ahead
 constexpr int kPtTile = kPtRows * kDim * 2;   // bytes of a Q tile, and of a stage
 constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
@@ -48,7 +48,7 @@ constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
 #ifndef PT_UNIT_COST
-#define PT_UNIT_COST 6
+#define PT_UNIT_COST 4
 #endif
 constexpr int kPtUnitCost = PT_UNIT_COST;
 
@@ -72,20 +72,33 @@ struct PtShared {
   uint64_t item_full[kPtItems], item_empty[kPtItems];
   uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [slot], [slot][half of the keys]
   uint64_t q_full[2], q_empty[2];                   // [tile]
-  uint64_t fin[2];                                  // a unit written (by the unit's parity on this CTA)
+  uint64_t fin[2], o_full[2], o_empty[2];           // [slot], a unit's: factors left, products done, O read
   uint64_t other;                                   // slot 1's statistics of a one-tile unit left
   uint64_t drain[2];                                // every product issued has ended (after a wait that gave up)
   uint32_t tmem;
   int special[8][4];                                // the last unit (by turns) in whose V warp 8 + i found something
   PtItem item[kPtItems];
-  float other_m[kPtRows], other_l[kPtRows], other_fix[kPtRows];
+  float factor[2][kPtRows];                         // of the rows of the slots' O
+  float other_m[kPtRows], other_l[kPtRows];
 };
-constexpr size_t kPtSmem = 1024 + 2 * kPtTile + (kPtK + kPtV) * kPtTile + sizeof(PtShared);
+constexpr size_t kPtSmem = 2 * kPtTile + (kPtK + kPtV) * kPtTile + sizeof(PtShared);
 static_assert(kPtSmem <= 232448, "227 KB of shared memory per CTA");
 
 struct PromptMaps {
   CUtensorMap q, k, v;
 };
+
+// The bounded waits of msa_device.cuh, kept short
+__device__ __forceinline__ bool pt_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t i = kSpinLimit;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (--i == 0u) return false;
+  return true;
+}
+__device__ __forceinline__ bool pt_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, pt_wait(bar, parity)) != 0;
+}
 
 // ---------------------------------------------------------------- the plan
 
@@ -254,23 +267,43 @@ __device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t w) {
       : "r"(w));
 }
 
+// Lane q of four has piece i of lane i's afterwards where it had its own piece i: w[i] of lane q <-> w[q] of lane i
+__device__ __forceinline__ void turn_pair(uint4& a, uint4& b, int bit) {  // (the lanes without the bit send b, the others a)
+  const bool odd = threadIdx.x & bit;
+  const uint4 give = odd ? a : b;
+  uint4 got;
+  got.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+  got.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+  got.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+  got.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+  if (odd)
+    a = got;
+  else
+    b = got;
+}
+__device__ __forceinline__ void turn_quad(uint4 (&w)[4]) {
+  turn_pair(w[0], w[1], 1);
+  turn_pair(w[2], w[3], 1);
+  turn_pair(w[0], w[2], 2);
+  turn_pair(w[1], w[3], 2);
+}
+
 // The top bits of the halves of w that are infinities or NaN (exponent all ones; no half's sum carries)
 __device__ __forceinline__ uint32_t bf16_special(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 // What was taken out of V comes back to the rows that see its key: the infinities and NaN of the unit's keys that not
-// every row sees, added to its outputs or its partial state, a row at a time by each of the 128 threads that call it.
-// (Not inlined, and not the softmax warps' work: what stands beside their loop costs that loop instruction fetches
-// and registers, 1.43 -> 1.68 ms for a prompt of 16K.)
-__device__ __noinline__ void pt_put_back(const PromptArgs& a, const PtItem& it) {
-  const int Hg = a.heads_per_group, H = a.groups * Hg, tt = kPtRows / Hg, place = (it.flags >> kPtPlace) - 1;
-  const uint16_t* v = a.v + it.key0 * a.v_stride + it.g * kDim;
+// every row sees, added to its outputs or its partial state by the threads that wrote these.
+__device__ __noinline__ void pt_put_back(const PromptArgs& a, int flags, int lo, int hi, int token0, int tokens, int pos0,
+                                         int key0, int g) {
+  const int Hg = a.heads_per_group, H = a.groups * Hg, tt = kPtRows / Hg, place = (flags >> kPtPlace) - 1;
+  const uint16_t* v = a.v + key0 * a.v_stride + g * kDim;
   float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + max(place, 0)) * kPtPlaceFloats;
   for (int pr = threadIdx.x & 127; pr < 2 * kPtRows; pr += 128) {
     const int r = pr & (kPtRows - 1), t = r / Hg + (pr >= kPtRows ? tt : 0);
-    if (r / Hg >= tt || t >= it.tokens) continue;
-    uint16_t* out = a.out + (static_cast<int64_t>(it.token0 + t) * H + it.g * Hg + r % Hg) * kDim;
-    const int last = min(it.pos0 + t, it.hi * kBlock - 1);
-    for (int j = max(it.pos0 + 1, it.lo * kBlock); j <= last; ++j)
+    if (r / Hg >= tt || t >= tokens) continue;
+    uint16_t* out = a.out + (static_cast<int64_t>(token0 + t) * H + g * Hg + r % Hg) * kDim;
+    const int last = min(pos0 + t, hi * kBlock - 1);
+    for (int j = max(pos0 + 1, lo * kBlock); j <= last; ++j)
       for (int d = 0; d < kDim; ++d) {
         const float y = __uint_as_float(static_cast<uint32_t>(v[j * a.v_stride + d]) << 16);
         if (fabsf(y) < INFINITY) continue;
@@ -288,8 +321,7 @@ __device__ __noinline__ void pt_put_back(const PromptArgs& a, const PtItem& it) 
 // ---------------------------------------------------------------- the kernel
 
 __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps, int own_plan) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* q_tile = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t q_tile[];
   uint8_t* k_ring = q_tile + 2 * kPtTile;
   uint8_t* v_ring = k_ring + kPtK * kPtTile;
   PtShared* sh = reinterpret_cast<PtShared*>(v_ring + kPtV * kPtTile);
@@ -319,7 +351,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       }
       mbar_init(&sh->q_full[i], 1);
       mbar_init(&sh->q_empty[i], 1);
-      mbar_init(&sh->fin[i], 8);
+      mbar_init(&sh->fin[i], 4);
+      mbar_init(&sh->o_full[i], 1);
+      mbar_init(&sh->o_empty[i], 4);
       mbar_init(&sh->drain[i], 1);
     }
     mbar_init(&sh->other, 4);
@@ -359,7 +393,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
 
   // The next record, for a whole warp; `n` counts records.
   auto take_item = [&](int n, PtItem& it) -> bool {
-    if (!mbar_wait_warp(&sh->item_full[n % kPtItems], (n / kPtItems) & 1)) return false;
+    if (!pt_wait_warp(&sh->item_full[n % kPtItems], (n / kPtItems) & 1)) return false;
     it = sh->item[n % kPtItems];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->item_empty[n % kPtItems]);
@@ -374,145 +408,53 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kPtO + slot * 128 + lane_base;
     const float f = finite_factor(a.scale_log2);
     const int my_token = r / Hg, my_head = r - my_token * Hg;
-    int done = 0, done_o = 0, edges = 0, uc = -1;  // steps of this slot and of the other one, edge blocks, units so far
-    bool mine = false, others = false, shared_par = false, one_before = false;
+    int done = 0, edges = 0, live = 0;             // steps of this slot, edge blocks, units with keys so far
+    bool shared_par = false;
     float M = -INFINITY, l = 0.f, l_bf16 = 0.f;    // (l_bf16: of P as it is multiplied)
     int pos = 0;
 
-    // writes the unit's rows (or its partial state)
-    auto finish = [&](const PtItem& it) -> bool {
-      const bool two = it.flags & kPtTwo;
-      const int place = (it.flags >> kPtPlace) - 1;
-      if (mine && !mbar_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) return false;
-      if (!two) {
-        if (slot == 1) {
-          sh->other_m[r] = M;
-          sh->other_l[r] = l;
-          sh->other_fix[r] = l_bf16 != 0.f ? l * rcp(l_bf16) : 1.f;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->other);
-          return true;
-        }
-        if (!mbar_wait_warp(&sh->other, shared_par)) return false;
-        if (others && !mbar_wait_warp(&sh->pv_done[1][1], (done_o - 1) & 1)) return false;
-      }
-      tc_fence_after();
-      // O is put right by the ratio of the sums of P before and after its rounding, the state of the row is
-      // then fa * own O + fb * the other slot's O
-      const float fix = mine && l_bf16 != 0.f ? l * rcp(l_bf16) : 1.f;
-      float fa = fix;
-      if (!two && others) {  // (slot 1 had blocks, so this slot had the first one)
-        const float mo = sh->other_m[r], lo = sh->other_l[r];
-        const float mn = fmaxf(M, mo);
-        const float wa = mn == -INFINITY ? 1.f : ex2(M - mn), wb = mn == -INFINITY ? 1.f : ex2(mo - mn);
-        const float fb = wb * sh->other_fix[r];
-        fa *= wa;
-        l = l * wa + lo * wb;
-        M = mn;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t x[16], y[16];
-          tmem_ld16(tO + 16 * c, x);
-          tmem_ld16(tO + 128 + 16 * c, y);
-          tmem_wait_ld(x);
-          tmem_wait_ld(y);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), fb, __uint_as_float(x[i]) * fa));
-          tmem_st16(tO + 16 * c, x);
-        }
-        tmem_wait_st();
-        fa = 1.f;
-      }
-      const int t = my_token + (two && slot ? tt : 0);  // token of the unit
-      const bool valid = my_token < tt && t < it.tokens;
-      const float inv = l != 0.f ? rcp(l) : 0.f;        // (NaN counts as a sum)
-      if (place < 0) fa *= inv;
-      const int64_t row0 = static_cast<int64_t>(it.token0) * H + it.g * Hg;  // row of the outputs of the unit's first one
-      const int off = t * H + my_head;
-      const int pr = r + (two && slot ? kPtRows : 0);   // row of the partial state
-      float* part = place < 0 ? nullptr : a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats;
-      if (!mine) {  // no key
-        uint4* dst = reinterpret_cast<uint4*>(a.out + (row0 + off) * kDim);
-        for (int c = 0; valid && c < kDim / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-      } else if (place < 0) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {  // 32 dims
-          uint32_t x[32];
-          tmem_ld32(tO + 32 * c, x);
-          tmem_wait_ld(x);
-          uint4 w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t* p = reinterpret_cast<uint32_t*>(&w[j]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              p[i] = pack_bf16x2(__uint_as_float(x[8 * j + 2 * i]) * fa, __uint_as_float(x[8 * j + 2 * i + 1]) * fa);
-          }
-          if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + (row0 + off) * kDim + 32 * c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dst[j] = w[j];
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {  // 16 dims: four of all rows together, the lanes of a store are neighbouring rows
-          uint32_t x[16];
-          tmem_ld16(tO + 16 * c, x);
-          tmem_wait_ld(x);
-          float4* dst = reinterpret_cast<float4*>(part) + 4 * c * (2 * kPtRows) + pr;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (valid)
-              dst[j * 2 * kPtRows] = make_float4(__uint_as_float(x[4 * j]) * fa, __uint_as_float(x[4 * j + 1]) * fa,
-                                                 __uint_as_float(x[4 * j + 2]) * fa, __uint_as_float(x[4 * j + 3]) * fa);
-        }
-      }
-      if (valid) {
-        if (place < 0) {
-          if (a.lse != nullptr) a.lse[row0 + off] = fp8_lse(M, l);
-        } else {
-          part[2 * kPtRows * kDim + pr] = M;
-          part[2 * kPtRows * (kDim + 1) + pr] = l;
-        }
-      }
-      tc_fence_before();
-      return true;
-    };
-
-    for (;;) {
+    for (int n = 0;; ++n) {
       PtItem it;
-      if (!take_item(++uc, it)) {
+      if (!take_item(n, it)) {
         failed = true;
         break;
       }
       if (it.flags & kPtEnd) break;
+      if (it.lo >= it.hi) continue;
       const bool two = it.flags & kPtTwo;
-      // slot 0 reads slot 1's O and statistics of a one-tile unit: slot 1 goes on when it has
-      if (slot == 1 && one_before && !mbar_wait_warp(&sh->fin[(uc - 1) & 1], ((uc - 1) >> 1) & 1)) {
-        failed = true;
-        break;
-      }
       M = -INFINITY;
       l = l_bf16 = 0.f;
       pos = it.pos0 + min(min(my_token, tt - 1) + (two && slot ? tt : 0), it.tokens - 1);
       // with one tile the blocks alternate between the slots
       const int edge = it.edge(), step = two ? 1 : 2, first = it.lo + (two ? 0 : slot);
       const int tile0 = it.pos0 + (two && slot ? tt : 0);  // position of the tile's first row
-      mine = first < it.hi;
-      others = two ? mine : it.lo + (slot ^ 1) < it.hi;
-      done_o += two ? it.hi - it.lo : (it.hi - it.lo + slot) / 2;
 #pragma unroll 1
       for (int p = first; p < it.hi; p += step) {
         // what the V warps found in a block that not every row sees whole they look up among themselves when the unit is
         // written (fin): seeing the stage ready here orders it before that (it is not used again before this step's P)
         const int e = edges + p - edge;
-        if (!mbar_wait_warp(&sh->s_full[slot], done & 1) ||
-            (p >= edge && !mbar_wait_warp(&sh->v_ok[e % kPtV], (e / kPtV) & 1))) {
+        if (!pt_wait_warp(&sh->s_full[slot], done & 1) ||
+            (p >= edge && !pt_wait_warp(&sh->v_ok[e % kPtV], (e / kPtV) & 1))) {
           failed = true;
           break;
         }
         tc_fence_after();
+        if (__builtin_expect(p * kBlock + kBlock - 1 > tile0, 0)) {
+          // some row of the tile must not see one of these keys: -inf over its scores, where they lie (a short loop: code that
+          // a unit runs once costs its instruction fetches)
+          const int vis = pos - p * kBlock + 1;  // visible columns
+#pragma unroll 1
+          for (int c = max(__reduce_min_sync(0xffffffffu, vis), 0) >> 5; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(tS + 32 * c, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 32 * c + j < vis ? x[j] : 0xff800000u;
+            tmem_st16(tS + 32 * c, x);
+            tmem_st16(tS + 32 * c + 16, x + 16);
+          }
+          tmem_wait_st();
+        }
         uint32_t v[2][64];
         float mx, mx1;
         tmem_ld64_max(tS, v[0], mx);
@@ -521,23 +463,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         tmem_wait_ld(v[1]);
         asm volatile("" : "+f"(mx), "+f"(mx1));
         mx = fmaxf(mx, mx1);
-        if (__builtin_expect(p * kBlock + kBlock - 1 > tile0, 0)) {
-          // some row of the tile must not see one of these keys: -inf over its scores, and the maximum again
-          const int vis = pos - p * kBlock + 1;  // visible columns
-          const int least = __reduce_min_sync(0xffffffffu, vis);
-          mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&x)[64] = v[c >> 1];
-            if (32 * c + 32 > least) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[32 * (c & 1) + j] = 32 * c + j < vis ? x[32 * (c & 1) + j] : 0xff800000u;
-            }
-#pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              mx = max3(mx, __uint_as_float(x[32 * (c & 1) + j]), __uint_as_float(x[32 * (c & 1) + j + 1]));
-          }
-        }
         mx *= f;
         if (__builtin_expect(__any_sync(0xffffffffu, mx > M), 0)) {
           float alpha = 1.f;
@@ -549,7 +474,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
             l_bf16 *= alpha;
           }
           if (p > first) {  // O as the products so far leave it, rescaled
-            if (!mbar_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) {
+            if (!pt_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) {
               failed = true;
               break;
             }
@@ -595,46 +520,181 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         l += sum.x + sum.y;
         l_bf16 += (sum_bf16[0] + sum_bf16[1]) + (sum_bf16[2] + sum_bf16[3]);
       }
-      if (failed || !finish(it)) {
+      edges += it.hi - edge;
+      // what is left to the V warps, who write the rows: the factors of O.  They have read the last unit's.
+      if (failed || (live > 0 && !pt_wait_warp(&sh->o_empty[slot], (live - 1) & 1))) {
         failed = true;
         break;
       }
-      edges += it.hi - edge;
-      one_before = !two;
-      if (!two) shared_par = !shared_par;
+      ++live;
+      // O is put right by the ratio of the sums of P before and after its rounding
+      float fa = l_bf16 != 0.f ? l * rcp(l_bf16) : 1.f;
+      if (!two) {  // slot 0 adds both slots' states
+        if (slot == 1) {
+          sh->other_m[r] = M;
+          sh->other_l[r] = l;
+          sh->factor[1][r] = fa;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh->other);
+            mbar_arrive(&sh->fin[1]);
+          }
+          continue;
+        }
+        if (!pt_wait_warp(&sh->other, shared_par)) {
+          failed = true;
+          break;
+        }
+        shared_par = !shared_par;
+      }
+      const int place = (it.flags >> kPtPlace) - 1;
+      float fb = 0.f;
+      if (!two) {
+        const float mo = sh->other_m[r], lo = sh->other_l[r];
+        const float mn = fmaxf(M, mo);
+        const float wa = mn == -INFINITY ? 1.f : ex2(M - mn), wb = mn == -INFINITY ? 1.f : ex2(mo - mn);
+        fa *= wa;
+        fb = wb * sh->factor[1][r];
+        l = l * wa + lo * wb;
+        M = mn;
+      }
+      const float inv = place >= 0 ? 1.f : l != 0.f ? rcp(l) : 0.f;  // (NaN counts as a sum)
+      sh->factor[slot][r] = fa * inv;
+      if (!two) sh->factor[1][r] = fb * inv;
+      const int t = my_token + (two && slot ? tt : 0);               // token of the unit
+      if (my_token < tt && t < it.tokens) {
+        if (place >= 0) {
+          float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats + 2 * kPtRows * kDim;
+          const int pr = r + (two && slot ? kPtRows : 0);            // row of the partial state
+          part[pr] = M;
+          part[2 * kPtRows + pr] = l;
+        } else if (a.lse != nullptr) {
+          a.lse[static_cast<int64_t>(it.token0 + t) * H + it.g * Hg + my_head] = fp8_lse(M, l);
+        }
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->fin[uc & 1]);
+      if (lane == 0) mbar_arrive(&sh->fin[slot]);
     }
   } else if (warp < 12) {
     registers_down<64>();
     // ---- V: infinities and NaN out of the rows that not every row of the unit sees
-    const int ct = tid - 256;
-    int blocks = 0, edges = 0;
+    // and the rows of a unit when its products are done
+    const int ct = tid - 256, my_token = ct / Hg, my_head = ct - my_token * Hg;
+    int blocks = 0, edges = 0, full0 = 0, full1 = 0;  // blocks, edge blocks, units with products in slot 0 and 1
     if (lane < 8) sh->special[lane][warp - 8] = -1;
     __syncwarp();
-    // unit n is written: its rows get back what was taken out
-    auto put_back = [&](int n, const PtItem& it) -> bool {
-      if (!mbar_wait_warp(&sh->fin[n & 1], (n >> 1) & 1)) return false;
+    // Unit n of those with keys: row ct of both tiles.
+    auto write = [&](int n, const PtItem& it) -> bool {
+      const bool two = it.flags & kPtTwo, both = !two && it.lo + 1 < it.hi;  // (one tile: slot 1 has blocks as well)
+      const int place = (it.flags >> kPtPlace) - 1;
+      float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + max(place, 0)) * kPtPlaceFloats;
+      uint16_t* out = a.out + (static_cast<int64_t>(it.token0 + my_token) * H + it.g * Hg + my_head) * kDim;
+      const uint32_t tO = tmem + kPtO + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      // with one tile slot 0 has the sum's factors, and all is done with it
+      if (!pt_wait_warp(&sh->fin[0], n & 1) || !pt_wait_warp(&sh->o_full[0], full0 & 1)) return false;
+      ++full0;
+      if (!two && !pt_wait_warp(&sh->fin[1], n & 1)) return false;
+      if (both && !pt_wait_warp(&sh->o_full[1], full1 & 1)) return false;
+      if (both) ++full1;
+#pragma unroll 1
+      for (int s = 0; s < (two ? 2 : 1); ++s) {
+        if (s == 1) {
+          if (!pt_wait_warp(&sh->fin[1], n & 1) || !pt_wait_warp(&sh->o_full[1], full1 & 1)) return false;
+          ++full1;
+        }
+        tc_fence_after();
+        float fa = sh->factor[s][ct]; const float fb = sh->factor[1][ct];
+        const bool valid = my_token < tt && my_token + s * tt < it.tokens;
+        uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(s) * tt * H * kDim);
+        if (both) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16], y[16];
+            tmem_ld16(tO + 16 * c, x);
+            tmem_ld16(tO + 128 + 16 * c, y);
+            tmem_wait_ld(x);
+            tmem_wait_ld(y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), fb, __uint_as_float(x[i]) * fa));
+            tmem_st16(tO + 16 * c, x);
+          }
+          tmem_wait_st();
+          fa = 1.f;
+        }
+        if (place < 0) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(tO + s * 128 + 32 * c, x);
+            tmem_wait_ld(x);
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t* p = reinterpret_cast<uint32_t*>(&w[j]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                p[i] = pack_bf16x2(__uint_as_float(x[8 * j + 2 * i]) * fa, __uint_as_float(x[8 * j + 2 * i + 1]) * fa);
+            }
+            turn_quad(w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int to = __shfl_sync(0xffffffffu, valid ? my_token * H + my_head : -1, (lane & ~3) + i);
+              if (to >= 0)
+                *reinterpret_cast<uint4*>(a.out + ((static_cast<int64_t>(it.token0) + s * tt) * H + it.g * Hg + to) * kDim + 32 * c +
+                                          8 * (lane & 3)) = w[i];
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[16];
+            tmem_ld16(tO + s * 128 + 16 * c, x);
+            tmem_wait_ld(x);
+            float4* to = reinterpret_cast<float4*>(part) + 4 * c * (2 * kPtRows) + ct + s * kPtRows;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (valid) to[j * 2 * kPtRows] = make_float4(__uint_as_float(x[4 * j]) * fa, __uint_as_float(x[4 * j + 1]) * fa, __uint_as_float(x[4 * j + 2]) * fa, __uint_as_float(x[4 * j + 3]) * fa);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh->o_empty[s]);
+          if (!two) mbar_arrive(&sh->o_empty[1]);
+        }
+      }
       const int* sp = sh->special[n & 7];
-      if (sp[0] == n || sp[1] == n || sp[2] == n || sp[3] == n) pt_put_back(a, it);
+      if (sp[0] == n || sp[1] == n || sp[2] == n || sp[3] == n)
+        pt_put_back(a, it.flags, it.lo, it.hi, it.token0, it.tokens, it.pos0, it.key0, it.g);
       return true;
     };
-    PtItem one{}, two{};  // the unit before, and the one before that
-    for (int uc = 0; !failed; ++uc) {
+    PtItem before{};  // the last unit with keys, not written yet
+    int live = 0;     // units with keys so far
+    for (int n = 0; !failed; ++n) {
       PtItem it;
-      if (!take_item(uc, it) || (uc >= 2 && !put_back(uc - 2, two))) {
+      if (!take_item(n, it)) {
         failed = true;
         break;
       }
-      if (it.flags & kPtEnd) {
-        failed = uc >= 1 && !put_back(uc - 1, one);
+      if (!(it.flags & kPtEnd) && it.lo >= it.hi) {  // no row has a key
+        for (int t = my_token; my_token < tt && t < it.tokens; t += tt) {
+          const int64_t row = static_cast<int64_t>(it.token0 + t) * H + it.g * Hg + my_head;
+          for (int c = 0; c < kDim / 8; ++c) reinterpret_cast<uint4*>(a.out + row * kDim)[c] = make_uint4(0, 0, 0, 0);
+          if (a.lse != nullptr) a.lse[row] = -INFINITY;
+        }
+        continue;
+      }
+      if (live > 0 && !write(live - 1, before)) {
+        failed = true;
         break;
       }
-      two = one;
-      one = it;
+      if (it.flags & kPtEnd) break;
+      before = it;
+      ++live;
+#pragma unroll 1
       for (int p = it.edge(); p < it.hi; ++p, ++edges) {
         const int vs = (blocks + p - it.lo) % kPtV;
-        if (!mbar_wait_warp(&sh->v_edge[edges % kPtV], (edges / kPtV) & 1)) {
+        if (!pt_wait_warp(&sh->v_edge[edges % kPtV], (edges / kPtV) & 1)) {
           failed = true;
           break;
         }
@@ -649,7 +709,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
           any |= r >= r0 ? s : 0u;
         }
         if (any != 0u) {
-          sh->special[uc & 7][warp - 8] = uc;
+          sh->special[(live - 1) & 7][warp - 8] = live - 1;
           auto clear = [](uint32_t w) {
             const uint32_t s = bf16_special(w);
             return w & ~(s | (s - (s >> 15)));  // (whole halves: the top bit and the 15 below it)
@@ -694,7 +754,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     const uint32_t q_bytes = static_cast<uint32_t>(tt) * Hg * 256;
     int n = 0, blocks = 0, tiles0 = 0, tiles1 = 0;  // units, blocks, units that used tile 0 and tile 1
     auto record = [&](const PtItem& it) -> bool {
-      if (n >= kPtItems && !mbar_wait_warp(&sh->item_empty[n % kPtItems], (n / kPtItems - 1) & 1)) return false;
+      if (n >= kPtItems && !pt_wait_warp(&sh->item_empty[n % kPtItems], (n / kPtItems - 1) & 1)) return false;
       if (lane == 0) {
         sh->item[n % kPtItems] = it;
         mbar_arrive(&sh->item_full[n % kPtItems]);
@@ -707,6 +767,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       const int q0 = a.cu_q[b], key0 = a.cu_k[b], Lq = a.cu_q[b + 1] - q0;
       const PtUnit t = pt_unit(Lq, a.cu_k[b + 1] - key0, i, tt);
       const int pages = max(t.pages, 1), cost = t.cost(), token0 = q0 + i * 2 * tt;
+#pragma unroll 1
       for (int g = 0; g < G && !failed; ++g) {
         const int64_t u0 = first + static_cast<int64_t>(g) * cost;
         if (u0 + cost <= x0) continue;
@@ -721,9 +782,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
           break;
         }
         if (t.pages == 0) continue;
+#pragma unroll 1
         for (int k = 0; k < t.width && !failed; ++k) {  // the unit's queries
           int& used = k ? tiles1 : tiles0;
-          if (used > 0 && !mbar_wait_warp(&sh->q_empty[k], (used - 1) & 1)) {
+          if (used > 0 && !pt_wait_warp(&sh->q_empty[k], (used - 1) & 1)) {
             failed = true;
             break;
           }
@@ -734,9 +796,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
             tma_box(q_tile + k * kPtTile + kPtHalf, &maps.q, 64, g * Hg, token0 + k * tt, &sh->q_full[k], once);
           }
         }
+#pragma unroll 1
         for (int p = lo; p < hi && !failed; ++p) {
           const int ks = blocks % kPtK;
-          if (blocks >= kPtK && !mbar_wait_warp(&sh->k_empty[ks], (blocks / kPtK - 1) & 1)) {
+          if (blocks >= kPtK && !pt_wait_warp(&sh->k_empty[ks], (blocks / kPtK - 1) & 1)) {
             failed = true;
             break;
           }
@@ -761,9 +824,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     if (!failed) failed = !record(PtItem{kPtEnd, 0, 0, 0, 0, 0, 0, 0});
     if (failed) {
       // wait (bounded) for the copies still in flight
-      for (int k = max(0, blocks - kPtK); k < blocks; ++k) mbar_wait(&sh->k_full[k % kPtK], (k / kPtK) & 1);
-      if (tiles0 > 0) mbar_wait(&sh->q_full[0], (tiles0 - 1) & 1);
-      if (tiles1 > 0) mbar_wait(&sh->q_full[1], (tiles1 - 1) & 1);
+#pragma unroll 1
+      for (int k = max(0, blocks - kPtK); k < blocks; ++k) pt_wait(&sh->k_full[k % kPtK], (k / kPtK) & 1);
+      if (tiles0 > 0) pt_wait(&sh->q_full[0], (tiles0 - 1) & 1);
+      if (tiles1 > 0) pt_wait(&sh->q_full[1], (tiles1 - 1) & 1);
     }
    } else if (warp == 15) {
     // ---- the copies of V
@@ -777,9 +841,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       }
       if (it.flags & kPtEnd) break;
       const int edge = it.edge();
+#pragma unroll 1
       for (int p = it.lo; p < it.hi; ++p) {
         const int vs = blocks % kPtV;
-        if (blocks >= kPtV && !mbar_wait_warp(&sh->v_empty[vs], (blocks / kPtV - 1) & 1)) {
+        if (blocks >= kPtV && !pt_wait_warp(&sh->v_empty[vs], (blocks / kPtV - 1) & 1)) {
           failed = true;
           break;
         }
@@ -795,8 +860,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       }
     }
     if (failed) {  // wait (bounded) for the copies still in flight
-      for (int k = max(0, plain - kPtV); k < plain; ++k) mbar_wait(&sh->v_full[k % kPtV], (k / kPtV) & 1);
-      for (int k = max(0, edges - kPtV); k < edges; ++k) mbar_wait(&sh->v_edge[k % kPtV], (k / kPtV) & 1);
+#pragma unroll 1
+      for (int k = max(0, plain - kPtV); k < plain; ++k) pt_wait(&sh->v_full[k % kPtV], (k / kPtV) & 1);
+#pragma unroll 1
+      for (int k = max(0, edges - kPtV); k < edges; ++k) pt_wait(&sh->v_edge[k % kPtV], (k / kPtV) & 1);
     }
    } else {
     // ---- product issuers: warp 13 S, warp 14 P V.  Two warps, because issuing blocks while the tensor
@@ -809,10 +876,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       const uint32_t qb = smem_u32(q_tile), kb = smem_u32(k_ring), vb = smem_u32(v_ring);
       int blocks = 0, done0 = 0, done1 = 0;             // blocks, steps of the slots so far
       int plain = 0, edges = 0;                         // blocks of the two kinds in the units before
+      int live = 0;                                     // units with keys before
       int tiles1 = 0, tiles0 = 0;                       // units that used tile 1 and tile 0
       bool bad = false;
       for (int n = 0; !bad; ++n) {
-        if (!mbar_wait(&sh->item_full[n % kPtItems], (n / kPtItems) & 1)) {
+        if (!pt_wait(&sh->item_full[n % kPtItems], (n / kPtItems) & 1)) {
           bad = true;
           break;
         }
@@ -823,22 +891,25 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         const int width = it.flags & kPtTwo ? 2 : 1, edge = it.edge();
         ++tiles0;
         if (width == 2) ++tiles1;
+        bool read0 = live == 0, read1 = live == 0;  // the last unit's O of slot 0 and 1 is known to be read
+#pragma unroll 1
         for (int p = it.lo; p < it.hi && !bad; ++p, ++blocks) {
           const int ks = blocks % kPtK, vs = blocks % kPtV;
           const int k = p < edge ? plain + p - it.lo : edges + p - edge;
-          if (scores ? !mbar_wait(&sh->k_full[ks], (blocks / kPtK) & 1)
-                     : !mbar_wait(p < edge ? &sh->v_full[k % kPtV] : &sh->v_ok[k % kPtV], (k / kPtV) & 1)) {
+          if (scores ? !pt_wait(&sh->k_full[ks], (blocks / kPtK) & 1)
+                     : !pt_wait(p < edge ? &sh->v_full[k % kPtV] : &sh->v_ok[k % kPtV], (k / kPtV) & 1)) {
             bad = true;
             break;
           }
-          for (int i = 0; i < width && !bad; ++i) {
+  #pragma unroll 1
+        for (int i = 0; i < width && !bad; ++i) {
             const int s = width == 2 ? i : (p - it.lo) & 1;
             const int d = s ? done1 : done0;
             const bool last = i == width - 1;
             if (scores) {
               // S overwrites the slot's P: it waits until that has been multiplied
-              if ((p == it.lo && !mbar_wait(&sh->q_full[i], ((i ? tiles1 : tiles0) - 1) & 1)) ||
-                  (d > 0 && !mbar_wait(&sh->pv_done[s][1], (d - 1) & 1))) {
+              if ((p == it.lo && !pt_wait(&sh->q_full[i], ((i ? tiles1 : tiles0) - 1) & 1)) ||
+                  (d > 0 && !pt_wait(&sh->pv_done[s][1], (d - 1) & 1))) {
                 bad = true;
                 break;
               }
@@ -854,8 +925,16 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
               if (last) umma_commit(&sh->k_empty[ks]);
             } else {
               const bool first = p < it.lo + 2 && (width == 2 ? p == it.lo : true);  // of the slot in this unit
+              const bool final = width == 2 ? p == it.hi - 1 : p >= it.hi - 2;
+              // a slot's O is overwritten when the last unit's has been read; both are asked for before the unit's last
+              // product, so that no phase of o_empty is missed
+              const bool end = last && p == it.hi - 1;
+              if ((first && s == 0 || end) && !read0) read0 = pt_wait(&sh->o_empty[0], (live - 1) & 1), bad |= !read0;
+              if ((first && s == 1 || end) && !read1) read1 = pt_wait(&sh->o_empty[1], (live - 1) & 1), bad |= !read1;
+              if (bad) break;
+#pragma unroll 1
               for (int h = 0; h < 2; ++h) {  // 64 keys: the products of the first half run beside the softmax of the second
-                if (!mbar_wait(&sh->p_full[s][h], d & 1)) {
+                if (!pt_wait(&sh->p_full[s][h], d & 1)) {
                   bad = true;
                   break;
                 }
@@ -866,6 +945,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
                   umma_f16_tmem_a(tmem + kPtO + s * 128, tmem + s * 128 + h * 64 + 8 * kk, vd + ((kk * 2048) >> 4), id_o,
                                   !first || h > 0 || kk > 0 ? 1u : 0u);
                 umma_commit(&sh->pv_done[s][h]);
+                if (final && h == 1) umma_commit(&sh->o_full[s]);
                 if (last && h == 1) umma_commit(&sh->v_empty[vs]);
               }
             }
@@ -874,11 +954,12 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         }
         plain += edge - it.lo;
         edges += it.hi - edge;
+        ++live;
       }
       if (bad) {  // the products still running end before TMEM is freed
         flag_error(a.err, MSA_DEVERR_TIMEOUT);
         umma_commit(&sh->drain[scores]);
-        mbar_wait(&sh->drain[scores], 0);
+        pt_wait(&sh->drain[scores], 0);
       }
     }
     __syncwarp();
