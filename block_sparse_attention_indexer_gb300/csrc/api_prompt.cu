@@ -17,9 +17,9 @@ msa_status_t check_packed(const msa_config_t* c, const msa_packed_t* p) {
   if (p == nullptr || p->batch < 0 || p->q_tokens < 0 || p->k_tokens < 0) return MSA_ERR_INVALID_ARG;
   if (p->batch > 0 && (p->cu_q == nullptr || p->cu_k == nullptr)) return MSA_ERR_INVALID_ARG;
   if (p->batch > kMaxBatchSmem || p->q_tokens > kMaxTokens || p->k_tokens > kMaxTokens) return MSA_ERR_UNSUPPORTED;
-  // the flat list of (tile of 128 rows, 128 keys) steps is counted in 32 bits
+  // the units' cost is counted in 32 bits
   const int64_t blocks = (p->k_tokens + 127) / 128;
-  if (2 * prompt_max_units(p->q_tokens, p->batch, c->heads_per_group) * (blocks > 1 ? blocks : 1) >
+  if (prompt_max_units(p->q_tokens, p->batch, c->heads_per_group) * (2 * (blocks > 1 ? blocks : 1) + kPromptUnitCost) >
       INT32_MAX / c->num_kv_groups)
     return MSA_ERR_UNSUPPORTED;
   return MSA_OK;

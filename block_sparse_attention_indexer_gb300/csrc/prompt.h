@@ -30,6 +30,8 @@ struct PromptArgs {
   float* partial;       // partial softmax states of units cut by the split of the work
 };
 
+// What the start of a unit counts in the split of the work, in (tile, 128 keys) steps.
+constexpr int kPromptUnitCost = 4;
 // Query tokens of a tile of 128 rows (token, head), and of a unit of two tiles.
 inline int prompt_tile_tokens(int heads_per_group) { return 128 / heads_per_group; }
 // At least as many units as the packed sequences have.

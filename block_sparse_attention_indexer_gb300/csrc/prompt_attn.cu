@@ -1,28 +1,41 @@
 // Causal attention of packed bf16 prompts on the tcgen05 tensor cores.
 //
-// Mathematics: P_j = 2^(e_j - M) with e_j = (q . k_j) softmax_scale log2(e), O = sum P_j v_j, l = sum P_j;
-// out = O / l, lse = ln 2 (M + log2 l).  M is an integer (rescaling O and l is exact) that is moved only where a
-// P would pass 1, to 2^8 above the largest so far, so that most pages move nothing.  P is rounded
-// to bf16 as the operand of P V: by 2^-8 of itself at most, whatever its size (bf16 has float32's range); l
-// adds what was before the rounding.  S, O, l and M are float32.
+// Mathematics: P_j = 2^(e_j - M) with e_j = (q . k_j) softmax_scale log2(e), O = sum P_j v_j, l = sum P_j; lse = ln 2 (M +
+// log2 l).  M is an integer (rescaling O and l is exact) that moves only where a P would pass 1, to 2^8 above the largest
+// so far, so that most blocks move nothing.  P is rounded to bf16, V's type, as the operand of P V: by 2^-8 of itself at
+// most, whatever its size (bf16 has float32's range).  O is divided by the sum of the rounded P: a common part of their
+// errors cancels, and a row's error is at most that of rounding its output, on average (with l, a row of one key
+// would be off by P's whole rounding).  l adds P before the rounding, for lse.  S, O, l and M are float32.
 //
 // Work.  A row is a (token, head) of a KV head; a tile is 128 rows, floor(128 / Hg) tokens with their Hg heads, a
 // unit two tiles (or one, of a sequence's last tokens) of a sequence and a KV head, so that keys loaded once meet
-// 256 rows and the causal border costs half a block of 128 keys for each tile, whatever Hg is.  A unit's
-// products are counted in (tile, 128 keys) steps; all units' steps are one flat list that a
-// persistent grid, one CTA an SM, cuts into equal ranges (tile_split.cuh).  Units that are cut leave partial
-// states, which a second kernel adds.  Two accumulator slots work in turn: with two tiles each block of keys
-// is used by slot 0 and slot 1, with one tile the blocks alternate between the slots.
+// 256 rows and the causal border costs half a block of 128 keys for each tile, whatever Hg is.  A unit's cost is
+// counted in (tile, 128 keys) steps and kPtUnitCost for its start; all units are one flat list that a persistent grid,
+// one CTA an SM, cuts into equal ranges (tile_split.cuh).  Units that are cut leave partial states, which a second
+// kernel adds.  Two accumulator slots work in turn: with two tiles each block of keys is used by slot 0 and
+// slot 1, with one tile the blocks alternate between the slots.
 //   * S = Q K^T: Q and K by tensor copies in 128-byte swizzle (a Q tile is one box of Hg heads by tokens).
 //   * O += P V: P in tensor memory over S (the A operand), V as it lies, as the MN-major B operand.
 // TMEM: S of the two slots, then O of the two slots: 4 x 128 columns, all of it.
 //
-// Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread), 8-11 look through the V rows that not
-// every row of the unit sees, 12 issues the copies, 13 the products S, 14 P V.
+// Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread, a block's 128 scores in registers), 8-11 write the
+// rows of a unit while the next one's softmax runs, and look through the V rows that not every row of a unit sees, 12 makes the
+// units known and copies Q and K, 13 issues the products S, 14 P V, 15 copies V.
 // What a row does not see cannot reach it: its S is replaced by -inf, and infinities and NaN in V are taken
 // out of the blocks where they could meet a P of 0; rows that do see them get them back at the end.
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
+//
+// What bounds it: a slot's chain (S, softmax, P V of a block, one after another) is about as long as both slots' products,
+// and the products run at the power limit's clock (1.65 PFLOP/s for a prompt of 16K tokens and 32 heads; without any
+// exponential it would be 1.76).  Measured on the way there, for that prompt: S by halves of 64 keys, so that a half's product
+// runs beside the other's softmax, 1.78 ms against 1.43 (an M 128 x N 64 product takes 390 cycles where half of N 128
+// takes 256: its operands fill the shared memory's bandwidth); 64 scores at a time 1.51 against 1.33; one hand-over of P
+// for 128 keys 1.41 against 1.35; the exponentials of the second half held back behind the first half's hand-over 1.37.
+// Stages of K and V and register shares: 1 to 3 %.  Code that a unit runs once costs its instruction fetches (the
+// epilogue, unrolled masks: 1 us and more each), so it is short loops, and the softmax's loop has nothing
+// rare inside it; function calls in that branch cost it registers (1.40 -> 1.48 ms).
+// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units) 2 us of a unit's 13 are not its steps.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -47,10 +60,11 @@ constexpr int kPtMergeRows = 32;              // rows of a CTA of the merge
 constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
-#ifndef PT_UNIT_COST
-#define PT_UNIT_COST 4
-#endif
-constexpr int kPtUnitCost = PT_UNIT_COST;
+constexpr int kPtUnitCost = kPromptUnitCost;
+// Cost of a unit up to which it is not cut: of few units (no more than CTAs: nobody waits for a second one) and of many.
+// A cut costs two partial states and a merge, a cut moved to the end of its unit leaves one CTA up to half of the unit
+// more than its share.  One prompt of 512 tokens 17 us with 24, 25 with 16; one of 2K 58 us with 16, 66 with 50.
+constexpr int kPtWholeFew = 24, kPtWholeMany = 16;
 
 // A unit, or the part of it that this CTA has: blocks lo .. hi - 1 of 128 keys (none of a unit whose rows see no key).
 struct alignas(16) PtItem {
@@ -138,17 +152,6 @@ __device__ __forceinline__ int pt_prefix(int v, int& carry, int* warp_sum) {
   const int at = carry + x - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
   carry += __reduce_add_sync(0xffffffffu, w);
   return at;
-}
-
-// Cost of a unit up to which it is not cut: a cut costs two partial states and a merge, about as much as
-// kPtCutSteps steps; of `all` units on n CTAs some take ceil(all / n), so that an uncut unit of S steps costs
-// idle * S / n more than its share.  Above 64 a unit is cut in any case.
-__device__ __forceinline__ int pt_whole(int64_t all, int n) {
-  constexpr int kPtWhole = 64, kPtCutSteps = 16;
-  if (all == 0) return kPtWhole;
-  const int64_t idle = n - 1 - (all - 1) % n;
-  const int64_t most = static_cast<int64_t>(kPtCutSteps) * n;
-  return idle * kPtWhole <= most ? kPtWhole : static_cast<int>(most / idle);
 }
 
 // The plan by a whole CTA: base[b], b = 0..batch: units of the sequences before b; prefix[u], u = 0..units: cost (per
@@ -359,6 +362,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     mbar_init(&sh->other, 4);
     fence_mbar_init();
   }
+  if (tid < 32) sh->special[tid >> 2][tid & 3] = -1;
   // rows of a tile behind its tokens (Hg does not divide 128): no copy writes them
   if (tt * Hg < kPtRows && tid < 2 * (kPtRows - tt * Hg) * 16) {
     const int i = tid / 16, t = i & 1, r = tt * Hg + (i >> 1), c = tid & 15;
@@ -581,8 +585,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     // and the rows of a unit when its products are done
     const int ct = tid - 256, my_token = ct / Hg, my_head = ct - my_token * Hg;
     int blocks = 0, edges = 0, full0 = 0, full1 = 0;  // blocks, edge blocks, units with products in slot 0 and 1
-    if (lane < 8) sh->special[lane][warp - 8] = -1;
-    __syncwarp();
     // Unit n of those with keys: row ct of both tiles.
     auto write = [&](int n, const PtItem& it) -> bool {
       const bool two = it.flags & kPtTwo, both = !two && it.lo + 1 < it.hi;  // (one tile: slot 1 has blocks as well)
@@ -739,8 +741,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
     int x0 = 0, x1 = 0, u = 0, b = 0;
     int64_t E = 0, first = 0;  // all cost, cost before unit u
     if (units > 0) {
-      const int whole = pt_whole(static_cast<int64_t>(units) * G, gridDim.x);
       E = static_cast<int64_t>(prefix[units]) * G;
+      const int whole = static_cast<int64_t>(units) * G > gridDim.x ? kPtWholeMany : kPtWholeFew;
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
         x0 = x1;
@@ -1072,7 +1074,8 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s)
   const int own_plan = a.batch <= kPtOwnBatch && most <= kPtOwnUnits ? 1 : 0;
   if (!own_plan && (e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a)) != cudaSuccess) return e;
   if ((e = launch_dependent(prompt_attn_kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps, own_plan)) != cudaSuccess) return e;
-  if (ctas == 1) return cudaSuccess;
+  // (no unit is longer than what pt_whole leaves whole)
+  if (ctas == 1 || 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost <= kPtWholeMany) return cudaSuccess;
   return ctas / units >= kFp8MergeSplitParts
              ? launch_dependent(prompt_merge_kernel<true>, dim3(ctas - 1, 2 * kPtRows), kFp8MergeThreads, 0, s, a, ctas)
              : launch_dependent(prompt_merge_kernel<false>, dim3(ctas - 1, 2 * kPtRows / kPtMergeRows), kFp8MergeThreads, 0, s, a, ctas);

@@ -431,8 +431,8 @@ msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int
  * row of one key.  The same arguments give the same bits in every call on one GPU.
  * workspace: msa_prompt_workspace_bytes(...); calls that can overlap need one each.
  * Errors: MSA_ERR_UNSUPPORTED for q_tokens or k_tokens above 2^28, or where the call's pairs of
- * 128 query rows and 128 keys cannot be counted in 31 bits: 2 * G * (floor(q_tokens / (2 * floor(128 / Hg))) + batch)
- * * ceil(k_tokens / 128) > 2^31 - 1 (about a million tokens of 32 heads).  MSA_ERR_CUDA also when the driver's tensor-map encoder is
+ * 128 query rows and 128 keys cannot be counted in 31 bits: G * (floor(q_tokens / (2 * floor(128 / Hg))) + batch) *
+ * (2 * ceil(k_tokens / 128) + 4) > 2^31 - 1 (about 900,000 tokens of 32 heads).  MSA_ERR_CUDA also when the driver's tensor-map encoder is
  * not available. */
 size_t msa_prompt_workspace_bytes(const msa_config_t* cfg, const msa_packed_t* packed);
 msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed, const void* q, int64_t q_stride,
