@@ -50,18 +50,21 @@ bool arrays_ok(const Range (&in)[kIn], const Range (&out)[kOut], const bool (&ow
 }
 
 struct PageLayout {
-  size_t pairs, src, dst, tokens, place, total;
+  size_t pairs, counts, need, first, src, dst, tokens, place, total;
 };
 PageLayout page_layout(int64_t pages, int64_t rows) {
   PageLayout w;
-  const size_t pairs = static_cast<size_t>(pages / 2 > rows ? pages / 2 : rows) * sizeof(int32_t);
-  const size_t row = static_cast<size_t>(rows) * sizeof(int32_t);
+  const size_t pairs = align_up(static_cast<size_t>(pages / 2 > rows ? pages / 2 : rows) * sizeof(int32_t));
+  const size_t row = align_up(static_cast<size_t>(rows + 1) * sizeof(int32_t));
   w.pairs = kErrBytes;
-  w.src = w.pairs + kWsAlign;
-  w.dst = w.src + align_up(pairs);
-  w.tokens = w.dst + align_up(pairs);
-  w.place = w.tokens + align_up(row);
-  w.total = w.place + align_up(row);
+  w.counts = w.pairs + kWsAlign;
+  w.need = w.counts + align_up(static_cast<size_t>(pages / kPageChunkPages + 1) * sizeof(int32_t));
+  w.first = w.need + row;
+  w.src = w.first + row;
+  w.dst = w.src + pairs;
+  w.tokens = w.dst + pairs;
+  w.place = w.tokens + row;
+  w.total = w.place + row;
   return w;
 }
 
@@ -79,6 +82,9 @@ msa_status_t page_args(const msa_page_pool_t* pool, int64_t rows, void* workspac
   a->num_buffers = pool->num_buffers;
   a->err = reinterpret_cast<uint32_t*>(ws);
   a->pairs = reinterpret_cast<int32_t*>(ws + w.pairs);
+  a->counts_free = reinterpret_cast<int32_t*>(ws + w.counts);
+  a->need = reinterpret_cast<int32_t*>(ws + w.need);
+  a->first = reinterpret_cast<int32_t*>(ws + w.first);
   a->src = reinterpret_cast<int32_t*>(ws + w.src);
   a->dst = reinterpret_cast<int32_t*>(ws + w.dst);
   a->tokens = reinterpret_cast<int32_t*>(ws + w.tokens);

@@ -12,9 +12,11 @@ namespace msa {
 
 // Rows whose needs a CTA sums: sequences of a call, children of a fork.
 constexpr int kPageRows = 2048;
+// Pages whose counts a CTA takes.
+constexpr int kPageChunkPages = 8192;
 
 struct PageArgs {
-  const int32_t* refs;      // [num_pages], read by the launch that copies them only (or refs_out itself)
+  const int32_t* refs;      // [num_pages] (or refs_out itself)
   int32_t* refs_out;
   int32_t num_pages;
   const int32_t* block_table;
@@ -30,8 +32,12 @@ struct PageArgs {
   int32_t rows, width;
   int32_t* page_map;          // compact
   int32_t* live_count;
-  // scratch: pages to copy, from, to, and how many tokens of each (fork); their number; fork: the
-  // child's place among them, or -1
+  // scratch.  Free pages of each chunk; extend, fork: pages that the rows before each need, and first blocks; fork,
+  // compact: pages to copy, from, to, and how many tokens of each (fork); their number; fork: the child's place
+  // among them, or -1
+  int32_t* counts_free;
+  int32_t* need;
+  int32_t* first;
   int32_t* src;
   int32_t* dst;
   int32_t* tokens;
