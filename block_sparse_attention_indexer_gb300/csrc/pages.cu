@@ -2,12 +2,14 @@
 //
 // What is free is known from the reference counts alone, and pages are handed out from the lowest free number up, so
 // a call needs the ranks of the free pages: a prefix sum over the counts.  page_count_kernel counts the free pages of
-// each chunk of 8,192 (and copies what the call leaves in other arrays, and sums what the rows of the call need, in one more
+// each chunk of 2,048 (and copies what the call leaves in other arrays, and sums what the rows of the call need, in one more
 // CTA); page_assign_kernel, a CTA for each chunk again, adds up the chunks before its own and gives every free page
-// its rank and what follows from that.  Two launches of the whole GPU: one cluster of eight CTAs that met in
-// distributed shared memory took 44 us for 890,000 pages of which 70,000 are handed out, and 7.3 against
-// 5.4 us for 8,700 pages.  Copies of pages (fork, compact) are a third launch, whose size the second one decides.
-// All of it is bound by the latency of its few rounds of loads, but for the copies, which are bound by memory.
+// its rank and what follows from that.  A pool of one chunk is one launch.  Copies of pages (fork, compact) are a launch of
+// their own, whose size the ranks decide.
+// The ranks are bound by latency, a few rounds of loads and barriers: 4.4 us in a graph for 38,000 pages of which 64
+// sequences take a few, 13 us for 890,000 of which 512 sequences take 70,000 (table and counts copied as well).  Measured
+// for these: one cluster of eight CTAs that meets in distributed shared memory 7.3 and 43 us; chunks of 8,192
+// pages 5.7 and 18 us.  Copies are bound by memory: 500 pages in 16 buffers of 64 KB a page 83 us, 6.3 TB/s.
 #include "fp8_kernels.h"
 #include "msa_device.cuh"
 #include "pages.h"
@@ -15,7 +17,7 @@
 namespace msa {
 
 constexpr int kPcThreads = 512, kPcWarps = kPcThreads / 32;
-constexpr int kPcLoads = 4;                                  // int4 loads of a lane: 16 counts
+constexpr int kPcLoads = 1;                                  // int4 loads of a lane, four counts each
 static_assert(kPageChunkPages == kPcThreads * kPcLoads * 4, "a chunk is what a CTA loads at once");
 
 enum PageOp { kExtend, kFork, kCompact };
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kPcThreads) page_assign_kernel(const PageArgs 
       const int p0 = first_page(c1);
       const unsigned b1 = free_bits(a.refs_out, P, p0, nullptr);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) n += (b1 >> i & 1u) && p0 + 128 * (i >> 2) + (i & 3) < live;
+      for (int i = 0; i < 4 * kPcLoads; ++i) n += (b1 >> i & 1u) && p0 + 128 * (i >> 2) + (i & 3) < live;
     }
     holes = cta_sum(n, warp_sum);
     if (blockIdx.x == 0 && tid == 0) {

@@ -13,7 +13,7 @@ namespace msa {
 // Rows whose needs a CTA sums: sequences of a call, children of a fork.
 constexpr int kPageRows = 2048;
 // Pages whose counts a CTA takes.
-constexpr int kPageChunkPages = 8192;
+constexpr int kPageChunkPages = 2048;
 
 struct PageArgs {
   const int32_t* refs;      // [num_pages] (or refs_out itself)
