@@ -56,7 +56,7 @@ constexpr int kPtK = 2, kPtV = 3;             // stages of 128 keys
 constexpr int kPtItems = 2;                   // units known ahead
 constexpr int kPtTile = kPtRows * kDim * 2;   // bytes of a Q tile, and of a stage
 constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
-constexpr int kPtMergeRows = 32;              // rows of a CTA of the merge
+constexpr int kPtMergeRows = 16;              // rows of a CTA of the merge
 constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
@@ -590,7 +590,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       const bool two = it.flags & kPtTwo, both = !two && it.lo + 1 < it.hi;  // (one tile: slot 1 has blocks as well)
       const int place = (it.flags >> kPtPlace) - 1;
       float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + max(place, 0)) * kPtPlaceFloats;
-      uint16_t* out = a.out + (static_cast<int64_t>(it.token0 + my_token) * H + it.g * Hg + my_head) * kDim;
       const uint32_t tO = tmem + kPtO + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       // with one tile slot 0 has the sum's factors, and all is done with it
       if (!pt_wait_warp(&sh->fin[0], n & 1) || !pt_wait_warp(&sh->o_full[0], full0 & 1)) return false;
@@ -607,7 +606,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
         tc_fence_after();
         float fa = sh->factor[s][ct]; const float fb = sh->factor[1][ct];
         const bool valid = my_token < tt && my_token + s * tt < it.tokens;
-        uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(s) * tt * H * kDim);
         if (both) {
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
@@ -976,53 +974,119 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
 
 // ---------------------------------------------------------------- units cut by range boundaries
 
-// The partial states that their CTAs left, added (fp8_merge.cuh).  blockIdx.x + 1 is a CTA that may have started inside a
-// unit: if it is the first one that did, its block here joins the unit.  blockIdx.y: the row (kSplit) or 32 rows.
+// The partial states that their CTAs left, added.  blockIdx.x + 1 is a CTA that may have started inside a unit: if it is
+// the first one that did, its block here joins the unit.  blockIdx.y: the row (kSplit, for many parts a unit:
+// fp8_merge.cuh) or 16 rows.  A thread has four dims of a row, without kSplit of two rows, whose loads of two parts
+// go out together: 40 MB of states (151 cuts) take 10 us, a row at a time they took 18.
 template <bool kSplit>
-__global__ void __launch_bounds__(kFp8MergeThreads) prompt_merge_kernel(const PromptArgs a, int ctas) {
+__global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge_kernel(const PromptArgs a, int ctas) {
   __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int c = blockIdx.x + 1, G = a.groups, Hg = a.heads_per_group, tt = kPtRows / Hg;
-  const PtCut cut = a.cuts[c];
-  if (cut.id < 0 || a.cuts[c - 1].id == cut.id) return;
+  const int c = blockIdx.x + 1, G = a.groups, Hg = a.heads_per_group, tt = kPtRows / Hg, lane = threadIdx.x & 31;
+  // every warp: the CTA before and those from c on, a lane each
+  const PtCut none{-1, 0, 0, 0, 0, 0, {0, 0}};
+  PtCut x = c - 1 + lane < ctas ? a.cuts[c - 1 + lane] : none;
+  const int id = __shfl_sync(0xffffffffu, x.id, 1), lo = __shfl_sync(0xffffffffu, x.lo, 1);
+  const int token0 = __shfl_sync(0xffffffffu, x.token0, 1), tokens = __shfl_sync(0xffffffffu, x.tokens, 1);
+  const int g = __shfl_sync(0xffffffffu, x.g, 1);
+  if (id < 0 || __shfl_sync(0xffffffffu, x.id, 0) == id) return;
   if (threadIdx.x < 32) {  // the CTAs with blocks of the unit, in order
-    int n = 0;
-    if (cut.lo > 0) {
-      if (threadIdx.x == 0) sh.list[0] = 2 * (c - 1) + 1;
-      n = 1;
+    int n = lo > 0;
+    if (lane == 0) {
+      if (lo > 0) sh.list[0] = 2 * (c - 1) + 1;
+      x = none;
     }
-    for (int c0 = c;; c0 += 32) {
-      const int k = c0 + threadIdx.x;
-      const PtCut x = k < ctas ? a.cuts[k] : PtCut{-1, 0, 0, 0, 0, 0, {0, 0}};
-      const unsigned same = __ballot_sync(0xffffffffu, x.id == cut.id);
-      const bool some = x.id == cut.id && x.lo < x.hi;
+    for (int c0 = c - 1;;) {
+      const bool some = x.id == id && x.lo < x.hi;
       const unsigned m = __ballot_sync(0xffffffffu, some);
-      if (some) sh.list[n + __popc(m & ((1u << threadIdx.x) - 1u))] = 2 * k + (x.lo == 0 ? 1 : 0);
+      if (some) sh.list[n + __popc(m & ((1u << lane) - 1u))] = 2 * (c0 + lane) + (x.lo == 0 ? 1 : 0);
       n += __popc(m);
-      if (same != 0xffffffffu) break;
+      const int last = __shfl_sync(0xffffffffu, x.id, 31);
+      if (last != id) break;
+      c0 += 32;
+      x = c0 + lane < ctas ? a.cuts[c0 + lane] : none;
     }
-    if (threadIdx.x == 0) sh.n = n;
+    if (lane == 0) sh.n = n;
   }
   __syncthreads();
-  if (sh.n < 2) return;  // one CTA's: written by it
-  // states lie by chunks of four dims: without kSplit a CTA's eight rows of a chunk are one 128-byte line
-  const int chunk = kSplit ? threadIdx.x & 31 : threadIdx.x >> 3;
-#pragma unroll 1
-  for (int i = 0; i < (kSplit ? 1 : kPtMergeRows / 8); ++i) {
-    const int pr = kSplit ? blockIdx.y : blockIdx.y * kPtMergeRows + 8 * i + (threadIdx.x & 7);
-    const int row = pr & (kPtRows - 1), token = row / Hg + (pr >= kPtRows ? tt : 0);
-    if (row / Hg >= tt || token >= cut.tokens) continue;
+  const int n = sh.n;
+  if (n < 2) return;  // one CTA's: written by it
+  const FtDiv by_hg(Hg);
+  // a row's place among the outputs' rows, -1 where it is none of the unit's
+  const int64_t hr0 = static_cast<int64_t>(token0) * G * Hg + g * Hg;
+  auto place = [&](int row) -> int {
+    const int r = row & (kPtRows - 1), token = by_hg(r), all = token + (row >= kPtRows ? tt : 0);
+    return token < tt && all < tokens ? all * G * Hg + r - token * Hg : -1;
+  };
+  auto write = [&](int at, int chunk, const float4& o, float M, float l) {
+    const float inv = l != 0.f ? rcp(l) : 0.f;
+    reinterpret_cast<uint2*>(a.out + (hr0 + at) * kDim)[chunk] =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (chunk == 0 && a.lse != nullptr) a.lse[hr0 + at] = fp8_lse(M, l);
+  };
+  if (kSplit) {
+    const int pr = blockIdx.y;
+    const int at = place(pr);
+    if (at < 0) return;
     float4 o;
     float M, l;
-    fp8_merge_row<kSplit>(a.partial, 2 * kPtRows, pr, chunk * 2 * kPtRows + pr, sh, o, M, l);
-    if (kSplit && threadIdx.x >= 32) return;
-    const int64_t hr = static_cast<int64_t>(cut.token0 + token) * G * Hg + cut.g * Hg + row % Hg;
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    reinterpret_cast<uint2*>(a.out + hr * kDim)[chunk] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (chunk == 0 && a.lse != nullptr) a.lse[hr] = fp8_lse(M, l);
+    fp8_merge_row<true>(a.partial, 2 * kPtRows, pr, lane * 2 * kPtRows + pr, sh, o, M, l);
+    if (threadIdx.x < 32) write(at, lane, o, M, l);
+    return;
   }
+  // states lie by chunks of four dims: eight rows of a chunk are one 128-byte line
+  constexpr int kRows = kPtMergeRows / 8, kParts = 2;
+  const int chunk = threadIdx.x >> 3, row0 = blockIdx.y * kPtMergeRows + (threadIdx.x & 7);
+  float M[kRows], l[kRows];
+  float4 o[kRows];
+  int at[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    at[i] = place(row0 + 8 * i);
+    M[i] = -INFINITY;
+    l[i] = 0.f;
+    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int k0 = 0; k0 < n; k0 += kParts) {
+    float ms[kRows][kParts], ls[kRows][kParts];
+    float4 os[kRows][kParts];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const float* part = a.partial + static_cast<int64_t>(sh.list[min(k0 + k, n - 1)]) * kPtPlaceFloats;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const bool in = k0 + k < n && at[i] >= 0;
+        ms[i][k] = in ? __ldcg(part + 2 * kPtRows * kDim + row0 + 8 * i) : -INFINITY;
+        ls[i][k] = in ? __ldcg(part + 2 * kPtRows * (kDim + 1) + row0 + 8 * i) : 0.f;
+        os[i][k] = in ? __ldcg(reinterpret_cast<const float4*>(part) + chunk * 2 * kPtRows + row0 + 8 * i)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float mb = M[i];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) mb = fmaxf(mb, ms[i][k]);
+      // (no key so far: the sums hold zeros, or NaN)
+      const float f = mb == -INFINITY ? 1.f : ex2(M[i] - mb);
+      l[i] *= f;
+      o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const float w = mb == -INFINITY ? 1.f : ex2(ms[i][k] - mb);
+        l[i] += w * ls[i][k];
+        o[i].x += w * os[i][k].x;
+        o[i].y += w * os[i][k].y;
+        o[i].z += w * os[i][k].z;
+        o[i].w += w * os[i][k].w;
+      }
+      M[i] = mb;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (at[i] >= 0) write(at[i], chunk, o[i], M[i], l[i]);
 }
 
 // ---------------------------------------------------------------- launch
