@@ -26,13 +26,15 @@ msa_status_t check_packed(const msa_config_t* c, const msa_packed_t* p) {
 }
 
 struct PromptLayout {
-  size_t plan, base, prefix, cuts, partial, total;
+  size_t plan, base, order, dealt, prefix, cuts, partial, total;
 };
 PromptLayout prompt_layout(const msa_config_t* c, const msa_packed_t* p) {
   PromptLayout w;
   w.plan = kErrBytes;
   w.base = w.plan + kWsAlign;
-  w.prefix = w.base + align_up((static_cast<size_t>(p->batch) + 1) * sizeof(int32_t));
+  w.order = w.base + align_up((static_cast<size_t>(p->batch) + 1) * sizeof(int32_t));
+  w.dealt = w.order + align_up(kPromptSpreadUnits * sizeof(int32_t));
+  w.prefix = w.dealt + align_up(prompt_dealt_bytes());
   w.cuts = w.prefix + align_up((prompt_max_units(p->q_tokens, p->batch, c->heads_per_group) + 1) * sizeof(int32_t));
   w.partial = w.cuts + align_up(prompt_cut_bytes());
   w.total = w.partial + align_up(prompt_partial_bytes());
@@ -103,6 +105,8 @@ msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed
   a.plan = reinterpret_cast<int32_t*>(ws + w.plan);
   a.base = reinterpret_cast<int32_t*>(ws + w.base);
   a.prefix = reinterpret_cast<int32_t*>(ws + w.prefix);
+  a.order = reinterpret_cast<int32_t*>(ws + w.order);
+  a.dealt = reinterpret_cast<int2*>(ws + w.dealt);
   a.cuts = reinterpret_cast<PtCut*>(ws + w.cuts);
   a.partial = reinterpret_cast<float*>(ws + w.partial);
   try {  // (the launch's bookkeeping allocates host memory: nothing may leave a C entry)

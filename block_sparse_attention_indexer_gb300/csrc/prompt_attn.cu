@@ -56,15 +56,20 @@ constexpr int kPtK = 2, kPtV = 3;             // stages of 128 keys
 constexpr int kPtItems = 2;                   // units known ahead
 constexpr int kPtTile = kPtRows * kDim * 2;   // bytes of a Q tile, and of a stage
 constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
-constexpr int kPtMergeRows = 16;              // rows of a CTA of the merge
+constexpr int kPtMergeRows = 64;              // rows of a CTA of the merge
 constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
 constexpr int kPtUnitCost = kPromptUnitCost;
-// Cost of a unit up to which it is not cut: of few units (no more than CTAs: nobody waits for a second one) and of many.
-// A cut costs two partial states and a merge, a cut moved to the end of its unit leaves one CTA up to half of the unit
-// more than its share.  One prompt of 512 tokens 17 us with 24, 25 with 16; one of 2K 58 us with 16, 66 with 50.
-constexpr int kPtWholeFew = 24, kPtWholeMany = 16;
+// Cost of a unit up to which it is not cut: a cut costs two partial states and a merge, a cut moved to the end of its
+// unit leaves one CTA up to half of the unit more than its share.
+constexpr int kPtWhole = 16;
+// What cutting costs a call (partial states, the merge of 150 units) in steps: without cuts a CTA may have so much more
+// than its share.  One prompt of 1K 31 us cut and 26 whole, of 2K 51 and 39, of 4K 116 and 106, of 8K 368 and 357; 32 of 2
+// to 2,000 tokens 380 and 358.  4 chunks on 16K, 120 units for 152 CTAs, are cut (their longest has twice a CTA's share).
+constexpr int kPtCutSteps = 14;
+// Units (of a KV head) up to which they are put in order for that.
+constexpr int kPtSpreadUnits = kPromptSpreadUnits;
 
 // A unit, or the part of it that this CTA has: blocks lo .. hi - 1 of 128 keys (none of a unit whose rows see no key).
 struct alignas(16) PtItem {
@@ -155,64 +160,126 @@ __device__ __forceinline__ int pt_prefix(int v, int& carry, int* warp_sum) {
 }
 
 // The plan by a whole CTA: base[b], b = 0..batch: units of the sequences before b; prefix[u], u = 0..units: cost (per
-// KV head) of the units before u.  Returns the units; 0 where the offsets are bad, and `flag` reports them.
-__device__ __noinline__ int pt_plan(const PromptArgs& a, int* base, int32_t* prefix, int* warp_sum, bool flag) {
-  const int tid = threadIdx.x, threads = blockDim.x, tt = kPtRows / a.heads_per_group;
+// KV head) of the units before u; order[r], for at most kPtSpreadUnits: the units by falling cost.  Returns the units (0
+// where the offsets are bad, and `flag` reports them), with kPtSpread where the units stay whole: dealt out by falling
+// cost, forth and back over the n CTAs (pt_dealt), none of these gets much more than its share.
+// The sort counts by classes of cost, of one cost each while the largest is below kPtClasses.  Which of a class comes
+// first is left open: whole units give the same rows wherever they run, and what is compared are the classes.
+constexpr int kPtSpread = 1 << 30;
+constexpr int kPtMaxDealt = 128;  // units of a CTA
+constexpr int kPtClasses = 2048;
+__device__ __forceinline__ int pt_dealt(int k, int c, int n) { return k & 1 ? (k + 1) * n - 1 - c : k * n + c; }
+struct PtPlanSpace {
+  int *base, *cost, *classes, *sum;  // shared: batch + 1, units, kPtClasses, 32
+  int32_t *prefix, *order;
+};
+__device__ __forceinline__ int pt_plan(const PromptArgs& a, const PtPlanSpace& s, bool flag, int n) {
+  const int tid = threadIdx.x, threads = blockDim.x, tt = kPtRows / a.heads_per_group, G = a.groups;
   bool bad = false;
   int units = 0;
   for (int b0 = 0; b0 < a.batch; b0 += threads) {
     const int b = b0 + tid;
-    int n = 0;
+    int x = 0;
     if (b < a.batch) {
       const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
       bad |= q0 < 0 || k0 < 0 || q1 < q0 || k1 < k0 || q1 > a.q_tokens || k1 > a.k_tokens;
-      n = bad ? 0 : (q1 - q0 + 2 * tt - 1) / (2 * tt);
+      x = bad ? 0 : (q1 - q0 + 2 * tt - 1) / (2 * tt);
     }
-    const int at = pt_prefix(n, units, warp_sum);
-    if (b < a.batch) base[b] = at;
+    const int at = pt_prefix(x, units, s.sum);
+    if (b < a.batch) s.base[b] = at;
   }
   if (__syncthreads_or(bad)) {  // nothing is done
     if (flag && tid == 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
     return 0;
   }
-  if (tid == 0) base[a.batch] = units;
+  if (tid == 0) s.base[a.batch] = units;
   __syncthreads();
-  int cost = 0;
+  const bool sorted = units <= kPtSpreadUnits && units * G <= (kPtMaxDealt - 1) * n;
+  int all = 0, largest = 0;
   for (int u0 = 0; u0 < units; u0 += threads) {
     const int u = u0 + tid;
-    int n = 0;
+    int x = 0;
     if (u < units) {
       int b = 0, left = a.batch;  // the last sequence with base <= u
       while (left > 1) {
         const int h = left / 2;
-        if (base[b + h] <= u) {
+        if (s.base[b + h] <= u) {
           b += h;
           left -= h;
         } else {
           left = h;
         }
       }
-      n = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], u - base[b], tt).cost();
+      x = pt_unit(a.cu_q[b + 1] - a.cu_q[b], a.cu_k[b + 1] - a.cu_k[b], u - s.base[b], tt).cost();
+      if (sorted) s.cost[u] = x;
     }
-    const int at = pt_prefix(n, cost, warp_sum);
-    if (u < units) prefix[u] = at;
+    largest = max(largest, x);
+    const int at = pt_prefix(x, all, s.sum);
+    if (u < units) s.prefix[u] = at;
   }
-  if (tid == 0) prefix[units] = cost;
-  return units;
+  if (tid == 0) s.prefix[units] = all;
+  if (!sorted || units == 0) return units;
+  largest = __reduce_max_sync(0xffffffffu, largest);
+  __syncthreads();
+  if ((tid & 31) == 0) s.sum[tid >> 5] = largest;
+  __syncthreads();
+  largest = __reduce_max_sync(0xffffffffu, (tid & 31) < threads / 32 ? s.sum[tid & 31] : 0);
+  if (largest <= kPtWhole) return units;  // nothing is cut in any case
+  static_assert(kPtClasses == 1 << 11, "");
+  const int shift = max(0, 32 - __clz(largest) - 11), top = largest >> shift;
+  for (int i = tid; i <= top; i += threads) s.classes[i] = 0;
+  __syncthreads();
+  for (int u = tid; u < units; u += threads) {
+    s.cost[u] >>= shift;
+    atomicAdd(&s.classes[top - s.cost[u]], 1);
+  }
+  __syncthreads();
+  int before = 0;
+  for (int i0 = 0; i0 <= top; i0 += threads) {
+    const int i = i0 + tid, x = i <= top ? s.classes[i] : 0, at = pt_prefix(x, before, s.sum);
+    if (i <= top) s.classes[i] = at;
+  }
+  __syncthreads();
+  for (int u = tid; u < units; u += threads) s.order[atomicAdd(&s.classes[top - s.cost[u]], 1)] = u;
+  __syncthreads();
+  int64_t most = 0;  // that a CTA gets
+  if (tid < n) {
+    const FtDiv by_g(G);
+    const int each = (units * G + n - 1) / n;
+#pragma unroll 4
+    for (int k = 0; k < each; ++k) {
+      const int at = pt_dealt(k, tid, n);
+      if (at < units * G) most += static_cast<int64_t>(s.cost[s.order[by_g(at)]] + (shift > 0)) << shift;
+    }
+  }
+  const bool much = most > static_cast<int64_t>(all) * G / n + kPtCutSteps;
+  return units | (__syncthreads_or(much) ? 0 : kPtSpread);
 }
 
-// Sequences and units up to which every CTA of the attention makes the plan for itself: one round of loads, a few of
-// sums.  More are planned by a launch before it.
+// Sequences and units up to which every CTA of the attention makes the plan for itself (8 short prompts 21.7 us with
+// a launch for the plan, 15.1 without).  More are planned by a launch before it.
 constexpr int kPtOwnBatch = kPtThreads, kPtOwnUnits = 2048;
 
+// The same in shared memory, by every CTA of the attention.
+struct PtOwnPlan {
+  int cost[kPtOwnUnits], classes[kPtClasses];
+  int32_t order[kPtOwnUnits], prefix[kPtOwnUnits + 1];
+  int base[kPtOwnBatch + 1], sum[32];
+};
+__device__ __noinline__ int pt_own_plan(const PromptArgs& a, PtOwnPlan& s) {
+  return pt_plan(a, PtPlanSpace{s.base, s.cost, s.classes, s.sum, s.prefix, s.order}, blockIdx.x == 0, gridDim.x);
+}
+
 constexpr int kPtPlanThreads = 1024;
-__global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const PromptArgs a) {
-  __shared__ int s_base[2048 + 1], s_sum[32];
+__global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const PromptArgs a, int ctas) {
+  __shared__ int s_base[2048 + 1], s_sum[32], s_cost[kPtSpreadUnits], s_classes[kPtClasses];
+  __shared__ int32_t s_order[kPtSpreadUnits];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int units = pt_plan(a, s_base, a.prefix, s_sum, true);
+  const int units = pt_plan(a, PtPlanSpace{s_base, s_cost, s_classes, s_sum, a.prefix, s_order}, true, ctas);
   if (threadIdx.x == 0) a.plan[0] = units;
   for (int b = threadIdx.x; units > 0 && b <= a.batch; b += kPtPlanThreads) a.base[b] = s_base[b];
+  for (int u = threadIdx.x; (units & kPtSpread) && u < (units & (kPtSpread - 1)); u += kPtPlanThreads) a.order[u] = s_order[u];
 }
 
 // The unit inside which a CTA's range starts (id -1: it starts with one), for the merge.
@@ -323,7 +390,8 @@ __device__ __noinline__ void pt_put_back(const PromptArgs& a, int flags, int lo,
 
 // ---------------------------------------------------------------- the kernel
 
-__global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps, int own_plan) {
+__global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptArgs a,
+                                                                    const __grid_constant__ PromptMaps maps, int own_plan) {
   extern __shared__ __align__(1024) uint8_t q_tile[];
   uint8_t* k_ring = q_tile + 2 * kPtTile;
   uint8_t* v_ring = k_ring + kPtK * kPtTile;
@@ -380,13 +448,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
   grid_dependency_wait();
   grid_dependents_launch();
   // the plan, in what will be the stages of K
-  int* base = a.base;
-  int32_t* prefix = a.prefix;
+  PtOwnPlan& own = *reinterpret_cast<PtOwnPlan*>(k_ring);
   int units = 0;
   if (own_plan) {
-    base = reinterpret_cast<int*>(k_ring);
-    prefix = base + kPtOwnBatch + 1;
-    units = pt_plan(a, base, prefix, prefix + kPtOwnUnits + 1, blockIdx.x == 0);
+    units = pt_own_plan(a, own);
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -736,18 +801,42 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
    if (warp == 12) {
     // ---- producer: units and the copies of Q and K
     if (!own_plan) units = a.plan[0];
-    int x0 = 0, x1 = 0, u = 0, b = 0;
-    int64_t E = 0, first = 0;  // all cost, cost before unit u
-    if (units > 0) {
+    const int* base = own_plan ? own.base : a.base;
+    const int32_t *prefix = own_plan ? own.prefix : a.prefix, *order = own_plan ? own.order : a.order;
+    const bool spread = units & kPtSpread;
+    units &= kPtSpread - 1;
+    int x0 = 0, x1 = 0, u = 0, b = 0, i = 0, dealt = 0;  // dealt: units of this CTA where they stay whole
+    int64_t E = 0, first = 0;                            // all cost, cost before unit u
+    int2* mine = a.dealt + blockIdx.x * kPtMaxDealt;
+    if (spread) {  // (looked up before the copies of K go over the plan)
+      const FtDiv by_g(G);
+      const int all = units * G, whole = all / gridDim.x;
+      dealt = whole + (pt_dealt(whole, blockIdx.x, gridDim.x) < all ? 1 : 0);
+      for (int k = lane; k < dealt; k += 32) {
+        const int at = pt_dealt(k, blockIdx.x, gridDim.x), unit = order[by_g(at)];
+        int s = 0, left = a.batch;  // the last sequence with base <= unit
+        while (left > 1) {
+          const int h = left / 2;
+          if (base[s + h] <= unit) {
+            s += h;
+            left -= h;
+          } else {
+            left = h;
+          }
+        }
+        mine[k] = make_int2(s | (at - by_g(at) * G) << 16, unit - base[s]);
+      }
+      __syncwarp();
+    } else if (units > 0) {
       E = static_cast<int64_t>(prefix[units]) * G;
-      const int whole = static_cast<int64_t>(units) * G > gridDim.x ? kPtWholeMany : kPtWholeFew;
 #pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < 2; ++k) {
         x0 = x1;
-        x1 = ft_cut(prefix, units, G, E, blockIdx.x + i, gridDim.x, whole);
+        x1 = ft_cut(prefix, units, G, E, blockIdx.x + k, gridDim.x, kPtWhole);
       }
       u = ft_find(prefix, units, G, static_cast<int>(min(static_cast<int64_t>(x0), E - 1)));
       b = ft_find(base, a.batch, 1, u);
+      i = u - base[b];
       first = static_cast<int64_t>(prefix[u]) * G;
     }
     const uint64_t keep = l2_evict_normal_policy(), once = l2_evict_first_policy();
@@ -763,18 +852,29 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
       return true;
     };
     PtCut cut{-1, 0, 0, 0, 0, 0, {0, 0}};
-    for (int i = units > 0 ? u - base[b] : 0; units > 0 && first <= x1 && !failed;) {  // unit i of sequence b
+    for (int k = 0; !failed && (spread ? k < dealt : units > 0 && first <= x1); ++k) {  // unit i of sequence b
+      int g = 0, g_end = G;
+      if (spread) {
+        const int2 x = __ldcg(mine + k);
+        b = x.x & 0xFFFF;
+        g = x.x >> 16;
+        g_end = g + 1;
+        i = x.y;
+      }
       const int q0 = a.cu_q[b], key0 = a.cu_k[b], Lq = a.cu_q[b + 1] - q0;
       const PtUnit t = pt_unit(Lq, a.cu_k[b + 1] - key0, i, tt);
       const int pages = max(t.pages, 1), cost = t.cost(), token0 = q0 + i * 2 * tt;
 #pragma unroll 1
-      for (int g = 0; g < G && !failed; ++g) {
-        const int64_t u0 = first + static_cast<int64_t>(g) * cost;
-        if (u0 + cost <= x0) continue;
-        const int lo = t.block_at(x0 - u0), hi = t.block_at(x1 - u0);
-        if (u0 < x0 && x0 < E) cut = PtCut{u * G + g, lo, hi, token0, t.tokens, g, {0, 0}};
-        if (u0 >= x1) break;
-        if (lo >= hi) continue;
+      for (; g < g_end && !failed; ++g) {
+        int lo = 0, hi = pages;
+        if (!spread) {
+          const int64_t u0 = first + static_cast<int64_t>(g) * cost;
+          if (u0 + cost <= x0) continue;
+          lo = t.block_at(x0 - u0), hi = t.block_at(x1 - u0);
+          if (u0 < x0 && x0 < E) cut = PtCut{u * G + g, lo, hi, token0, t.tokens, g, {0, 0}};
+          if (u0 >= x1) break;
+          if (lo >= hi) continue;
+        }
         const int place = lo == 0 && hi == pages ? -1 : lo == 0 ? 1 : 0;
         if (!record(PtItem{(t.width == 2 ? kPtTwo : 0) | (place + 1) << kPtPlace, lo, t.pages > 0 ? hi : lo, token0, t.tokens,
                            t.pos0, key0, g})) {
@@ -811,6 +911,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
           ++blocks;
         }
       }
+      if (spread) continue;
       // the next unit: of this sequence, or the first one of the next sequence that has any
       first += static_cast<int64_t>(cost) * G;
       if (++u >= units) break;
@@ -976,7 +1077,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const Prompt
 
 // The partial states that their CTAs left, added.  blockIdx.x + 1 is a CTA that may have started inside a unit: if it is
 // the first one that did, its block here joins the unit.  blockIdx.y: the row (kSplit, for many parts a unit:
-// fp8_merge.cuh) or 16 rows.  A thread has four dims of a row, without kSplit of two rows, whose loads of two parts
+// fp8_merge.cuh) or 64 rows, 16 at a time.  A thread has four dims of a row, without kSplit of two rows, whose loads of two parts
 // go out together: 40 MB of states (151 cuts) take 10 us, a row at a time they took 18.
 template <bool kSplit>
 __global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge_kernel(const PromptArgs a, int ctas) {
@@ -1036,8 +1137,11 @@ __global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge
     return;
   }
   // states lie by chunks of four dims: eight rows of a chunk are one 128-byte line
-  constexpr int kRows = kPtMergeRows / 8, kParts = 2;
-  const int chunk = threadIdx.x >> 3, row0 = blockIdx.y * kPtMergeRows + (threadIdx.x & 7);
+  constexpr int kRows = 2, kParts = 2;
+  const int chunk = threadIdx.x >> 3;
+#pragma unroll 1
+  for (int r = 0; r < kPtMergeRows; r += 8 * kRows) {
+  const int row0 = blockIdx.y * kPtMergeRows + r + (threadIdx.x & 7);
   float M[kRows], l[kRows];
   float4 o[kRows];
   int at[kRows];
@@ -1087,10 +1191,12 @@ __global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge
 #pragma unroll
   for (int i = 0; i < kRows; ++i)
     if (at[i] >= 0) write(at[i], chunk, o[i], M[i], l[i]);
+  }
 }
 
 // ---------------------------------------------------------------- launch
 
+size_t prompt_dealt_bytes() { return kFp8MaxCtas * kPtMaxDealt * sizeof(int2); }
 size_t prompt_cut_bytes() { return kFp8MaxCtas * sizeof(PtCut); }
 size_t prompt_partial_bytes() { return static_cast<size_t>(2) * kFp8MaxCtas * kPtPlaceFloats * sizeof(float); }
 
@@ -1136,10 +1242,10 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s)
   if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(prompt_attn_kernel), kPtSmem)) != cudaSuccess) return e;
   const int64_t most = prompt_max_units(a.q_tokens, a.batch, a.heads_per_group), units = most * a.groups;
   const int own_plan = a.batch <= kPtOwnBatch && most <= kPtOwnUnits ? 1 : 0;
-  if (!own_plan && (e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a)) != cudaSuccess) return e;
+  if (!own_plan && (e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a, ctas)) != cudaSuccess) return e;
   if ((e = launch_dependent(prompt_attn_kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps, own_plan)) != cudaSuccess) return e;
-  // (no unit is longer than what pt_whole leaves whole)
-  if (ctas == 1 || 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost <= kPtWholeMany) return cudaSuccess;
+  // (no unit can be long enough to be cut)
+  if (ctas == 1 || 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost <= kPtWhole) return cudaSuccess;
   return ctas / units >= kFp8MergeSplitParts
              ? launch_dependent(prompt_merge_kernel<true>, dim3(ctas - 1, 2 * kPtRows), kFp8MergeThreads, 0, s, a, ctas)
              : launch_dependent(prompt_merge_kernel<false>, dim3(ctas - 1, 2 * kPtRows / kPtMergeRows), kFp8MergeThreads, 0, s, a, ctas);

@@ -190,3 +190,84 @@ def test_single_token_agrees_with_the_prompt():
     assert err == 0
     close("out", o1[0], out[-1], np.abs(out[-1]) * 2.0 ** -7 + 2.0 ** -8)
     close("lse", l1[0], lse[-1], np.full(l1[0].shape, 1e-4))
+
+
+# How the work is split: units that stay whole and are dealt out by cost, cut units, plans made by the attention's blocks
+# themselves (up to 512 sequences) or by a launch before them, more units than are put in order.
+@pytest.mark.parametrize("lens_q,lens_k,G,Hg", [
+    ([1100], None, 2, 8),                                        # whole: a unit for nearly every block of the grid
+    ([2100, 3, 700], None, 2, 8),                                # whole, two a block
+    ([40], [5000], 2, 8),                                        # cut, few units
+    ([1], [6000], 1, 8),                                         # one row tile cut into nearly as many parts as pages
+    ([1, 1, 1], [3000, 20, 2000], 1, 1),
+    ([20] * 599 + [900], None, 1, 2),                            # planned by a launch: one much longer than the rest
+    ([300] * 8 + [9] * 592, None, 1, 4),                         # planned by a launch, whole
+    ([70] + [1] * 519, [4000] + [2] * 519, 1, 4),                # planned by a launch, cut
+    ([33] * 1029 + [300], None, 1, 8),                           # more units than are put in order
+])
+def test_split_of_the_work(lens_q, lens_k, G, Hg):
+    p = Prompts(len(lens_q) + sum(lens_q), lens_q, lens_k, G=G, Hg=Hg, before=2, behind=3)
+    first = run(p)
+    p.check(first)
+    p.out.fill_(7.0)
+    p.lse.fill_(7.0)
+    p.call()
+    again = p.results()
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([40, 3], [5000, 700]), ([1], [4000]), ([130, 1], [2000, 3000])])
+def test_values_of_later_keys_in_cut_units(lens_q, lens_k):
+    p = Prompts(93, lens_q, lens_k, G=1, Hg=8)
+    for b in range(p.B):
+        end = int(p.cu_k[b + 1])
+        for back, dim, what in ((1, 5, np.nan), (2, 127, np.inf), (17, 64, -np.inf), (33, 64, np.inf), (39, 0, np.inf),
+                                (129, 9, np.nan), (600, 11, np.inf)):
+            p.v[end - back, 0, dim] = what
+    ref = p.oracle()
+    got = run(p)
+    special = ~np.isfinite(ref["out"])
+    assert special.any()
+    ref["spread"] = np.where(special, 0.0, ref["spread"])
+    p.check(got, ref)
+
+
+def test_two_calls_at_once():
+    import torch
+    a, b = Prompts(94, [900, 50], G=2, Hg=4).upload(), Prompts(95, [30, 5], [4000, 3000], G=2, Hg=4).upload()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, s in zip((a, b), streams):
+            p.call(stream=s)
+    for p in (a, b):
+        p.check(p.results())
+
+
+def test_tokens_far_apart():
+    """Rows 2^27 elements apart: the last ones lie beyond 2^31 elements and 2^32 bytes."""
+    import torch
+    p = Prompts(96, [18], G=2, Hg=4)
+    ref = p.oracle()
+    p.upload()
+    wide = torch.empty(17 * 2 ** 27 + 4096, dtype=torch.bfloat16, device="cuda")
+    far = []
+    for i, x in enumerate(p.d):
+        v = wide[1024 * i:].as_strided((18,) + tuple(x.shape[1:]), (2 ** 27, 128, 1))
+        v.copy_(x)
+        far.append(v)
+    p.d = far
+    p.call()
+    p.check(p.results(), ref)
+
+
+def test_scores_that_are_all_minus_infinity():
+    # such a row is one without keys
+    p = Prompts(97, [40], G=1, Hg=2)
+    p.q[:, :, :] = 0.0
+    p.q[:, 0, 0], p.k[:, 0, 0] = 1.0, -np.inf
+    p.q[:, 1, 1] = 1.0
+    p.k[:, 0, 1:] = 0.0
+    p.q[:, 1, 0] = 1.0
+    got = run(p)
+    assert (got[0] == 0).all() and (got[1] == -np.inf).all() and got[2] == 0
