@@ -163,15 +163,14 @@ __device__ __forceinline__ int pt_prefix(int v, int& carry, int* warp_sum) {
 // KV head) of the units before u; order[r], for at most kPtSpreadUnits: the units by falling cost.  Returns the units (0
 // where the offsets are bad, and `flag` reports them), with kPtSpread where the units stay whole: dealt out by falling
 // cost, forth and back over the n CTAs (pt_dealt), none of these gets much more than its share.
-// The sort counts by classes of cost, of one cost each while the largest is below kPtClasses.  Which of a class comes
-// first is left open: whole units give the same rows wherever they run, and what is compared are the classes.
+// The sort goes through the cost's bits from the lowest on and keeps the order of what is equal: where every CTA makes
+// the plan for itself, all of them have to find the same one.
 constexpr int kPtSpread = 1 << 30;
 constexpr int kPtMaxDealt = 128;  // units of a CTA
-constexpr int kPtClasses = 2048;
 __device__ __forceinline__ int pt_dealt(int k, int c, int n) { return k & 1 ? (k + 1) * n - 1 - c : k * n + c; }
 struct PtPlanSpace {
-  int *base, *cost, *classes, *sum;  // shared: batch + 1, units, kPtClasses, 32
-  int32_t *prefix, *order;
+  int *base, *cost, *sum, *zeros;   // shared: batch + 1, units, 32, 64
+  int32_t *prefix, *order, *other;  // order and other (both shared): units
 };
 __device__ __forceinline__ int pt_plan(const PromptArgs& a, const PtPlanSpace& s, bool flag, int n) {
   const int tid = threadIdx.x, threads = blockDim.x, tt = kPtRows / a.heads_per_group, G = a.groups;
@@ -225,23 +224,31 @@ __device__ __forceinline__ int pt_plan(const PromptArgs& a, const PtPlanSpace& s
   __syncthreads();
   largest = __reduce_max_sync(0xffffffffu, (tid & 31) < threads / 32 ? s.sum[tid & 31] : 0);
   if (largest <= kPtWhole) return units;  // nothing is cut in any case
-  static_assert(kPtClasses == 1 << 11, "");
-  const int shift = max(0, 32 - __clz(largest) - 11), top = largest >> shift;
-  for (int i = tid; i <= top; i += threads) s.classes[i] = 0;
-  __syncthreads();
-  for (int u = tid; u < units; u += threads) {
-    s.cost[u] >>= shift;
-    atomicAdd(&s.classes[top - s.cost[u]], 1);
+  const int warp = tid >> 5, lane = tid & 31, warps = threads / 32, groups = (units + 31) / 32, bits = 32 - __clz(largest);
+  int32_t *from = nullptr, *to = bits & 1 ? s.order : s.other;  // (the last pass goes to s.order)
+  auto unit_at = [&](int bit, int i) { return bit == 0 ? i : from[i]; };
+  static_assert(kPtSpreadUnits / 32 <= 64, "two counts a lane");
+  for (int bit = 0; bit < bits; ++bit) {
+    // units without the bit in largest - cost come first: how many each 32 places have
+    for (int w = warp; w < groups; w += warps) {
+      const int i = 32 * w + lane;
+      const uint32_t zeros = __ballot_sync(0xffffffffu, i < units && !((largest - s.cost[unit_at(bit, i)]) >> bit & 1));
+      if (lane == 0) s.zeros[w] = __popc(zeros);
+    }
+    __syncthreads();
+    const int low = lane < groups ? s.zeros[lane] : 0, high = lane + 32 < groups ? s.zeros[lane + 32] : 0;
+    const int all_zeros = __reduce_add_sync(0xffffffffu, low + high);
+    for (int w = warp; w < groups; w += warps) {
+      const int i = 32 * w + lane, u = i < units ? unit_at(bit, i) : 0;
+      const bool zero = i < units && !((largest - s.cost[u]) >> bit & 1);
+      const int before = __reduce_add_sync(0xffffffffu, (lane < w ? low : 0) + (lane + 32 < w ? high : 0)) +
+                         __popc(__ballot_sync(0xffffffffu, zero) & ((1u << lane) - 1));
+      if (i < units) to[zero ? before : all_zeros + i - before] = u;
+    }
+    __syncthreads();
+    from = to;
+    to = to == s.order ? s.other : s.order;
   }
-  __syncthreads();
-  int before = 0;
-  for (int i0 = 0; i0 <= top; i0 += threads) {
-    const int i = i0 + tid, x = i <= top ? s.classes[i] : 0, at = pt_prefix(x, before, s.sum);
-    if (i <= top) s.classes[i] = at;
-  }
-  __syncthreads();
-  for (int u = tid; u < units; u += threads) s.order[atomicAdd(&s.classes[top - s.cost[u]], 1)] = u;
-  __syncthreads();
   int64_t most = 0;  // that a CTA gets
   if (tid < n) {
     const FtDiv by_g(G);
@@ -249,7 +256,7 @@ __device__ __forceinline__ int pt_plan(const PromptArgs& a, const PtPlanSpace& s
 #pragma unroll 4
     for (int k = 0; k < each; ++k) {
       const int at = pt_dealt(k, tid, n);
-      if (at < units * G) most += static_cast<int64_t>(s.cost[s.order[by_g(at)]] + (shift > 0)) << shift;
+      if (at < units * G) most += s.cost[s.order[by_g(at)]];
     }
   }
   const bool much = most > static_cast<int64_t>(all) * G / n + kPtCutSteps;
@@ -262,21 +269,20 @@ constexpr int kPtOwnBatch = kPtThreads, kPtOwnUnits = 2048;
 
 // The same in shared memory, by every CTA of the attention.
 struct PtOwnPlan {
-  int cost[kPtOwnUnits], classes[kPtClasses];
-  int32_t order[kPtOwnUnits], prefix[kPtOwnUnits + 1];
-  int base[kPtOwnBatch + 1], sum[32];
+  int cost[kPtOwnUnits], base[kPtOwnBatch + 1], sum[32], zeros[64];
+  int32_t prefix[kPtOwnUnits + 1], order[kPtOwnUnits], other[kPtOwnUnits];
 };
 __device__ __noinline__ int pt_own_plan(const PromptArgs& a, PtOwnPlan& s) {
-  return pt_plan(a, PtPlanSpace{s.base, s.cost, s.classes, s.sum, s.prefix, s.order}, blockIdx.x == 0, gridDim.x);
+  return pt_plan(a, PtPlanSpace{s.base, s.cost, s.sum, s.zeros, s.prefix, s.order, s.other}, blockIdx.x == 0, gridDim.x);
 }
 
 constexpr int kPtPlanThreads = 1024;
 __global__ void __launch_bounds__(kPtPlanThreads) prompt_plan_kernel(const PromptArgs a, int ctas) {
-  __shared__ int s_base[2048 + 1], s_sum[32], s_cost[kPtSpreadUnits], s_classes[kPtClasses];
-  __shared__ int32_t s_order[kPtSpreadUnits];
+  __shared__ int s_base[2048 + 1], s_sum[32], s_zeros[64], s_cost[kPtSpreadUnits];
+  __shared__ int32_t s_order[kPtSpreadUnits], s_other[kPtSpreadUnits];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int units = pt_plan(a, PtPlanSpace{s_base, s_cost, s_classes, s_sum, a.prefix, s_order}, true, ctas);
+  const int units = pt_plan(a, PtPlanSpace{s_base, s_cost, s_sum, s_zeros, a.prefix, s_order, s_other}, true, ctas);
   if (threadIdx.x == 0) a.plan[0] = units;
   for (int b = threadIdx.x; units > 0 && b <= a.batch; b += kPtPlanThreads) a.base[b] = s_base[b];
   for (int u = threadIdx.x; (units & kPtSpread) && u < (units & (kPtSpread - 1)); u += kPtPlanThreads) a.order[u] = s_order[u];

@@ -197,6 +197,7 @@ def test_single_token_agrees_with_the_prompt():
 @pytest.mark.parametrize("lens_q,lens_k,G,Hg", [
     ([1100], None, 2, 8),                                        # whole: a unit for nearly every block of the grid
     ([2100, 3, 700], None, 2, 8),                                # whole, two a block
+    ([1000] + [37 * i % 500 for i in range(1, 32)], None, 2, 8),  # whole, many units of the same cost
     ([40], [5000], 2, 8),                                        # cut, few units
     ([1], [6000], 1, 8),                                         # one row tile cut into nearly as many parts as pages
     ([1, 1, 1], [3000, 20, 2000], 1, 1),
