@@ -414,14 +414,14 @@ msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int
  * h / Hg with logits z_j = (q . k_j) * softmax_scale:
  *   out  = sum_j e^{z_j - lse} v_j   bfloat16 [q_tokens][G*Hg][D]
  *   lse  = ln sum_j e^{z_j}          float [q_tokens][G*Hg], may be NULL
- * A row with no key (Lk < Lq: the first Lq - Lk tokens) gives out 0 and lse -inf.  Rows of
- * tokens that belong to no sequence are left as they are.
+ * A row with no key (Lk < Lq: the first Lq - Lk tokens), or whose logits are all -inf, gives out 0
+ * and lse -inf.  Rows of tokens that belong to no sequence are left as they are.
  *   q        bfloat16 [q_tokens][G*Hg][D], k, v bfloat16 [k_tokens][G][D]: the heads of a token are
  *            contiguous, tokens are q_stride (k_stride, v_stride) elements apart, so that slices of
  *            one fused projection's rows need no copy.  Pointers and strides in bytes are multiples
  *            of 16, strides at least a token's elements.  out may not overlap an input.
  * Keys that a row does not see (later ones, other sequences') do not touch it, whatever they
- * hold.  A NaN or an infinity in q or k makes the rows whose logits it reaches what float
+ * hold.  Other NaN and infinities in q or k make the rows whose logits they reach what float
  * arithmetic makes of them; one in v the results of the rows that see it, in its dim.
  * cu_q and cu_k must not decrease, start below 0 or end past q_tokens and k_tokens: otherwise
  * MSA_DEVERR_BAD_SEQLEN is set and nothing is written.

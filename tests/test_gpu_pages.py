@@ -336,3 +336,83 @@ def test_captured_life_of_a_pool():
         assert np.array_equal(host(p.d_lens), lens) and host(live)[0] == n and np.array_equal(host(d_map), page_map)
         p.same_buffers()
     assert p.err() == 0
+
+
+def test_calls_with_nothing_in_them():
+    """No sequences, no children, lists without columns: counts and maps are still what they should be."""
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+    p = Pool(81, [], 9, 4, caches=[("fp8", 1)])
+    refs = np.array([0, 2, 0, 0, 1, 1, 0, 0, 3], np.int32)
+    p.d_refs.copy_(dev(refs))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = torch.full((9,), 77, **i32)
+    msa.msa_extend_pages(p.pool, p.batch, p.ws, new_tokens=torch.empty(0, **i32), refs_out=out)
+    assert np.array_equal(host(out), refs)
+    q = Pool(82, [300, 5], 9, 4, caches=[("fp8", 1)])
+    out.fill_(77)
+    msa.msa_fork_pages(q.pool, q.batch, torch.empty(0, **i32), torch.empty(0, 4, **i32), torch.empty(0, **i32), q.ws, refs_out=out)
+    assert np.array_equal(host(out), q.refs)
+    out.fill_(77)
+    msa.msa_free_pages(p.pool, torch.empty(3, 0, **i32), p.ws, refs_out=out)
+    assert np.array_equal(host(out), refs)
+    want = OP.compact(refs, p.table, p.lens, p.buffers)
+    d_map, live = torch.empty(9, **i32), torch.empty(1, **i32)
+    msa.msa_compact_pages(p.pool, p.batch, d_map, live, p.ws)
+    assert np.array_equal(host(p.d_refs), want[0]) and np.array_equal(host(d_map), want[2]) and host(live)[0] == want[3] == 4
+    p.same_buffers()
+    assert p.err() == q.err() == 0
+
+
+@pytest.mark.parametrize("P", [1, 2, 2047, 2048, 2049, 4096])
+@pytest.mark.parametrize("used", ["none", "all", "last"])
+def test_compact_pools_at_the_ends(P, used):
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+    p = Pool(83, [128, 0], P, 2)
+    refs = np.full(P, 2 if used == "all" else 0, np.int32)
+    refs[-1] = 0 if used == "none" else 5
+    p.table[0, 0] = P - 1
+    if used == "none":
+        p.lens[0] = 0
+    p.d_refs.copy_(dev(refs))
+    p.d_table.copy_(dev(p.table))
+    p.d_lens.copy_(dev(p.lens))
+    want = OP.compact(refs, p.table, p.lens)
+    d_map, live = torch.empty(P, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    msa.msa_compact_pages(p.pool, p.batch, d_map, live, p.ws)
+    for got, x in zip((p.d_refs, p.d_table, d_map), want):
+        assert np.array_equal(host(got), x)
+    assert host(live)[0] == want[3] and p.err() == want[4] == 0
+
+
+def test_two_pools_at_once_on_their_own_streams():
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+    pools = [Pool(84 + i, [700, 90, 1000, 3], n, 32, shared=0.2, caches=[("fp8", 2)]) for i, n in enumerate((60, 4100))]
+    streams = [torch.cuda.Stream() for _ in pools]
+    new, parents = np.array([300, 300, 1, 500], np.int32), np.array([2, 1, 1, 0, 3], np.int32)
+    space = [dict(to=torch.empty(5, 32, dtype=torch.int32, device="cuda"), lens=torch.empty(5, dtype=torch.int32, device="cuda"),
+                  map=torch.empty(len(p.refs), dtype=torch.int32, device="cuda"), live=torch.empty(1, dtype=torch.int32, device="cuda"),
+                  new=dev(new), parents=dev(parents)) for p in pools]
+    torch.cuda.synchronize()
+    for step in range(4):
+        for p, x, s in zip(pools, space, streams):
+            if step == 0:
+                msa.msa_extend_pages(p.pool, p.batch, p.ws, new_tokens=x["new"], stream=s)
+            elif step == 1:
+                msa.msa_fork_pages(p.pool, p.batch, x["parents"], x["to"], x["lens"], p.ws, stream=s)
+            elif step == 2:
+                msa.msa_free_pages(p.pool, p.d_table, p.ws, stream=s)
+            else:
+                msa.msa_compact_pages(p.pool, msa.Batch(x["to"], x["lens"]), x["map"], x["live"], p.ws, stream=s)
+    torch.cuda.synchronize()
+    for p, x in zip(pools, space):
+        refs, table, lens, e = OP.extend(p.refs, p.table, p.lens, new)
+        refs, kids, kid_lens, f = OP.fork(refs, table, lens, parents, p.buffers)
+        refs, g = OP.free(refs, table)
+        refs, kids, page_map, n, h = OP.compact(refs, kids, kid_lens, p.buffers)
+        assert e == f == g == h == p.err() == 0
+        assert np.array_equal(host(p.d_refs), refs) and np.array_equal(host(x["to"]), kids)
+        assert np.array_equal(host(x["lens"]), kid_lens) and np.array_equal(host(x["map"]), page_map) and host(x["live"])[0] == n
+        p.same_buffers()
