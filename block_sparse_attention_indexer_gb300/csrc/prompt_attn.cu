@@ -10,10 +10,11 @@
 // Work.  A row is a (token, head) of a KV head; a tile is 128 rows, floor(128 / Hg) tokens with their Hg heads, a
 // unit two tiles (or one, of a sequence's last tokens) of a sequence and a KV head, so that keys loaded once meet
 // 256 rows and the causal border costs half a block of 128 keys for each tile, whatever Hg is.  A unit's cost is
-// counted in (tile, 128 keys) steps and kPtUnitCost for its start; all units are one flat list that a persistent grid,
-// one CTA an SM, cuts into equal ranges (tile_split.cuh).  Units that are cut leave partial states, which a second
-// kernel adds.  Two accumulator slots work in turn: with two tiles each block of keys is used by slot 0 and
-// slot 1, with one tile the blocks alternate between the slots.
+// counted in (tile, 128 keys) steps and kPtUnitCost for its start.  A persistent grid, one CTA an SM, gets the units whole,
+// dealt out by falling cost, where that balances (kPtCutSteps); else all units are one flat list that is cut into equal
+// ranges (tile_split.cuh), and units that are cut leave partial states, which a second kernel adds.  Two accumulator
+// slots work in turn: with two tiles each block of keys is used by slot 0 and slot 1, with one tile the blocks
+// alternate between the slots.
 //   * S = Q K^T: Q and K by tensor copies in 128-byte swizzle (a Q tile is one box of Hg heads by tokens).
 //   * O += P V: P in tensor memory over S (the A operand), V as it lies, as the MN-major B operand.
 // TMEM: S of the two slots, then O of the two slots: 4 x 128 columns, all of it.
@@ -35,7 +36,8 @@
 // Stages of K and V and register shares: 1 to 3 %.  Code that a unit runs once costs its instruction fetches (the
 // epilogue, unrolled masks: 1 us and more each), so it is short loops, and the softmax's loop has nothing
 // rare inside it; function calls in that branch cost it registers (1.40 -> 1.48 ms).
-// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units) 2 us of a unit's 13 are not its steps.
+// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units, 358 us) 2 us of a unit's 12 are not its
+// steps, and tensor instructions run 58 % of the time (70 % for one prompt of 8K tokens, 357 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -56,7 +58,6 @@ constexpr int kPtK = 2, kPtV = 3;             // stages of 128 keys
 constexpr int kPtItems = 2;                   // units known ahead
 constexpr int kPtTile = kPtRows * kDim * 2;   // bytes of a Q tile, and of a stage
 constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
-constexpr int kPtMergeRows = 64;              // rows of a CTA of the merge
 constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
@@ -1081,16 +1082,37 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
 
 // ---------------------------------------------------------------- units cut by range boundaries
 
-// The partial states that their CTAs left, added.  blockIdx.x + 1 is a CTA that may have started inside a unit: if it is
-// the first one that did, its block here joins the unit.  blockIdx.y: the row (kSplit, for many parts a unit:
-// fp8_merge.cuh) or 64 rows, 16 at a time.  A thread has four dims of a row, without kSplit of two rows, whose loads of two parts
-// go out together: 40 MB of states (151 cuts) take 10 us, a row at a time they took 18.
+// The partial states that their CTAs left, added.  blockIdx.x: the unit, by its place among those that are cut or, where as
+// many units can be cut as there are CTAs, by the first CTA that starts inside it (the others' blocks find nothing to do).
+// blockIdx.y: the row (kSplit, for many parts a unit: fp8_merge.cuh) or every gridDim.y-th group of 16 of the unit's
+// `rows`.  A thread has four dims of a row, without kSplit of two rows, whose loads of two parts go out together (40 MB of
+// states, 151 cuts, take 10 us; a row at a time they took 18).
 template <bool kSplit>
-__global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge_kernel(const PromptArgs a, int ctas) {
+__global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge_kernel(const PromptArgs a, int ctas, int rows) {
   __shared__ Fp8MergeShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int c = blockIdx.x + 1, G = a.groups, Hg = a.heads_per_group, tt = kPtRows / Hg, lane = threadIdx.x & 31;
+  const int G = a.groups, Hg = a.heads_per_group, tt = kPtRows / Hg, lane = threadIdx.x & 31;
+  int c = blockIdx.x + 1;
+  if (static_cast<int>(gridDim.x) < ctas - 1) {  // (every warp)
+    int ids[kFp8MaxCtas / 32];
+#pragma unroll
+    for (int i = 0; i < kFp8MaxCtas / 32; ++i) ids[i] = 32 * i + lane < ctas ? a.cuts[32 * i + lane].id : -1;
+    int before = 0, last = -1;
+    c = -1;
+#pragma unroll
+    for (int i = 0; i < kFp8MaxCtas / 32; ++i) {
+      const int up = __shfl_up_sync(0xffffffffu, ids[i], 1);
+      const bool starts = ids[i] >= 0 && ids[i] != (lane == 0 ? last : up);
+      const unsigned m = __ballot_sync(0xffffffffu, starts);
+      const bool it = starts && before + __popc(m & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.x);
+      const unsigned mine = __ballot_sync(0xffffffffu, it);
+      if (mine != 0) c = 32 * i + __ffs(mine) - 1;
+      before += __popc(m);
+      last = __shfl_sync(0xffffffffu, ids[i], 31);
+    }
+    if (c < 0) return;
+  }
   // every warp: the CTA before and those from c on, a lane each
   const PtCut none{-1, 0, 0, 0, 0, 0, {0, 0}};
   PtCut x = c - 1 + lane < ctas ? a.cuts[c - 1 + lane] : none;
@@ -1146,8 +1168,8 @@ __global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge
   constexpr int kRows = 2, kParts = 2;
   const int chunk = threadIdx.x >> 3;
 #pragma unroll 1
-  for (int r = 0; r < kPtMergeRows; r += 8 * kRows) {
-  const int row0 = blockIdx.y * kPtMergeRows + r + (threadIdx.x & 7);
+  for (int r = 8 * kRows * blockIdx.y; r < rows; r += 8 * kRows * gridDim.y) {
+  const int row0 = r + (threadIdx.x & 7);
   float M[kRows], l[kRows];
   float4 o[kRows];
   int at[kRows];
@@ -1252,9 +1274,15 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s)
   if ((e = launch_dependent(prompt_attn_kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps, own_plan)) != cudaSuccess) return e;
   // (no unit can be long enough to be cut)
   if (ctas == 1 || 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost <= kPtWhole) return cudaSuccess;
-  return ctas / units >= kFp8MergeSplitParts
-             ? launch_dependent(prompt_merge_kernel<true>, dim3(ctas - 1, 2 * kPtRows), kFp8MergeThreads, 0, s, a, ctas)
-             : launch_dependent(prompt_merge_kernel<false>, dim3(ctas - 1, 2 * kPtRows / kPtMergeRows), kFp8MergeThreads, 0, s, a, ctas);
+  // Units that may be cut (many: by CTA, which needs no search), and the rows of the largest: blocks that find nothing to
+  // do are most of the time of a merge of few units (one token on 16K keys 57 us with 151 x 256 blocks, 23 with 4 x 32).
+  const int cut = static_cast<int>(units < ctas / 2 ? units : ctas - 1), tt = prompt_tile_tokens(a.heads_per_group);
+  const int rows = a.q_tokens <= tt ? static_cast<int>(a.q_tokens) * a.heads_per_group : 2 * kPtRows;
+  if (ctas / units >= kFp8MergeSplitParts)
+    return launch_dependent(prompt_merge_kernel<true>, dim3(cut, rows), kFp8MergeThreads, 0, s, a, ctas, rows);
+  int y = 4 * num_sms / cut;  // one wave (588 tokens on 10K, 24 units: 45 -> 41 us)
+  y = y < 1 ? 1 : y > (rows + 15) / 16 ? (rows + 15) / 16 : y;
+  return launch_dependent(prompt_merge_kernel<false>, dim3(cut, y), kFp8MergeThreads, 0, s, a, ctas, rows);
 }
 
 }  // namespace msa
