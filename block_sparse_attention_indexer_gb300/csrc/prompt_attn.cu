@@ -36,7 +36,7 @@
 // Stages of K and V and register shares: 1 to 3 %.  Code that a unit runs once costs its instruction fetches (the
 // epilogue, unrolled masks: 1 us and more each), so it is short loops, and the softmax's loop has nothing
 // rare inside it; function calls in that branch cost it registers (1.40 -> 1.48 ms).
-// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units, 358 us) 2 us of a unit's 12 are not its
+// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units, 357 us) 2 us of a unit's 12 are not its
 // steps, and tensor instructions run 58 % of the time (70 % for one prompt of 8K tokens, 357 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
     const uint32_t tS = tmem + slot * 128 + lane_base, tO = tmem + kPtO + slot * 128 + lane_base;
     const float f = finite_factor(a.scale_log2);
     const int my_token = r / Hg, my_head = r - my_token * Hg;
-    int done = 0, edges = 0, live = 0;             // steps of this slot, edge blocks, units with keys so far
+    int done = 0, live = 0;                        // steps of this slot, units with keys so far
     bool shared_par = false;
     float M = -INFINITY, l = 0.f, l_bf16 = 0.f;    // (l_bf16: of P as it is multiplied)
     int pos = 0;
@@ -502,15 +502,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       l = l_bf16 = 0.f;
       pos = it.pos0 + min(min(my_token, tt - 1) + (two && slot ? tt : 0), it.tokens - 1);
       // with one tile the blocks alternate between the slots
-      const int edge = it.edge(), step = two ? 1 : 2, first = it.lo + (two ? 0 : slot);
+      const int step = two ? 1 : 2, first = it.lo + (two ? 0 : slot);
       const int tile0 = it.pos0 + (two && slot ? tt : 0);  // position of the tile's first row
 #pragma unroll 1
       for (int p = first; p < it.hi; p += step) {
-        // what the V warps found in a block that not every row sees whole they look up among themselves when the unit is
-        // written (fin): seeing the stage ready here orders it before that (it is not used again before this step's P)
-        const int e = edges + p - edge;
-        if (!pt_wait_warp(&sh->s_full[slot], done & 1) ||
-            (p >= edge && !pt_wait_warp(&sh->v_ok[e % kPtV], (e / kPtV) & 1))) {
+        if (!pt_wait_warp(&sh->s_full[slot], done & 1)) {
           failed = true;
           break;
         }
@@ -596,7 +592,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         l += sum.x + sum.y;
         l_bf16 += (sum_bf16[0] + sum_bf16[1]) + (sum_bf16[2] + sum_bf16[3]);
       }
-      edges += it.hi - edge;
       // what is left to the V warps, who write the rows: the factors of O.  They have read the last unit's.
       if (failed || (live > 0 && !pt_wait_warp(&sh->o_empty[slot], (live - 1) & 1))) {
         failed = true;
@@ -735,6 +730,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
           if (!two) mbar_arrive(&sh->o_empty[1]);
         }
       }
+      // what the other V warps found in the unit's V: they have been through its last edge block
+      if (edges > 0 && !pt_wait_warp(&sh->v_ok[(edges - 1) % kPtV], ((edges - 1) / kPtV) & 1)) return false;
       const int* sp = sh->special[n & 7];
       if (sp[0] == n || sp[1] == n || sp[2] == n || sp[3] == n)
         pt_put_back(a, it.flags, it.lo, it.hi, it.token0, it.tokens, it.pos0, it.key0, it.g);
@@ -756,15 +753,20 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         }
         continue;
       }
-      if (live > 0 && !write(live - 1, before)) {
-        failed = true;
-        break;
-      }
-      if (it.flags & kPtEnd) break;
-      before = it;
-      ++live;
+      // A short unit's V is looked through before the last unit's rows are written, so that its products find it done (64 prompts
+      // of up to 100 tokens 34 -> 30 us).  In longer units the V of blocks from the kPtV-th on may lie in stages that only
+      // products behind that writing make free.
 #pragma unroll 1
-      for (int p = it.edge(); p < it.hi; ++p, ++edges) {
+      for (int p = it.edge(), state = it.hi - it.lo <= kPtV ? 1 : 0; ; ++p, ++edges) {
+        // state 0: the last unit's rows are to be written now; 1: behind this unit's blocks; 2: they are written
+        if (state == 0 || p >= it.hi) {
+          if (state < 2 && live > 0 && !write(live - 1, before)) {
+            failed = true;
+            break;
+          }
+          state = 2;
+          if (p >= it.hi) break;
+        }
         const int vs = (blocks + p - it.lo) % kPtV;
         if (!pt_wait_warp(&sh->v_edge[edges % kPtV], (edges / kPtV) & 1)) {
           failed = true;
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
           any |= r >= r0 ? s : 0u;
         }
         if (any != 0u) {
-          sh->special[(live - 1) & 7][warp - 8] = live - 1;
+          sh->special[live & 7][warp - 8] = live;
           auto clear = [](uint32_t w) {
             const uint32_t s = bf16_special(w);
             return w & ~(s | (s - (s >> 15)));  // (whole halves: the top bit and the 15 below it)
@@ -801,7 +803,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->v_ok[edges % kPtV]);
       }
+      if (failed || (it.flags & kPtEnd)) break;
       blocks += it.hi - it.lo;
+      before = it;
+      ++live;
     }
   } else {
    registers_down<64>();

@@ -233,6 +233,24 @@ def test_values_of_later_keys_in_cut_units(lens_q, lens_k):
     p.check(got, ref)
 
 
+@pytest.mark.parametrize("G,Hg,most", [(8, 3, 4), (4, 2, 200), (3, 1, 300)])
+def test_values_of_later_keys_in_short_units(G, Hg, most):
+    """Several short units a block of the grid, some with special values: what one holds stays out of the others."""
+    rng = np.random.default_rng(most)
+    lens = rng.integers(0, most + 1, 60).tolist()
+    p = Prompts(98, lens, G=G, Hg=Hg, behind=2)
+    for i in range(0, p.B, 3):
+        if lens[i]:
+            key, g = int(p.cu_k[i]) + int(rng.integers(lens[i])), int(rng.integers(G))
+            p.v[key, g, int(rng.integers(128))] = (np.nan, np.inf, -np.inf)[i % 3 if i % 2 else (i + 1) % 3]
+    ref = p.oracle()
+    got = run(p)
+    special = ~np.isfinite(ref["out"])
+    assert special.any()
+    ref["spread"] = np.where(special, 0.0, ref["spread"])
+    p.check(got, ref)
+
+
 def test_two_calls_at_once():
     import torch
     a, b = Prompts(94, [900, 50], G=2, Hg=4).upload(), Prompts(95, [30, 5], [4000, 3000], G=2, Hg=4).upload()
