@@ -841,10 +841,13 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       __syncwarp();
     } else if (units > 0) {
       E = static_cast<int64_t>(prefix[units]) * G;
+      const int n = gridDim.x, share = static_cast<int>(E) / n, rest = static_cast<int>(E) - share * n;
 #pragma unroll 1
       for (int k = 0; k < 2; ++k) {
         x0 = x1;
-        x1 = ft_cut(prefix, units, G, E, blockIdx.x + k, gridDim.x, kPtWhole);
+        const int c = blockIdx.x + k;  // (E c / n in 32 bits)
+        x1 = share * c + rest * c / n;
+        if (c > 0 && x1 < E) x1 = ft_cut_inside(prefix, units, G, x1, kPtWhole);
       }
       u = ft_find(prefix, units, G, static_cast<int>(min(static_cast<int64_t>(x0), E - 1)));
       b = ft_find(base, a.batch, 1, u);

@@ -23,15 +23,20 @@ __device__ __forceinline__ int ft_find(const int32_t* prefix, int units, int gro
   return lo;
 }
 
-// First step of CTA c of n as it is taken: a cut inside a unit that stays whole goes to the nearer of its ends.  A
-// whole warp calls it.
-__device__ __forceinline__ int ft_cut(const int32_t* prefix, int units, int G, int64_t E, int c, int n, int whole) {
-  const int x = ft_lo(E, c, n);
-  if (c == 0 || x >= E) return x;
+// A cut at place x of the list, in it: inside a unit that stays whole it goes to the nearer of its ends.  A whole warp
+// calls it.
+__device__ __forceinline__ int ft_cut_inside(const int32_t* prefix, int units, int G, int x, int whole) {
   const int u = ft_find(prefix, units, G, x), steps = prefix[u + 1] - prefix[u];
   if (steps > whole) return x;
   const int off = (x - prefix[u] * G) % steps;
   return x - off + (2 * off < steps ? 0 : steps);
+}
+
+// First step of CTA c of n as it is taken.
+__device__ __forceinline__ int ft_cut(const int32_t* prefix, int units, int G, int64_t E, int c, int n, int whole) {
+  const int x = ft_lo(E, c, n);
+  if (c == 0 || x >= E) return x;
+  return ft_cut_inside(prefix, units, G, x, whole);
 }
 
 // n / d for 0 <= n < 2^29 and 1 <= d <= 8: with m = ceil(2^32 / d), n m / 2^32 exceeds n / d by less than
