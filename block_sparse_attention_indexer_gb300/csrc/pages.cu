@@ -6,8 +6,8 @@
 // CTA); page_assign_kernel, a CTA for each chunk again, adds up the chunks before its own and gives every free page
 // its rank and what follows from that.  A pool of one chunk is one launch.  Copies of pages (fork, compact) are a launch of
 // their own, whose size the ranks decide.
-// The ranks are bound by latency, a few rounds of loads and barriers: 4.4 us in a graph for 38,000 pages of which 64
-// sequences take a few, 13 us for 890,000 of which 512 sequences take 70,000 (table and counts copied as well).  Measured
+// The ranks are bound by latency, a few rounds of loads and barriers: 4.2 us in a graph for 38,000 pages of which 64
+// sequences take a few, 11.5 us for 890,000 of which 512 sequences take 70,000 (table and counts copied as well).  Measured
 // for these: one cluster of eight CTAs that meets in distributed shared memory 7.3 and 43 us; chunks of 8,192
 // pages 5.7 and 18 us.  Copies are bound by memory: 500 pages in 16 buffers of 64 KB a page 83 us, 6.3 TB/s.
 #include "fp8_kernels.h"
@@ -479,8 +479,8 @@ static cudaError_t launch_ranks(const PageArgs& a, int num_sms, cudaStream_t s) 
   const int64_t table = kOp == kExtend && a.block_table != a.table_out ? static_cast<int64_t>(a.batch) * a.max_blocks : 0;
   if (chunks == 1 && table <= 16 * kPcThreads)
     return launch_dependent(page_assign_kernel<kOp, true>, dim3(1), kPcThreads, 0, s, a, chunks);
-  int64_t copies = (table + 16 * kPcThreads - 1) / (16 * kPcThreads);  // CTAs that copy the table, 16 words a thread
-  if (copies > 4 * num_sms) copies = 4 * num_sms;
+  int64_t copies = (table + 4 * kPcThreads - 1) / (4 * kPcThreads);  // CTAs that copy the table, 4 words a thread (16: 13.2 us)
+  if (copies > 8 * num_sms) copies = 8 * num_sms;
   const cudaError_t e = launch_dependent(page_count_kernel<kOp>, dim3(static_cast<unsigned>(1 + chunks + copies)), kPcThreads, 0, s,
                                          a, chunks);
   if (e != cudaSuccess) return e;

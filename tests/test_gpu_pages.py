@@ -103,15 +103,15 @@ def test_extend(lens, new, P, width, in_place):
 def test_extend_pool_sizes(P):
     """Pools of one round of the scan and of several, with free pages spread over all of it."""
     import block_sparse_attention_indexer_gb300 as msa
-    p = Pool(P, [0, 0, 0], P, 1024)
+    p = Pool(P, [0, 0, 0], P, 1000)
     refs = p.rng.integers(0, 2, P).astype(np.int32) if P > 5 else np.zeros(P, np.int32)
     refs[-1] = 0
     # the last free page is handed out as well, but for the large pools
     free = int((refs == 0).sum())
-    most = min(free, 3 * 1024)
-    new = np.array([128 * min(most, 1024), 128 * min(max(most - 1024, 0), 1024), 128 * max(most - 2048, 0)], np.int32)
-    if free > 3072:
-        refs[np.flatnonzero(refs == 0)[:free - 3072]] = 1     # the free ones lie at the end
+    most = min(free, 3 * 1000)
+    new = np.array([128 * min(most, 1000), 128 * min(max(most - 1000, 0), 1000), 128 * max(most - 2000, 0)], np.int32)
+    if free > 3000:
+        refs[np.flatnonzero(refs == 0)[:free - 3000]] = 1     # the free ones lie at the end
     p.d_refs.copy_(dev(refs))
     want = OP.extend(refs, p.table, p.lens, new)
     msa.msa_extend_pages(p.pool, p.batch, p.ws, new_tokens=dev(new))

@@ -66,7 +66,7 @@ def test_prompts_samples_decode_evict_compact():
     same(batch, table, lens)
 
     # steps of 100, 1 and 60 tokens, over the pages' ends, with collected weights; the last ones after a compaction
-    checker = Case(1, [128], 1, G, Hg, "bf16")
+    case = Case(1, [128], 1, G, Hg, "bf16")
     weight = torch.zeros(5, MB, device="cuda")
     for step, T in enumerate([100, 1, 60, 1]):
         if step == 2:
@@ -100,8 +100,8 @@ def test_prompts_samples_decode_evict_compact():
         w_before = weight.double().cpu().numpy()
         msa.msa_fp8_attn(cfg, cache, batch, q, out, lse, ws, weight_in=weight, weight_out=weight)
         torch.cuda.synchronize()
-        checker.T, checker.q = T, q.double().cpu().numpy()
-        ref = OF8.attention(checker.q, pools, table, lens, Hg, weight_in=w_before, decay=1.0)
+        case.T, case.q = T, q.double().cpu().numpy()
+        ref = OF8.attention(case.q, pools, table, lens, Hg, weight_in=w_before, decay=1.0)
         w_after = weight.double().cpu().numpy()
-        assert_attention(checker, (out.double().cpu().numpy(), lse.double().cpu().numpy(), w_after,
+        assert_attention(case, (out.double().cpu().numpy(), lse.double().cpu().numpy(), w_after,
                                    msa.msa_read_device_error(ws)), ref, weights=True)
