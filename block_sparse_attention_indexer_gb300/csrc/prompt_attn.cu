@@ -36,8 +36,9 @@
 // Stages of K and V and register shares: 1 to 3 %.  Code that a unit runs once costs its instruction fetches (the
 // epilogue, unrolled masks: 1 us and more each), so it is short loops, and the softmax's loop has nothing
 // rare inside it; function calls in that branch cost it registers (1.40 -> 1.48 ms).
-// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units, 357 us) 2 us of a unit's 12 are not its
-// steps, and tensor instructions run 58 % of the time (70 % for one prompt of 8K tokens, 357 us).
+// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units, 354 us) 2 us of a unit's 12 are not its
+// steps, and tensor instructions run 60 % of the time (71 % for one prompt of 8K tokens, 357 us).  Products of 64 keys
+// where a unit's last block has no more: the same to 2 % slower.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -264,8 +265,8 @@ __device__ __forceinline__ int pt_plan(const PromptArgs& a, const PtPlanSpace& s
   return units | (__syncthreads_or(much) ? 0 : kPtSpread);
 }
 
-// Sequences and units up to which every CTA of the attention makes the plan for itself (8 short prompts 21.7 us with
-// a launch for the plan, 15.1 without).  More are planned by a launch before it.
+// Sequences and units up to which every CTA of the attention makes the plan for itself (a launch for the plan cost 8 short
+// prompts 6.6 us more).  More are planned by a launch before it.
 constexpr int kPtOwnBatch = kPtThreads, kPtOwnUnits = 2048;
 
 // The same in shared memory, by every CTA of the attention.
