@@ -268,6 +268,9 @@ __device__ __forceinline__ int pt_plan(const PromptArgs& a, const PtPlanSpace& s
 // Sequences and units up to which every CTA of the attention makes the plan for itself (a launch for the plan cost 8 short
 // prompts 6.6 us more).  More are planned by a launch before it.
 constexpr int kPtOwnBatch = kPtThreads, kPtOwnUnits = 2048;
+// Sequences up to which, where no unit can be long enough to be cut, there is no plan: the units are dealt out as they
+// come, by the producer's warp alone (8 short prompts 11.3 -> 8.7 us).
+constexpr int kPtQuickBatch = 64;
 
 // The same in shared memory, by every CTA of the attention.
 struct PtOwnPlan {
@@ -398,6 +401,9 @@ __device__ __noinline__ void pt_put_back(const PromptArgs& a, int flags, int lo,
 
 // ---------------------------------------------------------------- the kernel
 
+// kQuick: a call without a plan.  A kernel of its own, so that its code is not in the way of the longer calls (in one
+// kernel they took 4 % more).
+template <bool kQuick>
 __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptArgs a,
                                                                     const __grid_constant__ PromptMaps maps, int own_plan) {
   extern __shared__ __align__(1024) uint8_t q_tile[];
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
   // the plan, in what will be the stages of K
   PtOwnPlan& own = *reinterpret_cast<PtOwnPlan*>(k_ring);
   int units = 0;
-  if (own_plan) {
+  if (!kQuick && own_plan) {
     units = pt_own_plan(a, own);
     fence_proxy_async_smem();
   }
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         }
         shared_par = !shared_par;
       }
-      const int place = (it.flags >> kPtPlace) - 1;
+      const int place = kQuick ? -1 : (it.flags >> kPtPlace) - 1;
       float fb = 0.f;
       if (!two) {
         const float mo = sh->other_m[r], lo = sh->other_l[r];
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
     // Unit n of those with keys: row ct of both tiles.
     auto write = [&](int n, const PtItem& it) -> bool {
       const bool two = it.flags & kPtTwo, both = !two && it.lo + 1 < it.hi;  // (one tile: slot 1 has blocks as well)
-      const int place = (it.flags >> kPtPlace) - 1;
+      const int place = kQuick ? -1 : (it.flags >> kPtPlace) - 1;
       float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + max(place, 0)) * kPtPlaceFloats;
       const uint32_t tO = tmem + kPtO + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       // with one tile slot 0 has the sum's factors, and all is done with it
@@ -813,11 +819,41 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
    registers_down<64>();
    if (warp == 12) {
     // ---- producer: units and the copies of Q and K
-    if (!own_plan) units = a.plan[0];
+    int base0 = 0, base1 = 0;  // kQuick: units of the sequences before sequence lane and 32 + lane
+    if (kQuick) {
+      bool bad = false;
+      int x[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int s = 32 * j + lane;
+        x[j] = 0;
+        if (s < a.batch) {
+          const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
+          bad |= q0 < 0 || k0 < 0 || q1 < q0 || k1 < k0 || q1 > a.q_tokens || k1 > a.k_tokens;
+          x[j] = (q1 - q0 + 2 * tt - 1) / (2 * tt);
+        }
+      }
+      base0 = x[0], base1 = x[1];
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int y0 = __shfl_up_sync(0xffffffffu, base0, s), y1 = __shfl_up_sync(0xffffffffu, base1, s);
+        if (lane >= s) base0 += y0, base1 += y1;
+      }
+      const int all0 = __shfl_sync(0xffffffffu, base0, 31);
+      units = all0 + __shfl_sync(0xffffffffu, base1, 31);
+      base0 -= x[0];
+      base1 += all0 - x[1];
+      if (__any_sync(0xffffffffu, bad)) {  // nothing is done
+        if (blockIdx.x == 0 && lane == 0) flag_error(a.err, MSA_DEVERR_BAD_SEQLEN);
+        units = 0;
+      }
+    } else if (!own_plan) {
+      units = a.plan[0];
+    }
     const int* base = own_plan ? own.base : a.base;
     const int32_t *prefix = own_plan ? own.prefix : a.prefix, *order = own_plan ? own.order : a.order;
-    const bool spread = units & kPtSpread;
-    units &= kPtSpread - 1;
+    const bool spread = !kQuick && units & kPtSpread;
+    if (!kQuick) units &= kPtSpread - 1;
     int x0 = 0, x1 = 0, u = 0, b = 0, i = 0, dealt = 0;  // dealt: units of this CTA where they stay whole
     int64_t E = 0, first = 0;                            // all cost, cost before unit u
     int2* mine = a.dealt + blockIdx.x * kPtMaxDealt;
@@ -840,7 +876,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         mine[k] = make_int2(s | (at - by_g(at) * G) << 16, unit - base[s]);
       }
       __syncwarp();
-    } else if (units > 0) {
+    } else if (!kQuick && units > 0) {
       E = static_cast<int64_t>(prefix[units]) * G;
       const int n = gridDim.x, share = static_cast<int>(E) / n, rest = static_cast<int>(E) - share * n;
 #pragma unroll 1
@@ -868,9 +904,17 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       return true;
     };
     PtCut cut{-1, 0, 0, 0, 0, 0, {0, 0}};
-    for (int k = 0; !failed && (spread ? k < dealt : units > 0 && first <= x1); ++k) {  // unit i of sequence b
+    for (int k = 0; !failed && (kQuick ? static_cast<int>(blockIdx.x + k * gridDim.x) < units * G
+                                       : spread ? k < dealt : units > 0 && first <= x1); ++k) {  // unit i of sequence b
       int g = 0, g_end = G;
-      if (spread) {
+      if (kQuick) {
+        const int at = blockIdx.x + k * gridDim.x, unit = FtDiv(G)(at);
+        b = __popc(__ballot_sync(0xffffffffu, base0 <= unit)) - 1;
+        if (b == 31) b += __popc(__ballot_sync(0xffffffffu, base1 <= unit));
+        i = unit - __shfl_sync(0xffffffffu, b < 32 ? base0 : base1, b & 31);
+        g = at - unit * G;
+        g_end = g + 1;
+      } else if (spread) {
         const int2 x = __ldcg(mine + k);
         b = x.x & 0xFFFF;
         g = x.x >> 16;
@@ -883,7 +927,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
 #pragma unroll 1
       for (; g < g_end && !failed; ++g) {
         int lo = 0, hi = pages;
-        if (!spread) {
+        if (!kQuick && !spread) {
           const int64_t u0 = first + static_cast<int64_t>(g) * cost;
           if (u0 + cost <= x0) continue;
           lo = t.block_at(x0 - u0), hi = t.block_at(x1 - u0);
@@ -927,7 +971,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
           ++blocks;
         }
       }
-      if (spread) continue;
+      if (kQuick || spread) continue;
       // the next unit: of this sequence, or the first one of the next sequence that has any
       first += static_cast<int64_t>(cost) * G;
       if (++u >= units) break;
@@ -937,7 +981,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         while (a.cu_q[b + 1] == a.cu_q[b]);
       }
     }
-    if (lane == 0) a.cuts[blockIdx.x] = cut;
+    if (!kQuick && lane == 0) a.cuts[blockIdx.x] = cut;
     if (!failed) failed = !record(PtItem{kPtEnd, 0, 0, 0, 0, 0, 0, 0});
     if (failed) {
       // wait (bounded) for the copies still in flight
@@ -1276,13 +1320,17 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s)
   cudaError_t e = prompt_maps(a, &maps);
   if (e != cudaSuccess) return e;
   const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas;
-  if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(prompt_attn_kernel), kPtSmem)) != cudaSuccess) return e;
   const int64_t most = prompt_max_units(a.q_tokens, a.batch, a.heads_per_group), units = most * a.groups;
-  const int own_plan = a.batch <= kPtOwnBatch && most <= kPtOwnUnits ? 1 : 0;
-  if (!own_plan && (e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a, ctas)) != cudaSuccess) return e;
-  if ((e = launch_dependent(prompt_attn_kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps, own_plan)) != cudaSuccess) return e;
   // (no unit can be long enough to be cut)
-  if (ctas == 1 || 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost <= kPtWhole) return cudaSuccess;
+  const bool whole = 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost <= kPtWhole;
+  const bool quick = whole && a.batch <= kPtQuickBatch;
+  const int own_plan = a.batch <= kPtOwnBatch && most <= kPtOwnUnits ? 1 : 0;
+  const auto kernel = quick ? prompt_attn_kernel<true> : prompt_attn_kernel<false>;
+  if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kPtSmem)) != cudaSuccess) return e;
+  if (!quick && !own_plan && (e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a, ctas)) != cudaSuccess)
+    return e;
+  if ((e = launch_dependent(kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps, own_plan)) != cudaSuccess) return e;
+  if (ctas == 1 || whole) return cudaSuccess;
   // Units that may be cut (many: by CTA, which needs no search), and the rows of the largest: blocks that find nothing to
   // do are most of the time of a merge of few units (one token on 16K keys 57 us with 151 x 256 blocks, 23 with 4 x 32).
   const int cut = static_cast<int>(units < ctas / 2 ? units : ctas - 1), tt = prompt_tile_tokens(a.heads_per_group);
