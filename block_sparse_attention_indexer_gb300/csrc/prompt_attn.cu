@@ -268,9 +268,24 @@ __device__ __forceinline__ int pt_plan(const PromptArgs& a, const PtPlanSpace& s
 // Sequences and units up to which every CTA of the attention makes the plan for itself (a launch for the plan cost 8 short
 // prompts 6.6 us more).  More are planned by a launch before it.
 constexpr int kPtOwnBatch = kPtThreads, kPtOwnUnits = 2048;
-// Sequences up to which, where no unit can be long enough to be cut, there is no plan: the units are dealt out as they
-// come, by the producer's warp alone (8 short prompts 11.3 -> 8.7 us).
-constexpr int kPtQuickBatch = 64;
+// Calls without a plan: the units are dealt out whole, as they come, by the producer's warp alone.  For up to so many
+// sequences, where no unit can cost more than kPtQuickCost, and for one prompt (lengths as its tokens say) that has a unit
+// for every CTA, where none can cost more than kPtQuickOne and what a CTA would get above its share is little.  8 short
+// prompts 11.3 -> 8.1 us, one of 512 tokens 15.7 -> 12.9, of 1K 25.5 -> 20.3, of 2K 38.7 -> 33.2, of 3,500 86 -> 81; where
+// cuts help most, 100 tokens on 1,500 keys, 24.9 -> 26.0.  With the larger limit for more sequences, 5 of up to 900 tokens took
+// 29 us instead of 24.
+constexpr int kPtQuickBatch = 64, kPtQuickCost = 32, kPtQuickOne = 64, kPtQuickSteps = 20;
+static bool pt_quick(const PromptArgs& a, int64_t largest, int ctas) {
+  if (a.batch > kPtQuickBatch) return false;
+  if (largest <= kPtQuickCost) return true;
+  const int pair = 2 * prompt_tile_tokens(a.heads_per_group), units = (a.q_tokens + pair - 1) / pair * a.groups;
+  if (a.batch > 1 || largest > kPtQuickOne || units < ctas) return false;
+  const int before = a.k_tokens > a.q_tokens ? a.k_tokens - a.q_tokens : 0, rest = units % ctas;
+  const float least = 2.f * ((before + pair + kBlock - 1) / kBlock) + kPtUnitCost;  // cost of the first unit
+  const float rise = (largest - least) / units, half = (units / ctas & 1) ? .5f * rise * ctas : 0.f;
+  const float more = rest > 0 ? least + .5f * rise * rest - half : 0.f;             // a round begun
+  return (more > half ? more : half) <= kPtQuickSteps;
+}
 
 // The same in shared memory, by every CTA of the attention.
 struct PtOwnPlan {
@@ -904,11 +919,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       return true;
     };
     PtCut cut{-1, 0, 0, 0, 0, 0, {0, 0}};
-    for (int k = 0; !failed && (kQuick ? static_cast<int>(blockIdx.x + k * gridDim.x) < units * G
+    // kQuick: a prompt's units cost more and more, so the last ones come first; the CTAs that start first get the units of
+    // one round, or the second units of more
+    const int c = units * G > static_cast<int>(gridDim.x) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    for (int k = 0; !failed && (kQuick ? pt_dealt(k, c, gridDim.x) < units * G
                                        : spread ? k < dealt : units > 0 && first <= x1); ++k) {  // unit i of sequence b
       int g = 0, g_end = G;
       if (kQuick) {
-        const int at = blockIdx.x + k * gridDim.x, unit = FtDiv(G)(at);
+        const int at = units * G - 1 - pt_dealt(k, c, gridDim.x), unit = FtDiv(G)(at);
         b = __popc(__ballot_sync(0xffffffffu, base0 <= unit)) - 1;
         if (b == 31) b += __popc(__ballot_sync(0xffffffffu, base1 <= unit));
         i = unit - __shfl_sync(0xffffffffu, b < 32 ? base0 : base1, b & 31);
@@ -1321,16 +1339,15 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s)
   if (e != cudaSuccess) return e;
   const int ctas = num_sms < kFp8MaxCtas ? num_sms : kFp8MaxCtas;
   const int64_t most = prompt_max_units(a.q_tokens, a.batch, a.heads_per_group), units = most * a.groups;
-  // (no unit can be long enough to be cut)
-  const bool whole = 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost <= kPtWhole;
-  const bool quick = whole && a.batch <= kPtQuickBatch;
+  const int64_t largest = 2 * ((static_cast<int64_t>(a.k_tokens) + kBlock - 1) / kBlock) + kPtUnitCost;  // cost of a unit
+  const bool quick = pt_quick(a, largest, ctas);
   const int own_plan = a.batch <= kPtOwnBatch && most <= kPtOwnUnits ? 1 : 0;
   const auto kernel = quick ? prompt_attn_kernel<true> : prompt_attn_kernel<false>;
   if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kPtSmem)) != cudaSuccess) return e;
   if (!quick && !own_plan && (e = launch_dependent(prompt_plan_kernel, dim3(1), kPtPlanThreads, 0, s, a, ctas)) != cudaSuccess)
     return e;
   if ((e = launch_dependent(kernel, dim3(ctas), kPtThreads, kPtSmem, s, a, maps, own_plan)) != cudaSuccess) return e;
-  if (ctas == 1 || whole) return cudaSuccess;
+  if (ctas == 1 || quick || largest <= kPtWhole) return cudaSuccess;  // nothing can be cut
   // Units that may be cut (many: by CTA, which needs no search), and the rows of the largest: blocks that find nothing to
   // do are most of the time of a merge of few units (one token on 16K keys 57 us with 151 x 256 blocks, 23 with 4 x 32).
   const int cut = static_cast<int>(units < ctas / 2 ? units : ctas - 1), tt = prompt_tile_tokens(a.heads_per_group);

@@ -198,6 +198,9 @@ def test_single_token_agrees_with_the_prompt():
     ([1100], None, 2, 8),                                        # whole: a unit for nearly every block of the grid
     ([2100, 3, 700], None, 2, 8),                                # whole, two a block
     ([1000] + [37 * i % 500 for i in range(1, 32)], None, 2, 8),  # whole, many units of the same cost
+    ([2100], None, 8, 3),                                        # no plan: one prompt, more units than blocks
+    ([0, 90, 1, 0, 33] * 11 + [200], None, 3, 5),                # no plan: short ones, some of them empty, over 32 of them
+    ([40, 0, 7], [600, 500, 20], 8, 1),                          # no plan: chunks
     ([40], [5000], 2, 8),                                        # cut, few units
     ([1], [6000], 1, 8),                                         # one row tile cut into nearly as many parts as pages
     ([1, 1, 1], [3000, 20, 2000], 1, 1),
