@@ -145,6 +145,19 @@ def test_bad_offsets(cu_q, cu_k):
     assert err == msa.MSA_DEVERR_BAD_SEQLEN and (out == 7).all() and (lse == 7).all()
 
 
+@pytest.mark.parametrize("lens,at", [([900, 500, 600], 2), ([5] * 600, 599), ([4] * 70, 66)])
+@pytest.mark.parametrize("which", ["cu_q", "cu_k"])
+def test_bad_offsets_of_longer_lists(lens, at, which):
+    """The same where the plan is made by every block, by a launch before, and for more than 64 sequences."""
+    import block_sparse_attention_indexer_gb300 as msa
+    p = Prompts(99, lens, G=1, Hg=2)
+    cu = getattr(p, which).copy()
+    cu[at] = cu[at - 1] - 1
+    setattr(p, which, cu)
+    out, lse, err = run(p)
+    assert err == msa.MSA_DEVERR_BAD_SEQLEN and (out == 7).all() and (lse == 7).all()
+
+
 def test_without_lse_same_bits():
     p = Prompts(90, [513, 64, 900], G=2, Hg=5)
     first = run(p)
@@ -173,6 +186,27 @@ def test_captured_and_on_another_stream():
         p.packed.cu_q.copy_(torch.from_numpy(cu))
         p.packed.cu_k.copy_(torch.from_numpy(cu))
         p.cu_q = p.cu_k = cu
+        p.out.fill_(7.0)
+        p.lse.fill_(7.0)
+        g.replay()
+        p.check(p.results())
+
+
+@pytest.mark.parametrize("room,batch,G,Hg", [(2100, 1, 8, 3), (3000, 3, 2, 8), (3000, 600, 1, 2)])
+def test_captured_with_room_for_more(room, batch, G, Hg):
+    """A graph whose lists have room for more tokens than a replay's sequences take: how the work is split is chosen by the
+    room, the rows behind the last sequence stay as they were."""
+    import torch
+    p = Prompts(100, [room] + [0] * (batch - 1), G=G, Hg=Hg).upload()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.call()
+    for lens_q, lens_k in (([1], [900]), ([0, 130], [7, 140]), ([200, 3, 40], [200, 800, 41])):
+        n = min(batch, len(lens_q))
+        p.cu_q, p.cu_k = (np.cumsum([0] + list(x[:n]) + [0] * (batch - n)).astype(np.int32) for x in (lens_q, lens_k))
+        p.packed.cu_q.copy_(torch.from_numpy(p.cu_q))
+        p.packed.cu_k.copy_(torch.from_numpy(p.cu_k))
+        p.used_q = np.arange(p.Nq) < p.cu_q[-1]
         p.out.fill_(7.0)
         p.lse.fill_(7.0)
         g.replay()
