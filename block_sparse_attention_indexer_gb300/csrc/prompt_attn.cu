@@ -35,7 +35,8 @@
 // for 128 keys 1.41 against 1.35; the exponentials of the second half held back behind the first half's hand-over 1.37.
 // Stages of K and V and register shares: 1 to 3 %.  Code that a unit runs once costs its instruction fetches (the
 // epilogue, unrolled masks: 1 us and more each), so it is short loops, and the softmax's loop has nothing
-// rare inside it; function calls in that branch cost it registers (1.40 -> 1.48 ms).
+// rare inside it; function calls in that branch cost it registers (1.40 -> 1.48 ms).  The compiler's report should show no
+// spills for it: changes of the V warps' code that brought 8 to 16 bytes of them cost 2 to 4 %, wherever they were.
 // Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units, 354 us) 2 us of a unit's 12 are not its
 // steps, and tensor instructions run 60 % of the time (71 % for one prompt of 8K tokens, 357 us).  Products of 64 keys
 // where a unit's last block has no more: the same to 2 % slower.
