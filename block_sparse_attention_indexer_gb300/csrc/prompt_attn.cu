@@ -891,7 +891,6 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         }
         mine[k] = make_int2(s | (at - by_g(at) * G) << 16, unit - base[s]);
       }
-      __syncwarp();
     } else if (!kQuick && units > 0) {
       E = static_cast<int64_t>(prefix[units]) * G;
       const int n = gridDim.x, share = static_cast<int>(E) / n, rest = static_cast<int>(E) - share * n;
@@ -907,6 +906,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       i = u - base[b];
       first = static_cast<int64_t>(prefix[u]) * G;
     }
+    __syncwarp();  // (lane 0's copies go over the plan that all lanes have read, and all read what others left in `mine`)
     const uint64_t keep = l2_evict_normal_policy(), once = l2_evict_first_policy();
     const uint32_t q_bytes = static_cast<uint32_t>(tt) * Hg * 256;
     int n = 0, blocks = 0, tiles0 = 0, tiles1 = 0;  // units, blocks, units that used tile 0 and tile 1

@@ -327,3 +327,21 @@ def test_scores_that_are_all_minus_infinity():
     p.q[:, 1, 0] = 1.0
     got = run(p)
     assert (got[0] == 0).all() and (got[1] == -np.inf).all() and got[2] == 0
+
+
+@pytest.mark.parametrize("lens_q,lens_k,G,Hg", [([40, 90], [5000, 700], 2, 8), ([1], [4000], 1, 8), ([1100], None, 2, 8)])
+def test_the_plan_is_read_before_keys_are_copied_over_it(lens_q, lens_k, G, Hg):
+    """The plan that every block makes for itself lies where the first keys are copied to: a lane that read it late would find
+    keys there.  Cut and whole units, many calls one after another, the same bits in all of them."""
+    import torch
+    p = Prompts(101, lens_q, lens_k, G=G, Hg=Hg)
+    first = run(p)
+    p.check(first)
+    out, lse = p.out.clone(), p.lse.clone()
+    different = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        p.out.fill_(7.0)
+        p.lse.fill_(7.0)
+        p.call()
+        different += (p.out != out).sum() + (p.lse != lse).sum()
+    assert int(different) == 0 and p.results()[2] == 0
