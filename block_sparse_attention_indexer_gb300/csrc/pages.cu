@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(256) page_free_kernel(const PageArgs a) {
       continue;
     }
     const int32_t* row = a.pages + static_cast<int64_t>(r) * a.width;
-    for (int n0 = blockIdx.x * 1024 + threadIdx.x; n0 < c; n0 += gridDim.x * 1024) {
+    // (64 bits: the row's end and a step of the grid together may pass 2^31)
+    for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x; n0 < c; n0 += static_cast<int64_t>(gridDim.x) * 1024) {
       int page[4], was[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) page[j] = n0 + 256 * j < c ? row[n0 + 256 * j] : -1;
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(256) page_refs_kernel(const PageArgs a) {
 
 // Rows of a table (or list) by blockIdx.y, 1,024 entries of one by blockIdx.x.
 static dim3 row_grid(int rows, int width, int num_sms) {
-  const int x = width > 0 ? (width + 1023) / 1024 : 1, most = num_sms * 8 / x + 1;
+  const int x = width > 0 ? (width - 1) / 1024 + 1 : 1, most = num_sms * 8 / x + 1;
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>(rows < 1 ? 1 : rows < most ? rows : most));
 }
 

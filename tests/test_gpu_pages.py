@@ -416,3 +416,24 @@ def test_two_pools_at_once_on_their_own_streams():
         assert np.array_equal(host(p.d_refs), refs) and np.array_equal(host(x["to"]), kids)
         assert np.array_equal(host(x["lens"]), kid_lens) and np.array_equal(host(x["map"]), page_map) and host(x["live"])[0] == n
         p.same_buffers()
+
+
+@pytest.mark.parametrize("width", [1_200_000_000, 2 ** 31 - 1])
+def test_free_of_long_rows(width):
+    """Rows of more than 2^30 entries: the place behind the last one and the grid's step together pass 2^31."""
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+    p = Pool(91, [128 * 20], 30, 20)
+    p.d_refs.copy_(dev(np.full(30, 9, np.int32)))
+    pages = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    want = np.full(30, 9, np.int32)
+    for at in (0, 255, 1023, 1024, 2 ** 30 - 1, 2 ** 30, width - 1025, width - 257, width - 2):
+        pages[0, at] = at % 30
+        want[at % 30] -= 1
+    pages[0, width - 1] = 30                                   # behind the row's count
+    msa.msa_free_pages(p.pool, pages, p.ws, counts=dev(np.array([width - 1], np.int32)))
+    assert np.array_equal(host(p.d_refs), want) and p.err() == 0
+    msa.msa_free_pages(p.pool, pages, p.ws)
+    for at in (0, 255, 1023, 1024, 2 ** 30 - 1, 2 ** 30, width - 1025, width - 257, width - 2):
+        want[at % 30] -= 1
+    assert np.array_equal(host(p.d_refs), want) and p.err() == 1
