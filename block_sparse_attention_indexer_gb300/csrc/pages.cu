@@ -519,7 +519,7 @@ static cudaError_t launch_move(const PageArgs& a, int64_t most_pairs, int num_sm
       const bool runs = kOp == kFork && x.token_bytes > 0;
       x.run_bytes = runs ? x.token_bytes * kBlock : static_cast<int32_t>(x.page_bytes);
       x.runs = static_cast<int32_t>(x.page_bytes / x.run_bytes);
-      x.chunks = (x.run_bytes + kPageChunk - 1) / kPageChunk;
+      x.chunks = (x.run_bytes - 1) / kPageChunk + 1;  // (run_bytes may be 2^31 - 1)
       const int64_t items = most_pairs * x.runs * x.chunks;
       most = items > most ? items : most;
     }

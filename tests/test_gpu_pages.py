@@ -437,3 +437,34 @@ def test_free_of_long_rows(width):
     for at in (0, 255, 1023, 1024, 2 ** 30 - 1, 2 ** 30, width - 1025, width - 257, width - 2):
         want[at % 30] -= 1
     assert np.array_equal(host(p.d_refs), want) and p.err() == 1
+
+
+@pytest.mark.parametrize("page", [2 ** 31 - 1, 2 ** 31 - 16384, 2 ** 31 - 16383])
+def test_pages_of_two_gigabytes(page):
+    """Pages whose bytes and a copy's piece together pass 2^31, moved by a compaction and copied by a fork."""
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+
+    class Pages:                                               # what a pool asks of a cache
+        num_pages = 3
+        data = torch.zeros(3, page, dtype=torch.uint8, device="cuda")
+
+        def tensors(self):
+            return (self.data,)
+
+    cache = Pages()
+    data, marks = cache.data, [0, 16383, 16384, 2 ** 30, page - 16384, page - 2, page - 1]
+    data[2, :] = 9
+    data[2, marks] = torch.arange(1, 8, dtype=torch.uint8, device="cuda")
+    want = data[2].clone()
+    pool = msa.PagePool([cache], refs=dev(np.array([0, 0, 1], np.int32)))
+    table, lens = dev(np.array([[2]], np.int32)), dev(np.array([5], np.int32))
+    batch, ws = msa.Batch(table, lens), msa.alloc_page_workspace(pool, 1)
+    page_map, live = torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    msa.msa_compact_pages(pool, batch, page_map, live, ws)
+    assert host(page_map).tolist() == [-1, -1, 0] and host(table).tolist() == [[0]] and host(live).tolist() == [1]
+    assert torch.equal(data[0], want)
+    kids, kid_lens = torch.empty(1, 1, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    msa.msa_fork_pages(pool, batch, dev(np.array([0], np.int32)), kids, kid_lens, ws)
+    assert host(kids).tolist() == [[1]] and host(pool.refs).tolist() == [1, 1, 0]
+    assert torch.equal(data[1], want) and msa.msa_read_device_error(ws) == 0
