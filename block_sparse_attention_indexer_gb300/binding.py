@@ -379,7 +379,8 @@ class Packed:
 
 class PagePool:
     """A pool of pages: refs (int32 [num_pages] on the device, 0 for a free page), and the caches
-    whose pools hold the pages (of every layer that goes by the same block table)."""
+    whose pools hold the pages (of every layer that goes by the same block table).  refs may be replaced by
+    another such tensor, a call's refs_out for example; the tensors of a PagedCache too: the next call goes by the new ones."""
 
     def __init__(self, caches=(), refs: Optional[torch.Tensor] = None, num_pages: Optional[int] = None, device=None):
         self.caches = tuple(caches)
@@ -393,26 +394,48 @@ class PagePool:
             raise ValueError(f"refs counts {refs.numel()} pages, the caches have {sorted(counts)}")
         if refs.dim() != 1:
             raise ValueError(f"refs must be [num_pages], got {tuple(refs.shape)}")
-        self.refs, self.num_pages, self.device_index = refs, refs.numel(), _on(refs, "refs")
-        _at(refs, (self.num_pages,), torch.int32, self.device_index, "refs")
-        buffers = []
+        self.num_pages, self.device_index = refs.numel(), _on(refs, "refs")
+        self._c = _PagePool(None, None, self.num_pages, None, 0)
+        self.refs = refs
+        self._take_buffers()
+
+    @property
+    def refs(self):
+        return self._refs
+
+    @refs.setter
+    def refs(self, refs: torch.Tensor):
+        self._c.refs = self._c.refs_out = _at(refs, (self.num_pages,), torch.int32, self.device_index, "refs")
+        self._refs = refs
+
+    def _take_buffers(self):
+        buffers, held = [], []
         for c in self.caches:
-            for t in c.tensors():
+            held.append(c.tensors())
+            for t in held[-1]:
                 if t.dtype != torch.uint8 or t.get_device() != self.device_index or not t.is_contiguous():
                     raise ValueError("the caches' pools must be contiguous uint8 tensors on the device of refs")
+                if t.shape[0] != self.num_pages:
+                    raise ValueError(f"the pool has {self.num_pages} pages, a cache's tensor {t.shape[0]}")
                 page = t.numel() // self.num_pages if self.num_pages else 0
                 # [P, groups, block, bytes] or [P, block, bytes]; FP8 scales [P, groups] belong to whole pages
                 buffers.append(_PageBuffer(t.data_ptr(), page, t.shape[-1] if t.dim() > 2 else 0))
         self._buffers = (_PageBuffer * max(1, len(buffers)))(*buffers)
-        self._count = len(buffers)
-        self._c = _PagePool(refs.data_ptr(), refs.data_ptr(), self.num_pages, self._buffers, self._count)
+        self._held = held  # (the C structs have their addresses)
+        self._c.buffers, self._c.num_buffers = self._buffers, len(buffers)
 
-    def c(self, refs_out: Optional[torch.Tensor] = None):
-        """The C struct for a call that leaves the new counts in refs_out (None: in refs)."""
+    def c(self, refs_out: Optional[torch.Tensor] = None, pages=False):
+        """The C struct for a call that leaves the new counts in refs_out (None: in refs); pages: one that copies pages."""
+        if pages:
+            for c, held in zip(self.caches, self._held):
+                now = c.tensors()
+                if now is not held and (len(now) != len(held) or any(x is not y for x, y in zip(now, held))):
+                    self._take_buffers()
+                    break
         if refs_out is None:
             return ctypes.byref(self._c)
         out = _at(refs_out, (self.num_pages,), torch.int32, self.device_index, "refs_out")
-        return ctypes.byref(_PagePool(self._c.refs, out, self.num_pages, self._buffers, self._count))
+        return ctypes.byref(_PagePool(self._c.refs, out, self.num_pages, self._buffers, self._c.num_buffers))
 
 
 def _pool_batch(pool: PagePool, batch: Batch) -> int:
@@ -672,7 +695,7 @@ def msa_fork_pages(pool: PagePool, batch: Batch, parents: torch.Tensor, table_ou
     if parents.dim() != 1:
         raise ValueError(f"parents must be [children], got {tuple(parents.shape)}")
     n, i32 = parents.shape[0], torch.int32
-    _launch("msa_fork_pages", _lib.msa_fork_pages, dev, stream, pool.c(refs_out), batch.c(),
+    _launch("msa_fork_pages", _lib.msa_fork_pages, dev, stream, pool.c(refs_out, True), batch.c(),
             _at(parents, (n,), i32, dev, "parents"), n, _at(table_out, (n, batch.max_blocks), i32, dev, "table_out"),
             _at(seq_lens_out, (n,), i32, dev, "seq_lens_out"), *_space(workspace, dev))
 
@@ -699,7 +722,7 @@ def msa_compact_pages(pool: PagePool, batch: Batch, page_map: torch.Tensor, live
     workspace: alloc_page_workspace(pool, 0)."""
     dev = _pool_batch(pool, batch)
     to, i32 = batch.block_table if table_out is None else table_out, torch.int32
-    _launch("msa_compact_pages", _lib.msa_compact_pages, dev, stream, pool.c(refs_out), batch.c(),
+    _launch("msa_compact_pages", _lib.msa_compact_pages, dev, stream, pool.c(refs_out, True), batch.c(),
             _at(to, batch.block_table.shape, i32, dev, "table_out"),
             _at(page_map, (pool.num_pages,), i32, dev, "page_map"), _at(live_count, (1,), i32, dev, "live_count"),
             *_space(workspace, dev))

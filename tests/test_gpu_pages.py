@@ -468,3 +468,29 @@ def test_pages_of_two_gigabytes(page):
     msa.msa_fork_pages(pool, batch, dev(np.array([0], np.int32)), kids, kid_lens, ws)
     assert host(kids).tolist() == [[1]] and host(pool.refs).tolist() == [1, 1, 0]
     assert torch.equal(data[1], want) and msa.msa_read_device_error(ws) == 0
+
+
+def test_counts_and_tensors_replaced_between_calls():
+    """A program that goes on from a call's refs_out as the pool's counts, and with other tensors in a cache."""
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+    p = Pool(92, [700, 90, 300], 40, 8, caches=[("nvfp4", 2), ("fp8", 1)])
+    new, out = np.array([200, 60, 1], np.int32), torch.empty(40, dtype=torch.int32, device="cuda")
+    msa.msa_extend_pages(p.pool, p.batch, p.ws, new_tokens=dev(new), refs_out=out)
+    refs, table, lens, err = OP.extend(p.refs, p.table, p.lens, new)
+    assert np.array_equal(host(out), refs) and np.array_equal(host(p.d_refs), p.refs)
+    p.pool.refs = out
+    msa.msa_extend_pages(p.pool, p.batch, p.ws, new_tokens=dev(new))
+    refs, table, lens, err2 = OP.extend(refs, table, lens, new)
+    assert np.array_equal(host(out), refs) and np.array_equal(host(p.d_table), table)
+    assert np.array_equal(host(p.d_refs), p.refs)                               # the first counts are left alone
+    old, p.caches[0].k_data = p.caches[0].k_data, p.caches[0].k_data.clone()
+    before = old.clone()
+    parents = np.array([1, 1, 0, 2], np.int32)
+    refs, kids, kid_lens, err3 = OP.fork(refs, table, lens, parents, p.buffers)
+    to, to_lens = torch.empty(4, 8, dtype=torch.int32, device="cuda"), torch.empty(4, dtype=torch.int32, device="cuda")
+    msa.msa_fork_pages(p.pool, p.batch, dev(parents), to, to_lens, p.ws)
+    assert np.array_equal(host(out), refs) and np.array_equal(host(to), kids) and err == err3 == 0
+    assert p.err() == err2 == OP.BAD_SEQLEN                                     # (the first one has no room for 200 more)
+    p.same_buffers()
+    assert torch.equal(old, before)

@@ -162,3 +162,41 @@ def test_oracle_pages_pins():
     assert OP.free(refs, np.array([[2, 2, 2, 0]], np.int32)) [0].tolist() == [0, 0, 0, 0, 1, 0]
     got = OP.compact(refs, table, lens)
     assert got[0].tolist() == [1, 1, 2, 0, 0, 0] and got[1].tolist() == [[2, 0, -1], [2, 1, -1]] and got[3] == 3
+
+
+def test_pool_goes_by_its_present_tensors(msa, monkeypatch):
+    """Counts and caches' tensors that were replaced after the pool was made: the next call's struct has the new ones, and
+    what the struct points to stays alive."""
+    import gc
+    import weakref
+
+    import torch
+    monkeypatch.setattr(msa.binding, "_on", lambda t, name: t.get_device())     # tensors of the host stand for the device's
+    cache, other = msa.PagedCache(5, groups=2, device="cpu"), msa.PagedCache(5, groups=1, device="cpu")
+    pool = msa.PagePool([cache, other], refs=torch.zeros(5, dtype=torch.int32))
+    new = torch.ones(5, dtype=torch.int32)
+    pool.refs = new
+    c = pool.c()._obj
+    assert pool.refs is new and c.refs == c.refs_out == new.data_ptr()
+    out = torch.empty(5, dtype=torch.int32)
+    c = pool.c(out, True)._obj
+    assert c.refs == new.data_ptr() and c.refs_out == out.data_ptr()
+    for bad, error in ((torch.ones(4, dtype=torch.int32), ValueError), (torch.ones(5), TypeError),
+                       (torch.ones(10, dtype=torch.int32)[::2], ValueError)):
+        with pytest.raises(error):
+            pool.refs = bad
+    assert pool.refs is new and pool.c()._obj.refs == new.data_ptr()
+
+    at = lambda: [(b.data, b.page_bytes, b.token_bytes) for b in (pool.c(None, True)._obj.buffers[i] for i in range(12))]  # noqa: E731
+    want = lambda: [(t.data_ptr(), t.numel() // 5, t.shape[-1]) for k in (cache, other) for t in k.tensors()]  # noqa: E731
+    assert at() == want()
+    old = weakref.ref(cache.v_data)
+    cache.v_data = cache.v_data.clone()
+    gc.collect()
+    assert old() is not None                                                    # the pool's struct still has it
+    assert at() == want() and pool.c(out, True)._obj.buffers[2].data == cache.v_data.data_ptr()
+    gc.collect()
+    assert old() is None
+    cache.k_scale = torch.zeros(4, 2, 128, 8, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        pool.c(None, True)
