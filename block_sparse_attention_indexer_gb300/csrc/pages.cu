@@ -342,7 +342,7 @@ struct PageBuffers {
   int32_t count;
 };
 
-// n bytes; both addresses have the same place within 16 bytes, or are copied byte by byte.
+// n bytes, 16 at a time where both addresses are multiples of 16, otherwise one at a time.
 __device__ __forceinline__ void copy_bytes(char* dst, const char* src, int n) {
   const int tid = threadIdx.x;
   const uintptr_t d = reinterpret_cast<uintptr_t>(dst), s = reinterpret_cast<uintptr_t>(src);

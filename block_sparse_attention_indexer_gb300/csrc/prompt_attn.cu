@@ -92,7 +92,7 @@ struct PtShared {
   uint64_t k_full[kPtK], k_empty[kPtK], v_empty[kPtV];
   uint64_t v_full[kPtV], v_edge[kPtV], v_ok[kPtV];  // plain blocks by turns; edge blocks by turns: copied, looked through
   uint64_t item_full[kPtItems], item_empty[kPtItems];
-  uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [slot], [slot][half of the keys]
+  uint64_t s_full[2], p_full[2][2], pv_done[2];     // [slot], [slot][half of the keys], [slot]
   uint64_t q_full[2], q_empty[2];                   // [tile]
   uint64_t fin[2], o_full[2], o_empty[2];           // [slot], a unit's: factors left, products done, O read
   uint64_t other;                                   // slot 1's statistics of a one-tile unit left
@@ -337,13 +337,6 @@ __device__ __forceinline__ void registers_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The largest of three (a NaN is left aside)
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // 1 / x to one unit in the last place, for x from 2^-126 to 2^126
 __device__ __forceinline__ float rcp(float x) {
   float y;
@@ -446,10 +439,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(&sh->p_full[i][h], 4);
-        mbar_init(&sh->pv_done[i][h], 1);
-      }
+      for (int h = 0; h < 2; ++h) mbar_init(&sh->p_full[i][h], 4);
+      mbar_init(&sh->pv_done[i], 1);
       mbar_init(&sh->q_full[i], 1);
       mbar_init(&sh->q_empty[i], 1);
       mbar_init(&sh->fin[i], 4);
@@ -569,7 +560,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
             l_bf16 *= alpha;
           }
           if (p > first) {  // O as the products so far leave it, rescaled
-            if (!pt_wait_warp(&sh->pv_done[slot][1], (done - 1) & 1)) {
+            if (!pt_wait_warp(&sh->pv_done[slot], (done - 1) & 1)) {
               failed = true;
               break;
             }
@@ -1089,7 +1080,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
             if (scores) {
               // S overwrites the slot's P: it waits until that has been multiplied
               if ((p == it.lo && !pt_wait(&sh->q_full[i], ((i ? tiles1 : tiles0) - 1) & 1)) ||
-                  (d > 0 && !pt_wait(&sh->pv_done[s][1], (d - 1) & 1))) {
+                  (d > 0 && !pt_wait(&sh->pv_done[s], (d - 1) & 1))) {
                 bad = true;
                 break;
               }
@@ -1124,7 +1115,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
                 for (int kk = 0; kk < 4; ++kk)  // 16 keys: 8 TMEM columns of P, two 8-row groups of V
                   umma_f16_tmem_a(tmem + kPtO + s * 128, tmem + s * 128 + h * 64 + 8 * kk, vd + ((kk * 2048) >> 4), id_o,
                                   !first || h > 0 || kk > 0 ? 1u : 0u);
-                umma_commit(&sh->pv_done[s][h]);
+                if (h == 1) umma_commit(&sh->pv_done[s]);
                 if (final && h == 1) umma_commit(&sh->o_full[s]);
                 if (last && h == 1) umma_commit(&sh->v_empty[vs]);
               }
