@@ -2,10 +2,11 @@
 //
 // Mathematics: P_j = 2^(e_j - M) with e_j = (q . k_j) softmax_scale log2(e), O = sum P_j v_j, l = sum P_j; lse = ln 2 (M +
 // log2 l).  M is an integer (rescaling O and l is exact) that moves only where a P would pass 1, to 2^8 above the largest
-// so far, so that most blocks move nothing.  P is rounded to bf16, V's type, as the operand of P V: by 2^-8 of itself at
-// most, whatever its size (bf16 has float32's range).  O is divided by the sum of the rounded P: a common part of their
-// errors cancels, and a row's error is at most that of rounding its output, on average (with l, a row of one key
-// would be off by P's whole rounding).  l adds P before the rounding, for lse.  S, O, l and M are float32.
+// so far, so that most blocks move nothing; rows with an e of 2^27 or more have a way of their own (kPtFused).
+// P is rounded to bf16, V's type, as the operand of P V: by 2^-8 of itself at most, whatever its size (bf16 has
+// float32's range).  O is divided by the sum of the rounded P: a common part of their errors cancels, and a row's
+// error is at most that of rounding its output, on average (with l, a row of one key would be off by P's whole
+// rounding).  l adds P before the rounding, for lse.  S, O, l and M are float32.
 //
 // Work.  A row is a (token, head) of a KV head; a tile is 128 rows, floor(128 / Hg) tokens with their Hg heads, a
 // unit two tiles (or one, of a sequence's last tokens) of a sequence and a KV head, so that keys loaded once meet
@@ -63,6 +64,12 @@ constexpr int kPtHalf = kPtTile / 2;          // 64 dims of it
 constexpr int kPtPlaceFloats = 2 * kPtRows * (kDim + 2);
 constexpr uint32_t kPtO = 256;                // TMEM column of slot 0's O
 constexpr float kPtRefSet = 8.f;
+// From this size of a row's largest e on, e is rounded to float32 before M is subtracted, and M is the largest e itself.  Below it
+// S f - M is one fma, with S f exact, while M comes from the rounded S f: the two differ by up to half a unit in the last
+// place, 4 below 2^27 but 256 and more from 2^32 on, where every P would be 0 or the largest infinite.  For such rows
+// (e - M) / f takes the place of S, and 0 that of M, so that the others' code stays as it is: with a factor and a reference of their
+// own for every row, 32 ragged prompts took 363 us instead of 357.
+constexpr float kPtFused = 134217728.f;
 constexpr int kPtUnitCost = kPromptUnitCost;
 // Cost of a unit up to which it is not cut: a cut costs two partial states and a merge, a cut moved to the end of its
 // unit leaves one CTA up to half of the unit more than its share.
@@ -501,6 +508,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
     int done = 0, live = 0;                        // steps of this slot, units with keys so far
     bool shared_par = false;
     float M = -INFINITY, l = 0.f, l_bf16 = 0.f;    // (l_bf16: of P as it is multiplied)
+    float fused = -INFINITY;                       // M, but -inf in rows whose e is rounded first (kPtFused)
     int pos = 0;
 
     for (int n = 0;; ++n) {
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       if (it.flags & kPtEnd) break;
       if (it.lo >= it.hi) continue;
       const bool two = it.flags & kPtTwo;
-      M = -INFINITY;
+      M = fused = -INFINITY;
       l = l_bf16 = 0.f;
       pos = it.pos0 + min(min(my_token, tt - 1) + (two && slot ? tt : 0), it.tokens - 1);
       // with one tile the blocks alternate between the slots
@@ -550,12 +558,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
         asm volatile("" : "+f"(mx), "+f"(mx1));
         mx = fmaxf(mx, mx1);
         mx *= f;
-        if (__builtin_expect(__any_sync(0xffffffffu, mx > M), 0)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, mx > fused), 0)) {
           float alpha = 1.f;
           if (mx > M) {
-            const float mn = ceilf(mx) + kPtRefSet;
+            const bool large = !(fabsf(mx) < kPtFused);
+            const float mn = large ? mx : ceilf(mx) + kPtRefSet;
             alpha = ex2(M - mn);
             M = mn;
+            fused = large ? -INFINITY : mn;
             l *= alpha;
             l_bf16 *= alpha;
           }
@@ -575,9 +585,30 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
               tmem_st16(tO + 16 * c, y);
             }
           }
+          if (__builtin_expect(__any_sync(0xffffffffu, fused != M), 0)) {  // in those rows (e - M) / f in the place of S
+            float rf;
+            asm("rcp.approx.f32 %0, %1;" : "=f"(rf) : "f"(f));  // (f may be above 2^126)
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t x[16];
+              tmem_ld16(tS + 16 * c, x);
+              tmem_wait_ld(x);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float e = __fmul_rn(__uint_as_float(x[j]), f);
+                x[j] = fused != M ? __float_as_uint((e - M) * rf) : x[j];
+              }
+              tmem_st16(tS + 16 * c, x);
+            }
+            tmem_wait_st();
+            tmem_ld64(tS, v[0]);
+            tmem_ld64(tS + 64, v[1]);
+            tmem_wait_ld(v[0]);
+            tmem_wait_ld(v[1]);
+          }
         }
         // P goes over the first 32 columns of each half of S
-        const float c0 = M == -INFINITY ? 0.f : -M;
+        const float c0 = fused == -INFINITY ? 0.f : -fused;
         const float2 ff = make_float2(f, f), cc = make_float2(c0, c0);
         float2 sum = make_float2(0.f, 0.f);
         float sum_bf16[4] = {0.f, 0.f, 0.f, 0.f};

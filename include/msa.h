@@ -425,7 +425,8 @@ msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int
  * arithmetic makes of them; one in v the results of the rows that see it, in its dim.
  * cu_q and cu_k must not decrease, start below 0 or end past q_tokens and k_tokens: otherwise
  * MSA_DEVERR_BAD_SEQLEN is set and nothing is written.
- * Rounding: logits, sums and lse are float32.  A probability meets its V row as bfloat16, and out is divided
+ * Rounding: logits, sums and lse are float32 (a logit that float32 does not hold, or not times log2(e), counts as infinite).
+ * A probability meets its V row as bfloat16, and out is divided
  * by the sum of the rounded ones (lse has the sum before the rounding), so that before its own rounding
  * out[d] is off by at most (2^-7 + 2^-14 + twice the largest error of a logit) * sum_j p_j |v_jd|, by nothing for a
  * row of one key.  The same arguments give the same bits in every call on one GPU.

@@ -345,3 +345,36 @@ def test_the_plan_is_read_before_keys_are_copied_over_it(lens_q, lens_k, G, Hg):
         p.call()
         different += (p.out != out).sum() + (p.lse != lse).sum()
     assert int(different) == 0 and p.results()[2] == 0
+
+
+# Scores from small ones to where float32 numbers lie 2^80 apart.
+@pytest.mark.parametrize("scale", [0.0, 1.0, 100.0, 2.0 ** 70])
+@pytest.mark.parametrize("lens_q,lens_k,G,Hg", [
+    ([1], [1], 1, 1), ([1, 2, 5], None, 1, 8), ([300, 40], None, 2, 5),     # dealt out as they come
+    ([1100], None, 2, 8),                                                    # planned, whole
+    ([40], [5000], 2, 8), ([1], [6000], 1, 8), ([130, 1], [2000, 3000], 1, 4),   # cut
+])
+def test_large_logits(scale, lens_q, lens_k, G, Hg):
+    """Finite scores of any size.  Every element of a query is x and of a key 24,576 s, x and s powers of two or 3 or 9 times
+    one: 128 equal products, whose sums are exact in float32 in any order.  So equal scores stay equal, others are apart by far more than
+    the softmax can tell, and a row is the mean of V over its keys with the largest score: the tolerance of out has no term
+    for the logits.  lse is off by the factor's three roundings, one of the product, two of the sum with log2 l, two of ln 2:
+    8 * 2^-24 of it."""
+    import torch
+    p = Prompts(102, lens_q, lens_k, G=G, Hg=Hg, scale=scale)
+    x = torch.tensor([24576.0, -24576.0, 18432.0, 1.0, 98304.0, -98304.0, 2.0 ** -6, 49152.0]).to(torch.bfloat16)
+    p.q[:] = x[:p.Hg].repeat(p.G)[None, :, None]
+    for b in range(p.B):
+        n = int(p.cu_k[b + 1] - p.cu_k[b])
+        j = torch.arange(n)
+        # signs by turns; all positive; rising, from a size that is not large
+        s = (torch.tensor([1.0, -1.0, 1.0, 0.5])[j % 4], torch.tensor([0.5, 1.0, 0.25, 1.0])[j % 4],
+             torch.exp2(torch.floor(24.0 * j / n) - 23))[(b + len(lens_q) + G) % 3]
+        p.k[int(p.cu_k[b]):int(p.cu_k[b + 1])] = (24576.0 * s).to(torch.bfloat16)[:, None, None]
+    ref = p.oracle()
+    assert np.isfinite(ref["lse"]).all()
+    out, lse, err = run(p)
+    assert err == 0 and np.isfinite(out).all()
+    rel = 2.0 ** -20 + ref["keys"] * 2.0 ** -24 + 2.0 ** -7 + 2.0 ** -14
+    close("out", out, ref["out"], 2.0 ** -8 * np.abs(ref["out"]) + rel[..., None] * ref["spread"] + 1e-30)
+    close("lse", lse, ref["lse"], 2.0 ** -20 + ref["keys"] * 2.0 ** -24 + 2.0 ** -21 * np.abs(ref["lse"]))
