@@ -26,7 +26,7 @@ msa_status_t check_packed(const msa_config_t* c, const msa_packed_t* p) {
 }
 
 struct PromptLayout {
-  size_t plan, base, order, dealt, prefix, cuts, partial, total;
+  size_t plan, base, order, dealt, prefix, cuts, row_max, partial, total;
 };
 PromptLayout prompt_layout(const msa_config_t* c, const msa_packed_t* p) {
   PromptLayout w;
@@ -36,7 +36,8 @@ PromptLayout prompt_layout(const msa_config_t* c, const msa_packed_t* p) {
   w.dealt = w.order + align_up(kPromptSpreadUnits * sizeof(int32_t));
   w.prefix = w.dealt + align_up(prompt_dealt_bytes());
   w.cuts = w.prefix + align_up((prompt_max_units(p->q_tokens, p->batch, c->heads_per_group) + 1) * sizeof(int32_t));
-  w.partial = w.cuts + align_up(prompt_cut_bytes());
+  w.row_max = w.cuts + align_up(prompt_cut_bytes());
+  w.partial = w.row_max + align_up(prompt_row_max_bytes());
   w.total = w.partial + align_up(prompt_partial_bytes());
   return w;
 }
@@ -108,6 +109,7 @@ msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed
   a.order = reinterpret_cast<int32_t*>(ws + w.order);
   a.dealt = reinterpret_cast<int2*>(ws + w.dealt);
   a.cuts = reinterpret_cast<PtCut*>(ws + w.cuts);
+  a.row_max = reinterpret_cast<float*>(ws + w.row_max);
   a.partial = reinterpret_cast<float*>(ws + w.partial);
   try {  // (the launch's bookkeeping allocates host memory: nothing may leave a C entry)
     return launch_prompt_attn(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;

@@ -29,6 +29,7 @@ struct PromptArgs {
   int32_t* order;       // [kPromptSpreadUnits]: the units by falling cost
   int2* dealt;          // [CTAs][...]: each CTA's units, where they stay whole
   PtCut* cuts;   // [CTAs]: the unit inside which each CTA's range starts
+  float* row_max;       // [CTAs][2][two tiles]: M of the rows of each CTA's last two units
   float* partial;       // partial softmax states of units cut by the split of the work
 };
 
@@ -44,6 +45,7 @@ inline int64_t prompt_max_units(int64_t q_tokens, int batch, int heads_per_group
 }
 size_t prompt_dealt_bytes();
 size_t prompt_cut_bytes();
+size_t prompt_row_max_bytes();
 size_t prompt_partial_bytes();
 cudaError_t launch_prompt_attn(const PromptArgs& a, int num_sms, cudaStream_t s);
 

@@ -23,8 +23,8 @@
 // Warps: 0-3 and 4-7 softmax of slot 0 and 1 (one row per thread, a block's 128 scores in registers), 8-11 write the
 // rows of a unit while the next one's softmax runs, and look through the V rows that not every row of a unit sees, 12 makes the
 // units known and copies Q and K, 13 issues the products S, 14 P V, 15 copies V.
-// What a row does not see cannot reach it: its S is replaced by -inf, and infinities and NaN in V are taken
-// out of the blocks where they could meet a P of 0; rows that do see them get them back at the end.
+// What a row does not see cannot reach it: its S is replaced by -inf, and infinities and NaN in V are taken out of the blocks
+// that not every row of the unit sees; rows that do see them get them back at the end, times their probability.
 // Every wait is bounded; a role that gives up flags MSA_DEVERR_TIMEOUT, leaves its loop and meets
 // the others at the end, where TMEM is freed.
 //
@@ -44,6 +44,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <limits.h>
 
 #include "fp8_device.cuh"
 #include "fp8_kernels.h"
@@ -389,29 +390,47 @@ __device__ __forceinline__ void turn_quad(uint4 (&w)[4]) {
 __device__ __forceinline__ uint32_t bf16_special(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 // What was taken out of V comes back to the rows that see its key: the infinities and NaN of the unit's keys that not
-// every row sees, added to its outputs or its partial state by the threads that wrote these.
+// every row sees, times the row's probability (an infinity is NaN where that is 0, as it is in a product), added to the
+// row's outputs or its partial state by the threads that wrote these.  flags: the unit's, the top bit set in every other unit,
+// by which the rows' M are found.  (More registers in here are spills in the caller: what is only needed for a value that
+// comes back is computed from the arguments there.)
 __device__ __noinline__ void pt_put_back(const PromptArgs& a, int flags, int lo, int hi, int token0, int tokens, int pos0,
                                          int key0, int g) {
-  const int Hg = a.heads_per_group, H = a.groups * Hg, tt = kPtRows / Hg, place = (flags >> kPtPlace) - 1;
-  const uint16_t* v = a.v + key0 * a.v_stride + g * kDim;
-  float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + max(place, 0)) * kPtPlaceFloats;
+#pragma unroll 1
   for (int pr = threadIdx.x & 127; pr < 2 * kPtRows; pr += 128) {
-    const int r = pr & (kPtRows - 1), t = r / Hg + (pr >= kPtRows ? tt : 0);
-    if (r / Hg >= tt || t >= tokens) continue;
-    uint16_t* out = a.out + (static_cast<int64_t>(token0 + t) * H + g * Hg + r % Hg) * kDim;
-    const int last = min(pos0 + t, hi * kBlock - 1);
-    for (int j = max(pos0 + 1, lo * kBlock); j <= last; ++j)
+    const int Hg = a.heads_per_group, tt = kPtRows / Hg, row = (pr & (kPtRows - 1)) / Hg, h = (pr & (kPtRows - 1)) - row * Hg;
+    const int t = row + (pr >= kPtRows ? tt : 0);
+    if (row >= tt || t >= tokens) continue;
+#pragma unroll 1
+    for (int j = max(pos0 + 1, lo * kBlock); j <= min(pos0 + t, hi * kBlock - 1); ++j) {
+      float p = -1.f;  // the row's probability of the key, once it is asked for
+#pragma unroll 1
       for (int d = 0; d < kDim; ++d) {
-        const float y = __uint_as_float(static_cast<uint32_t>(v[j * a.v_stride + d]) << 16);
+        float y = __uint_as_float(static_cast<uint32_t>(a.v[(key0 + j) * a.v_stride + g * kDim + d]) << 16);
         if (fabsf(y) < INFINITY) continue;
+        const int head = g * a.heads_per_group + h;
+        if (p == -1.f) {
+          const uint16_t *q = a.q + (token0 + t) * a.q_stride + head * kDim, *k = a.k + (key0 + j) * a.k_stride + g * kDim;
+          float z = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < kDim; ++i, ++q, ++k)
+            z += __uint_as_float(static_cast<uint32_t>(*q) << 16) * __uint_as_float(static_cast<uint32_t>(*k) << 16);
+          const float m = *static_cast<const volatile float*>(a.row_max + (2 * blockIdx.x + (flags < 0 ? 0 : 1)) * (2 * kPtRows) + pr);
+          const float f = finite_factor(a.scale_log2);
+          p = m == -INFINITY ? 0.f : ex2(fabsf(m) < kPtFused ? fmaf(z, f, -m) : __fmul_rn(z, f) - m);
+        }
+        y *= p;
+        const int place = ((flags & 0x7FFFFFFF) >> kPtPlace) - 1;
         if (place < 0) {
-          volatile uint16_t* dst = out + d;
+          volatile uint16_t* dst = a.out + ((token0 + t) * static_cast<int64_t>(a.groups * a.heads_per_group) + head) * kDim + d;
           *dst = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(static_cast<uint32_t>(*dst) << 16) + y, 0.f));
         } else {
-          volatile float* dst = part + (d / 4) * (8 * kPtRows) + 4 * pr + (d & 3);
+          volatile float* dst = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats + (d / 4) * (8 * kPtRows) +
+                                4 * pr + (d & 3);
           *dst += y;
         }
       }
+    }
   }
 }
 
@@ -678,10 +697,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       sh->factor[slot][r] = fa * inv;
       if (!two) sh->factor[1][r] = fb * inv;
       const int t = my_token + (two && slot ? tt : 0);               // token of the unit
+      const int pr = r + (two && slot ? kPtRows : 0);                // row of the unit
+      a.row_max[(2 * blockIdx.x + (live & 1)) * (2 * kPtRows) + pr] = M;
       if (my_token < tt && t < it.tokens) {
         if (place >= 0) {
           float* part = a.partial + (2 * static_cast<int64_t>(blockIdx.x) + place) * kPtPlaceFloats + 2 * kPtRows * kDim;
-          const int pr = r + (two && slot ? kPtRows : 0);            // row of the partial state
           part[pr] = M;
           part[2 * kPtRows + pr] = l;
         } else if (a.lse != nullptr) {
@@ -779,7 +799,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) prompt_attn_kernel(const __grid
       if (edges > 0 && !pt_wait_warp(&sh->v_ok[(edges - 1) % kPtV], ((edges - 1) / kPtV) & 1)) return false;
       const int* sp = sh->special[n & 7];
       if (sp[0] == n || sp[1] == n || sp[2] == n || sp[3] == n)
-        pt_put_back(a, it.flags, it.lo, it.hi, it.token0, it.tokens, it.pos0, it.key0, it.g);
+        pt_put_back(a, it.flags | (n & 1 ? INT_MIN : 0), it.lo, it.hi, it.token0, it.tokens, it.pos0, it.key0, it.g);
       return true;
     };
     PtItem before{};  // the last unit with keys, not written yet
@@ -1320,6 +1340,7 @@ __global__ void __launch_bounds__(kFp8MergeThreads, kSplit ? 1 : 4) prompt_merge
 
 size_t prompt_dealt_bytes() { return kFp8MaxCtas * kPtMaxDealt * sizeof(int2); }
 size_t prompt_cut_bytes() { return kFp8MaxCtas * sizeof(PtCut); }
+size_t prompt_row_max_bytes() { return static_cast<size_t>(kFp8MaxCtas) * 4 * kPtRows * sizeof(float); }
 size_t prompt_partial_bytes() { return static_cast<size_t>(2) * kFp8MaxCtas * kPtPlaceFloats * sizeof(float); }
 
 static cudaError_t prompt_maps(const PromptArgs& a, PromptMaps* maps) {

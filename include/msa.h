@@ -414,15 +414,17 @@ msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int
  * h / Hg with logits z_j = (q . k_j) * softmax_scale:
  *   out  = sum_j e^{z_j - lse} v_j   bfloat16 [q_tokens][G*Hg][D]
  *   lse  = ln sum_j e^{z_j}          float [q_tokens][G*Hg], may be NULL
- * A row with no key (Lk < Lq: the first Lq - Lk tokens), or whose logits are all -inf, gives out 0
- * and lse -inf.  Rows of tokens that belong to no sequence are left as they are.
+ * A row with no key (Lk < Lq: the first Lq - Lk tokens), or whose logits are all -inf and what it sees of v
+ * finite, gives out 0 and lse -inf.  Rows of tokens that belong to no sequence are left as they are.
  *   q        bfloat16 [q_tokens][G*Hg][D], k, v bfloat16 [k_tokens][G][D]: the heads of a token are
  *            contiguous, tokens are q_stride (k_stride, v_stride) elements apart, so that slices of
  *            one fused projection's rows need no copy.  Pointers and strides in bytes are multiples
  *            of 16, strides at least a token's elements.  out may not overlap an input.
  * Keys that a row does not see (later ones, other sequences') do not touch it, whatever they
  * hold.  Other NaN and infinities in q or k make the rows whose logits they reach what float
- * arithmetic makes of them; one in v the results of the rows that see it, in its dim.
+ * arithmetic makes of them.  One in v makes the results of the rows that see it, in its dim, what adding its product with
+ * the probability makes of them: NaN for a NaN, and for an infinity itself, or NaN where the probability is 0 (a logit
+ * of -inf, alone or beside others, or one further below the row's largest than float32's exponents go; close to that either).
  * cu_q and cu_k must not decrease, start below 0 or end past q_tokens and k_tokens: otherwise
  * MSA_DEVERR_BAD_SEQLEN is set and nothing is written.
  * Rounding: logits, sums and lse are float32 (a logit that float32 does not hold, or not times log2(e), counts as infinite).

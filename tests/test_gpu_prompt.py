@@ -378,3 +378,50 @@ def test_large_logits(scale, lens_q, lens_k, G, Hg):
     rel = 2.0 ** -20 + ref["keys"] * 2.0 ** -24 + 2.0 ** -7 + 2.0 ** -14
     close("out", out, ref["out"], 2.0 ** -8 * np.abs(ref["out"]) + rel[..., None] * ref["spread"] + 1e-30)
     close("lse", lse, ref["lse"], 2.0 ** -20 + ref["keys"] * 2.0 ** -24 + 2.0 ** -21 * np.abs(ref["lse"]))
+
+
+@pytest.mark.parametrize("what", ["minus infinity", "far below"])
+@pytest.mark.parametrize("lens_q,lens_k,G,Hg", [
+    ([300, 40, 6], None, 2, 8), ([150, 10], None, 1, 3),                     # dealt out as they come
+    ([1100], None, 2, 8),                                                    # planned, whole
+    ([40], [5000], 2, 8), ([1], [6000], 1, 8), ([130, 1], [2000, 3000], 1, 4),   # cut
+])
+def test_special_values_of_no_probability(lens_q, lens_k, G, Hg, what):
+    """Infinities and NaN in v at keys whose probability is 0: what 0 times them gives, wherever the key lies in a unit."""
+    p = Prompts(104, lens_q, lens_k, G=G, Hg=Hg)
+    p.q[:, :, 0] = 64.0
+    low = []
+    for b in range(p.B):
+        a, n = int(p.cu_k[b]), int(p.cu_k[b + 1] - p.cu_k[b])
+        low += [a + x for x in {1, 5, n // 3, n // 2, n - 129, n - 33, n - 18, n - 2, n - 1} if 0 < x < n]
+    for i, key in enumerate(sorted(low)):
+        p.v[key, :, 3 + 5 * i % 120] = np.inf
+        p.v[key, :, 4 + 5 * i % 120] = -np.inf
+        p.v[key, :, 5 + 5 * i % 120] = np.nan
+        p.v[key - 1, 0, 3 + 5 * i % 120] = np.inf                            # and one that has a probability beside it
+    k = p.k.clone()
+    k[low] = 0.0
+    p.k[low, :, 0] = -np.inf if what == "minus infinity" else -4096.0        # e^-23,000
+    ref = p.oracle()
+    special = ~np.isfinite(ref["out"])
+    assert np.isnan(ref["out"]).any() and np.isfinite(ref["lse"]).all()
+    ref["spread"] = np.where(special, 0.0, ref["spread"])
+    got = run(p)
+    p.k = k                                                                  # the other keys' logits are what has an error
+    ref["logit"] = p.oracle()["logit"]
+    p.check(got, ref)
+
+
+@pytest.mark.parametrize("lens_q,lens_k,Hg", [([40], None, 2), ([300], None, 8), ([30], [5000], 8), ([1], [4000], 8)])
+def test_special_values_in_rows_of_minus_infinity(lens_q, lens_k, Hg):
+    """Rows whose logits are all -inf: 0, and NaN in the dims where what they see of v is not finite."""
+    p = Prompts(105, lens_q, lens_k, G=1, Hg=Hg)
+    p.q[:], p.k[:] = 0.0, 0.0
+    p.q[:, :, 0], p.k[:, :, 0] = 1.0, -np.inf
+    want = np.zeros((p.Nq, p.H, 128))
+    for back, dim, what in ((p.Nk - 3, 7, np.inf), (20, 1, np.nan), (7, 9, -np.inf), (1, 100, np.inf), (min(p.Nk, 250), 50, np.inf)):
+        p.v[p.Nk - back, 0, dim] = what
+        want[max(0, p.Nq - back):, :, dim] = np.nan
+    got = run(p)
+    close("out", got[0], want, np.zeros_like(want))
+    assert (got[1] == -np.inf).all() and got[2] == 0
