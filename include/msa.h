@@ -435,8 +435,8 @@ msa_status_t msa_evict_blocks(const msa_batch_t* batch, const float* weight, int
  * workspace: msa_prompt_workspace_bytes(...); calls that can overlap need one each.
  * Errors: MSA_ERR_UNSUPPORTED for q_tokens or k_tokens above 2^28, or where the call's pairs of
  * 128 query rows and 128 keys cannot be counted in 31 bits: G * (floor(q_tokens / (2 * floor(128 / Hg))) + batch) *
- * (2 * ceil(k_tokens / 128) + 4) > 2^31 - 1 (about 900,000 tokens of 32 heads).  MSA_ERR_CUDA also when the driver's tensor-map encoder is
- * not available. */
+ * (2 * max(1, ceil(k_tokens / 128)) + 4) > 2^31 - 1 (about 1,048,000 tokens of 32 heads).  MSA_ERR_CUDA also when the
+ * driver's tensor-map encoder is not available. */
 size_t msa_prompt_workspace_bytes(const msa_config_t* cfg, const msa_packed_t* packed);
 msa_status_t msa_prompt_attn(const msa_config_t* cfg, const msa_packed_t* packed, const void* q, int64_t q_stride,
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, uint16_t* out,

@@ -200,3 +200,20 @@ def test_pool_goes_by_its_present_tensors(msa, monkeypatch):
     cache.k_scale = torch.zeros(4, 2, 128, 8, dtype=torch.uint8)
     with pytest.raises(ValueError):
         pool.c(None, True)
+
+
+@pytest.mark.parametrize("G,Hg,batch", [(4, 8, 1), (8, 4, 1), (8, 8, 3), (1, 1, 1), (2, 3, 700)])
+def test_prompt_limit(msa, G, Hg, batch):
+    """Tokens that a call may have, from the formula in msa.h: the last number that is taken and the first that is not."""
+    b = msa.binding
+    cfg = b._Config(G, Hg, 128, 128, 128, 16, 0, 1, 0.0)
+    taken = lambda q, k: b._lib.msa_prompt_workspace_bytes(r(cfg), r(b._Packed(P, P, batch, q, k))) > 0  # noqa: E731
+    fits = lambda q, k: G * (q // (2 * (128 // Hg)) + batch) * (2 * max(1, -(-k // 128)) + 4) <= 2 ** 31 - 1  # noqa: E731
+    for both in (True, False):               # as many keys as queries; no keys
+        lo, hi = 1, 1 << 28
+        while lo < hi:
+            mid = (lo + hi + 1) // 2
+            lo, hi = (mid, hi) if fits(mid, mid if both else 0) else (lo, mid - 1)
+        assert taken(lo, lo if both else 0) and not taken(lo + 1, lo + 1 if both else 0)
+        if both and G * Hg == 32:
+            assert 1_045_000 < lo < 1_050_000
