@@ -494,3 +494,48 @@ def test_counts_and_tensors_replaced_between_calls():
     assert p.err() == err2 == OP.BAD_SEQLEN                                     # (the first one has no room for 200 more)
     p.same_buffers()
     assert torch.equal(old, before)
+
+
+# One launch up to 2,048 pages and 8,192 copied entries of a table, two beyond.
+@pytest.mark.parametrize("P", [2047, 2048, 2049, 4096, 4097])
+@pytest.mark.parametrize("rows,width", [(64, 128), (3, 2731), (129, 64), (1, 1)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_extend_and_fork_around_one_launch(P, rows, width, in_place):
+    import torch
+    import block_sparse_attention_indexer_gb300 as msa
+    p = Pool(P + rows, [0] * rows, P, width, caches=[("fp8", 1)])
+    refs = p.rng.integers(0, 3, P).astype(np.int32)
+    refs[-2:] = 0                                               # the last free pages are handed out as well
+    lens = p.rng.integers(0, width * 64, rows).astype(np.int32)
+    table = p.rng.integers(0, P, (rows, width)).astype(np.int32)
+    free, new = int((refs == 0).sum()), np.zeros(rows, np.int32)
+    for b in range(rows):                                       # as many tokens as there are pages for, the first row the most
+        blocks = min(free, width - OP.blocks(lens[b]), free if b == 0 else 7)
+        new[b] = blocks * 128
+        free -= blocks
+    p.d_refs.copy_(dev(refs))
+    p.d_table.copy_(dev(table))
+    p.d_lens.copy_(dev(lens))
+    want = OP.extend(refs, table, lens, new)
+    kw = outs(p, rows, in_place)
+    if not in_place:
+        kw["seq_lens_out"] = torch.full((rows,), 77, dtype=torch.int32, device="cuda")
+    msa.msa_extend_pages(p.pool, p.batch, p.ws, new_tokens=dev(new), **kw)
+    for got, x in zip((kw.get("refs_out", p.d_refs), kw.get("table_out", p.d_table), kw.get("seq_lens_out", p.d_lens)), want):
+        assert np.array_equal(host(got), x)
+    assert p.err() == want[3] == 0
+    # children of the rows as they were, every row once and the first ones again; the counts as they were
+    parents = (np.arange(rows + 5) % rows).astype(np.int32)
+    refs[:] = np.where(p.rng.random(P) < 0.9, np.maximum(refs, 1), 0)
+    refs[-2:] = 0
+    table = p.rng.choice(np.flatnonzero(refs), (rows, width)).astype(np.int32)
+    p.d_refs.copy_(dev(refs))
+    p.d_table.copy_(dev(table))
+    p.d_lens.copy_(dev(lens))
+    refs, kids, kid_lens, err = OP.fork(refs, table, lens, parents, p.buffers)
+    to, out_lens = torch.empty(rows + 5, width, dtype=torch.int32, device="cuda"), torch.empty(rows + 5, dtype=torch.int32, device="cuda")
+    kw = {k: v for k, v in outs(p, rows, in_place).items() if k == "refs_out"}
+    msa.msa_fork_pages(p.pool, p.batch, dev(parents), to, out_lens, p.ws, **kw)
+    assert np.array_equal(host(kw.get("refs_out", p.d_refs)), refs) and p.err() == err
+    assert np.array_equal(host(to), kids) and np.array_equal(host(out_lens), kid_lens)
+    p.same_buffers()
