@@ -9,7 +9,9 @@
 // The ranks are bound by latency, a few rounds of loads and barriers: 4.2 us in a graph for 38,000 pages of which 64
 // sequences take a few, 11.5 us for 890,000 of which 512 sequences take 70,000 (table and counts copied as well).  Measured
 // for these: one cluster of eight CTAs that meets in distributed shared memory 7.3 and 43 us; chunks of 8,192
-// pages 5.7 and 18 us.  Copies are bound by memory: 500 pages in 16 buffers of 64 KB a page 83 us, 6.3 TB/s.
+// pages 5.7 and 18 us.  Copies are bound by memory: a compaction that moves 500 pages in 8 buffers of 64 KB a page (and 8 of
+// four bytes) 88 us, 5.9 TB/s.  Every CTA of page_assign_kernel adds up the counts of all chunks: work that grows with the square of the
+// pool, nothing for a million pages (435 chunks), 17 GB read out of L2 for the 2^27 that a pool may have.
 #include "fp8_kernels.h"
 #include "msa_device.cuh"
 #include "pages.h"

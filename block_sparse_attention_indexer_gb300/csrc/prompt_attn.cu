@@ -29,18 +29,18 @@
 // the others at the end, where TMEM is freed.
 //
 // What bounds it: a slot's chain (S, softmax, P V of a block, one after another) is about as long as both slots' products,
-// and the products run at the power limit's clock (1.65 PFLOP/s for a prompt of 16K tokens and 32 heads; without any
-// exponential it would be 1.76).  Measured on the way there, for that prompt: S by halves of 64 keys, so that a half's product
-// runs beside the other's softmax, 1.78 ms against 1.43 (an M 128 x N 64 product takes 390 cycles where half of N 128
+// and the products run at the power limit's clock: 1.42 to 1.45 ms, 1.52 to 1.55 PFLOP/s, for a prompt of 16K tokens and 32
+// heads, 7 % less without any exponential.  Measured on the way there, for that prompt: S by halves of 64 keys, so that a half's
+// product runs beside the other's softmax, 1.78 ms against 1.43 (an M 128 x N 64 product takes 390 cycles where half of N 128
 // takes 256: its operands fill the shared memory's bandwidth); 64 scores at a time 1.51 against 1.33; one hand-over of P
 // for 128 keys 1.41 against 1.35; the exponentials of the second half held back behind the first half's hand-over 1.37.
 // Stages of K and V and register shares: 1 to 3 %.  Code that a unit runs once costs its instruction fetches (the
 // epilogue, unrolled masks: 1 us and more each), so it is short loops, and the softmax's loop has nothing
 // rare inside it; function calls in that branch cost it registers (1.40 -> 1.48 ms).  The compiler's report should show no
 // spills for it: changes of the V warps' code that brought 8 to 16 bytes of them cost 2 to 4 %, wherever they were.
-// Short units wait for latencies: for 32 prompts of 2 to 2,000 tokens (4,612 units, 354 us) 2 us of a unit's 12 are not its
-// steps, and tensor instructions run 60 % of the time (71 % for one prompt of 8K tokens, 357 us).  Products of 64 keys
-// where a unit's last block has no more: the same to 2 % slower.
+// Short units wait for latencies: for 31 prompts of 310 to 2,000 tokens (4,612 units, 357 to 361 us) 2 us of a unit's 12 are
+// not its steps, and tensor instructions run 58 % of the time (69 % for one prompt of 8K tokens, 365 us).  Products of 64
+// keys where a unit's last block has no more: the same to 2 % slower.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -69,14 +69,14 @@ constexpr float kPtRefSet = 8.f;
 // S f - M is one fma, with S f exact, while M comes from the rounded S f: the two differ by up to half a unit in the last
 // place, 4 below 2^27 but 256 and more from 2^32 on, where every P would be 0 or the largest infinite.  For such rows
 // (e - M) / f takes the place of S, and 0 that of M, so that the others' code stays as it is: with a factor and a reference of their
-// own for every row, 32 ragged prompts took 363 us instead of 357.
+// own for every row, 31 ragged prompts took 363 us instead of 357.
 constexpr float kPtFused = 134217728.f;
 constexpr int kPtUnitCost = kPromptUnitCost;
 // Cost of a unit up to which it is not cut: a cut costs two partial states and a merge, a cut moved to the end of its
 // unit leaves one CTA up to half of the unit more than its share.
 constexpr int kPtWhole = 16;
 // What cutting costs a call (partial states, the merge of 150 units) in steps: without cuts a CTA may have so much more
-// than its share.  One prompt of 1K 31 us cut and 26 whole, of 2K 51 and 39, of 4K 116 and 106, of 8K 368 and 357; 32 of 2
+// than its share.  One prompt of 1K 31 us cut and 26 whole, of 2K 51 and 39, of 4K 116 and 106, of 8K 368 and 357; 31 of 310
 // to 2,000 tokens 380 and 358.  4 chunks on 16K, 120 units for 152 CTAs, are cut (their longest has twice a CTA's share).
 constexpr int kPtCutSteps = 14;
 // Units (of a KV head) up to which they are put in order for that.
